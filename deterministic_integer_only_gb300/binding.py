@@ -26,7 +26,8 @@ ERRORS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "token id o
 SYMBOLS = ["detint_load", "detint_prefill", "detint_decode_step", "detint_gemm_i8",
            "detint_reset_seq", "detint_seq_len", "detint_status", "detint_set_graph",
            "detint_set_option", "detint_argmax_noalloc", "detint_sample", "detint_fork_seq", "detint_gemm_w16", "detint_split_w16",
-           "detint_int8_peak_loop", "detint_model_info", "detint_free", "detint_strerror", "detint_last_error"]
+           "detint_int8_peak_loop", "detint_kv4_append", "detint_kv4_workspace", "detint_kv4_decode",
+           "detint_kv4_prefill", "detint_model_info", "detint_free", "detint_strerror", "detint_last_error"]
 
 
 class DetintError(RuntimeError):
@@ -60,6 +61,11 @@ def lib():
         L.detint_split_w16.argtypes = [vp, vp, vp, C.c_longlong, vp]
         L.detint_sample.argtypes = [vp, C.c_int, C.c_int, C.POINTER(SamplingParams), vp, vp]
         L.detint_int8_peak_loop.argtypes = [C.c_int, C.c_int, C.c_int, vp, C.POINTER(C.c_longlong), vp]
+        ll = C.c_longlong
+        L.detint_kv4_append.argtypes = [vp, vp, vp, ll, vp, vp, C.c_int, vp, vp, vp, vp, vp, vp]
+        L.detint_kv4_workspace.argtypes = [vp, C.c_int, C.c_int, C.POINTER(ll)]
+        L.detint_kv4_decode.argtypes = [vp, vp, vp, vp, vp, vp, C.c_int, C.c_int, C.c_int, vp, ll, vp, ll, vp]
+        L.detint_kv4_prefill.argtypes = [vp, vp, vp, vp, vp, vp, C.c_int, C.c_int, C.c_int, vp, ll, vp]
         L.detint_model_info.argtypes = [vp, i32p]
         L.detint_free.argtypes = [vp]
         L.detint_free.restype = None
@@ -169,6 +175,188 @@ def detint_int8_peak_loop(kind: int, blocks: int, iters: int, sink, stream=None)
     _check(lib().detint_int8_peak_loop(int(kind), int(blocks), int(iters), _ptr(sink), C.byref(ops),
                                        _stream(stream)), "detint_int8_peak_loop")
     return int(ops.value)
+
+
+# ------------------------------------------------- the 4-bit paged K/V cache
+class _Kv4(C.Structure):
+    """detint_kv4_t"""
+    _fields_ = [(n, C.c_int32) for n in ("n_q", "n_kv", "head_dim", "n_blocks", "n_seq", "max_blocks")] + \
+               [(n, C.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "block_table", "params", "status")]
+
+
+class _Rope(C.Structure):
+    """detint_rope_t"""
+    _fields_ = [("cos", C.c_void_p), ("sin", C.c_void_p), ("max_pos", C.c_int32), ("rot_dim", C.c_int32),
+                ("interleaved", C.c_int32), ("eps", C.c_int32), ("q_gamma", C.c_void_p), ("k_gamma", C.c_void_p)]
+
+
+def _expect(where, name, t, dtype, numel, device):
+    """A contiguous tensor of `dtype` on `device` that holds numel elements."""
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() < numel:
+        raise ValueError(f"{where}: {name}: a contiguous {dtype} tensor of {numel} elements on {device} expected, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+class KV4Cache:
+    """A view of a 4-bit paged K/V cache in caller-owned cuda tensors.
+
+    k, v: uint8 with n_blocks * n_kv * 32 * head_dim elements, k as
+    [n_blocks, n_kv, 64, head_dim // 2]; k_scale, v_scale: uint8
+    [n_blocks, n_kv, 64]; block_table: int32 [n_seq, max_blocks]; params: int32
+    [n_kv, 8 + head_dim]; status: int32 [8] or None. The tensors are kept
+    alive with the view, and their memory is used in place."""
+
+    def __init__(self, k, v, k_scale, v_scale, block_table, params, n_q: int, status=None):
+        import torch
+        n_blocks, n_kv, blk, half = k.shape
+        if not k.is_cuda or blk != 64:
+            raise ValueError("KV4Cache: k: a cuda tensor [n_blocks, n_kv, 64, head_dim // 2] expected")
+        dev, d = k.device, 2 * half
+        n_seq, max_blocks = block_table.shape
+        pages = n_blocks * n_kv * 64
+        for name, t, dt, n in (("k", k, torch.uint8, pages * half), ("v", v, torch.uint8, pages * half),
+                               ("k_scale", k_scale, torch.uint8, pages), ("v_scale", v_scale, torch.uint8, pages),
+                               ("block_table", block_table, torch.int32, n_seq * max_blocks),
+                               ("params", params, torch.int32, n_kv * (8 + d))):
+            _expect("KV4Cache", name, t, dt, n, dev)
+        if status is not None:
+            _expect("KV4Cache", "status", status, torch.int32, 8, dev)
+        self.n_q, self.n_kv, self.head_dim, self.device = int(n_q), n_kv, d, dev
+        self._keep = (k, v, k_scale, v_scale, block_table, params, status)
+        self._c = _Kv4(int(n_q), n_kv, d, n_blocks, n_seq, max_blocks, _ptr(k), _ptr(v), _ptr(k_scale),
+                       _ptr(v_scale), _ptr(block_table), _ptr(params), _ptr(status))
+        self._ref = C.addressof(self._c)
+
+
+class RopeNorm:
+    """Rotation tables (int16 Q14 cuda tensors [max_pos, rot_dim // 2], or None
+    for no rotation), pair layout, and the optional per-head norm (int16 Q12
+    gammas, eps = round(eps 2^24)) of detint_kv4_append."""
+
+    def __init__(self, cos, sin, interleaved: bool = False, q_gamma=None, k_gamma=None, eps: int = 0,
+                 max_pos: int | None = None):
+        import torch
+        if (cos is None) != (sin is None) or (cos is None and max_pos is None):
+            raise ValueError("RopeNorm: both tables, or none and max_pos")
+        rot = 0
+        self.device = None
+        if cos is not None:
+            max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+            self.device = cos.device
+            _expect("RopeNorm", "cos", cos, torch.int16, max_pos * rot // 2, cos.device)
+            _expect("RopeNorm", "sin", sin, torch.int16, max_pos * rot // 2, cos.device)
+        self._gammas = 0 if q_gamma is None else q_gamma.numel()
+        for name, t in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+            if t is not None:
+                self.device = self.device or t.device
+                _expect("RopeNorm", name, t, torch.int16, self._gammas, self.device)
+        self._keep = (cos, sin, q_gamma, k_gamma)
+        self._c = _Rope(_ptr(cos), _ptr(sin), int(max_pos), rot, int(bool(interleaved)), int(eps), _ptr(q_gamma),
+                        _ptr(k_gamma))
+        self._ref = C.addressof(self._c)
+
+
+def _kv4_tokens(where, cache, tok_seq, tok_pos):
+    import torch
+    n = tok_pos.numel()
+    _expect(where, "tok_pos", tok_pos, torch.int32, n, cache.device)
+    _expect(where, "tok_seq", tok_seq, torch.int32, n, cache.device)
+    if torch.cuda.current_device() != cache.device.index:
+        raise ValueError(f"{where}: the cache is on {cache.device}, which is not the current device")
+    return n
+
+
+def _new(stream, shape, dtype, device):
+    """A tensor for a kernel on `stream` (None: the current one)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def detint_kv4_append(cache, rope, qkv, tok_seq, tok_pos, q8=None, mq=None, kq=None, k_val=None, v_val=None,
+                      stream=None):
+    """Norm, rotate and quantise the Q12 projections qkv [n_tok, (n_q + 2 n_kv)
+    head_dim] (int32, rows may be strided) and append keys and values to the
+    cache; returns (q8, mq, kq). k_val, v_val (int16 [n_tok, n_kv, head_dim])
+    receive the cached integers where given."""
+    import torch
+    w, dev = "detint_kv4_append", cache.device
+    n = _kv4_tokens(w, cache, tok_seq, tok_pos)
+    nq, d = cache.n_q, cache.head_dim
+    if qkv.dtype != torch.int32 or qkv.device != dev or qkv.dim() != 2 or qkv.shape[0] < n or \
+            qkv.shape[1] < (nq + 2 * cache.n_kv) * d or qkv.stride(1) != 1:
+        raise ValueError(f"{w}: qkv: int32 rows [n_tok, (n_q + 2 n_kv) head_dim] on {dev} expected")
+    if rope.device is not None and rope.device != dev or rope._gammas not in (0, d):
+        raise ValueError(f"{w}: tables or gammas do not fit the cache")
+    q8 = _new(stream, (n, nq, d), torch.int8, dev) if q8 is None else q8
+    mq = _new(stream, (n, nq), torch.int32, dev) if mq is None else mq
+    kq = _new(stream, (n, nq), torch.int32, dev) if kq is None else kq
+    _expect(w, "q8", q8, torch.int8, n * nq * d, dev)
+    _expect(w, "mq", mq, torch.int32, n * nq, dev)
+    _expect(w, "kq", kq, torch.int32, n * nq, dev)
+    for name, t in (("k_val", k_val), ("v_val", v_val)):
+        if t is not None:
+            _expect(w, name, t, torch.int16, n * cache.n_kv * d, dev)
+    stride = qkv.stride(0) if qkv.shape[0] > 1 else qkv.shape[1]
+    _check(lib().detint_kv4_append(cache._ref, rope._ref, qkv.data_ptr(), stride, tok_seq.data_ptr(),
+                                   tok_pos.data_ptr(), n, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), _ptr(k_val),
+                                   _ptr(v_val), _stream(stream)), w)
+    return q8, mq, kq
+
+
+def detint_kv4_workspace(cache, n_tok: int, max_len: int) -> int:
+    """Bytes of workspace of detint_kv4_decode; 0 for most sizes."""
+    n = C.c_longlong(0)
+    _check(lib().detint_kv4_workspace(cache._ref, int(n_tok), int(max_len), C.byref(n)), "detint_kv4_workspace")
+    return int(n.value)
+
+
+def _kv4_attn(w, cache, q8, mq, kq, tok_seq, tok_pos, out, stream):
+    import torch
+    n, dev = _kv4_tokens(w, cache, tok_seq, tok_pos), cache.device
+    nq, d = cache.n_q, cache.head_dim
+    _expect(w, "q8", q8, torch.int8, n * nq * d, dev)
+    _expect(w, "mq", mq, torch.int32, n * nq, dev)
+    _expect(w, "kq", kq, torch.int32, n * nq, dev)
+    if out is None:
+        out = _new(stream, (n, nq * d), torch.int32, dev)
+    elif out.dtype != torch.int32 or out.device != dev or out.dim() != 2 or out.shape[0] < n or \
+            out.shape[1] < nq * d or out.stride(1) != 1:
+        raise ValueError(f"{w}: out: int32 rows [n_tok, n_q head_dim] on {dev} expected")
+    return n, out, out.stride(0) if out.shape[0] > 1 else out.shape[1]
+
+
+def detint_kv4_decode(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, window: int = 0, out=None,
+                      workspace=None, stream=None):
+    """Attention of single tokens over the cache (detint_kv4_decode): int32 Q12
+    rows [n_tok, n_q head_dim]. workspace: a cuda uint8 tensor of
+    detint_kv4_workspace bytes (made here when it is needed and not given)."""
+    w = "detint_kv4_decode"
+    n, out, stride = _kv4_attn(w, cache, q8, mq, kq, tok_seq, tok_pos, out, stream)
+    if workspace is None:
+        import torch
+        need = detint_kv4_workspace(cache, n, max_len)
+        workspace = _new(stream, need, torch.uint8, cache.device) if need else None
+    elif workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError(f"{w}: workspace: a contiguous tensor on {cache.device} expected")
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().detint_kv4_decode(cache._ref, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), tok_seq.data_ptr(),
+                                   tok_pos.data_ptr(), n, int(max_len), int(window), out.data_ptr(), stride,
+                                   _ptr(workspace), size, _stream(stream)), w)
+    return out
+
+
+def detint_kv4_prefill(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, window: int = 0, out=None, stream=None):
+    """The attention of detint_kv4_decode, bit for bit, for blocks of tokens of
+    the same sequence (tokens of a sequence stand together)."""
+    w = "detint_kv4_prefill"
+    n, out, stride = _kv4_attn(w, cache, q8, mq, kq, tok_seq, tok_pos, out, stream)
+    _check(lib().detint_kv4_prefill(cache._ref, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), tok_seq.data_ptr(),
+                                    tok_pos.data_ptr(), n, int(max_len), int(window), out.data_ptr(), stride,
+                                    _stream(stream)), w)
+    return out
 
 
 def chain_hash(rows, prev: bytes | None = None) -> bytes:

@@ -1,6 +1,6 @@
 """Builds libdetint.so (the CUDA kernels and the C ABI) for sm_103a, in tree.
 
-nvcc compiles the two translation units in parallel, then links a shared
+nvcc compiles the translation units in parallel, then links a shared
 library next to this file. Nothing is installed into site-packages.
 """
 import os
@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libdetint.so")
 BUILD = os.path.join(HERE, "_build")
-SOURCES = ["launch.cu", "runtime.cu", "noalloc.cu", "sample.cu", "peak.cu"]
+SOURCES = ["launch.cu", "runtime.cu", "noalloc.cu", "sample.cu", "peak.cu", "kv4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "--expt-relaxed-constexpr"]

@@ -230,4 +230,49 @@ int32_t* standalone_status();
 
 cudaError_t kernels_init();
 
+// the 4-bit paged K/V cache (k_kv4.cuh): geometry and device memory
+struct Kv4Args {
+    int nq, n_kv, n_blocks, n_seq, max_blocks;
+    int gmul;                     // ceil(65536 / (q heads per kv head)): q head -> kv head
+    uint8_t *k, *v, *ks, *vs;
+    const int32_t* block_table;   // [n_seq][max_blocks]
+    const int32_t* params;        // [n_kv][8 + D]
+    int32_t* status;              // [ST_N] or null
+};
+struct Kv4Append {
+    const int32_t* qkv;
+    size_t qkv_stride;
+    const int32_t *tok_seq, *tok_pos;
+    int T, tile, qk_blocks;       // tokens, tokens per CTA, CTAs of q and k heads per tile
+    const int16_t *cos, *sin;     // [max_pos][rot / 2]
+    int max_pos, rot, inter;
+    const int16_t *q_gamma, *k_gamma;
+    long long eps;
+    int8_t* q8;
+    int32_t *mq, *kq;
+    int16_t *k_val, *v_val;       // or null
+};
+struct Kv4Attn {
+    const int8_t* q8;
+    const int32_t *mq, *kq, *tok_seq, *tok_pos;
+    int32_t* o;
+    size_t o_stride;
+    int T, t0, G, max_len, window;
+    int cap;                      // decode: keys a CTA's shared memory holds
+    unsigned long long smul;      // decode: ceil(2^32 / CTAs of a unit)
+    int lgGp;                     // prefill: log2 of the power of two >= G
+    int32_t* ws_max;              // decode in a cooperative launch: exchange memory
+    unsigned *ws_sum, *ws_cnt;
+    long long* ws_num;
+};
+cudaError_t launch_kv4_append(const Kv4Args& a, const Kv4Append& p, int d, cudaStream_t s);
+cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p, int d, cudaStream_t s);
+// bytes of workspace the decode attention of T tokens needs (0: none)
+size_t kv4_decode_ws(const Kv4Args& a, int d, int T, int max_len);
+cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p, int d, void* ws, cudaStream_t s);
+cudaError_t kv4_init();           // once per device, outside any stream capture
+
+// records the detail that detint_last_error reports; returns code
+int set_last_error(int code, const char* what);
+
 }  // namespace detint

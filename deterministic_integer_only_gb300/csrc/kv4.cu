@@ -1,0 +1,363 @@
+// Host side of the 4-bit paged K/V cache: launch shapes, argument checks and
+// the C entry points detint_kv4_*. Kernel code lives in k_kv4.cuh.
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "../../include/detint.h"
+#include "k_kv4.cuh"
+
+namespace detint {
+
+namespace {
+
+constexpr int KV4_MAX_LEN = 1 << 19;       // keys: the limb sums stay in int32
+constexpr size_t KV4_SMEM_CTA = 200 * 1024;  // dynamic shared memory of one decode CTA at most
+constexpr size_t KV4_SMEM_2 = 96 * 1024;   // up to here two decode CTAs share an SM
+
+struct DevInfo {
+    bool ready = false;
+    int sms = 0;
+    int max_cluster = 8;                   // CTAs of a cluster at full shared memory
+};
+DevInfo g_dev[64];
+std::mutex g_mu;
+
+DevInfo* dev_info() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    return &g_dev[dev];
+}
+
+using DecFn = void (*)(Kv4Args, Kv4Attn);
+template <bool GRID>
+DecFn dec_kernel(int d, int gt) {
+    if (d == 128) {
+        if (gt == 1) return k_kv4_decode<128, 1, GRID>;
+        if (gt == 2) return k_kv4_decode<128, 2, GRID>;
+        if (gt == 4) return k_kv4_decode<128, 4, GRID>;
+        return k_kv4_decode<128, 8, GRID>;
+    }
+    if (gt == 1) return k_kv4_decode<64, 1, GRID>;
+    if (gt == 2) return k_kv4_decode<64, 2, GRID>;
+    if (gt == 4) return k_kv4_decode<64, 4, GRID>;
+    return k_kv4_decode<64, 8, GRID>;
+}
+
+size_t dec_smem(int d, int gt, int cap) {
+    return (size_t)gt * d * 8 + (size_t)(((cap >> 6) + 3) & ~3) * 4 + (size_t)gt * (cap + 8) * 4;
+}
+
+// how a decode call is split
+struct DecPlan {
+    int gt, hg, S, cap;
+    bool grid;
+    size_t smem;
+};
+
+DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len, int window) {
+    DecPlan p{};
+    const int G = a.nq / a.n_kv;
+    int mp = (max_len + 63) >> 6;                                   // pages a token can have
+    if (window > 0) mp = std::min(mp, ((window + 62) >> 6) + 1);
+    // q heads per CTA: all of a kv head's up to 8; fewer where the scores
+    // of so many keys would not fit even split over every CTA of the device
+    for (p.gt = G >= 5 ? 8 : (G >= 3 ? 4 : G);; p.gt >>= 1) {
+        p.hg = (G + p.gt - 1) / p.gt;
+        const long long units = (long long)T * a.n_kv * p.hg;
+        // a cluster: as many CTAs as keep two on every SM busy, at least 2 pages each
+        int S = 1;
+        while (S < di.max_cluster && units * S < 2 * di.sms && mp >= 4 * S) S <<= 1;
+        while (S < di.max_cluster && dec_smem(d, p.gt, ((mp + S - 1) / S) << 6) > KV4_SMEM_2) S <<= 1;
+        p.S = S;
+        p.cap = ((mp + S - 1) / S) << 6;
+        p.smem = dec_smem(d, p.gt, p.cap);
+        p.grid = false;
+        // a cooperative launch where the clusters would leave SMs idle on a long context
+        if (units * S < di.sms && mp >= 8 * S) {
+            const int Sg = (int)std::min<long long>((2 * di.sms) / units, mp / 4);
+            const int cap = ((mp + Sg - 1) / Sg) << 6;
+            if (Sg > S && dec_smem(d, p.gt, cap) <= KV4_SMEM_2) {
+                p.S = Sg;
+                p.cap = cap;
+                p.smem = dec_smem(d, p.gt, cap);
+                p.grid = true;
+            }
+        }
+        if (p.smem <= KV4_SMEM_CTA || p.gt == 1) return p;
+    }
+}
+
+size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
+struct WsLayout { size_t cnt, mx, sum, num, total; };
+WsLayout ws_layout(const DecPlan& p, long long units, int d) {
+    WsLayout w{};
+    size_t o = 0;
+    const size_t n = (size_t)units * p.S * p.gt;
+    w.cnt = o; o += a256((size_t)units * 4);
+    w.mx = o; o += a256(n * 4);
+    w.sum = o; o += a256(n * 8);
+    w.num = o; o += a256(n * d * 8);
+    w.total = o;
+    return w;
+}
+
+}  // namespace
+
+cudaError_t kv4_init() {
+    DevInfo* di = dev_info();
+    if (!di) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (di->ready) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&di->sms, cudaDevAttrMultiProcessorCount, dev);
+    int mc = 16;
+    for (int d : {64, 128})
+        for (int gt : {1, 2, 4, 8}) {
+            for (DecFn f : {dec_kernel<false>(d, gt), dec_kernel<true>(d, gt)}) {
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)KV4_SMEM_CTA);
+            }
+            DecFn f = dec_kernel<false>(d, gt);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) continue;
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = 16;
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(16);
+            cfg.blockDim = dim3(KV4_DT);
+            cfg.dynamicSmemBytes = KV4_SMEM_CTA;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, f, &cfg) != cudaSuccess || n < 1) {
+                cudaGetLastError();
+                mc = 8;
+            }
+        }
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_kv4_prefill<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Kv4Pf<64>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_kv4_prefill<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Kv4Pf<128>::SMEM);
+    if (e == cudaSuccess) {
+        di->max_cluster = mc;
+        di->ready = true;
+    }
+    return e;
+}
+
+cudaError_t launch_kv4_append(const Kv4Args& a, const Kv4Append& p0, int d, cudaStream_t s) {
+    Kv4Append p = p0;
+    DevInfo* di = dev_info();
+    if (!di || !di->ready) return cudaErrorInvalidDevice;
+    const int hpb = d == 128 ? 4 : 8;
+    p.qk_blocks = (a.nq + a.n_kv + hpb - 1) / hpb;
+    // tokens per CTA: whole pages of tokens where there are enough CTAs for it
+    const int per_tile = p.qk_blocks + a.n_kv;
+    p.tile = KV4_VTILE;
+    while (p.tile > 1 && (long long)((p.T + p.tile - 1) / p.tile) * per_tile < 8LL * di->sms) p.tile >>= 1;
+    const dim3 grid((p.T + p.tile - 1) / p.tile, per_tile);
+    if (d == 128) k_kv4_append<32><<<grid, KV4_APT, 0, s>>>(a, p);
+    else k_kv4_append<16><<<grid, KV4_APT, 0, s>>>(a, p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p0, int d, cudaStream_t s) {
+    Kv4Attn p = p0;
+    p.lgGp = 0;
+    while ((1 << p.lgGp) < p.G) ++p.lgGp;
+    const int bq = KV4_PROWS >> p.lgGp;
+    const int tiles = (p.T + bq - 1) / bq;
+    for (int b0 = 0; b0 < tiles; b0 += 65535) {
+        const int n = std::min(65535, tiles - b0);
+        p.t0 = b0 * bq;
+        const dim3 grid(a.n_kv, n);
+        if (d == 128) k_kv4_prefill<128><<<grid, KV4_PT, Kv4Pf<128>::SMEM, s>>>(a, p);
+        else k_kv4_prefill<64><<<grid, KV4_PT, Kv4Pf<64>::SMEM, s>>>(a, p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// Enough for every window: a cooperative launch has at most two CTAs on an SM
+// and needs clusters that leave SMs idle; each CTA exchanges at most 8 heads.
+size_t kv4_decode_ws(const Kv4Args& a, int d, int T, int max_len) {
+    DevInfo* di = dev_info();
+    if (!di || !di->ready) return 0;
+    const int G = a.nq / a.n_kv, mp = (max_len + 63) >> 6;
+    const long long units = (long long)T * a.n_kv * ((G + 7) / 8);
+    if (units * di->max_cluster >= di->sms || mp < 8 * di->max_cluster) return 0;
+    return a256((size_t)2 * di->sms * 4) + (size_t)2 * di->sms * 8 * (4 + 8 + 8 * d) + 3 * 256;
+}
+
+cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p0, int d, void* ws, cudaStream_t s) {
+    DevInfo* di = dev_info();
+    if (!di || !di->ready) return cudaErrorInvalidDevice;
+    Kv4Attn p = p0;
+    const DecPlan pl = dec_plan(*di, a, d, p.T, p.max_len, p.window);
+    p.cap = pl.cap;
+    p.smul = ((1ull << 32) + pl.S - 1) / pl.S;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.blockDim = dim3(KV4_DT);
+    cfg.dynamicSmemBytes = pl.smem;
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (pl.grid) {
+        const WsLayout w = ws_layout(pl, (long long)p.T * a.n_kv * pl.hg, d);
+        unsigned char* b = (unsigned char*)ws;
+        p.ws_cnt = (unsigned*)(b + w.cnt);
+        p.ws_max = (int32_t*)(b + w.mx);
+        p.ws_sum = (unsigned*)(b + w.sum);
+        p.ws_num = (long long*)(b + w.num);
+        cudaError_t e = cudaMemsetAsync(p.ws_cnt, 0, w.mx - w.cnt, s);
+        if (e != cudaSuccess) return e;
+        p.t0 = 0;
+        cfg.gridDim = dim3(pl.S, a.n_kv * pl.hg, p.T);
+        at[0].id = cudaLaunchAttributeCooperative;
+        at[0].val.cooperative = 1;
+        return cudaLaunchKernelEx(&cfg, dec_kernel<true>(d, pl.gt), a, p);
+    }
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = pl.S;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.numAttrs = pl.S > 1 ? 1 : 0;
+    for (int t0 = 0; t0 < p.T; t0 += 65535) {
+        p.t0 = t0;
+        cfg.gridDim = dim3(pl.S, a.n_kv * pl.hg, std::min(65535, p.T - t0));
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, dec_kernel<false>(d, pl.gt), a, p);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace detint
+
+using namespace detint;
+
+namespace {
+
+int failed(int code, const char* where, const char* what) {
+    char msg[160];
+    snprintf(msg, sizeof msg, "%s: %s", where, what);
+    return set_last_error(code, msg);
+}
+int cuda_fail(const char* where, cudaError_t e) { return failed(DETINT_E_CUDA, where, cudaGetErrorString(e)); }
+bool mis(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) != 0; }
+
+// the checks every entry point shares; fills the kernels' view of the cache
+int check_cache(const char* where, const detint_kv4_t* c, Kv4Args* a) {
+    auto err = [&](int code, const char* what) { return failed(code, where, what); };
+    if (!c) return err(DETINT_E_ARG, "null cache");
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->block_table || !c->params) return err(DETINT_E_ARG, "null pointer in the cache");
+    if (c->head_dim != 64 && c->head_dim != 128) return err(DETINT_E_SHAPE, "head_dim must be 64 or 128");
+    if (c->n_kv < 1 || c->n_q < 1 || c->n_q > 1024 || c->n_q % c->n_kv || c->n_q / c->n_kv > 64)
+        return err(DETINT_E_SHAPE, "n_q must be n_kv times 1..64, at most 1024");
+    if (c->n_blocks < 1 || c->n_seq < 1 || c->max_blocks < 1) return err(DETINT_E_ARG, "n_blocks, n_seq and max_blocks must be positive");
+    if (mis(c->k, 16) || mis(c->v, 16) || mis(c->k_scale, 16) || mis(c->v_scale, 16) || mis(c->params, 16))
+        return err(DETINT_E_ARG, "pages, scale codes and parameters must be 16-byte aligned");
+    a->nq = c->n_q; a->n_kv = c->n_kv; a->n_blocks = c->n_blocks; a->n_seq = c->n_seq; a->max_blocks = c->max_blocks;
+    a->gmul = (65536 + c->n_q / c->n_kv - 1) / (c->n_q / c->n_kv);
+    a->k = c->k; a->v = c->v; a->ks = c->k_scale; a->vs = c->v_scale;
+    a->block_table = c->block_table; a->params = c->params; a->status = c->status;
+    const cudaError_t e = kv4_init();
+    return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
+}
+
+int check_attn(const char* where, const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq,
+               const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int max_len, int window, int32_t* o,
+               long long o_stride, Kv4Args* a, Kv4Attn* p) {
+    auto err = [&](int code, const char* what) { return failed(code, where, what); };
+    const int rc = check_cache(where, c, a);
+    if (rc) return rc;
+    if (!q8 || !mq || !kq || !tok_seq || !tok_pos || !o) return err(DETINT_E_ARG, "null pointer");
+    if (n_tok < 1) return err(DETINT_E_ARG, "n_tok must be positive");
+    if (max_len < 1 || max_len > KV4_MAX_LEN) return err(DETINT_E_ARG, "max_len must be in 1..524288");
+    if (window < 0) return err(DETINT_E_ARG, "window must not be negative");
+    if (mis(q8, 16) || mis(o, 8)) return err(DETINT_E_ARG, "q8 must be 16-byte and o 8-byte aligned");
+    if (o_stride < (long long)c->n_q * c->head_dim || (o_stride & 1)) return err(DETINT_E_ARG, "o_stride must be even and hold a row");
+    *p = Kv4Attn{};
+    p->q8 = q8; p->mq = mq; p->kq = kq; p->tok_seq = tok_seq; p->tok_pos = tok_pos; p->o = o; p->o_stride = (size_t)o_stride;
+    p->T = n_tok; p->G = c->n_q / c->n_kv; p->max_len = max_len; p->window = window;
+    return DETINT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int detint_kv4_append(const detint_kv4_t* c, const detint_rope_t* r, const int32_t* qkv, long long qkv_stride,
+                      const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int8_t* q8, int32_t* mq, int32_t* kq,
+                      int16_t* k_val, int16_t* v_val, detint_stream_t sp) {
+    const char* where = "detint_kv4_append";
+    auto err = [&](int code, const char* what) { return failed(code, where, what); };
+    Kv4Args a{};
+    const int rc = check_cache(where, c, &a);
+    if (rc) return rc;
+    const int d = c->head_dim;
+    if (!r || !qkv || !tok_seq || !tok_pos || !q8 || !mq || !kq) return err(DETINT_E_ARG, "null pointer");
+    if (n_tok < 1) return err(DETINT_E_ARG, "n_tok must be positive");
+    if (r->rot_dim < 0 || r->rot_dim > d || (r->rot_dim & 7)) return err(DETINT_E_SHAPE, "rot_dim must be a multiple of 8 up to head_dim");
+    if (r->max_pos < 1 || (r->rot_dim && (!r->cos || !r->sin))) return err(DETINT_E_ARG, "rotation tables missing");
+    if (r->interleaved != 0 && r->interleaved != 1) return err(DETINT_E_ARG, "interleaved must be 0 or 1");
+    if (!r->q_gamma != !r->k_gamma) return err(DETINT_E_ARG, "both gammas or none");
+    if (r->eps < 0 || r->eps > 32767) return err(DETINT_E_ARG, "eps must be in 0..32767");
+    if (mis(r->cos, 8) || mis(r->sin, 8) || mis(r->q_gamma, 8) || mis(r->k_gamma, 8)) return err(DETINT_E_ARG, "tables and gammas must be 8-byte aligned");
+    if (qkv_stride < (long long)(c->n_q + 2 * c->n_kv) * d || (qkv_stride & 3) || mis(qkv, 16))
+        return err(DETINT_E_ARG, "qkv rows must be 16-byte aligned and hold every head");
+    if (mis(q8, 16) || mis(k_val, 8) || mis(v_val, 8)) return err(DETINT_E_ARG, "outputs misaligned");
+    Kv4Append p{};
+    p.qkv = qkv; p.qkv_stride = (size_t)qkv_stride; p.tok_seq = tok_seq; p.tok_pos = tok_pos; p.T = n_tok;
+    p.cos = r->cos; p.sin = r->sin; p.max_pos = r->max_pos; p.rot = r->rot_dim; p.inter = r->interleaved;
+    p.q_gamma = r->q_gamma; p.k_gamma = r->k_gamma; p.eps = r->eps;
+    p.q8 = q8; p.mq = mq; p.kq = kq; p.k_val = k_val; p.v_val = v_val;
+    const cudaError_t e = launch_kv4_append(a, p, d, (cudaStream_t)sp);
+    return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
+}
+
+int detint_kv4_workspace(const detint_kv4_t* c, int n_tok, int max_len, long long* bytes) {
+    Kv4Args a{};
+    const int rc = check_cache("detint_kv4_workspace", c, &a);
+    if (rc) return rc;
+    if (!bytes || n_tok < 1 || max_len < 1 || max_len > KV4_MAX_LEN)
+        return set_last_error(DETINT_E_ARG, "detint_kv4_workspace: bad arguments");
+    *bytes = (long long)kv4_decode_ws(a, c->head_dim, n_tok, max_len);
+    return DETINT_OK;
+}
+
+int detint_kv4_decode(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq,
+                      const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int max_len, int window, int32_t* o,
+                      long long o_stride, void* workspace, long long workspace_bytes, detint_stream_t sp) {
+    const char* where = "detint_kv4_decode";
+    Kv4Args a{};
+    Kv4Attn p{};
+    const int rc = check_attn(where, c, q8, mq, kq, tok_seq, tok_pos, n_tok, max_len, window, o, o_stride, &a, &p);
+    if (rc) return rc;
+    const size_t need = kv4_decode_ws(a, c->head_dim, n_tok, max_len);
+    if (need && (!workspace || workspace_bytes < (long long)need || mis(workspace, 16)))
+        return set_last_error(DETINT_E_ARG, "detint_kv4_decode: a 16-byte aligned workspace of detint_kv4_workspace bytes is needed");
+    const cudaError_t e = launch_kv4_decode(a, p, c->head_dim, workspace, (cudaStream_t)sp);
+    return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
+}
+
+int detint_kv4_prefill(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq,
+                       const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int max_len, int window, int32_t* o,
+                       long long o_stride, detint_stream_t sp) {
+    const char* where = "detint_kv4_prefill";
+    Kv4Args a{};
+    Kv4Attn p{};
+    const int rc = check_attn(where, c, q8, mq, kq, tok_seq, tok_pos, n_tok, max_len, window, o, o_stride, &a, &p);
+    if (rc) return rc;
+    const cudaError_t e = launch_kv4_prefill(a, p, c->head_dim, (cudaStream_t)sp);
+    return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
+}
+
+}  // extern "C"

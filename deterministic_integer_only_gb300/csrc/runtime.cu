@@ -24,6 +24,15 @@ static int fail(int code, const std::string& msg) {
     g_last_error = msg;
     return code;
 }
+namespace detint {
+int set_last_error(int code, const char* what) {
+    try {
+        return fail(code, what);
+    } catch (...) {          // no memory for the text: the code alone
+        return code;
+    }
+}
+}  // namespace detint
 #define CK(call)                                                                         \
     do {                                                                                 \
         cudaError_t e_ = (call);                                                         \

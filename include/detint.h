@@ -238,6 +238,91 @@ int detint_int8_peak_loop(int kind, int blocks, int iters, int32_t* sink, long l
  * head_dim, ffn, vocab, max_pos, qk_norm, max_batch; info[10] = max_ctx. */
 int detint_model_info(detint_model* m, int32_t* info);
 
+/* ---- The 4-bit paged key/value cache (arithmetic specification, section 16).
+ * The pages keep K and V in int8 with fixed scales (DetLLM blog, "DetLLM");
+ * no passage of them defines a narrower cache. Here a cached integer is a
+ * 4-bit code in -7..7 times the scale code (1..255) of its token and kv head,
+ * so a token takes head_dim + 2 bytes per kv head for K and V together.
+ *
+ * Every call works on the caller's device memory and allocates nothing. The
+ * tokens of a call are given by device arrays, so that a captured call can be
+ * replayed after they changed: tok_seq[t] is a row of the block table,
+ * tok_pos[t] the token's position in its sequence. A negative position marks
+ * a padding token: nothing is appended for it, its query codes are zero and
+ * its attention output is a zero row. A position or a block outside its range
+ * sets slot 1 of `status`; the token is then treated as padding, the page as
+ * masked. All three operators are exact integer arithmetic: the same inputs
+ * give the same bits whatever the batch, the split or the kernel. */
+typedef struct {
+    int32_t n_q, n_kv;           /* heads; n_q = n_kv times 1..64, at most 1024 */
+    int32_t head_dim;            /* 64 or 128 */
+    int32_t n_blocks;            /* pages; a page holds 64 tokens of every kv head */
+    int32_t n_seq, max_blocks;   /* block_table [n_seq][max_blocks] */
+    uint8_t* k;                  /* [n_blocks][n_kv][64 * head_dim / 2] codes, 16-byte aligned */
+    uint8_t* v;                  /* the same size; layout in the specification */
+    uint8_t* k_scale;            /* [n_blocks][n_kv][64] scale codes */
+    uint8_t* v_scale;
+    const int32_t* block_table;  /* page of each 64 positions of a sequence */
+    const int32_t* params;       /* [n_kv][8 + head_dim]: KQM KQS VQM VQS MV KV CSTM CSTK, then the
+                                    key exponent 0..3 of every channel */
+    int32_t* status;             /* device int32[8] (the slots of detint_status), or NULL */
+} detint_kv4_t;
+
+/* Rotation and normalisation of the query and key heads. The first rot_dim
+ * channels rotate, in pairs (i, i + rot_dim / 2) or, interleaved, (2i, 2i+1),
+ * by row tok_pos of the Q14 tables; the others pass. The tables are data
+ * (README, "Layout": precomputed int16 sin/cos tables): positions scaled for
+ * long contexts are scaled when they are made. q_gamma and k_gamma (Q12,
+ * magnitudes up to 2^14) ask for the per-head RMS norm; without them the Q12
+ * inputs are used as they are. */
+typedef struct {
+    const int16_t *cos, *sin;            /* [max_pos][rot_dim / 2], 8-byte aligned */
+    int32_t max_pos;
+    int32_t rot_dim;                     /* a multiple of 8, 0 (none) .. head_dim */
+    int32_t interleaved;                 /* 0 or 1 */
+    int32_t eps;                         /* round(eps 2^24), 0 .. 32767 */
+    const int16_t *q_gamma, *k_gamma;    /* [head_dim] both, or NULL both */
+} detint_rope_t;
+
+/* Norm, rotate and quantise the projections of n_tok tokens, and append their
+ * keys and values to the pages. qkv: device int32 rows (Q12) of n_q query,
+ * n_kv key and n_kv value heads, qkv_stride elements apart (a multiple of 4).
+ * q8 [n_tok][n_q][head_dim] and mq, kq [n_tok][n_q] receive the query codes
+ * and their dyadic scales; k_val, v_val [n_tok][n_kv][head_dim], where given,
+ * the integers the cache now holds for these tokens (zeros for a token that
+ * was not appended). No two tokens of a call may fall on the same place of a
+ * page: the codes there would be undefined.
+ * Errors: ARG, SHAPE, CUDA. */
+int detint_kv4_append(const detint_kv4_t* c, const detint_rope_t* r, const int32_t* qkv, long long qkv_stride,
+                      const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int8_t* q8, int32_t* mq,
+                      int32_t* kq, int16_t* k_val, int16_t* v_val, detint_stream_t s);
+
+/* Bytes of workspace (16-byte aligned) that detint_kv4_decode of n_tok tokens
+ * with contexts up to max_len needs; 0 for most sizes. Two calls that may
+ * overlap on the GPU, captured ones included, need a workspace each.
+ * Errors: ARG, SHAPE, CUDA. */
+int detint_kv4_workspace(const detint_kv4_t* c, int n_tok, int max_len, long long* bytes);
+
+/* Attention of single tokens over the cache: token t sees the keys 0..tok_pos[t]
+ * of its sequence, or the last `window` of them where window > 0. o: int32
+ * Q12 rows [n_tok], o_stride elements apart (even). max_len (1..524288) is a
+ * bound of every tok_pos + 1 of the call; a token beyond it is flagged and
+ * gets a zero row. Each token is a unit of its own whose keys are split over
+ * CTAs, so this is the call for one or a few tokens of each sequence.
+ * Errors: ARG, SHAPE, CUDA. */
+int detint_kv4_decode(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq,
+                      const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int max_len, int window,
+                      int32_t* o, long long o_stride, void* workspace, long long workspace_bytes,
+                      detint_stream_t s);
+
+/* The same attention with the same result, bit for bit, for many tokens of a
+ * sequence: blocks of consecutive tokens of the call share one sweep over
+ * their keys on the int8 tensor pipe. Tokens of one sequence should stand
+ * together. No workspace. Errors: ARG, SHAPE, CUDA. */
+int detint_kv4_prefill(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq,
+                       const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int max_len, int window,
+                       int32_t* o, long long o_stride, detint_stream_t s);
+
 /* Release everything the model owns. NULL is a no-op. No passage of the
  * pages: library housekeeping. */
 void detint_free(detint_model* m);
