@@ -222,6 +222,7 @@ class KV4Cache:
         if status is not None:
             _expect("KV4Cache", "status", status, torch.int32, 8, dev)
         self.n_q, self.n_kv, self.head_dim, self.device = int(n_q), n_kv, d, dev
+        self._index, self._torch = dev.index, torch
         self._keep = (k, v, k_scale, v_scale, block_table, params, status)
         self._c = _Kv4(int(n_q), n_kv, d, n_blocks, n_seq, max_blocks, _ptr(k), _ptr(v), _ptr(k_scale),
                        _ptr(v_scale), _ptr(block_table), _ptr(params), _ptr(status))
@@ -250,20 +251,50 @@ class RopeNorm:
             if t is not None:
                 self.device = self.device or t.device
                 _expect("RopeNorm", name, t, torch.int16, self._gammas, self.device)
+        self._index = None if self.device is None else self.device.index
         self._keep = (cos, sin, q_gamma, k_gamma)
         self._c = _Rope(_ptr(cos), _ptr(sin), int(max_pos), rot, int(bool(interleaved)), int(eps), _ptr(q_gamma),
                         _ptr(k_gamma))
         self._ref = C.addressof(self._c)
 
 
-def _kv4_tokens(where, cache, tok_seq, tok_pos):
-    import torch
-    n = tok_pos.numel()
-    _expect(where, "tok_pos", tok_pos, torch.int32, n, cache.device)
-    _expect(where, "tok_seq", tok_seq, torch.int32, n, cache.device)
-    if torch.cuda.current_device() != cache.device.index:
+def _unfit(t, dtype, numel, index) -> bool:
+    """Whether t is not a contiguous cuda tensor of that type and device with
+    room for numel elements. A decode step makes these calls once per layer:
+    the checks stay a few hundred nanoseconds each, and _expect words the
+    error once one fails."""
+    return t.dtype is not dtype or t.get_device() != index or t.numel() < numel or not t.is_contiguous()
+
+
+def _row_stride(where, name, t, dtype, rows, width, index) -> int:
+    """The stride of rows of at least `width` elements, which may be strided."""
+    if t.dtype is dtype and t.get_device() == index:
+        if t.numel() == rows * width and t.is_contiguous():
+            return width
+        if t.dim() == 2 and t.size(0) >= rows and t.size(1) >= width and t.stride(1) == 1:
+            return t.stride(0) if t.size(0) > 1 else t.size(1)
+    raise ValueError(f"{where}: {name}: {dtype} rows [{rows}, {width}] on cuda:{index} expected, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}")
+
+
+def _kv4_call(where, cache, q8, mq, kq, tok_seq, tok_pos, stream):
+    """The checks the kv4 operators share: tokens and query buffers (None:
+    to be made). Returns (tokens, raw stream)."""
+    index, torch, n = cache._index, cache._torch, tok_pos.numel()
+    i32 = torch.int32
+    if torch._C._cuda_getDevice() != index:
         raise ValueError(f"{where}: the cache is on {cache.device}, which is not the current device")
-    return n
+    rows = n * cache.n_q
+    if _unfit(tok_pos, i32, n, index) or _unfit(tok_seq, i32, n, index) or \
+            mq is not None and _unfit(mq, i32, rows, index) or kq is not None and _unfit(kq, i32, rows, index) or \
+            q8 is not None and _unfit(q8, torch.int8, rows * cache.head_dim, index):
+        for name, t, dt, m in (("tok_pos", tok_pos, i32, n), ("tok_seq", tok_seq, i32, n), ("mq", mq, i32, rows),
+                               ("kq", kq, i32, rows), ("q8", q8, torch.int8, rows * cache.head_dim)):
+            if t is not None:
+                _expect(where, name, t, dt, m, cache.device)
+    if stream is None:
+        return n, torch._C._cuda_getCurrentRawStream(index)
+    return n, stream.cuda_stream
 
 
 def _new(stream, shape, dtype, device):
@@ -281,28 +312,28 @@ def detint_kv4_append(cache, rope, qkv, tok_seq, tok_pos, q8=None, mq=None, kq=N
     head_dim] (int32, rows may be strided) and append keys and values to the
     cache; returns (q8, mq, kq). k_val, v_val (int16 [n_tok, n_kv, head_dim])
     receive the cached integers where given."""
-    import torch
-    w, dev = "detint_kv4_append", cache.device
-    n = _kv4_tokens(w, cache, tok_seq, tok_pos)
+    w, torch, dev, index = "detint_kv4_append", cache._torch, cache.device, cache._index
+    n, raw = _kv4_call(w, cache, q8, mq, kq, tok_seq, tok_pos, stream)
     nq, d = cache.n_q, cache.head_dim
-    if qkv.dtype != torch.int32 or qkv.device != dev or qkv.dim() != 2 or qkv.shape[0] < n or \
-            qkv.shape[1] < (nq + 2 * cache.n_kv) * d or qkv.stride(1) != 1:
-        raise ValueError(f"{w}: qkv: int32 rows [n_tok, (n_q + 2 n_kv) head_dim] on {dev} expected")
-    if rope.device is not None and rope.device != dev or rope._gammas not in (0, d):
+    stride = _row_stride(w, "qkv", qkv, torch.int32, n, (nq + 2 * cache.n_kv) * d, index)
+    if rope._index not in (None, index) or rope._gammas not in (0, d):
         raise ValueError(f"{w}: tables or gammas do not fit the cache")
     q8 = _new(stream, (n, nq, d), torch.int8, dev) if q8 is None else q8
     mq = _new(stream, (n, nq), torch.int32, dev) if mq is None else mq
     kq = _new(stream, (n, nq), torch.int32, dev) if kq is None else kq
-    _expect(w, "q8", q8, torch.int8, n * nq * d, dev)
-    _expect(w, "mq", mq, torch.int32, n * nq, dev)
-    _expect(w, "kq", kq, torch.int32, n * nq, dev)
-    for name, t in (("k_val", k_val), ("v_val", v_val)):
-        if t is not None:
-            _expect(w, name, t, torch.int16, n * cache.n_kv * d, dev)
-    stride = qkv.stride(0) if qkv.shape[0] > 1 else qkv.shape[1]
-    _check(lib().detint_kv4_append(cache._ref, rope._ref, qkv.data_ptr(), stride, tok_seq.data_ptr(),
-                                   tok_pos.data_ptr(), n, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), _ptr(k_val),
-                                   _ptr(v_val), _stream(stream)), w)
+    kp = vp = 0
+    if k_val is not None:
+        if _unfit(k_val, torch.int16, n * cache.n_kv * d, index):
+            _expect(w, "k_val", k_val, torch.int16, n * cache.n_kv * d, dev)
+        kp = k_val.data_ptr()
+    if v_val is not None:
+        if _unfit(v_val, torch.int16, n * cache.n_kv * d, index):
+            _expect(w, "v_val", v_val, torch.int16, n * cache.n_kv * d, dev)
+        vp = v_val.data_ptr()
+    rc = lib().detint_kv4_append(cache._ref, rope._ref, qkv.data_ptr(), stride, tok_seq.data_ptr(),
+                                 tok_pos.data_ptr(), n, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), kp, vp, raw)
+    if rc:
+        _check(rc, w)
     return q8, mq, kq
 
 
@@ -313,19 +344,11 @@ def detint_kv4_workspace(cache, n_tok: int, max_len: int) -> int:
     return int(n.value)
 
 
-def _kv4_attn(w, cache, q8, mq, kq, tok_seq, tok_pos, out, stream):
-    import torch
-    n, dev = _kv4_tokens(w, cache, tok_seq, tok_pos), cache.device
-    nq, d = cache.n_q, cache.head_dim
-    _expect(w, "q8", q8, torch.int8, n * nq * d, dev)
-    _expect(w, "mq", mq, torch.int32, n * nq, dev)
-    _expect(w, "kq", kq, torch.int32, n * nq, dev)
+def _kv4_out(w, cache, n, out, stream):
+    torch, width = cache._torch, cache.n_q * cache.head_dim
     if out is None:
-        out = _new(stream, (n, nq * d), torch.int32, dev)
-    elif out.dtype != torch.int32 or out.device != dev or out.dim() != 2 or out.shape[0] < n or \
-            out.shape[1] < nq * d or out.stride(1) != 1:
-        raise ValueError(f"{w}: out: int32 rows [n_tok, n_q head_dim] on {dev} expected")
-    return n, out, out.stride(0) if out.shape[0] > 1 else out.shape[1]
+        return _new(stream, (n, width), torch.int32, cache.device), width
+    return out, _row_stride(w, "out", out, torch.int32, n, width, cache._index)
 
 
 def detint_kv4_decode(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, window: int = 0, out=None,
@@ -334,17 +357,22 @@ def detint_kv4_decode(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, window:
     rows [n_tok, n_q head_dim]. workspace: a cuda uint8 tensor of
     detint_kv4_workspace bytes (made here when it is needed and not given)."""
     w = "detint_kv4_decode"
-    n, out, stride = _kv4_attn(w, cache, q8, mq, kq, tok_seq, tok_pos, out, stream)
-    if workspace is None:
-        import torch
-        need = detint_kv4_workspace(cache, n, max_len)
-        workspace = _new(stream, need, torch.uint8, cache.device) if need else None
-    elif workspace.device != cache.device or not workspace.is_contiguous():
-        raise ValueError(f"{w}: workspace: a contiguous tensor on {cache.device} expected")
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().detint_kv4_decode(cache._ref, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), tok_seq.data_ptr(),
-                                   tok_pos.data_ptr(), n, int(max_len), int(window), out.data_ptr(), stride,
-                                   _ptr(workspace), size, _stream(stream)), w)
+    n, raw = _kv4_call(w, cache, q8, mq, kq, tok_seq, tok_pos, stream)
+    out, stride = _kv4_out(w, cache, n, out, stream)
+    ws = size = 0
+    if workspace is not None:
+        if workspace.get_device() != cache._index or not workspace.is_contiguous():
+            raise ValueError(f"{w}: workspace: a contiguous tensor on {cache.device} expected")
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = lib().detint_kv4_decode(cache._ref, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), tok_seq.data_ptr(),
+                                 tok_pos.data_ptr(), n, max_len, window, out.data_ptr(), stride, ws, size, raw)
+    if rc and workspace is None:
+        size = detint_kv4_workspace(cache, n, max_len)    # refused for want of one?
+        if size:
+            workspace = _new(stream, size, cache._torch.uint8, cache.device)
+            return detint_kv4_decode(cache, q8, mq, kq, tok_seq, tok_pos, max_len, window, out, workspace, stream)
+    if rc:
+        _check(rc, w)
     return out
 
 
@@ -352,10 +380,12 @@ def detint_kv4_prefill(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, window
     """The attention of detint_kv4_decode, bit for bit, for blocks of tokens of
     the same sequence (tokens of a sequence stand together)."""
     w = "detint_kv4_prefill"
-    n, out, stride = _kv4_attn(w, cache, q8, mq, kq, tok_seq, tok_pos, out, stream)
-    _check(lib().detint_kv4_prefill(cache._ref, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), tok_seq.data_ptr(),
-                                    tok_pos.data_ptr(), n, int(max_len), int(window), out.data_ptr(), stride,
-                                    _stream(stream)), w)
+    n, raw = _kv4_call(w, cache, q8, mq, kq, tok_seq, tok_pos, stream)
+    out, stride = _kv4_out(w, cache, n, out, stream)
+    rc = lib().detint_kv4_prefill(cache._ref, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), tok_seq.data_ptr(),
+                                  tok_pos.data_ptr(), n, max_len, window, out.data_ptr(), stride, raw)
+    if rc:
+        _check(rc, w)
     return out
 
 

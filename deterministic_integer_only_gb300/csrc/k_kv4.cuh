@@ -29,7 +29,7 @@
 namespace detint {
 
 constexpr int KV4_XMAX = 1785;             // 7 * 255
-constexpr int KV4_NEG = -2147483647 - 1;   // score of a masked key
+constexpr int KV4_NEG = -2147483647 - 1;   // maximum of no key
 
 __device__ __forceinline__ int kv4_lo(int w) { return w & 0x0f0f0f0f; }
 __device__ __forceinline__ int kv4_hi(int w) { return (int)((unsigned)w >> 4) & 0x0f0f0f0f; }
@@ -47,12 +47,6 @@ template <int LPH>
 __device__ __forceinline__ unsigned seg_max(unsigned v) {
     return __reduce_max_sync(seg_mask<LPH>(), v);
 }
-template <int LPH>
-__device__ __forceinline__ u64 seg_sum64(u64 v) {
-#pragma unroll
-    for (int o = LPH / 2; o; o >>= 1) v += __shfl_xor_sync(seg_mask<LPH>(), v, o);
-    return v;
-}
 __device__ __forceinline__ unsigned uabs32(int v) { return v < 0 ? 0u - (unsigned)v : (unsigned)v; }
 
 // (page row or -1, offset in the page) of a token, -1 for a position or a
@@ -69,270 +63,524 @@ __device__ __forceinline__ int kv4_slot(const Kv4Args& a, int seq, int pos, int*
     return blk;
 }
 
-// the scale code of a row of cached integers x and the four codes (+ 8) of
-// this lane: c = max(1, ceil(max|x| / 7)), q = rshr(x R, b + 16) with
-// R = floor(2^(b + 16) / c), b = bitlen(c); |x| / c <= 7, so no clamp
-template <int LPH>
-__device__ __forceinline__ int kv4_codes(const int (&x)[4], int (&q)[4]) {
-    unsigned m = max(max(uabs32(x[0]), uabs32(x[1])), max(uabs32(x[2]), uabs32(x[3])));
-    m = seg_max<LPH>(m);
-    const int c = max(1, (int)((m + 6) / 7));
-    const int b = 32 - __clz(c);
-    const int R = (int)pow2_recip((u64)c, b, 1, 16);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = rshr32(x[j] * R, b + 16) + 8;   // |x R| < 2^11 2^17
-    return c;
+__device__ __forceinline__ unsigned max4(const int (&x)[4]) {
+    return max(max(uabs32(x[0]), uabs32(x[1])), max(uabs32(x[2]), uabs32(x[3])));
+}
+__device__ __forceinline__ int pack4(const int (&q)[4]) { return q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24); }
+__device__ __forceinline__ short4 val4(const int (&q)[4], int c) {
+    return make_short4((short)((q[0] - 8) * c), (short)((q[1] - 8) * c), (short)((q[2] - 8) * c), (short)((q[3] - 8) * c));
 }
 
-// a warp's q or k heads of one token: norm, rotation, quantisation
+// What a row needs once. Norm: from sum x'^2 (x' the row with its largest
+// magnitude brought to 24 bits, cl = clz of that magnitude), the floor square
+// root r and R = floor(2^(bl + 23) / r), bl = bitlen(r).
+struct Kv4Inv {
+    unsigned R;
+    int bl;
+};
+__device__ __forceinline__ Kv4Inv kv4_inv_rms(u64 ss, int lg_d, int cl, i64 eps) {
+    Kv4Inv v = {0u, 20};
+    if (cl < 32) {
+        const int sig = 8 - cl;                              // bitlen - 24
+        const u64 es = sig >= 0 ? (u64)eps >> (2 * sig) : (u64)eps << (-2 * sig);   // eps < 2^15: < 2^61
+        const u64 r = isqrt_fast((ss >> lg_d) + es);
+        v.bl = bitlen_u64(r);
+        v.R = (unsigned)pow2_recip(r, v.bl, 1, 23);          // <= 2^24
+    }
+    return v;
+}
+// x' of one channel: |x| aligned to bit 31 and cut by 8, sign put back
+__device__ __forceinline__ int kv4_cut(int x, int cl) {
+    const int m = (int)((uabs32(x) << (cl & 31)) >> 8), s = x >> 31;
+    return (m ^ s) - s;
+}
+// y = rshr(x' gamma R, bl + 21); r >= 2^23 / sqrt(d), so the shift is 41 or
+// more and only the high word of the product matters; |x'| / r <= sqrt(d), so
+// |y| < 2^21 and nothing that follows saturates
+__device__ __forceinline__ int kv4_scale(int x, int g, unsigned R, int bl) {
+    const i64 z = (i64)x * g;
+    const int hi = (int)(z >> 32) * (int)R + (int)__umulhi((unsigned)z, R);
+    return (hi + (1 << (bl - 12))) >> (bl - 11);
+}
+// without the norm: sat32(4 x)
+__device__ __forceinline__ int kv4_x4(int x) {
+    return x >= (1 << 29) ? 2147483647 : (x <= -(1 << 29) ? -2147483647 : 4 * x);
+}
+// rshr(x0 c0 + x1 c1, 14); without the norm saturating to 32 bits
+template <bool NORM>
+__device__ __forceinline__ int kv4_turn(int x0, int c0, int x1, int c1) {
+    const i64 v = (i64)x0 * c0 + ((i64)x1 * c1 + 8192);
+    const int hi = (int)(v >> 32), r = (int)__funnelshift_r((unsigned)v, (unsigned)hi, 14);
+    if (NORM) return r;
+    const int top = hi >> 13;                                // 0 or -1 when the result fits
+    return max((unsigned)(top + 1) > 1u ? (hi < 0 ? -2147483647 : 2147483647) : r, -2147483647);
+}
+// the rotation of a head held as four consecutive channels per lane
+template <int LPH, bool NORM>
+__device__ __forceinline__ void kv4_rotate(const Kv4Append& p, int pos, int (&y)[4]) {
+    const int lane = threadIdx.x & (LPH - 1), R2 = p.rot >> 1;
+    if (p.inter) {
+        if (4 * lane < p.rot) {
+            const unsigned at = (unsigned)max(pos, 0) * R2 + 2 * lane;
+            const short2 c = __ldg((const short2*)(p.cos + at)), s = __ldg((const short2*)(p.sin + at));
+            const int a0 = y[0], a1 = y[1], a2 = y[2], a3 = y[3];
+            y[0] = kv4_turn<NORM>(a0, c.x, a1, -s.x);
+            y[1] = kv4_turn<NORM>(a1, c.x, a0, s.x);
+            y[2] = kv4_turn<NORM>(a2, c.y, a3, -s.y);
+            y[3] = kv4_turn<NORM>(a3, c.y, a2, s.y);
+        }
+    } else if (R2) {
+        const int sh = R2 >> 2;                              // lanes between a pair's halves
+        const bool first = lane < sh, in = lane < 2 * sh;
+        const int src = (threadIdx.x & 31) + (first ? sh : (in ? -sh : 0));
+        const unsigned at = (unsigned)max(pos, 0) * R2 + 4 * (first ? lane : (in ? lane - sh : 0));
+        const short4 c = __ldg((const short4*)(p.cos + at)), s = __ldg((const short4*)(p.sin + at));
+        const int c4[4] = {c.x, c.y, c.z, c.w};
+        const int s4[4] = {first ? -s.x : s.x, first ? -s.y : s.y, first ? -s.z : s.z, first ? -s.w : s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int z = __shfl_sync(seg_mask<LPH>(), y[j], src);
+            const int v = kv4_turn<NORM>(y[j], c4[j], z, s4[j]);
+            y[j] = in ? v : y[j];
+        }
+    }
+}
+// query quantisation: R = floor(127 2^(e + 16) / am), e = bitlen(am), and the
+// dyadic scale of am / 127: with a = am aligned to 32 bits, am 2^k / 127 is
+// a / (127 2^11) or twice that, whichever is at least 2^14
+__device__ __forceinline__ void kv4_qscale(unsigned am, int* R, int* m, int* k) {
+    *R = *m = *k = 0;
+    if (!am) return;
+    const int bl = 32 - __clz(am);
+    *R = (int)pow2_recip(am, bl, 127, 16);                   // < 2^24
+    const unsigned al = am << (32 - bl);
+    const int up = al < (127u << 25);
+    *m = (int)((unsigned)((((u64)al << up) + (127u << 10)) >> 11) / 127);
+    *k = 35 - bl + up;
+}
+// rshr(y R, e + 16): aligned by 31 - e the shift is 47, the high word's 15
+__device__ __forceinline__ int kv4_q8(int y, unsigned am, int R) {
+    const int al = max((int)__clz(am), 1) - 1;
+    return (__mulhi(y << (al & 31), R) + (1 << 14)) >> 15;
+}
+// sat(rshr(v M, s), 1785) for M < 2^30, 0 <= s <= 62: past lim the result
+// saturates, and clamping there keeps the shifted product in 32 bits
+struct Kv4Fix {
+    int M, s, lim;
+};
+__device__ __forceinline__ Kv4Fix kv4_fix(int M, int s) {
+    Kv4Fix f = {min(max(M, 0), 1 << 27), min(max(s, 0), 62), 2147483647};
+    if (f.M > 0 && f.s < 50) {
+        const u64 n = (u64)(KV4_XMAX + 1) << f.s;            // < 2^61
+        if (n < ((u64)f.M << 30)) f.lim = (int)udiv_small(n, (u64)f.M) + 1;
+    }
+    return f;
+}
+__device__ __forceinline__ int kv4_fixed(const Kv4Fix& f, int e, int v) {
+    const int lim = f.lim == 2147483647 ? f.lim : (f.lim >> e) + 1;
+    const i64 p = (i64)min(max(v, -lim), lim) * (f.M << e) + (f.s ? 1ll << (f.s - 1) : 0ll);
+    const unsigned lo = (unsigned)p, hi = (unsigned)((u64)p >> 32);
+    const bool far = f.s >= 32;
+    const int x = (int)__funnelshift_r(far ? hi : lo, far ? (unsigned)((int)hi >> 31) : hi, f.s & 31);
+    return min(max(x, -KV4_XMAX), KV4_XMAX);
+}
+// scale code c = max(1, ceil(max|x| / 7)) and R = floor(2^(b + 16) / c), b =
+// bitlen(c): the codes are rshr(x R, b + 16), |x| / c <= 7 (no clamp needed),
+// |x R| < 2^11 2^17
+__device__ __forceinline__ int kv4_code_scale(unsigned am) { return max(1, (int)((am + 6) / 7)); }
+__device__ __forceinline__ int kv4_code_inv(int c) { return (int)pow2_recip((u64)c, 32 - __clz(c), 1, 16); }
+__device__ __forceinline__ int kv4_code(int x, int R, int c) { return rshr32(x * R, 48 - __clz(c)) + 8; }
+
+// one k row's codes into its page
 template <int LPH>
-__device__ void kv4_qk_head(const Kv4Args& a, const Kv4Append& p, int t, int slot, bool live) {
+__device__ __forceinline__ void kv4_put_k(const Kv4Args& a, const Kv4Append& p, int t, int kvh, int blk, int off,
+                                          const int (&q)[4], int c, bool live) {
+    constexpr int D = 4 * LPH;
+    const int lane = threadIdx.x & (LPH - 1);
+    const int w4 = pack4(q);
+    const int up = __shfl_down_sync(seg_mask<LPH>(), w4, 1);
+    if (blk >= 0) {
+        const size_t row = ((size_t)blk * a.n_kv + kvh) * KV_BLK + off;
+        if (!(lane & 1)) *(int*)(a.k + row * (D / 2) + 2 * lane) = w4 | (up << 4);
+        if (lane == 0) a.ks[row] = (uint8_t)c;
+    }
+    if (live && p.k_val)
+        *(short4*)(p.k_val + ((size_t)t * a.n_kv + kvh) * D + 4 * lane) = blk < 0 ? make_short4(0, 0, 0, 0) : val4(q, c);
+}
+// the page of a token of the call, -1 where nothing is appended
+__device__ __forceinline__ int kv4_page_of(const Kv4Args& a, const Kv4Append& p, int t, int pos, int* off) {
+    *off = 0;
+    return pos >= 0 && pos < p.max_pos ? kv4_slot(a, p.tok_seq[t], pos, off) : -1;
+}
+
+// Single tokens: q or k head `slot` of token t, every lane of the head
+// repeating what the row needs once (the latency of one row is all there is).
+template <int LPH, bool NORM>
+__device__ __forceinline__ void kv4_qk_row(const Kv4Args& a, const Kv4Append& p, int t, int slot, bool live) {
     constexpr int D = 4 * LPH;
     const int lane = threadIdx.x & (LPH - 1);
     const bool isq = slot < a.nq;
     const int kvh = isq ? (slot * a.gmul) >> 16 : slot - a.nq;
-    const int pos = live ? p.tok_pos[t] : -1;
-    const bool ok = pos >= 0 && pos < p.max_pos;
-    if (live && pos >= p.max_pos && lane == 0 && a.status) a.status[ST_CTX] = 1;
-    int y[4] = {0, 0, 0, 0};
-    if (ok) {
-        const int4 v = *(const int4*)(p.qkv + (size_t)t * p.qkv_stride + (size_t)slot * D + 4 * lane);
-        y[0] = v.x; y[1] = v.y; y[2] = v.z; y[3] = v.w;
+    int pos = live ? p.tok_pos[t] : -1;
+    if (pos >= p.max_pos) {
+        if (lane == 0 && a.status) a.status[ST_CTX] = 1;
+        pos = -1;
     }
-    const int16_t* gamma = isq ? p.q_gamma : p.k_gamma;
-    if (gamma) {
-        const unsigned ax = seg_max<LPH>(max(max(uabs32(y[0]), uabs32(y[1])), max(uabs32(y[2]), uabs32(y[3]))));
-        const int sig = (32 - __clz(ax)) - 24;
-        int xp[4];
+    int4 v = make_int4(0, 0, 0, 0);
+    if (pos >= 0) v = __ldg((const int4*)(p.qkv + (size_t)t * p.qkv_stride + (size_t)slot * D + 4 * lane));
+    int y[4] = {v.x, v.y, v.z, v.w};
+    const int32_t* kvp = a.params + (size_t)kvh * (8 + D);
+    const int4 ev = __ldg((const int4*)(kvp + 8 + 4 * lane));
+    const int e4[4] = {ev.x & 3, ev.y & 3, ev.z & 3, ev.w & 3};
+    if (NORM) {
+        const int cl = __clz(seg_max<LPH>(max4(y)));
         u64 ss = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const unsigned u = uabs32(y[j]);
-            const int m = (int)(sig >= 0 ? u >> sig : u << min(-sig, 31));
-            xp[j] = y[j] < 0 ? -m : m;
-            ss += (u64)((i64)xp[j] * xp[j]);
+            y[j] = kv4_cut(y[j], cl);
+            ss += (u64)((i64)y[j] * y[j]);
         }
-        ss = seg_sum64<LPH>(ss);
-        const i64 eps_s = !ax ? 0 : (sig >= 0 ? p.eps >> (2 * sig) : p.eps << (-2 * sig));   // eps < 2^15: < 2^61
-        const u64 r = isqrt_fast((ss >> (LPH == 32 ? 7 : 6)) + (u64)eps_s);
-        const int bl = bitlen_u64(r);
-        const i64 Rr = ax ? (i64)pow2_recip(r, bl, 1, 23) : 0;
-        const short4 gm = *(const short4*)(gamma + 4 * lane);
+#pragma unroll
+        for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(seg_mask<LPH>(), ss, o);
+        const Kv4Inv n = kv4_inv_rms(ss, LPH == 32 ? 7 : 6, cl, p.eps);
+        const short4 gm = __ldg((const short4*)((isq ? p.q_gamma : p.k_gamma) + 4 * lane));
         const int g4[4] = {gm.x, gm.y, gm.z, gm.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = sat32(rshr((i64)xp[j] * g4[j] * Rr, bl + 21));
+        for (int j = 0; j < 4; ++j) y[j] = kv4_scale(y[j], g4[j], n.R, n.bl);
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = sat32((i64)y[j] * 4);
+        for (int j = 0; j < 4; ++j) y[j] = kv4_x4(y[j]);
     }
-    // rotation of the first rot channels
-    const int R2 = p.rot >> 1;
-    if (p.inter) {
-        if (4 * lane < p.rot) {
-            short2 c = make_short2(0, 0), s = c;
-            if (ok) {
-                c = *(const short2*)(p.cos + (size_t)pos * R2 + 2 * lane);
-                s = *(const short2*)(p.sin + (size_t)pos * R2 + 2 * lane);
-            }
-            const int a0 = y[0], a1 = y[1], a2 = y[2], a3 = y[3];
-            y[0] = sat32(rshr((i64)a0 * c.x - (i64)a1 * s.x, 14));
-            y[1] = sat32(rshr((i64)a1 * c.x + (i64)a0 * s.x, 14));
-            y[2] = sat32(rshr((i64)a2 * c.y - (i64)a3 * s.y, 14));
-            y[3] = sat32(rshr((i64)a3 * c.y + (i64)a2 * s.y, 14));
-        }
-    } else if (R2) {
-        const int sh = R2 >> 2;                     // lanes between a pair's halves
-        const bool first = lane < sh, in = lane < 2 * sh;
-        const int src = (threadIdx.x & 31) + (first ? sh : (in ? -sh : 0));
-        int z[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z[j] = __shfl_sync(seg_mask<LPH>(), y[j], src);
-        if (in) {
-            short4 c = make_short4(0, 0, 0, 0), s = c;
-            if (ok) {
-                const int i0 = 4 * (first ? lane : lane - sh);
-                c = *(const short4*)(p.cos + (size_t)pos * R2 + i0);
-                s = *(const short4*)(p.sin + (size_t)pos * R2 + i0);
-            }
-            const int c4[4] = {c.x, c.y, c.z, c.w}, s4[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const i64 m = (i64)y[j] * c4[j], n = (i64)z[j] * s4[j];
-                y[j] = sat32(rshr(first ? m - n : m + n, 14));
-            }
-        }
-    }
-    const int32_t* kvp = a.params + (size_t)kvh * (8 + D);
-    const int4 ev = *(const int4*)(kvp + 8 + 4 * lane);
-    const int e4[4] = {ev.x & 3, ev.y & 3, ev.z & 3, ev.w & 3};
+    kv4_rotate<LPH, NORM>(p, pos, y);
     if (isq) {
         const int E = (int)seg_max<LPH>((unsigned)max(max(e4[0], e4[1]), max(e4[2], e4[3])));
-        unsigned am = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            y[j] = sat32((i64)y[j] << (E - e4[j]));
-            am = max(am, uabs32(y[j]));
-        }
-        am = seg_max<LPH>(am);
-        const int e = 32 - __clz(am);
-        const i64 R = am ? (i64)pow2_recip(am, e, 127, 16) : 0;
-        int q[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = (int)rshr((i64)y[j] * R, e + 16);
+        for (int j = 0; j < 4; ++j) y[j] = NORM ? y[j] << (E - e4[j]) : sat32((i64)y[j] << (E - e4[j]));
+        const unsigned am = seg_max<LPH>(max4(y));
+        int R, m, k;
+        kv4_qscale(am, &R, &m, &k);
         if (live) {
             const size_t qi = (size_t)t * a.nq + slot;
-            *(char4*)(p.q8 + qi * D + 4 * lane) = make_char4((signed char)q[0], (signed char)q[1], (signed char)q[2], (signed char)q[3]);
-            if (lane == 0) {
-                int m = 0, k = 0;
-                if (am) { dyadic_fast(am, 127ull, &m, &k); k += 14; }
-                p.mq[qi] = m;
-                p.kq[qi] = k;
-            }
+            *(char4*)(p.q8 + qi * D + 4 * lane) = make_char4((signed char)kv4_q8(y[0], am, R), (signed char)kv4_q8(y[1], am, R),
+                                                             (signed char)kv4_q8(y[2], am, R), (signed char)kv4_q8(y[3], am, R));
+            if (lane == 0) { p.mq[qi] = m; p.kq[qi] = k; }
         }
     } else {
-        int x[4], q[4];
-        const i64 KQM = kvp[0];
-        const int KQS = min(max(kvp[1], 0), 62);
+        const Kv4Fix f = kv4_fix(kvp[0], kvp[1]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = (int)sat_b(rshr((i64)y[j] * (KQM << e4[j]), KQS), KV4_XMAX);
-        const int c = kv4_codes<LPH>(x, q);
-        const int w4 = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
-        const int up = __shfl_down_sync(seg_mask<LPH>(), w4, 1);
-        int off = 0, blk = -1;
-        if (ok) blk = kv4_slot(a, p.tok_seq[t], pos, &off);
-        if (blk >= 0) {
-            const size_t row = ((size_t)blk * a.n_kv + kvh) * KV_BLK + off;
-            if (!(lane & 1)) *(int*)(a.k + row * (D / 2) + 2 * lane) = w4 | (up << 4);
-            if (lane == 0) a.ks[row] = (uint8_t)c;
+        for (int j = 0; j < 4; ++j) y[j] = kv4_fixed(f, e4[j], y[j]);
+        const int c = kv4_code_scale(seg_max<LPH>(max4(y))), R = kv4_code_inv(c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = kv4_code(y[j], R, c);
+        int off;
+        const int blk = kv4_page_of(a, p, t, pos, &off);
+        kv4_put_k<LPH>(a, p, t, kvh, blk, off, y, c, live);
+    }
+}
+
+// Chunks of up to LPH tokens of one head: three passes over the rows, which
+// wait in shared memory, with what a row needs once computed between the
+// passes by one lane per row. (With each row's lanes repeating the square
+// root, reciprocals and dyadic scale, 4 x 4096 tokens of 16 + 8 + 8 heads of
+// 128 channels took 535 us, most of it that scalar code.) In a batch of 8
+// rows, row i's sum ends up in lanes i LPR .. i LPR + LPR - 1 (LPR = LPH / 8);
+// lane l of the head owns row 8 (l % LPR) + l / LPR.
+template <int LPH>
+__device__ __forceinline__ u64 rows_sum(u64 (&v)[8]) {
+    const unsigned mask = seg_mask<LPH>();
+    int n = 8;
+#pragma unroll
+    for (int o = LPH / 2; o; o >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+                if (h < n) {
+                    const bool up = (threadIdx.x & o) != 0;
+                    const u64 keep = up ? v[h + n] : v[h], give = up ? v[h] : v[h + n];
+                    v[h] = keep + __shfl_xor_sync(mask, give, o);
+                }
+        } else {
+            v[0] += __shfl_xor_sync(mask, v[0], o);
         }
-        if (live && p.k_val) {
-            const size_t o = ((size_t)t * a.n_kv + kvh) * D + 4 * lane;
-            *(short4*)(p.k_val + o) = blk < 0 ? make_short4(0, 0, 0, 0)
-                : make_short4((short)((q[0] - 8) * c), (short)((q[1] - 8) * c), (short)((q[2] - 8) * c), (short)((q[3] - 8) * c));
+    }
+    return v[0];
+}
+
+template <int LPH, bool NORM>
+__device__ __forceinline__ void kv4_qk_chunk(const Kv4Args& a, const Kv4Append& p, int t0, int n, int slot, bool live,
+                                             int* st) {
+    constexpr int D = 4 * LPH, LPR = LPH / 8;
+    const unsigned mask = seg_mask<LPH>();
+    const int lane = threadIdx.x & (LPH - 1), base = threadIdx.x & 31 & ~(LPH - 1);
+    const bool isq = slot < a.nq;
+    const int kvh = isq ? (slot * a.gmul) >> 16 : slot - a.nq;
+    st += 4 * lane;                                          // row r at st + r D
+    // lane l: position (and for keys the page) of token t0 + l
+    int pos_l = lane < n ? p.tok_pos[t0 + lane] : -1;
+    if (pos_l >= p.max_pos) {
+        if (a.status) a.status[ST_CTX] = 1;
+        pos_l = -1;
+    }
+    int blk_l = -1, off_l = 0;
+    if (!isq && pos_l >= 0) blk_l = kv4_slot(a, p.tok_seq[t0 + lane], pos_l, &off_l);
+    const int32_t* row = p.qkv + (size_t)t0 * p.qkv_stride + (size_t)slot * D + 4 * lane;
+    const int4 ev = __ldg((const int4*)(a.params + (size_t)kvh * (8 + D) + 8 + 4 * lane));
+    const int e4[4] = {ev.x & 3, ev.y & 3, ev.z & 3, ev.w & 3};
+    Kv4Inv inv = {0u, 20};
+    int g4[4] = {0, 0, 0, 0};
+    if (NORM) {
+        const short4 gm = __ldg((const short4*)((isq ? p.q_gamma : p.k_gamma) + 4 * lane));
+        g4[0] = gm.x; g4[1] = gm.y; g4[2] = gm.z; g4[3] = gm.w;
+        u64 ss_l = 0;
+        int cl_l = 32;
+        const int32_t* r = row;
+#pragma unroll 1
+        for (int b = 0; 8 * b < n; ++b) {
+            int4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i, r += p.qkv_stride) {
+                v[i] = make_int4(0, 0, 0, 0);
+                if (__shfl_sync(mask, pos_l, base + 8 * b + i) >= 0) v[i] = __ldg((const int4*)r);
+            }
+            u64 ss[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                int y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                const int cl = __clz(seg_max<LPH>(max4(y)));
+                ss[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    y[j] = kv4_cut(y[j], cl);
+                    ss[i] += (u64)((i64)y[j] * y[j]);
+                }
+                if (lane == i * LPR + b) cl_l = cl;
+                *(int4*)(st + (8 * b + i) * D) = make_int4(y[0], y[1], y[2], y[3]);
+            }
+            const u64 s = rows_sum<LPH>(ss);
+            if ((lane & (LPR - 1)) == b) ss_l = s;
+        }
+        inv = kv4_inv_rms(ss_l, LPH == 32 ? 7 : 6, cl_l, p.eps);
+    }
+    const int E = isq ? (int)seg_max<LPH>((unsigned)max(max(e4[0], e4[1]), max(e4[2], e4[3]))) : 0;
+    Kv4Fix f = {0, 0, 0};
+    if (!isq) f = kv4_fix(a.params[(size_t)kvh * (8 + D)], a.params[(size_t)kvh * (8 + D) + 1]);
+    unsigned am_l = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i, row += p.qkv_stride) {
+        const int own = (i & 7) * LPR + (i >> 3);
+        const int pos = __shfl_sync(mask, pos_l, base + i);
+        int4 v = make_int4(0, 0, 0, 0);
+        if (NORM) v = *(const int4*)(st + i * D);
+        else if (pos >= 0) v = __ldg((const int4*)row);
+        int y[4] = {v.x, v.y, v.z, v.w};
+        const unsigned R = NORM ? __shfl_sync(mask, inv.R, base + own) : 0u;
+        const int bl = NORM ? __shfl_sync(mask, inv.bl, base + own) : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = NORM ? kv4_scale(y[j], g4[j], R, bl) : kv4_x4(y[j]);
+        kv4_rotate<LPH, NORM>(p, pos, y);
+        if (isq) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = NORM ? y[j] << (E - e4[j]) : sat32((i64)y[j] << (E - e4[j]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[j] = kv4_fixed(f, e4[j], y[j]);
+        }
+        const unsigned am = seg_max<LPH>(max4(y));
+        if (lane == own) am_l = am;
+        *(int4*)(st + i * D) = make_int4(y[0], y[1], y[2], y[3]);
+    }
+    // (a lane reads back only what it stored itself)
+    int R_l = 0, c_l = 1;
+    if (isq) {
+        int m, k;
+        kv4_qscale(am_l, &R_l, &m, &k);
+        const int mine = 8 * (lane & (LPR - 1)) + lane / LPR;
+        if (live && mine < n) {
+            p.mq[(size_t)(t0 + mine) * a.nq + slot] = m;
+            p.kq[(size_t)(t0 + mine) * a.nq + slot] = k;
+        }
+        int8_t* qd = p.q8 + ((size_t)t0 * a.nq + slot) * D + 4 * lane;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i, qd += a.nq * D) {
+            const int own = base + (i & 7) * LPR + (i >> 3);
+            const int R = __shfl_sync(mask, R_l, own);
+            const unsigned am = __shfl_sync(mask, am_l, own);
+            const int4 y = *(const int4*)(st + i * D);
+            if (live)
+                *(char4*)qd = make_char4((signed char)kv4_q8(y.x, am, R), (signed char)kv4_q8(y.y, am, R),
+                                         (signed char)kv4_q8(y.z, am, R), (signed char)kv4_q8(y.w, am, R));
+        }
+    } else {
+        c_l = kv4_code_scale(am_l);
+        R_l = kv4_code_inv(c_l);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const int own = base + (i & 7) * LPR + (i >> 3);
+            const int R = __shfl_sync(mask, R_l, own), c = __shfl_sync(mask, c_l, own);
+            const int4 y = *(const int4*)(st + i * D);
+            const int q[4] = {kv4_code(y.x, R, c), kv4_code(y.y, R, c), kv4_code(y.z, R, c), kv4_code(y.w, R, c)};
+            kv4_put_k<LPH>(a, p, t0 + i, kvh, __shfl_sync(mask, blk_l, base + i), __shfl_sync(mask, off_l, base + i), q, c, live);
         }
     }
 }
 
 // blockIdx.x is a tile of consecutive tokens. blockIdx.y below qk_blocks: one
-// warp (half a warp for 64 channels) per q or k head, a token at a time;
-// above: the values of one kv head, quantised a token at a time into shared
-// memory and then written by words of 8 keys. A run of tokens that fills a
-// word is one store; a shorter run changes its own nibbles with two atomics,
-// so that another CTA's tokens in the same word are kept (the nibbles are
-// distinct, so the order of the atomics does not matter).
+// warp (half a warp for 64 channels) per q or k head; above: the values of one
+// kv head, whose codes are collected in shared memory and then written by
+// words of 8 keys. A run of tokens that fills a word is one store; a shorter
+// run changes its own nibbles with two atomics, so that another CTA's tokens
+// in the same word are kept (the nibbles are distinct, so the order of the
+// atomics does not matter).
 constexpr int KV4_APT = 128;     // append threads
 constexpr int KV4_VTILE = 64;    // most tokens in a tile
 
-template <int LPH>
+template <int LPH, bool NORM, bool CHUNK>
 __global__ void __launch_bounds__(KV4_APT) k_kv4_append(Kv4Args a, Kv4Append p) {
     constexpr int D = 4 * LPH, HPW = 32 / LPH, HPB = (KV4_APT / 32) * HPW;
-    const int warp = threadIdx.x >> 5;
+    extern __shared__ __align__(16) unsigned char kv4_raw[];
     const int t0 = (int)blockIdx.x * p.tile, nt = min(p.tile, p.T - t0);
+    const int lane = threadIdx.x & (LPH - 1), hd = (int)threadIdx.x / LPH;
     if ((int)blockIdx.y < p.qk_blocks) {
-        const int slot = (int)blockIdx.y * HPB + (int)(threadIdx.x / LPH);
+        const int slot = (int)blockIdx.y * HPB + hd;
         const bool live = slot < a.nq + a.n_kv;
-        for (int i = 0; i < nt; ++i) kv4_qk_head<LPH>(a, p, t0 + i, live ? slot : 0, live);
+        if (CHUNK) {
+            for (int i = 0; i < nt; i += LPH)
+                kv4_qk_chunk<LPH, NORM>(a, p, t0 + i, min(LPH, nt - i), live ? slot : 0, live, (int*)kv4_raw + hd * (LPH * D));
+        } else {
+            for (int i = 0; i < nt; ++i) kv4_qk_row<LPH, NORM>(a, p, t0 + i, live ? slot : 0, live);
+        }
         return;
     }
-    __shared__ uint8_t codes[KV4_VTILE][D];
-    __shared__ int page[KV4_VTILE], offs[KV4_VTILE];
+    __shared__ int page[KV4_VTILE], offs[KV4_VTILE], code[KV4_VTILE], cinv[KV4_VTILE];
+    short4* xs = (short4*)kv4_raw;                           // [nt][LPH] cached integers before coding
+    int* cw = (int*)(xs + p.tile * LPH);                     // [nt][LPH] four codes each
     const int g = (int)blockIdx.y - p.qk_blocks;
     const int32_t* kvp = a.params + (size_t)g * (8 + D);
-    const i64 VQM = kvp[2];
-    const int VQS = min(max(kvp[3], 0), 62);
-    for (int i0 = warp * HPW; i0 < nt; i0 += HPB) {
-        const int i = i0 + (int)((threadIdx.x & 31) / LPH), lane = threadIdx.x & (LPH - 1);
-        const bool live = i < nt;
-        const int t = t0 + (live ? i : 0);
-        const int pos = live ? p.tok_pos[t] : -1;
-        int off = 0, blk = -1;
-        if (pos >= 0 && pos < p.max_pos) blk = kv4_slot(a, p.tok_seq[t], pos, &off);
-        int x[4] = {0, 0, 0, 0}, q[4];
-        if (blk >= 0) {
-            const int4 v = *(const int4*)(p.qkv + (size_t)t * p.qkv_stride + (size_t)(a.nq + a.n_kv + g) * D + 4 * lane);
-            const int v4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = (int)sat_b(rshr((i64)v4[j] * VQM, VQS), KV4_XMAX);
-        }
-        const int c = kv4_codes<LPH>(x, q);
-        if (live) {
-            *(int*)&codes[i][4 * lane] = q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24);
-            if (lane == 0) {
-                page[i] = blk;
-                offs[i] = off;
-                if (blk >= 0) a.vs[((size_t)blk * a.n_kv + g) * KV_BLK + off] = (uint8_t)c;
-            }
-            if (p.v_val)
-                *(short4*)(p.v_val + ((size_t)t * a.n_kv + g) * D + 4 * lane) = blk < 0 ? make_short4(0, 0, 0, 0)
-                    : make_short4((short)((q[0] - 8) * c), (short)((q[1] - 8) * c), (short)((q[2] - 8) * c), (short)((q[3] - 8) * c));
+    const Kv4Fix f = kv4_fix(kvp[2], kvp[3]);
+    if ((int)threadIdx.x < nt) {
+        int off;
+        page[threadIdx.x] = kv4_page_of(a, p, t0 + (int)threadIdx.x, p.tok_pos[t0 + threadIdx.x], &off);
+        offs[threadIdx.x] = off;
+    }
+    __syncthreads();
+    const int32_t* row = p.qkv + (size_t)t0 * p.qkv_stride + (size_t)(a.nq + a.n_kv + g) * D + 4 * lane;
+    const int rounds = (nt + HPB - 1) / HPB;
+#pragma unroll 4
+    for (int k = 0; k < rounds; ++k) {
+        const int i = k * HPB + hd;
+        int4 v = make_int4(0, 0, 0, 0);
+        if (i < nt && page[i] >= 0) v = __ldg((const int4*)(row + (size_t)i * p.qkv_stride));
+        const int x[4] = {kv4_fixed(f, 0, v.x), kv4_fixed(f, 0, v.y), kv4_fixed(f, 0, v.z), kv4_fixed(f, 0, v.w)};
+        const unsigned am = seg_max<LPH>(max4(x));
+        if (i < nt) {
+            xs[i * LPH + lane] = make_short4((short)x[0], (short)x[1], (short)x[2], (short)x[3]);
+            if (lane == 0) code[i] = (int)am;
         }
     }
     __syncthreads();
-    for (int i = 0; i < nt; ++i) {
+    if ((int)threadIdx.x < nt) {
+        const int c = kv4_code_scale((unsigned)code[threadIdx.x]), blk = page[threadIdx.x];
+        code[threadIdx.x] = c;
+        cinv[threadIdx.x] = kv4_code_inv(c);
+        if (blk >= 0) a.vs[((size_t)blk * a.n_kv + g) * KV_BLK + offs[threadIdx.x]] = (uint8_t)c;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int k = 0; k < rounds; ++k) {
+        const int i = k * HPB + hd;
+        if (i >= nt) break;
+        const short4 x = xs[i * LPH + lane];
+        const int R = cinv[i], c = code[i];
+        const int q[4] = {kv4_code(x.x, R, c), kv4_code(x.y, R, c), kv4_code(x.z, R, c), kv4_code(x.w, R, c)};
+        cw[i * LPH + lane] = pack4(q);
+        if (p.v_val)
+            *(short4*)(p.v_val + ((size_t)(t0 + i) * a.n_kv + g) * D + 4 * lane) =
+                page[i] < 0 ? make_short4(0, 0, 0, 0) : val4(q, c);
+    }
+    __syncthreads();
+    // words: a head's lanes take a run of tokens, each its four channels
+    for (int i = hd; i < nt; i += HPB) {
         const int blk = page[i], off = offs[i];
-        if (blk < 0) continue;
         // a run starts where the word changes or the positions stop ascending
-        if (i > 0 && page[i - 1] == blk && (offs[i - 1] >> 3) == (off >> 3) && offs[i - 1] < off) continue;
-        uint32_t* vp = (uint32_t*)(a.v + ((size_t)blk * a.n_kv + g) * (D * KV_BLK / 2));
-        for (int ch = threadIdx.x; ch < D; ch += KV4_APT) {
-            unsigned w = 0, mask = 0;
-            int last = -1;
-            for (int j = i; j < nt && page[j] == blk && (offs[j] >> 3) == (off >> 3) && offs[j] > last; ++j) {
-                last = offs[j];
-                const int sh = 8 * (last & 3) + (last & 4);
-                w |= (unsigned)codes[j][ch] << sh;
-                mask |= 15u << sh;
-            }
-            uint32_t* d = vp + (ch >> 4) * 128 + (ch & 7) * 16 + (off >> 4) * 4 + ((ch >> 3) & 1) * 2 + ((off >> 3) & 1);
-            if (mask == 0xffffffffu) {
-                *d = w;
+        if (blk < 0 || (i > 0 && page[i - 1] == blk && (offs[i - 1] >> 3) == (off >> 3) && offs[i - 1] < off)) continue;
+        int w[8];                                            // codes of the word's keys
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = 0;
+        unsigned have = 0;
+        int last = -1;
+        for (int j = i; j < nt && page[j] == blk && (offs[j] >> 3) == (off >> 3) && offs[j] > last; ++j) {
+            last = offs[j];
+            have |= 1u << (last & 7);
+            const int v = cw[j * LPH + lane];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if ((last & 7) == k) w[k] = v;
+        }
+        // nibbles: key k and k + 4 share a byte; then a 4 x 4 byte transpose
+        const int b0 = w[0] | (w[4] << 4), b1 = w[1] | (w[5] << 4), b2 = w[2] | (w[6] << 4), b3 = w[3] | (w[7] << 4);
+        const unsigned p01 = __byte_perm(b0, b1, 0x5140), q01 = __byte_perm(b0, b1, 0x7362);
+        const unsigned p23 = __byte_perm(b2, b3, 0x5140), q23 = __byte_perm(b2, b3, 0x7362);
+        const unsigned o[4] = {__byte_perm(p01, p23, 0x5410), __byte_perm(p01, p23, 0x7632),
+                               __byte_perm(q01, q23, 0x5410), __byte_perm(q01, q23, 0x7632)};
+        uint32_t* vp = (uint32_t*)(a.v + ((size_t)blk * a.n_kv + g) * (D * KV_BLK / 2)) + (off >> 4) * 4 + ((off >> 3) & 1);
+        unsigned keep = 0;                                   // nibbles of keys that are not in the run
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (!(have >> k & 1)) keep |= 15u << (8 * (k & 3) + (k & 4));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int ch = 4 * lane + j;
+            uint32_t* d = vp + (ch >> 4) * 128 + (ch & 7) * 16 + ((ch >> 3) & 1) * 2;
+            if (!keep) {
+                *d = o[j];
             } else {
-                atomicAnd(d, ~mask);
-                atomicOr(d, w);
+                atomicAnd(d, keep);
+                atomicOr(d, o[j]);
             }
         }
     }
 }
 
 // ------------------------------------------------------------ attention
-// What a query row's scores become: E = exp2q(rshr((t - T) M, sh)). Below
-// t - T = dmin the result is zero, and clamping there keeps the shifted
-// product in 32 bits: |dmin M| < (24577 << sh) + M.
+// What a query row's scores become: E = exp2q(rshr(d M, sh)) with d = t - T
+// <= 0. M is brought to [2^29, 2^30] (and sh with it), and d to a multiple
+// that makes the shift at least 33, so that the shifted sum is the high word
+// of one 32 x 32 product plus a rounding constant: rshr(d M, sh) = (hi(d mul M)
+// + 2^(s2 - 1)) >> s2. From dmin on the result is zero; clamping there keeps
+// d mul in 32 bits. (A shift below 3 gives zero for every d < 0, as 3 does.)
 struct Kv4Row {
-    int M, sh, dmin;
-    unsigned rlo;      // 2^(sh - 1), the rounding constant
-    unsigned rhi;
+    int M, mul, dmin, s2;
 };
 __device__ __forceinline__ Kv4Row kv4_row(int mq, int kq, int cstm, int cstk) {
-    Kv4Row r;
-    const i64 M = (i64)mq * cstm;                       // <= 2^30 for dyadic mantissas
-    r.M = (int)min(max(M, 0ll), 2147483647ll);
-    r.sh = min(max(kq + cstk - 10, 0), 62);
-    r.dmin = -(1 << 28);                                // |t - T| < 2^27
-    if (r.M > 0 && r.sh < 44) {
-        const u64 n = 24577ull << r.sh;
-        if (n < ((u64)r.M << 28)) r.dmin = -(int)udiv_small(n, (u64)r.M) - 1;
-    }
-    const u64 h = r.sh ? 1ull << (r.sh - 1) : 0;
-    r.rlo = (unsigned)h;
-    r.rhi = (unsigned)(h >> 32);
+    Kv4Row r = {0, 1, 0, 1};                            // M = 0: every kept key has delta 0
+    const i64 m = (i64)mq * cstm;
+    if (m <= 0 || m > (1ll << 30)) return r;
+    const int z = max(__clz((int)m) - 2, 0);
+    const int sh = max(min(max(kq + cstk - 10, 0), 62) + z, 3);
+    const int s1 = max(33 - sh, 0);
+    if (sh + s1 - 32 >= 28) return r;                   // |d M| < 2^57: rounds to 0
+    r.M = (int)(m << z);
+    r.mul = 1 << s1;
+    r.s2 = sh + s1 - 32;
+    r.dmin = -(1 << 27);                                // |t - T| < 2^26
+    if (sh < 44) r.dmin = max(r.dmin, -(int)udiv_small(24577ull << sh, (u64)r.M) - 1);
     return r;
 }
-// 15-bit probability of score t against the row maximum T
+__device__ __forceinline__ unsigned shr_clamp(unsigned x, int n) {   // 0 for n >= 32
+    unsigned y;
+    asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(n));
+    return y;
+}
+// 15-bit probability of score t against the row maximum T: exp2q with the
+// constants of its Horner steps inside the shifted sums
 __device__ __forceinline__ int kv4_E(const Kv4Row& r, int t, int T) {
-    const int d = max(t - T, r.dmin);
-    const i64 p = (i64)d * r.M + (i64)(((u64)r.rhi << 32) | r.rlo);
-    const unsigned lo = (unsigned)p, hi = (unsigned)((u64)p >> 32);
-    const bool far = r.sh >= 32;
-    const int delta = (int)__funnelshift_r(far ? hi : lo, far ? (unsigned)((int)hi >> 31) : hi, r.sh & 31);
-    const int n = -(delta >> 10);
+    const int delta = (__mulhi(max(t - T, r.dmin) * r.mul, r.M) + (1 << (r.s2 - 1))) >> r.s2;
     const int f = delta & 1023;
-    const int inner = 7419 + ((2562 * f + 512) >> 10);
-    const int mid = 22787 + ((f * inner + 512) >> 10);
-    const int p2 = 32768 + ((f * mid + 512) >> 10);
-    const int ns = min(n, 24);
-    const int e = (p2 + ((1 << ns) >> 1)) >> ns;
-    return n >= 24 ? 0 : min(e, 32767);
+    const int v1 = (2562 * f + (512 + (7419 << 10))) >> 10;
+    const int v2 = (f * v1 + (512 + (22787 << 10))) >> 10;
+    const int p2 = (f * v2 + (512 + (32768 << 10))) >> 10;
+    return (int)min((shr_clamp(2u * (unsigned)p2, -(delta >> 10)) + 1) >> 1, 32767u);
 }
 __device__ __forceinline__ int kv4_W(int E, int cv) { return (E * cv + 64) >> 7; }   // < 2^16
 
@@ -362,18 +610,31 @@ __device__ __forceinline__ int kv4_out(i64 num, i64 RS, int bl, i64 MV, int KVS)
 // settle the maximum, and later the sums, among themselves: as one
 // thread-block cluster (S <= 16, distributed shared memory), or as CTAs of a
 // cooperative launch through a workspace.
-//   scores: a lane holds 32 channels of a key (one 16-byte load) and the
+//   scores: a warp takes a page. A lane holds 32 channels of a key and the
 //     matching 8 words of every q head in registers; dp4a, then a
-//     reduce-scatter over the key's lanes leaves each lane its own heads;
+//     reduce-scatter over the key's lanes leaves each lane its own heads (a
+//     lane keeps its heads in an order of its own, so that no select is
+//     needed to pick what it keeps);
 //   probabilities: four keys of a head per thread, split into the two bytes
 //     of W, tiles of 8 pages in shared memory;
 //   P V: mma.sync, V^T codes as the 16-row operand and the bytes of W as its
-//     columns 2 h + limb; a warp owns 16 channels, so nothing is reduced
-//     between warps at 128 channels.
-// dp4a and mma.sync run on different pipes (a loop of one does not slow the
-// other), so the two products overlap between the CTAs of an SM.
+//     columns 2 h + limb; a warp owns 16 channels. Low and high nibbles have
+//     accumulators of their own, the high ones 16 times the sum (no shift).
+// Each warp streams what it alone reads, whole K pages and then its 512-byte
+// slices of the V pages, through a ring of its own by bulk copies: no barrier
+// between warps while scores are formed, and the first V slices travel while
+// the unit settles its maximum. dp4a and mma.sync run on different pipes (a
+// loop of one does not slow the other).
 constexpr int KV4_DT = 256;      // decode threads
 constexpr int KV4_TP = 8;        // pages per probability tile
+
+template <int D>
+struct Kv4Ring {
+    static constexpr int PG = KV_BLK * D / 2;            // bytes of a K or V page
+    static constexpr int SLOT = PG + KV_BLK;             // a K page and its scale codes, or a tile's V slices
+    static constexpr int NST = D == 128 ? 2 : 4;         // slots per warp
+    static constexpr int BYTES = 8 * NST * SLOT;
+};
 
 template <int GT>
 struct Kv4DecSm {
@@ -432,16 +693,19 @@ __device__ __forceinline__ bool kv4_unit_barrier(unsigned* cnt, unsigned target,
 
 template <int D, int GT, bool GRID>
 __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) {
-    constexpr int LPK = D / 32, KPL = 32 / LPK, UK = 4 * KPL, UPP = KV_BLK / UK;
-    constexpr int HPL = GT >= LPK ? GT / LPK : 1;
+    using C = Kv4Ring<D>;
+    constexpr int LPK = D / 32, KPL = 32 / LPK;          // lanes per key, keys per load
+    constexpr int HPL = GT >= LPK ? GT / LPK : 1;        // heads a lane ends up with
+    constexpr int LPG = GT >= LPK ? 1 : LPK / GT;        // lanes that end up with the same head
     constexpr int NG = D / 16, WPG = 8 / NG, NV = KV4_TP / WPG;
     constexpr int NT = (2 * GT + 7) / 8, NPASS = (GT + 1) / 2;
     extern __shared__ __align__(16) unsigned char kv4_raw[];
     __shared__ Kv4DecSm<GT> sm;
-    i64* num_s = (i64*)kv4_raw;                       // [GT][D]
-    int* pg = (int*)(num_s + GT * D);                 // [cap / 64]
-    const int pitch = p.cap + 8;                      // 8 banks between heads
-    int* ts = pg + (((p.cap >> 6) + 3) & ~3);         // [GT][pitch]
+    __shared__ unsigned long long full[8][C::NST];
+    i64* num_s = (i64*)(kv4_raw + C::BYTES);             // [GT][D]
+    int* pg = (int*)(num_s + GT * D);                    // [cap / 64]
+    const int pitch = p.cap + 8;                         // 8 banks between heads
+    int* ts = pg + (((p.cap >> 6) + 3) & ~3);            // [GT][pitch]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int t = blockIdx.z + p.t0;
@@ -464,7 +728,7 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
     const int b0 = j0 >> 6, nb = ((j1 + 63) >> 6) - b0;
     const int per = (int)(((u64)(nb + (int)S - 1) * p.smul) >> 32);     // ceil(nb / S)
     const int pg0 = b0 + (int)rank * per, np = max(0, min(per, b0 + nb - pg0));
-    // this CTA's pages
+    // this CTA's pages, -1 for an entry outside the pool (its keys are masked)
     for (int i = tid; i < np; i += KV4_DT) {
         int blk = a.block_table[(size_t)seq * a.max_blocks + pg0 + i];
         if (blk < 0 || blk >= a.n_blocks) {
@@ -477,57 +741,93 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
         const size_t qi = (size_t)t * a.nq + h0 + min(tid, nh - 1);
         sm.row[tid] = kv4_row(p.mq[qi], p.kq[qi], kvp[6], kvp[7]);
     }
+    if (lane == 0)
+        for (int i = 0; i < C::NST; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     const int sub = lane & (LPK - 1), kl = lane / LPK;
+    // register head i is head HPL (i / HPL ^ sub') + i % HPL, sub' the lane's
+    // place among the lanes that keep heads apart
+    const int subh = sub / LPG;
     int qw[GT][8], qoff[GT];
 #pragma unroll
-    for (int h = 0; h < GT; ++h) {
+    for (int i = 0; i < GT; ++i) {
+        const int h = HPL * ((i / HPL) ^ subh) + (i & (HPL - 1));
         int4 u = make_int4(0, 0, 0, 0), v = u;
         if (h < nh) {
             const int4* qp = (const int4*)(p.q8 + ((size_t)t * a.nq + h0 + h) * D + sub * 32);
-            u = qp[0];
-            v = qp[1];
+            u = __ldg(qp);
+            v = __ldg(qp + 1);
         }
-        qw[h][0] = u.x; qw[h][1] = u.y; qw[h][2] = u.z; qw[h][3] = u.w;
-        qw[h][4] = v.x; qw[h][5] = v.y; qw[h][6] = v.z; qw[h][7] = v.w;
+        qw[i][0] = u.x; qw[i][1] = u.y; qw[i][2] = u.z; qw[i][3] = u.w;
+        qw[i][4] = v.x; qw[i][5] = v.y; qw[i][6] = v.z; qw[i][7] = v.w;
         int sq = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sq = __dp4a(qw[h][j], 0x01010101, sq);
-        qoff[h] = -8 * sq;                             // the codes are values + 8
+        for (int j = 0; j < 8; ++j) sq = __dp4a(qw[i][j], 0x01010101, sq);
+        qoff[i] = -8 * sq;                               // the codes are values + 8
     }
     __syncthreads();
+
+    // ---- this warp's stream: its K pages (warp, warp + 8, ...), then its
+    // channel group's slices of the V pages, a tile of KV4_TP pages at a time
+    const int cg = warp & (NG - 1), ph = warp / NG;
+    const int nk = np > warp ? (np - warp + 7) >> 3 : 0, ntile = (np + KV4_TP - 1) / KV4_TP;
+    unsigned char* ring = kv4_raw + warp * (C::NST * C::SLOT);
+    auto issue = [&](int q) {                            // whole warp
+        if (q >= nk + ntile) return;
+        const int st = q & (C::NST - 1);
+        const uint32_t bar = smem_u32(&full[warp][st]), dst = smem_u32(ring + st * C::SLOT);
+        if (q < nk) {
+            const int blk = pg[warp + 8 * q];
+            if (lane == 0) {
+                if (blk < 0) {
+                    mbar_arrive(bar);
+                } else {
+                    const size_t u = (size_t)blk * a.n_kv + g;
+                    mbar_arrive_expect_tx(bar, C::PG + KV_BLK);
+                    bulk_g2s(dst, a.k + u * C::PG, C::PG, bar);
+                    bulk_g2s(dst + C::PG, a.ks + u * KV_BLK, KV_BLK, bar);
+                }
+            }
+        } else {
+            const int pi = (q - nk) * KV4_TP + lane * WPG + ph;
+            const int blk = lane < NV && pi < np ? pg[pi] : -1;
+            const unsigned m = __ballot_sync(0xffffffffu, blk >= 0);
+            if (lane == 0) {
+                if (m) mbar_arrive_expect_tx(bar, 512 * __popc(m));
+                else mbar_arrive(bar);
+            }
+            __syncwarp();
+            if (blk >= 0) bulk_g2s(dst + lane * 512, a.v + ((size_t)blk * a.n_kv + g) * C::PG + cg * 512, 512, bar);
+        }
+    };
+    auto wait = [&](int q) {
+        if (!mbar_wait(smem_u32(&full[warp][q & (C::NST - 1)]), (q / C::NST) & 1) && a.status) a.status[ST_TIMEOUT] = 1;
+    };
+#pragma unroll
+    for (int q = 0; q < C::NST; ++q) issue(q);
 
     // ---- scores
     int tm[HPL];
 #pragma unroll
     for (int x = 0; x < HPL; ++x) tm[x] = KV4_NEG;
-    const int hb = GT >= LPK ? sub * HPL : (sub * GT) / LPK;
-    const bool writer = GT >= LPK || (sub & (LPK / GT - 1)) == 0;
-    const int nu = np * UPP;
-    auto load = [&](int u, int4 (&w)[4], int& blk) {
-        blk = -1;
-        if (u < nu) blk = pg[u / UPP];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = make_int4(0, 0, 0, 0);
-        if (blk < 0) return;
-        const uint8_t* base = a.k + (((size_t)blk * a.n_kv + g) * KV_BLK + (u & (UPP - 1)) * UK + kl) * (D / 2) + sub * 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __ldg((const int4*)(base + (size_t)i * KPL * (D / 2)));
-    };
-    int4 cur[4];
-    int cblk;
-    load(warp, cur, cblk);
-    for (int u = warp; u < nu; u += 8) {
-        int4 nxt[4];
-        int nblk;
-        load(u + 8, nxt, nblk);
-        const uint8_t* ckp = a.ks + ((size_t)max(cblk, 0) * a.n_kv + g) * KV_BLK + (u & (UPP - 1)) * UK + kl;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int ck = __ldg(ckp + i * KPL);
+    const int hb = subh * HPL;
+    const bool writer = (sub & (LPG - 1)) == 0;
+    for (int q = 0; q < nk; ++q) {
+        const int pi = warp + 8 * q, jb = (pg0 + pi) << 6;
+        const bool ok = pg[pi] >= 0, clear = ok && jb >= j0 && jb + 64 <= j1;     // no masked key
+        wait(q);
+        const unsigned char* base = ring + (q & (C::NST - 1)) * C::SLOT;
+        const unsigned char* kr = base + kl * (D / 2) + sub * 16;
+        const unsigned char* cr = base + C::PG + kl;
+        int* tw = ts + hb * pitch + pi * KV_BLK + kl;
+#pragma unroll 4
+        for (int i = 0; i < KV_BLK / KPL; ++i) {
+            const int4 kv = *(const int4*)(kr + i * (KPL * D / 2));
+            const int ck = cr[i * KPL];
+            const int w[4] = {kv.x, kv.y, kv.z, kv.w};
             int acc[GT];
 #pragma unroll
             for (int h = 0; h < GT; ++h) acc[h] = qoff[h];
-            const int w[4] = {cur[i].x, cur[i].y, cur[i].z, cur[i].w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int lo = kv4_lo(w[x]), hi = kv4_hi(w[x]);
@@ -536,7 +836,8 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
 #pragma unroll
                 for (int h = 0; h < GT; ++h) acc[h] = __dp4a(hi, qw[h][2 * x + 1], acc[h]);
             }
-            // reduce over the key's lanes; each keeps HPL heads where it can
+            // reduce over the key's lanes; the upper half of a lane's registers
+            // is its partner's lower half
             int n = GT;
 #pragma unroll
             for (int o = LPK / 2; o; o >>= 1) {
@@ -544,29 +845,22 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
                     n >>= 1;
 #pragma unroll
                     for (int h = 0; h < GT / 2; ++h)
-                        if (h < n) {
-                            const bool upper = (sub & o) != 0;
-                            const int keep = upper ? acc[h + n] : acc[h];
-                            const int give = upper ? acc[h] : acc[h + n];
-                            acc[h] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-                        }
+                        if (h < n) acc[h] += __shfl_xor_sync(0xffffffffu, acc[h + n], o);
                 } else {
                     acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
                 }
             }
-            const int key = u * UK + i * KPL + kl;
-            const int j = (pg0 << 6) + key;
-            const bool in = cblk >= 0 && j >= j0 && j < j1;
+            const int j = jb + i * KPL + kl;
+            const bool in = clear || (ok && j >= j0 && j < j1);
 #pragma unroll
             for (int x = 0; x < HPL; ++x) {
-                const int tv = in ? acc[x] * ck : KV4_NEG;
-                tm[x] = max(tm[x], tv);
-                if (writer) ts[(hb + x) * pitch + key] = tv;
+                const int tv = acc[x] * ck;
+                if (in) tm[x] = max(tm[x], tv);
+                if (writer) tw[x * pitch + i * KPL] = tv;
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) cur[i] = nxt[i];
-        cblk = nblk;
+        __syncwarp();
+        issue(q + C::NST);
     }
 #pragma unroll
     for (int x = 0; x < HPL; ++x) {
@@ -589,78 +883,88 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
     if (GRID) alive = kv4_unit_barrier(cnt, S, alive, a.status);
     else if (S > 1) cl_sync();
     else __syncthreads();
-    if (warp == 0) {
-        for (int h = 0; h < GT; ++h) {
-            int m = KV4_NEG;
-            for (unsigned r = lane; r < S; r += 32)
-                m = max(m, GRID ? __ldcg(p.ws_max + ((size_t)unit * S + r) * GT + h)
-                                : (S > 1 ? cl_ld32(&sm.cmax[h], r) : sm.cmax[h]));
-            m = __reduce_max_sync(0xffffffffu, m);
-            if (lane == 0) sm.tmax[h] = m;
-        }
+    for (int h = warp; h < GT; h += 8) {
+        int m = KV4_NEG;
+        for (unsigned r = lane; r < S; r += 32)
+            m = max(m, GRID ? __ldcg(p.ws_max + ((size_t)unit * S + r) * GT + h)
+                            : (S > 1 ? cl_ld32(&sm.cmax[h], r) : sm.cmax[h]));
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) sm.tmax[h] = m;
     }
     __syncthreads();
 
     // ---- probabilities and P V, tiles of KV4_TP pages
-    const int cg = warp & (NG - 1), ph = warp / NG;
     const int gid = lane >> 2, tig = lane & 3;
-    int acc[NT][4];
+    int acc[NT][2][4];                                   // low nibbles; high nibbles, times 16
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0;
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][0][e] = acc[n][1][e] = 0;
     unsigned sumE[NPASS], sumW[NPASS];
 #pragma unroll
     for (int x = 0; x < NPASS; ++x) sumE[x] = sumW[x] = 0;
-    int buf = 0;
-    for (int p0 = 0; p0 < np; p0 += KV4_TP, buf ^= 1) {
-        int4 vv[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int pi = p0 + i * WPG + ph;
-            const int blk = pi < np ? pg[pi] : -1;
-            vv[i] = make_int4(0, 0, 0, 0);
-            if (blk >= 0)
-                vv[i] = __ldg((const int4*)(a.v + ((size_t)blk * a.n_kv + g) * (D * KV_BLK / 2) + cg * 512) + lane);
-        }
+    const int qd = tid & 127;                            // this thread's four keys of a tile
+    auto load_cv = [&](int tile) -> uint32_t {
+        const int pi = tile * KV4_TP + (qd >> 4);
+        const int blk = pi < np ? pg[pi] : -1;
+        return blk >= 0 ? __ldg((const uint32_t*)(a.vs + ((size_t)blk * a.n_kv + g) * KV_BLK) + (qd & 15)) : 0u;
+    };
+    uint32_t cv_next = load_cv(0);
+    for (int tile = 0; tile < ntile; ++tile) {
+        const int buf = tile & 1;
+        const uint32_t cvw = cv_next;
+        cv_next = load_cv(tile + 1);
         {
-            const int qd = tid & 127, pi = p0 + (qd >> 4);
-            const int blk = pi < np ? pg[pi] : -1;
-            const uint32_t cvw = blk >= 0 ? __ldg((const uint32_t*)(a.vs + ((size_t)blk * a.n_kv + g) * KV_BLK) + (qd & 15)) : 0;
+            const int pi = tile * KV4_TP + (qd >> 4), jb = ((pg0 + pi) << 6) + 4 * (qd & 15);
+            const bool ok = pi < np && pg[pi] >= 0;
+            const bool clear = ok && jb >= j0 && jb + 4 <= j1;
 #pragma unroll
             for (int x = 0; x < NPASS; ++x) {
                 const int h = 2 * x + (tid >> 7);
                 if (h < GT) {
                     int w[4] = {0, 0, 0, 0};
-                    if (blk >= 0) {
+                    if (ok) {
                         const Kv4Row rw = sm.row[h];
                         const int T = sm.tmax[h];
-                        const int4 tv = *(const int4*)(ts + h * pitch + p0 * KV_BLK + qd * 4);
+                        const int4 tv = *(const int4*)(ts + h * pitch + pi * KV_BLK + 4 * (qd & 15));
                         const int t4[4] = {tv.x, tv.y, tv.z, tv.w};
+                        int e[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int E = t4[k] == KV4_NEG ? 0 : kv4_E(rw, t4[k], T);
-                            w[k] = kv4_W(E, (int)(cvw >> (8 * k)) & 255);
-                            sumE[x] += E;
-                            sumW[x] += w[k];
+                        for (int k = 0; k < 4; ++k) e[k] = kv4_E(rw, t4[k], T);
+                        if (!clear) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (jb + k < j0 || jb + k >= j1) e[k] = 0;
                         }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) w[k] = kv4_W(e[k], (int)(cvw >> (8 * k)) & 255);
+                        sumE[x] += (unsigned)(e[0] + e[1] + e[2] + e[3]);
+                        sumW[x] += (unsigned)(w[0] + w[1] + w[2] + w[3]);
                     }
-                    const unsigned wa = (unsigned)w[0] | ((unsigned)w[1] << 16), wb = (unsigned)w[2] | ((unsigned)w[3] << 16);
+                    const unsigned wa = (unsigned)w[0] + ((unsigned)w[1] << 16), wb = (unsigned)w[2] + ((unsigned)w[3] << 16);
                     sm.wp[buf][qd >> 4][2 * h][qd & 15] = __byte_perm(wa, wb, 0x6420);
                     sm.wp[buf][qd >> 4][2 * h + 1][qd & 15] = __byte_perm(wa, wb, 0x7531);
                 }
             }
         }
         __syncthreads();
+        wait(nk + tile);
+        const unsigned char* vb = ring + ((nk + tile) & (C::NST - 1)) * C::SLOT + lane * 16;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int pt = i * WPG + ph;
+            if (tile * KV4_TP + pt >= np) break;         // (a page outside the pool has W = 0)
+            const int4 v = *(const int4*)(vb + i * 512);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 int4 b = make_int4(0, 0, 0, 0);
                 if (8 * n + gid < 2 * GT) b = *(const int4*)&sm.wp[buf][pt][8 * n + gid][4 * tig];
-                mma_u8u8(acc[n], kv4_lo(vv[i].x), kv4_lo(vv[i].z), kv4_hi(vv[i].x), kv4_hi(vv[i].z), b.x, b.y);
-                mma_u8u8(acc[n], kv4_lo(vv[i].y), kv4_lo(vv[i].w), kv4_hi(vv[i].y), kv4_hi(vv[i].w), b.z, b.w);
+                mma_u8u8(acc[n][0], kv4_lo(v.x), kv4_lo(v.z), kv4_lo(v.y), kv4_lo(v.w), b.x, b.z);
+                mma_u8u8(acc[n][1], v.x & 0xf0f0f0f0, v.z & 0xf0f0f0f0, v.y & 0xf0f0f0f0, v.w & 0xf0f0f0f0, b.y, b.w);
             }
         }
+        __syncwarp();
+        issue(nk + tile + C::NST);
     }
     // ---- this CTA's sums: numerators [GT][D], sum E and sum W per head
 #pragma unroll
@@ -677,7 +981,10 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
                 const int h = 4 * n + tig;
                 if (h < GT) {
                     i64* d0 = num_s + h * D + cg * 16 + gid;
-                    const i64 v0 = (i64)acc[n][0] + (i64)acc[n][1] * 256, v1 = (i64)acc[n][2] + (i64)acc[n][3] * 256;
+                    int c[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c[e] = acc[n][0][e] + (acc[n][1][e] >> 4);
+                    const i64 v0 = (i64)c[0] + (i64)c[1] * 256, v1 = (i64)c[2] + (i64)c[3] * 256;
                     d0[0] = part ? d0[0] + v0 : v0;
                     d0[8] = part ? d0[8] + v1 : v1;
                 }
@@ -916,17 +1223,15 @@ __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p)
                         const int c = (int)(ck[j >> 1] >> (8 * ((2 * j + e) & 3))) & 255;
                         const int key = kb + 16 * tig + 2 * j + e;
                         const bool inA = clear || (key <= hiA && key >= loA), inB = clear || (key <= hiB && key >= loB);
-                        S[j][e] = inA ? S[j][e] * c : KV4_NEG;
-                        S[j][2 + e] = inB ? S[j][2 + e] * c : KV4_NEG;
+                        S[j][e] *= c;
+                        S[j][2 + e] *= c;
+                        if (i < np) {
+                            T[0] = inA ? max(T[0], S[j][e]) : T[0];
+                            T[1] = inB ? max(T[1], S[j][2 + e]) : T[1];
+                        }
                     }
                 }
-                if (i < np) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        T[0] = max(T[0], max(S[j][0], S[j][1]));
-                        T[1] = max(T[1], max(S[j][2], S[j][3]));
-                    }
-                } else {
+                if (i >= np) {
                     const uint4 cvv = *(const uint4*)(base + 2 * C::PG + KV_BLK + 16 * tig);
                     const unsigned cv[4] = {cvv.x, cvv.y, cvv.z, cvv.w};
                     int wl[2][4], wh[2][4];              // [row][4 keys]
@@ -939,7 +1244,9 @@ __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 const int s = S[2 * k + (e >> 1)][2 * x + (e & 1)];
-                                const int E = s == KV4_NEG ? 0 : kv4_E(rw[x], s, T[x]);
+                                int E = kv4_E(rw[x], s, T[x]);
+                                const int key = kb + 16 * tig + 4 * k + e;
+                                if (!clear && (key > (x ? hiB : hiA) || key < (x ? loB : loA))) E = 0;
                                 w[e] = kv4_W(E, (int)(cv[k] >> (8 * e)) & 255);
                                 te += E;
                                 tw += w[e];

@@ -16,7 +16,6 @@ namespace {
 
 constexpr int KV4_MAX_LEN = 1 << 19;       // keys: the limb sums stay in int32
 constexpr size_t KV4_SMEM_CTA = 200 * 1024;  // dynamic shared memory of one decode CTA at most
-constexpr size_t KV4_SMEM_2 = 96 * 1024;   // up to here two decode CTAs share an SM
 
 struct DevInfo {
     bool ready = false;
@@ -47,8 +46,24 @@ DecFn dec_kernel(int d, int gt) {
     return k_kv4_decode<64, 8, GRID>;
 }
 
+using AppFn = void (*)(Kv4Args, Kv4Append);
+AppFn append_kernel(int d, bool norm, bool chunk) {
+    static const AppFn f[2][2][2] = {
+        {{k_kv4_append<16, false, false>, k_kv4_append<16, false, true>}, {k_kv4_append<16, true, false>, k_kv4_append<16, true, true>}},
+        {{k_kv4_append<32, false, false>, k_kv4_append<32, false, true>}, {k_kv4_append<32, true, false>, k_kv4_append<32, true, true>}}};
+    return f[d == 128][norm][chunk];
+}
+
 size_t dec_smem(int d, int gt, int cap) {
-    return (size_t)gt * d * 8 + (size_t)(((cap >> 6) + 3) & ~3) * 4 + (size_t)gt * (cap + 8) * 4;
+    const size_t ring = d == 128 ? Kv4Ring<128>::BYTES : Kv4Ring<64>::BYTES;
+    return ring + (size_t)gt * d * 8 + (size_t)(((cap >> 6) + 3) & ~3) * 4 + (size_t)gt * (cap + 8) * 4;
+}
+
+// dynamic shared memory up to which two decode CTAs share an SM (228 KB, 1 KB
+// of it reserved for each CTA)
+size_t dec_smem2(int gt) {
+    const size_t fixed = gt == 8 ? sizeof(Kv4DecSm<8>) : gt == 4 ? sizeof(Kv4DecSm<4>) : gt == 2 ? sizeof(Kv4DecSm<2>) : sizeof(Kv4DecSm<1>);
+    return 114 * 1024 - 1024 - 1024 - fixed;
 }
 
 // how a decode call is split
@@ -71,7 +86,7 @@ DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len,
         // a cluster: as many CTAs as keep two on every SM busy, at least 2 pages each
         int S = 1;
         while (S < di.max_cluster && units * S < 2 * di.sms && mp >= 4 * S) S <<= 1;
-        while (S < di.max_cluster && dec_smem(d, p.gt, ((mp + S - 1) / S) << 6) > KV4_SMEM_2) S <<= 1;
+        while (S < di.max_cluster && dec_smem(d, p.gt, ((mp + S - 1) / S) << 6) > dec_smem2(p.gt)) S <<= 1;
         p.S = S;
         p.cap = ((mp + S - 1) / S) << 6;
         p.smem = dec_smem(d, p.gt, p.cap);
@@ -80,7 +95,7 @@ DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len,
         if (units * S < di.sms && mp >= 8 * S) {
             const int Sg = (int)std::min<long long>((2 * di.sms) / units, mp / 4);
             const int cap = ((mp + Sg - 1) / Sg) << 6;
-            if (Sg > S && dec_smem(d, p.gt, cap) <= KV4_SMEM_2) {
+            if (Sg > S && dec_smem(d, p.gt, cap) <= dec_smem2(p.gt)) {
                 p.S = Sg;
                 p.cap = cap;
                 p.smem = dec_smem(d, p.gt, cap);
@@ -141,6 +156,10 @@ cudaError_t kv4_init() {
                 mc = 8;
             }
         }
+    for (int d : {64, 128})
+        for (int norm = 0; norm < 2; ++norm)
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(append_kernel(d, norm, true), cudaFuncAttributeMaxDynamicSharedMemorySize, d * 512);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k_kv4_prefill<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Kv4Pf<64>::SMEM);
     if (e == cudaSuccess)
@@ -158,13 +177,16 @@ cudaError_t launch_kv4_append(const Kv4Args& a, const Kv4Append& p0, int d, cuda
     if (!di || !di->ready) return cudaErrorInvalidDevice;
     const int hpb = d == 128 ? 4 : 8;
     p.qk_blocks = (a.nq + a.n_kv + hpb - 1) / hpb;
-    // tokens per CTA: whole pages of tokens where there are enough CTAs for it
+    // Tokens per CTA: as many as a page where that still makes 4 CTAs per SM;
+    // below 8 the chunk's three passes have too few rows (T = 32 tokens of
+    // 32 + 8 + 8 heads: one row at a time)
     const int per_tile = p.qk_blocks + a.n_kv;
     p.tile = KV4_VTILE;
-    while (p.tile > 1 && (long long)((p.T + p.tile - 1) / p.tile) * per_tile < 8LL * di->sms) p.tile >>= 1;
+    while (p.tile > 1 && (long long)((p.T + p.tile - 1) / p.tile) * per_tile < 4LL * di->sms) p.tile >>= 1;
     const dim3 grid((p.T + p.tile - 1) / p.tile, per_tile);
-    if (d == 128) k_kv4_append<32><<<grid, KV4_APT, 0, s>>>(a, p);
-    else k_kv4_append<16><<<grid, KV4_APT, 0, s>>>(a, p);
+    // values: 3 bytes per channel and token; chunks: a warp's 32 x 128 (or 2 x 16 x 64) integers
+    const size_t smem = p.tile < 8 ? (size_t)p.tile * d * 3 : (size_t)d * 512;
+    append_kernel(d, p.q_gamma != nullptr, p.tile >= 8)<<<grid, KV4_APT, smem, s>>>(a, p);
     return cudaGetLastError();
 }
 
@@ -311,6 +333,7 @@ int detint_kv4_append(const detint_kv4_t* c, const detint_rope_t* r, const int32
     if (!r->q_gamma != !r->k_gamma) return err(DETINT_E_ARG, "both gammas or none");
     if (r->eps < 0 || r->eps > 32767) return err(DETINT_E_ARG, "eps must be in 0..32767");
     if (mis(r->cos, 8) || mis(r->sin, 8) || mis(r->q_gamma, 8) || mis(r->k_gamma, 8)) return err(DETINT_E_ARG, "tables and gammas must be 8-byte aligned");
+    if ((long long)r->max_pos * r->rot_dim > 0x7fffffffLL) return err(DETINT_E_SHAPE, "rotation tables too large");
     if (qkv_stride < (long long)(c->n_q + 2 * c->n_kv) * d || (qkv_stride & 3) || mis(qkv, 16))
         return err(DETINT_E_ARG, "qkv rows must be 16-byte aligned and hold every head");
     if (mis(q8, 16) || mis(k_val, 8) || mis(v_val, 8)) return err(DETINT_E_ARG, "outputs misaligned");
