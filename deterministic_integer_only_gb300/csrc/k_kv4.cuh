@@ -607,9 +607,8 @@ __device__ __forceinline__ int kv4_out(i64 num, i64 RS, int bl, i64 MV, int KVS)
 // ------------------------------------------- attention of single tokens
 // One unit is a token, a kv head and up to GT of its q heads; its keys are
 // split by pages over S CTAs, which keep their scores in shared memory and
-// settle the maximum, and later the sums, among themselves: as one
-// thread-block cluster (S <= 16, distributed shared memory), or as CTAs of a
-// cooperative launch through a workspace.
+// settle the maximum, and later the sums, among themselves as one thread-block
+// cluster (S <= 16, distributed shared memory).
 //   scores: a warp takes a page. A lane holds 32 channels of a key and the
 //     matching 8 words of every q head in registers; dp4a, then a
 //     reduce-scatter over the key's lanes leaves each lane its own heads (a
@@ -672,31 +671,125 @@ __device__ __forceinline__ i64 cl_ld64(const i64* p, unsigned rank) {
     return v;
 }
 
-// all S CTAs of a unit of a cooperative launch; false when the bounded wait
-// ran out (recorded; the results are then invalid)
-__device__ __forceinline__ bool kv4_unit_barrier(unsigned* cnt, unsigned target, bool alive, int32_t* status) {
-    __shared__ int s_ok;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        __threadfence();
-        atomicAdd(cnt, 1u);
-        bool ok = false;
-        if (alive)
-            for (int i = 0; i < (1 << 20) && !ok; ++i) ok = *(volatile unsigned*)cnt >= target;
-        if (!ok && status) status[ST_TIMEOUT] = 1;
-        __threadfence();
-        s_ok = ok;
+// q heads of a lane: register head i is head HPL (i / HPL ^ subh) + i % HPL,
+// subh the lane's place among the lanes that keep heads apart
+template <int D, int GT>
+struct Kv4Q {
+    static constexpr int LPK = D / 32, KPL = 32 / LPK;               // lanes per key, keys per load
+    static constexpr int HPL = GT >= LPK ? GT / LPK : 1;             // heads a lane ends up with
+    static constexpr int LPG = GT >= LPK ? 1 : LPK / GT;             // lanes that end up with the same head
+    int w[GT][8], off[GT];
+
+    __device__ __forceinline__ void load(const int8_t* q8, int nh) { // q8: the unit's first head
+        const int sub = threadIdx.x & (LPK - 1), subh = sub / LPG;
+#pragma unroll
+        for (int i = 0; i < GT; ++i) {
+            const int h = HPL * ((i / HPL) ^ subh) + (i & (HPL - 1));
+            int4 u = make_int4(0, 0, 0, 0), v = u;
+            if (h < nh) {
+                const int4* qp = (const int4*)(q8 + (size_t)h * D + sub * 32);
+                u = __ldg(qp);
+                v = __ldg(qp + 1);
+            }
+            w[i][0] = u.x; w[i][1] = u.y; w[i][2] = u.z; w[i][3] = u.w;
+            w[i][4] = v.x; w[i][5] = v.y; w[i][6] = v.z; w[i][7] = v.w;
+            int sq = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sq = __dp4a(w[i][j], 0x01010101, sq);
+            off[i] = -8 * sq;                                        // the codes are values + 8
+        }
     }
-    __syncthreads();
-    return s_ok != 0;
+    // scores of a page in shared memory (K codes, then 64 scale codes): this
+    // lane's heads [HPL] of key i KPL + lane / LPK go to out[x * pitch + i KPL];
+    // keys outside [lo, hi) do not count for the maxima tm
+    __device__ __forceinline__ void page(const unsigned char* base, int* out, int pitch, bool clear, int lo, int hi, int (&tm)[HPL]) const {
+        const int lane = threadIdx.x & 31, sub = lane & (LPK - 1), kl = lane / LPK;
+        const unsigned char* kr = base + kl * (D / 2) + sub * 16;
+        const unsigned char* cr = base + KV_BLK * D / 2 + kl;
+        const bool writer = (sub & (LPG - 1)) == 0;
+#pragma unroll 4
+        for (int i = 0; i < KV_BLK / KPL; ++i) {
+            const int4 kv = *(const int4*)(kr + i * (KPL * D / 2));
+            const int ck = cr[i * KPL];
+            const int ww[4] = {kv.x, kv.y, kv.z, kv.w};
+            int acc[GT];
+#pragma unroll
+            for (int h = 0; h < GT; ++h) acc[h] = off[h];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int l = kv4_lo(ww[x]), u = kv4_hi(ww[x]);
+#pragma unroll
+                for (int h = 0; h < GT; ++h) acc[h] = __dp4a(l, w[h][2 * x], acc[h]);
+#pragma unroll
+                for (int h = 0; h < GT; ++h) acc[h] = __dp4a(u, w[h][2 * x + 1], acc[h]);
+            }
+            // reduce over the key's lanes; the upper half of a lane's registers
+            // is its partner's lower half
+            int n = GT;
+#pragma unroll
+            for (int o = LPK / 2; o; o >>= 1) {
+                if (n > 1) {
+                    n >>= 1;
+#pragma unroll
+                    for (int h = 0; h < GT / 2; ++h)
+                        if (h < n) acc[h] += __shfl_xor_sync(0xffffffffu, acc[h + n], o);
+                } else {
+                    acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+                }
+            }
+            const int j = i * KPL + kl;
+            const bool in = clear || (j >= lo && j < hi);
+#pragma unroll
+            for (int x = 0; x < HPL; ++x) {
+                const int tv = acc[x] * ck;
+                if (in) tm[x] = max(tm[x], tv);
+                if (writer) out[x * pitch + i * KPL] = tv;
+            }
+        }
+    }
+};
+
+// the probabilities of four keys of one head: W's low and high bytes, packed,
+// and their sums
+__device__ __forceinline__ void kv4_probs(const Kv4Row& rw, int T, const int4& tv, uint32_t cvw, bool clear, int lo, int hi,
+                                          uint32_t* wl, uint32_t* wh, unsigned* sumE, unsigned* sumW) {
+    const int t4[4] = {tv.x, tv.y, tv.z, tv.w};
+    int e[4], w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) e[k] = kv4_E(rw, t4[k], T);
+    if (!clear) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < lo || k >= hi) e[k] = 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = kv4_W(e[k], (int)(cvw >> (8 * k)) & 255);
+    *sumE += (unsigned)(e[0] + e[1] + e[2] + e[3]);
+    *sumW += (unsigned)(w[0] + w[1] + w[2] + w[3]);
+    const unsigned wa = (unsigned)w[0] + ((unsigned)w[1] << 16), wb = (unsigned)w[2] + ((unsigned)w[3] << 16);
+    *wl = __byte_perm(wa, wb, 0x6420);
+    *wh = __byte_perm(wa, wb, 0x7531);
+}
+// one page's P V of a warp's 16 channels: vb its 512-byte slice (+ lane * 16),
+// wp the page's probability bytes [2 GT][16 words]
+template <int GT, int NT>
+__device__ __forceinline__ void kv4_pv_page(int (&acc)[NT][2][4], const unsigned char* vb, const uint32_t (*wp)[16]) {
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    const int4 v = *(const int4*)vb;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        int4 b = make_int4(0, 0, 0, 0);
+        if (8 * n + gid < 2 * GT) b = *(const int4*)&wp[8 * n + gid][4 * tig];
+        mma_u8u8(acc[n][0], kv4_lo(v.x), kv4_lo(v.z), kv4_lo(v.y), kv4_lo(v.w), b.x, b.z);
+        mma_u8u8(acc[n][1], v.x & 0xf0f0f0f0, v.z & 0xf0f0f0f0, v.y & 0xf0f0f0f0, v.w & 0xf0f0f0f0, b.y, b.w);
+    }
 }
 
-template <int D, int GT, bool GRID>
+template <int D, int GT>
 __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) {
     using C = Kv4Ring<D>;
-    constexpr int LPK = D / 32, KPL = 32 / LPK;          // lanes per key, keys per load
-    constexpr int HPL = GT >= LPK ? GT / LPK : 1;        // heads a lane ends up with
-    constexpr int LPG = GT >= LPK ? 1 : LPK / GT;        // lanes that end up with the same head
+    using Q = Kv4Q<D, GT>;
+    constexpr int LPK = Q::LPK, HPL = Q::HPL;
     constexpr int NG = D / 16, WPG = 8 / NG, NV = KV4_TP / WPG;
     constexpr int NT = (2 * GT + 7) / 8, NPASS = (GT + 1) / 2;
     extern __shared__ __align__(16) unsigned char kv4_raw[];
@@ -744,27 +837,8 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
     if (lane == 0)
         for (int i = 0; i < C::NST; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    const int sub = lane & (LPK - 1), kl = lane / LPK;
-    // register head i is head HPL (i / HPL ^ sub') + i % HPL, sub' the lane's
-    // place among the lanes that keep heads apart
-    const int subh = sub / LPG;
-    int qw[GT][8], qoff[GT];
-#pragma unroll
-    for (int i = 0; i < GT; ++i) {
-        const int h = HPL * ((i / HPL) ^ subh) + (i & (HPL - 1));
-        int4 u = make_int4(0, 0, 0, 0), v = u;
-        if (h < nh) {
-            const int4* qp = (const int4*)(p.q8 + ((size_t)t * a.nq + h0 + h) * D + sub * 32);
-            u = __ldg(qp);
-            v = __ldg(qp + 1);
-        }
-        qw[i][0] = u.x; qw[i][1] = u.y; qw[i][2] = u.z; qw[i][3] = u.w;
-        qw[i][4] = v.x; qw[i][5] = v.y; qw[i][6] = v.z; qw[i][7] = v.w;
-        int sq = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sq = __dp4a(qw[i][j], 0x01010101, sq);
-        qoff[i] = -8 * sq;                               // the codes are values + 8
-    }
+    Q qr;
+    qr.load(p.q8 + ((size_t)t * a.nq + h0) * D, nh);
     __syncthreads();
 
     // ---- this warp's stream: its K pages (warp, warp + 8, ...), then its
@@ -810,55 +884,13 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
     int tm[HPL];
 #pragma unroll
     for (int x = 0; x < HPL; ++x) tm[x] = KV4_NEG;
-    const int hb = subh * HPL;
-    const bool writer = (sub & (LPG - 1)) == 0;
+    const int sub = lane & (LPK - 1), hb = sub / Q::LPG * HPL;
     for (int q = 0; q < nk; ++q) {
         const int pi = warp + 8 * q, jb = (pg0 + pi) << 6;
-        const bool ok = pg[pi] >= 0, clear = ok && jb >= j0 && jb + 64 <= j1;     // no masked key
+        const bool ok = pg[pi] >= 0;
         wait(q);
-        const unsigned char* base = ring + (q & (C::NST - 1)) * C::SLOT;
-        const unsigned char* kr = base + kl * (D / 2) + sub * 16;
-        const unsigned char* cr = base + C::PG + kl;
-        int* tw = ts + hb * pitch + pi * KV_BLK + kl;
-#pragma unroll 4
-        for (int i = 0; i < KV_BLK / KPL; ++i) {
-            const int4 kv = *(const int4*)(kr + i * (KPL * D / 2));
-            const int ck = cr[i * KPL];
-            const int w[4] = {kv.x, kv.y, kv.z, kv.w};
-            int acc[GT];
-#pragma unroll
-            for (int h = 0; h < GT; ++h) acc[h] = qoff[h];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int lo = kv4_lo(w[x]), hi = kv4_hi(w[x]);
-#pragma unroll
-                for (int h = 0; h < GT; ++h) acc[h] = __dp4a(lo, qw[h][2 * x], acc[h]);
-#pragma unroll
-                for (int h = 0; h < GT; ++h) acc[h] = __dp4a(hi, qw[h][2 * x + 1], acc[h]);
-            }
-            // reduce over the key's lanes; the upper half of a lane's registers
-            // is its partner's lower half
-            int n = GT;
-#pragma unroll
-            for (int o = LPK / 2; o; o >>= 1) {
-                if (n > 1) {
-                    n >>= 1;
-#pragma unroll
-                    for (int h = 0; h < GT / 2; ++h)
-                        if (h < n) acc[h] += __shfl_xor_sync(0xffffffffu, acc[h + n], o);
-                } else {
-                    acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
-                }
-            }
-            const int j = jb + i * KPL + kl;
-            const bool in = clear || (ok && j >= j0 && j < j1);
-#pragma unroll
-            for (int x = 0; x < HPL; ++x) {
-                const int tv = acc[x] * ck;
-                if (in) tm[x] = max(tm[x], tv);
-                if (writer) tw[x * pitch + i * KPL] = tv;
-            }
-        }
+        qr.page(ring + (q & (C::NST - 1)) * C::SLOT, ts + hb * pitch + pi * KV_BLK + lane / LPK, pitch,
+                ok && jb >= j0 && jb + 64 <= j1, j0 - jb, ok ? j1 - jb : -1, tm);
         __syncwarp();
         issue(q + C::NST);
     }
@@ -866,35 +898,28 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
     for (int x = 0; x < HPL; ++x) {
 #pragma unroll
         for (int o = LPK; o < 32; o <<= 1) tm[x] = max(tm[x], __shfl_xor_sync(0xffffffffu, tm[x], o));
-        if (lane < LPK && writer) sm.red[warp][hb + x] = tm[x];
+        if (lane < LPK && (sub & (Q::LPG - 1)) == 0) sm.red[warp][hb + x] = tm[x];
     }
     __syncthreads();
     // ---- the maximum over every CTA of the unit
-    const int unit = (blockIdx.z * gridDim.y + blockIdx.y);
-    unsigned* cnt = GRID ? p.ws_cnt + unit : nullptr;
-    bool alive = true;
     if (tid < GT) {
         int m = sm.red[0][tid];
 #pragma unroll
         for (int w = 1; w < 8; ++w) m = max(m, sm.red[w][tid]);
         sm.cmax[tid] = m;
-        if (GRID) p.ws_max[((size_t)unit * S + rank) * GT + tid] = m;
     }
-    if (GRID) alive = kv4_unit_barrier(cnt, S, alive, a.status);
-    else if (S > 1) cl_sync();
+    if (S > 1) cl_sync();
     else __syncthreads();
     for (int h = warp; h < GT; h += 8) {
         int m = KV4_NEG;
         for (unsigned r = lane; r < S; r += 32)
-            m = max(m, GRID ? __ldcg(p.ws_max + ((size_t)unit * S + r) * GT + h)
-                            : (S > 1 ? cl_ld32(&sm.cmax[h], r) : sm.cmax[h]));
+            m = max(m, S > 1 ? cl_ld32(&sm.cmax[h], r) : sm.cmax[h]);
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) sm.tmax[h] = m;
     }
     __syncthreads();
 
     // ---- probabilities and P V, tiles of KV4_TP pages
-    const int gid = lane >> 2, tig = lane & 3;
     int acc[NT][2][4];                                   // low nibbles; high nibbles, times 16
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -922,28 +947,12 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
             for (int x = 0; x < NPASS; ++x) {
                 const int h = 2 * x + (tid >> 7);
                 if (h < GT) {
-                    int w[4] = {0, 0, 0, 0};
-                    if (ok) {
-                        const Kv4Row rw = sm.row[h];
-                        const int T = sm.tmax[h];
-                        const int4 tv = *(const int4*)(ts + h * pitch + pi * KV_BLK + 4 * (qd & 15));
-                        const int t4[4] = {tv.x, tv.y, tv.z, tv.w};
-                        int e[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) e[k] = kv4_E(rw, t4[k], T);
-                        if (!clear) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (jb + k < j0 || jb + k >= j1) e[k] = 0;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = kv4_W(e[k], (int)(cvw >> (8 * k)) & 255);
-                        sumE[x] += (unsigned)(e[0] + e[1] + e[2] + e[3]);
-                        sumW[x] += (unsigned)(w[0] + w[1] + w[2] + w[3]);
-                    }
-                    const unsigned wa = (unsigned)w[0] + ((unsigned)w[1] << 16), wb = (unsigned)w[2] + ((unsigned)w[3] << 16);
-                    sm.wp[buf][qd >> 4][2 * h][qd & 15] = __byte_perm(wa, wb, 0x6420);
-                    sm.wp[buf][qd >> 4][2 * h + 1][qd & 15] = __byte_perm(wa, wb, 0x7531);
+                    uint32_t wl = 0, wh = 0;
+                    if (ok)
+                        kv4_probs(sm.row[h], sm.tmax[h], *(const int4*)(ts + h * pitch + pi * KV_BLK + 4 * (qd & 15)), cvw,
+                                  clear, j0 - jb, j1 - jb, &wl, &wh, &sumE[x], &sumW[x]);
+                    sm.wp[buf][qd >> 4][2 * h][qd & 15] = wl;
+                    sm.wp[buf][qd >> 4][2 * h + 1][qd & 15] = wh;
                 }
             }
         }
@@ -954,14 +963,7 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
         for (int i = 0; i < NV; ++i) {
             const int pt = i * WPG + ph;
             if (tile * KV4_TP + pt >= np) break;         // (a page outside the pool has W = 0)
-            const int4 v = *(const int4*)(vb + i * 512);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                int4 b = make_int4(0, 0, 0, 0);
-                if (8 * n + gid < 2 * GT) b = *(const int4*)&sm.wp[buf][pt][8 * n + gid][4 * tig];
-                mma_u8u8(acc[n][0], kv4_lo(v.x), kv4_lo(v.z), kv4_lo(v.y), kv4_lo(v.w), b.x, b.z);
-                mma_u8u8(acc[n][1], v.x & 0xf0f0f0f0, v.z & 0xf0f0f0f0, v.y & 0xf0f0f0f0, v.w & 0xf0f0f0f0, b.y, b.w);
-            }
+            kv4_pv_page<GT, NT>(acc, vb + i * 512, sm.wp[buf][pt]);
         }
         __syncwarp();
         issue(nk + tile + C::NST);
@@ -978,9 +980,9 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
         if (ph == part) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int h = 4 * n + tig;
+                const int h = 4 * n + (lane & 3);
                 if (h < GT) {
-                    i64* d0 = num_s + h * D + cg * 16 + gid;
+                    i64* d0 = num_s + h * D + cg * 16 + (lane >> 2);
                     int c[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) c[e] = acc[n][0][e] + (acc[n][1][e] >> 4);
@@ -999,28 +1001,16 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
         for (int k = 0; k < 4; ++k) { e += sm.se[wbase + k][tid]; w += sm.sw[wbase + k][tid]; }
         sm.csum[0][tid] = e;
         sm.csum[1][tid] = w;
-        if (GRID) {
-            p.ws_sum[(((size_t)unit * S + rank) * GT + tid) * 2] = e;
-            p.ws_sum[(((size_t)unit * S + rank) * GT + tid) * 2 + 1] = w;
-        }
     }
-    if (GRID)
-        for (int i = tid; i < GT * D; i += KV4_DT) p.ws_num[((size_t)unit * S + rank) * (GT * D) + i] = num_s[i];
-    if (GRID) kv4_unit_barrier(cnt, 2 * S, alive, a.status);
-    else if (S > 1) cl_sync();
+    if (S > 1) cl_sync();
     else __syncthreads();
     // ---- the row sums, then this CTA's share of the outputs
     if (warp < GT) {
         for (int h = warp; h < GT; h += 8) {
             u64 e = 0, w = 0;
             for (unsigned r = lane; r < S; r += 32) {
-                if (GRID) {
-                    e += __ldcg(p.ws_sum + (((size_t)unit * S + r) * GT + h) * 2);
-                    w += __ldcg(p.ws_sum + (((size_t)unit * S + r) * GT + h) * 2 + 1);
-                } else {
-                    e += (unsigned)(S > 1 ? cl_ld32((const int*)&sm.csum[0][h], r) : (int)sm.csum[0][h]);
-                    w += (unsigned)(S > 1 ? cl_ld32((const int*)&sm.csum[1][h], r) : (int)sm.csum[1][h]);
-                }
+                e += (unsigned)(S > 1 ? cl_ld32((const int*)&sm.csum[0][h], r) : (int)sm.csum[0][h]);
+                w += (unsigned)(S > 1 ? cl_ld32((const int*)&sm.csum[1][h], r) : (int)sm.csum[1][h]);
             }
             e = redux_sum_u64(e);
             w = redux_sum_u64(w);
@@ -1040,10 +1030,287 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
         const int h = i / D;
         i64 num = sm.tot[2][h];
         for (unsigned r = 0; r < S; ++r)
-            num += GRID ? __ldcg(p.ws_num + ((size_t)unit * S + r) * (GT * D) + i) : (S > 1 ? cl_ld64(num_s + i, r) : num_s[i]);
+            num += S > 1 ? cl_ld64(num_s + i, r) : num_s[i];
         orow[i] = kv4_out(num, sm.tot[0][h], (int)sm.tot[1][h], MV, KVS);
     }
-    if (!GRID && S > 1) cl_sync();      // no CTA leaves while another reads its shared memory
+    if (S > 1) cl_sync();      // no CTA leaves while another reads its shared memory
+}
+
+// ---- the same in two launches, for contexts that keep the whole device busy.
+// k_kv4_scores: a warp takes up to 8 pages of one unit by itself and writes
+// their scores and its maxima to the workspace; nothing waits for another
+// warp. k_kv4_pv: a CTA takes a chunk of pages, settles the maximum from the
+// first launch's, forms probabilities and P V, adds its sums to the unit's by
+// 64-bit integer atomics (exact, so their order does not matter), and the
+// unit's last CTA divides. Scores cost 8 bytes of traffic per key and head,
+// mostly in L2; K and V are read once, with an evict-first policy.
+template <int D, int GT>
+__global__ void __launch_bounds__(128) k_kv4_scores(Kv4Args a, Kv4Attn p) {
+    using C = Kv4Ring<D>;
+    using Q = Kv4Q<D, GT>;
+    constexpr int LPK = Q::LPK, HPL = Q::HPL, NST = C::NST;
+    extern __shared__ __align__(16) unsigned char kv4_raw[];
+    __shared__ unsigned long long full[4][NST];
+    pdl_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.z + p.t0, c = blockIdx.x * 4 + warp;
+    int g = blockIdx.y, hg = 0;
+    while (g >= a.n_kv) { g -= a.n_kv; ++hg; }
+    const int nh = min(GT, p.G - hg * GT), h0 = g * p.G + hg * GT;
+    const int pos = p.tok_pos[t], seq = p.tok_seq[t];
+    if (pos < 0 || pos >= p.max_len || seq < 0 || seq >= a.n_seq || (pos >> 6) >= a.max_blocks) return;
+    const int j1 = pos + 1, j0 = p.window > 0 ? max(0, j1 - p.window) : 0;
+    const int b0 = j0 >> 6, nb = ((j1 + 63) >> 6) - b0;
+    const size_t unit = (size_t)blockIdx.z * gridDim.y + blockIdx.y;
+    if (c == 0) {
+        for (int i = lane; i < GT * D; i += 32) p.ws_num[unit * (GT * D) + i] = 0;
+        for (int i = lane; i < 2 * GT; i += 32) p.ws_sum[unit * (2 * GT) + i] = 0;
+        if (lane == 0) p.ws_cnt[unit] = 0;
+    }
+    const int k0 = c * p.pw, n = min(p.pw, nb - k0);     // pages b0 + k0 ..
+    if (n <= 0) return;
+    int blk_l = -1;
+    if (lane < n) {
+        blk_l = a.block_table[(size_t)seq * a.max_blocks + b0 + k0 + lane];
+        if (blk_l < 0 || blk_l >= a.n_blocks) {
+            blk_l = -1;
+            if (a.status) a.status[ST_CTX] = 1;
+        }
+    }
+    if (lane == 0)
+        for (int i = 0; i < NST; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    unsigned char* ring = kv4_raw + warp * (NST * C::SLOT);
+    const uint64_t pol = l2_evict_first();
+    auto issue = [&](int q) {
+        if (q >= n) return;
+        const int blk = __shfl_sync(0xffffffffu, blk_l, q);
+        if (lane == 0) {
+            const uint32_t bar = smem_u32(&full[warp][q & (NST - 1)]), dst = smem_u32(ring + (q & (NST - 1)) * C::SLOT);
+            if (blk < 0) {
+                mbar_arrive(bar);
+            } else {
+                const size_t u = (size_t)blk * a.n_kv + g;
+                mbar_arrive_expect_tx(bar, C::PG + KV_BLK);
+                bulk_g2s_hint(dst, a.k + u * C::PG, C::PG, bar, pol);
+                bulk_g2s(dst + C::PG, a.ks + u * KV_BLK, KV_BLK, bar);
+            }
+        }
+    };
+#pragma unroll
+    for (int q = 0; q < NST; ++q) issue(q);
+    Q qr;
+    qr.load(p.q8 + ((size_t)t * a.nq + h0) * D, nh);
+    int tm[HPL];
+#pragma unroll
+    for (int x = 0; x < HPL; ++x) tm[x] = KV4_NEG;
+    const int sub = lane & (LPK - 1), hb = sub / Q::LPG * HPL;
+    int* out = p.ws_t + (unit * GT + hb) * p.ts_pitch + (size_t)k0 * KV_BLK + lane / LPK;
+    for (int q = 0; q < n; ++q, out += KV_BLK) {
+        const bool ok = __shfl_sync(0xffffffffu, blk_l, q) >= 0;
+        const int jb = (b0 + k0 + q) << 6;
+        if (!mbar_wait(smem_u32(&full[warp][q & (NST - 1)]), (q / NST) & 1) && a.status) a.status[ST_TIMEOUT] = 1;
+        qr.page(ring + (q & (NST - 1)) * C::SLOT, out, p.ts_pitch, ok && jb >= j0 && jb + 64 <= j1, j0 - jb,
+                ok ? j1 - jb : -1, tm);
+        __syncwarp();
+        issue(q + NST);
+    }
+#pragma unroll
+    for (int x = 0; x < HPL; ++x) {
+#pragma unroll
+        for (int o = LPK; o < 32; o <<= 1) tm[x] = max(tm[x], __shfl_xor_sync(0xffffffffu, tm[x], o));
+        if (lane < LPK && (sub & (Q::LPG - 1)) == 0) p.ws_max[(unit * p.n_sw + c) * GT + hb + x] = tm[x];
+    }
+}
+
+template <int D, int GT>
+__global__ void __launch_bounds__(KV4_DT, GT == 8 ? 2 : 3) k_kv4_pv(Kv4Args a, Kv4Attn p) {
+    constexpr int PG = KV_BLK * D / 2, NST = 2;
+    constexpr int NG = D / 16, WPG = 8 / NG, NV = KV4_TP / WPG, SLOT = NV * 512;
+    constexpr int NT = (2 * GT + 7) / 8, NPASS = (GT + 1) / 2;
+    extern __shared__ __align__(16) unsigned char kv4_raw[];             // 8 warps x 2 slots
+    __shared__ uint32_t wp[2][KV4_TP][2 * GT][16];
+    __shared__ Kv4Row row[GT];
+    __shared__ int tmax[GT];
+    __shared__ unsigned se[8][GT], sw[8][GT];
+    __shared__ i64 tot[3][GT];
+    __shared__ int last;
+    __shared__ unsigned long long full[8][NST];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int t = blockIdx.z + p.t0;
+    int g = blockIdx.y, hg = 0;
+    while (g >= a.n_kv) { g -= a.n_kv; ++hg; }
+    const int nh = min(GT, p.G - hg * GT), h0 = g * p.G + hg * GT;
+    const int pos = p.tok_pos[t], seq = p.tok_seq[t];
+    int32_t* orow = p.o + (size_t)t * p.o_stride + (size_t)h0 * D;
+    const int32_t* kvp = a.params + (size_t)g * (8 + D);
+    if (pos < 0 || pos >= p.max_len || seq < 0 || seq >= a.n_seq || (pos >> 6) >= a.max_blocks) {
+        if (blockIdx.x == 0) {                                           // no key: a zero row
+            for (int i = tid; i < nh * D; i += KV4_DT) orow[i] = 0;
+            if (pos >= 0 && tid == 0 && a.status) a.status[ST_CTX] = 1;
+        }
+        pdl_wait();
+        return;
+    }
+    const int j1 = pos + 1, j0 = p.window > 0 ? max(0, j1 - p.window) : 0;
+    const int b0 = j0 >> 6, nb = ((j1 + 63) >> 6) - b0;
+    const size_t unit = (size_t)blockIdx.z * gridDim.y + blockIdx.y;
+    const int k0 = (int)blockIdx.x << p.lg_cp, np = min(1 << p.lg_cp, nb - k0), ntile = (np + KV4_TP - 1) / KV4_TP;
+    if (np <= 0) {
+        pdl_wait();                                      // this launch ends after the first, whatever its CTAs do
+        return;
+    }
+    if (tid < GT) {
+        const size_t qi = (size_t)t * a.nq + h0 + min(tid, nh - 1);
+        row[tid] = kv4_row(p.mq[qi], p.kq[qi], kvp[6], kvp[7]);
+    }
+    if (lane == 0)
+        for (int i = 0; i < NST; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    const int32_t* bt = a.block_table + (size_t)seq * a.max_blocks + b0 + k0;
+    auto page_of = [&](int i) {                          // -1: past the chunk, or outside the pool
+        const int blk = i < np ? bt[i] : -1;
+        return blk < a.n_blocks ? max(blk, -1) : -1;
+    };
+    const int cg = warp & (NG - 1), ph = warp / NG;
+    unsigned char* ring = kv4_raw + warp * (NST * SLOT);
+    const uint64_t pol = l2_evict_first();
+    auto issue = [&](int q) {                            // this warp's slices of tile q
+        if (q >= ntile) return;
+        const uint32_t bar = smem_u32(&full[warp][q & (NST - 1)]), dst = smem_u32(ring + (q & (NST - 1)) * SLOT);
+        const int blk = lane < NV ? page_of(q * KV4_TP + lane * WPG + ph) : -1;
+        const unsigned m = __ballot_sync(0xffffffffu, blk >= 0);
+        if (lane == 0) {
+            if (m) mbar_arrive_expect_tx(bar, 512 * __popc(m));
+            else mbar_arrive(bar);
+        }
+        __syncwarp();
+        if (blk >= 0) bulk_g2s_hint(dst + lane * 512, a.v + ((size_t)blk * a.n_kv + g) * PG + cg * 512, 512, bar, pol);
+    };
+    issue(0);
+    issue(1);
+    const int qd = tid & 127, hh = tid >> 7;             // this thread's four keys of a tile, its heads 2 x + hh
+    uint32_t cv_next = 0;
+    int blk_next = -1;
+    auto load_cv = [&](int tile) {
+        blk_next = page_of(tile * KV4_TP + (qd >> 4));
+        cv_next = blk_next >= 0 ? __ldg((const uint32_t*)(a.vs + ((size_t)blk_next * a.n_kv + g) * KV_BLK) + (qd & 15)) : 0u;
+    };
+    load_cv(0);
+    pdl_wait();                                          // the scores are complete
+    for (int h = warp; h < GT; h += 8) {
+        int m = KV4_NEG;
+        const int nw = (int)(((u64)(nb + p.pw - 1) * p.pwmul) >> 32);    // ceil(nb / pw) warps wrote maxima
+        for (int r = lane; r < nw; r += 32) m = max(m, __ldcg(p.ws_max + (unit * p.n_sw + r) * GT + h));
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) tmax[h] = m;
+    }
+    const int* tsrc = p.ws_t + unit * GT * p.ts_pitch + (size_t)k0 * KV_BLK + 4 * qd;
+    int4 t_next[NPASS];
+    auto load_t = [&](int tile) {
+#pragma unroll
+        for (int x = 0; x < NPASS; ++x)
+            if (2 * x + hh < GT && blk_next >= 0) t_next[x] = __ldcg((const int4*)(tsrc + (size_t)(2 * x + hh) * p.ts_pitch + tile * (KV4_TP * KV_BLK)));
+    };
+#pragma unroll
+    for (int x = 0; x < NPASS; ++x) t_next[x] = make_int4(0, 0, 0, 0);
+    load_t(0);
+    int acc[NT][2][4];                                   // low nibbles; high nibbles, times 16
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][0][e] = acc[n][1][e] = 0;
+    unsigned sumE[NPASS], sumW[NPASS];
+#pragma unroll
+    for (int x = 0; x < NPASS; ++x) sumE[x] = sumW[x] = 0;
+    __syncthreads();
+    for (int tile = 0; tile < ntile; ++tile) {
+        const int buf = tile & 1;
+        const bool ok = blk_next >= 0;
+        const int jb = ((b0 + k0 + tile * KV4_TP) << 6) + 4 * qd;
+        const bool clear = jb >= j0 && jb + 4 <= j1;
+        uint32_t wl[NPASS], wh[NPASS];
+#pragma unroll
+        for (int x = 0; x < NPASS; ++x) {
+            const int h = 2 * x + hh;
+            wl[x] = wh[x] = 0;
+            if (h < GT && ok)
+                kv4_probs(row[h], tmax[h], t_next[x], cv_next, clear, j0 - jb, j1 - jb, &wl[x], &wh[x], &sumE[x], &sumW[x]);
+        }
+        load_cv(tile + 1);
+        load_t(tile + 1);
+#pragma unroll
+        for (int x = 0; x < NPASS; ++x) {
+            const int h = 2 * x + hh;
+            if (h < GT) {
+                wp[buf][qd >> 4][2 * h][qd & 15] = wl[x];
+                wp[buf][qd >> 4][2 * h + 1][qd & 15] = wh[x];
+            }
+        }
+        __syncthreads();
+        if (!mbar_wait(smem_u32(&full[warp][tile & (NST - 1)]), (tile / NST) & 1) && a.status) a.status[ST_TIMEOUT] = 1;
+        const unsigned char* vb = ring + (tile & (NST - 1)) * SLOT + lane * 16;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (tile * KV4_TP + i * WPG + ph >= np) break;               // (a page outside the pool has W = 0)
+            kv4_pv_page<GT, NT>(acc, vb + i * 512, wp[buf][i * WPG + ph]);
+        }
+        __syncwarp();
+        issue(tile + NST);
+    }
+    // ---- add this chunk's sums; the unit's last chunk divides
+#pragma unroll
+    for (int x = 0; x < NPASS; ++x) {
+        const int h = 2 * x + hh;
+        const unsigned e = __reduce_add_sync(0xffffffffu, sumE[x]), w = __reduce_add_sync(0xffffffffu, sumW[x]);
+        if (lane == 0 && h < GT) { se[warp][h] = e; sw[warp][h] = w; }
+    }
+    unsigned long long* un = (unsigned long long*)p.ws_num + unit * (GT * D);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int h = 4 * n + (lane & 3);
+        if (h < GT) {
+            int c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] = acc[n][0][e] + (acc[n][1][e] >> 4);
+            unsigned long long* d = un + h * D + cg * 16 + (lane >> 2);
+            atomicAdd(d, (unsigned long long)((i64)c[0] + (i64)c[1] * 256));
+            atomicAdd(d + 8, (unsigned long long)((i64)c[2] + (i64)c[3] * 256));
+        }
+    }
+    __syncthreads();
+    unsigned long long* us = p.ws_sum + unit * (2 * GT);
+    if (tid < GT) {
+        unsigned e = 0, w = 0;
+        const int wbase = (tid & 1) * 4;                                 // head h = 2 x + (warp >= 4)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) { e += se[wbase + k][tid]; w += sw[wbase + k][tid]; }
+        atomicAdd(us + 2 * tid, (unsigned long long)e);
+        atomicAdd(us + 2 * tid + 1, (unsigned long long)w);
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        const unsigned chunks = (unsigned)((nb + (1 << p.lg_cp) - 1) >> p.lg_cp);
+        last = atomicAdd(p.ws_cnt + unit, 1u) == chunks - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    if (tid < GT) {
+        const u64 e = __ldcg(us + 2 * tid), w = __ldcg(us + 2 * tid + 1);
+        const int bl = bitlen_u64(e);
+        tot[0][tid] = e ? (i64)pow2_recip(e, bl, 1, 23) : 0;
+        tot[1][tid] = bl;
+        tot[2][tid] = -8 * (i64)w;
+    }
+    __syncthreads();
+    for (int i = tid; i < nh * D; i += KV4_DT) {
+        const int h = i / D;
+        orow[i] = kv4_out((i64)__ldcg(un + i) + tot[2][h], tot[0][h], (int)tot[1][h], kvp[4], kvp[5]);
+    }
 }
 
 // -------------------------------------------- attention of token blocks

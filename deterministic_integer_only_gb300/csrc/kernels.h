@@ -261,14 +261,22 @@ struct Kv4Attn {
     int cap;                      // decode: keys a CTA's shared memory holds
     unsigned long long smul;      // decode: ceil(2^32 / CTAs of a unit)
     int lgGp;                     // prefill: log2 of the power of two >= G
-    int32_t* ws_max;              // decode in a cooperative launch: exchange memory
-    unsigned *ws_sum, *ws_cnt;
+    // decode in two launches: pages per warp of the first (and ceil(2^32 / pw)),
+    // its warps per unit, log2 pages per CTA of the second; the workspace:
+    // scores [unit][heads][ts_pitch], maxima [unit][n_sw][heads], sums
+    int pw, n_sw, lg_cp;
+    unsigned long long pwmul;
+    size_t ts_pitch;
+    int32_t *ws_t, *ws_max;
+    unsigned* ws_cnt;
+    unsigned long long* ws_sum;
     long long* ws_num;
 };
 cudaError_t launch_kv4_append(const Kv4Args& a, const Kv4Append& p, int d, cudaStream_t s);
 cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p, int d, cudaStream_t s);
 // bytes of workspace the decode attention of T tokens needs (0: none)
 size_t kv4_decode_ws(const Kv4Args& a, int d, int T, int max_len);
+bool kv4_decode_needs_ws(const Kv4Args& a, int d, int T, int max_len, int window);
 cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p, int d, void* ws, cudaStream_t s);
 cudaError_t kv4_init();           // once per device, outside any stream capture
 

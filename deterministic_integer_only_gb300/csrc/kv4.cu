@@ -15,7 +15,10 @@ namespace detint {
 namespace {
 
 constexpr int KV4_MAX_LEN = 1 << 19;       // keys: the limb sums stay in int32
-constexpr size_t KV4_SMEM_CTA = 200 * 1024;  // dynamic shared memory of one decode CTA at most
+#ifndef TWO
+#define TWO 4096
+#endif
+constexpr long long KV4_TWO = TWO;         // pages of all units from which a decode call takes two launches
 
 struct DevInfo {
     bool ready = false;
@@ -32,19 +35,16 @@ DevInfo* dev_info() {
 }
 
 using DecFn = void (*)(Kv4Args, Kv4Attn);
-template <bool GRID>
-DecFn dec_kernel(int d, int gt) {
-    if (d == 128) {
-        if (gt == 1) return k_kv4_decode<128, 1, GRID>;
-        if (gt == 2) return k_kv4_decode<128, 2, GRID>;
-        if (gt == 4) return k_kv4_decode<128, 4, GRID>;
-        return k_kv4_decode<128, 8, GRID>;
-    }
-    if (gt == 1) return k_kv4_decode<64, 1, GRID>;
-    if (gt == 2) return k_kv4_decode<64, 2, GRID>;
-    if (gt == 4) return k_kv4_decode<64, 4, GRID>;
-    return k_kv4_decode<64, 8, GRID>;
-}
+int lg2(int n) { return n >= 8 ? 3 : n >= 4 ? 2 : n >= 2 ? 1 : 0; }
+// [head_dim 128][log2 heads per CTA]: one launch; scores; probabilities and P V
+const DecFn DEC_FUSED[2][4] = {{k_kv4_decode<64, 1>, k_kv4_decode<64, 2>, k_kv4_decode<64, 4>, k_kv4_decode<64, 8>},
+                               {k_kv4_decode<128, 1>, k_kv4_decode<128, 2>, k_kv4_decode<128, 4>, k_kv4_decode<128, 8>}};
+const DecFn DEC_SCORES[2][4] = {{k_kv4_scores<64, 1>, k_kv4_scores<64, 2>, k_kv4_scores<64, 4>, k_kv4_scores<64, 8>},
+                                {k_kv4_scores<128, 1>, k_kv4_scores<128, 2>, k_kv4_scores<128, 4>, k_kv4_scores<128, 8>}};
+const DecFn DEC_PV[2][4] = {{k_kv4_pv<64, 1>, k_kv4_pv<64, 2>, k_kv4_pv<64, 4>, k_kv4_pv<64, 8>},
+                            {k_kv4_pv<128, 1>, k_kv4_pv<128, 2>, k_kv4_pv<128, 4>, k_kv4_pv<128, 8>}};
+int scores_smem(int d) { return (d == 128 ? Kv4Ring<128>::BYTES : Kv4Ring<64>::BYTES) / 2; }   // 4 of 8 warps
+int pv_smem(int d) { return 8 * 2 * (d == 128 ? 8 : 4) * 512; }
 
 using AppFn = void (*)(Kv4Args, Kv4Append);
 AppFn append_kernel(int d, bool norm, bool chunk) {
@@ -68,9 +68,11 @@ size_t dec_smem2(int gt) {
 
 // how a decode call is split
 struct DecPlan {
-    int gt, hg, S, cap;
-    bool grid;
+    int gt, hg;
+    bool two;                // two launches
+    int S, cap;              // one launch: CTAs per unit, keys per CTA
     size_t smem;
+    int pw, n_sw, lg_cp, pitch;
 };
 
 DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len, int window) {
@@ -78,44 +80,39 @@ DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len,
     const int G = a.nq / a.n_kv;
     int mp = (max_len + 63) >> 6;                                   // pages a token can have
     if (window > 0) mp = std::min(mp, ((window + 62) >> 6) + 1);
-    // q heads per CTA: all of a kv head's up to 8; fewer where the scores
-    // of so many keys would not fit even split over every CTA of the device
-    for (p.gt = G >= 5 ? 8 : (G >= 3 ? 4 : G);; p.gt >>= 1) {
-        p.hg = (G + p.gt - 1) / p.gt;
-        const long long units = (long long)T * a.n_kv * p.hg;
-        // a cluster: as many CTAs as keep two on every SM busy, at least 2 pages each
-        int S = 1;
-        while (S < di.max_cluster && units * S < 2 * di.sms && mp >= 4 * S) S <<= 1;
-        while (S < di.max_cluster && dec_smem(d, p.gt, ((mp + S - 1) / S) << 6) > dec_smem2(p.gt)) S <<= 1;
-        p.S = S;
-        p.cap = ((mp + S - 1) / S) << 6;
-        p.smem = dec_smem(d, p.gt, p.cap);
-        p.grid = false;
-        // a cooperative launch where the clusters would leave SMs idle on a long context
-        if (units * S < di.sms && mp >= 8 * S) {
-            const int Sg = (int)std::min<long long>((2 * di.sms) / units, mp / 4);
-            const int cap = ((mp + Sg - 1) / Sg) << 6;
-            if (Sg > S && dec_smem(d, p.gt, cap) <= dec_smem2(p.gt)) {
-                p.S = Sg;
-                p.cap = cap;
-                p.smem = dec_smem(d, p.gt, cap);
-                p.grid = true;
-            }
-        }
-        if (p.smem <= KV4_SMEM_CTA || p.gt == 1) return p;
+    p.gt = G >= 5 ? 8 : (G >= 3 ? 4 : G);
+    p.hg = (G + p.gt - 1) / p.gt;
+    const long long units = (long long)T * a.n_kv * p.hg;
+    // one launch: as many CTAs as keep two on every SM busy, at least 2 pages each
+    int S = 1;
+    while (S < di.max_cluster && units * S < 2 * di.sms && mp >= 4 * S) S <<= 1;
+    while (S < di.max_cluster && dec_smem(d, p.gt, ((mp + S - 1) / S) << 6) > dec_smem2(p.gt)) S <<= 1;
+    p.S = S;
+    p.cap = ((mp + S - 1) / S) << 6;
+    p.smem = dec_smem(d, p.gt, p.cap);
+    p.two = p.smem > dec_smem2(p.gt) || units * mp >= KV4_TWO;
+    if (p.two) {
+        p.pw = 8;
+        while (p.pw > 1 && units * ((mp + p.pw - 1) / p.pw) < 16LL * di.sms) p.pw >>= 1;
+        p.n_sw = (mp + p.pw - 1) / p.pw;
+        p.lg_cp = 5;
+        while (p.lg_cp > 3 && units * ((mp + (1 << p.lg_cp) - 1) >> p.lg_cp) < 6LL * di.sms) --p.lg_cp;
+        p.pitch = ((mp + 7) & ~7) << 6;                             // whole tiles
     }
+    return p;
 }
 
 size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
-struct WsLayout { size_t cnt, mx, sum, num, total; };
+struct WsLayout { size_t t, mx, sum, num, cnt, total; };
 WsLayout ws_layout(const DecPlan& p, long long units, int d) {
     WsLayout w{};
     size_t o = 0;
-    const size_t n = (size_t)units * p.S * p.gt;
-    w.cnt = o; o += a256((size_t)units * 4);
-    w.mx = o; o += a256(n * 4);
-    w.sum = o; o += a256(n * 8);
+    const size_t n = (size_t)units * p.gt;
+    w.t = o; o += a256(n * p.pitch * 4);
+    w.mx = o; o += a256(n * p.n_sw * 4);
+    w.sum = o; o += a256(n * 16);
     w.num = o; o += a256(n * d * 8);
+    w.cnt = o; o += a256((size_t)units * 4);
     w.total = o;
     return w;
 }
@@ -132,13 +129,13 @@ cudaError_t kv4_init() {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&di->sms, cudaDevAttrMultiProcessorCount, dev);
     int mc = 16;
     for (int d : {64, 128})
-        for (int gt : {1, 2, 4, 8}) {
-            for (DecFn f : {dec_kernel<false>(d, gt), dec_kernel<true>(d, gt)}) {
-                if (e == cudaSuccess)
-                    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)KV4_SMEM_CTA);
-            }
-            DecFn f = dec_kernel<false>(d, gt);
+        for (int l = 0; l < 4; ++l) {
+            const DecFn f = DEC_FUSED[d == 128][l];
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dec_smem2(1 << l));
             if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(DEC_SCORES[d == 128][l], cudaFuncAttributeMaxDynamicSharedMemorySize, scores_smem(d));
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(DEC_PV[d == 128][l], cudaFuncAttributeMaxDynamicSharedMemorySize, pv_smem(d));
             if (e != cudaSuccess) continue;
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute at[1];
@@ -147,7 +144,7 @@ cudaError_t kv4_init() {
             at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
             cfg.gridDim = dim3(16);
             cfg.blockDim = dim3(KV4_DT);
-            cfg.dynamicSmemBytes = KV4_SMEM_CTA;
+            cfg.dynamicSmemBytes = dec_smem2(1 << l);
             cfg.attrs = at;
             cfg.numAttrs = 1;
             int n = 0;
@@ -208,54 +205,75 @@ cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p0, int d, cudaS
     return cudaSuccess;
 }
 
-// Enough for every window: a cooperative launch has at most two CTAs on an SM
-// and needs clusters that leave SMs idle; each CTA exchanges at most 8 heads.
+// Enough for every window: fewer keys take less of each array, but may need
+// more warps and CTAs per page, which only the maxima depend on.
 size_t kv4_decode_ws(const Kv4Args& a, int d, int T, int max_len) {
     DevInfo* di = dev_info();
     if (!di || !di->ready) return 0;
-    const int G = a.nq / a.n_kv, mp = (max_len + 63) >> 6;
-    const long long units = (long long)T * a.n_kv * ((G + 7) / 8);
-    if (units * di->max_cluster >= di->sms || mp < 8 * di->max_cluster) return 0;
-    return a256((size_t)2 * di->sms * 4) + (size_t)2 * di->sms * 8 * (4 + 8 + 8 * d) + 3 * 256;
+    const int Tc = std::min(T, 65535);
+    DecPlan pl = dec_plan(*di, a, d, Tc, max_len, 0);
+    if (!pl.two) return 0;
+    pl.n_sw = (max_len + 63) >> 6;
+    return ws_layout(pl, (long long)Tc * a.n_kv * pl.hg, d).total;
+}
+bool kv4_decode_needs_ws(const Kv4Args& a, int d, int T, int max_len, int window) {
+    DevInfo* di = dev_info();
+    return di && di->ready && dec_plan(*di, a, d, std::min(T, 65535), max_len, window).two;
 }
 
 cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p0, int d, void* ws, cudaStream_t s) {
     DevInfo* di = dev_info();
     if (!di || !di->ready) return cudaErrorInvalidDevice;
     Kv4Attn p = p0;
-    const DecPlan pl = dec_plan(*di, a, d, p.T, p.max_len, p.window);
-    p.cap = pl.cap;
-    p.smul = ((1ull << 32) + pl.S - 1) / pl.S;
+    const DecPlan pl = dec_plan(*di, a, d, std::min(p.T, 65535), p.max_len, p.window);
+    const int d128 = d == 128, l = lg2(pl.gt);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
-    cfg.blockDim = dim3(KV4_DT);
-    cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = s;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (pl.grid) {
-        const WsLayout w = ws_layout(pl, (long long)p.T * a.n_kv * pl.hg, d);
-        unsigned char* b = (unsigned char*)ws;
-        p.ws_cnt = (unsigned*)(b + w.cnt);
-        p.ws_max = (int32_t*)(b + w.mx);
-        p.ws_sum = (unsigned*)(b + w.sum);
-        p.ws_num = (long long*)(b + w.num);
-        cudaError_t e = cudaMemsetAsync(p.ws_cnt, 0, w.mx - w.cnt, s);
-        if (e != cudaSuccess) return e;
-        p.t0 = 0;
-        cfg.gridDim = dim3(pl.S, a.n_kv * pl.hg, p.T);
-        at[0].id = cudaLaunchAttributeCooperative;
-        at[0].val.cooperative = 1;
-        return cudaLaunchKernelEx(&cfg, dec_kernel<true>(d, pl.gt), a, p);
-    }
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = pl.S;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.numAttrs = pl.S > 1 ? 1 : 0;
     for (int t0 = 0; t0 < p.T; t0 += 65535) {
+        const int nt = std::min(65535, p.T - t0);
         p.t0 = t0;
-        cfg.gridDim = dim3(pl.S, a.n_kv * pl.hg, std::min(65535, p.T - t0));
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, dec_kernel<false>(d, pl.gt), a, p);
+        cudaError_t e;
+        if (!pl.two) {
+            p.cap = pl.cap;
+            p.smul = ((1ull << 32) + pl.S - 1) / pl.S;
+            cfg.gridDim = dim3(pl.S, a.n_kv * pl.hg, nt);
+            cfg.blockDim = dim3(KV4_DT);
+            cfg.dynamicSmemBytes = pl.smem;
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = pl.S;
+            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+            cfg.numAttrs = pl.S > 1 ? 1 : 0;
+            e = cudaLaunchKernelEx(&cfg, DEC_FUSED[d128][l], a, p);
+        } else {
+            const WsLayout w = ws_layout(pl, (long long)nt * a.n_kv * pl.hg, d);
+            unsigned char* b = (unsigned char*)ws;
+            p.ws_t = (int32_t*)(b + w.t);
+            p.ws_max = (int32_t*)(b + w.mx);
+            p.ws_sum = (unsigned long long*)(b + w.sum);
+            p.ws_num = (long long*)(b + w.num);
+            p.ws_cnt = (unsigned*)(b + w.cnt);
+            p.pw = pl.pw;
+            p.pwmul = ((1ull << 32) + pl.pw - 1) / pl.pw;
+            p.n_sw = pl.n_sw;
+            p.lg_cp = pl.lg_cp;
+            p.ts_pitch = pl.pitch;
+            cfg.gridDim = dim3((pl.n_sw + 3) / 4, a.n_kv * pl.hg, nt);
+            cfg.blockDim = dim3(128);
+            cfg.dynamicSmemBytes = scores_smem(d);
+            cfg.numAttrs = 0;
+            e = cudaLaunchKernelEx(&cfg, DEC_SCORES[d128][l], a, p);
+            if (e != cudaSuccess) return e;
+            // starts while the first launch drains: its V slices travel before it waits
+            cfg.gridDim = dim3((pl.pitch / 64 + (1 << pl.lg_cp) - 1) >> pl.lg_cp, a.n_kv * pl.hg, nt);
+            cfg.blockDim = dim3(KV4_DT);
+            cfg.dynamicSmemBytes = pv_smem(d);
+            at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, DEC_PV[d128][l], a, p);
+        }
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -364,9 +382,11 @@ int detint_kv4_decode(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq
     Kv4Attn p{};
     const int rc = check_attn(where, c, q8, mq, kq, tok_seq, tok_pos, n_tok, max_len, window, o, o_stride, &a, &p);
     if (rc) return rc;
-    const size_t need = kv4_decode_ws(a, c->head_dim, n_tok, max_len);
-    if (need && (!workspace || workspace_bytes < (long long)need || mis(workspace, 16)))
-        return set_last_error(DETINT_E_ARG, "detint_kv4_decode: a 16-byte aligned workspace of detint_kv4_workspace bytes is needed");
+    if (kv4_decode_needs_ws(a, c->head_dim, n_tok, max_len, window)) {
+        const size_t need = kv4_decode_ws(a, c->head_dim, n_tok, max_len);
+        if (!need || !workspace || workspace_bytes < (long long)need || mis(workspace, 16))
+            return failed(DETINT_E_ARG, where, "a 16-byte aligned workspace of detint_kv4_workspace bytes is needed");
+    }
     const cudaError_t e = launch_kv4_decode(a, p, c->head_dim, workspace, (cudaStream_t)sp);
     return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
 }
