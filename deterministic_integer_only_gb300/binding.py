@@ -23,7 +23,7 @@ ERRORS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "token id o
           9: "bad sequence id", 10: "saturation recorded"}
 
 # every entry point of include/detint.h
-SYMBOLS = ["detint_load", "detint_prefill", "detint_decode_step", "detint_gemm_i8",
+SYMBOLS = ["detint_load", "detint_load_kv", "detint_prefill", "detint_decode_step", "detint_gemm_i8",
            "detint_reset_seq", "detint_seq_len", "detint_status", "detint_set_graph",
            "detint_set_option", "detint_argmax_noalloc", "detint_sample", "detint_fork_seq", "detint_gemm_w16", "detint_split_w16",
            "detint_int8_peak_loop", "detint_kv4_append", "detint_kv4_workspace", "detint_kv4_decode",
@@ -47,6 +47,7 @@ def lib():
         L = C.CDLL(LIB_PATH)
         vp, i32p = C.c_void_p, C.POINTER(C.c_int32)
         L.detint_load.argtypes = [C.c_char_p, C.c_int, C.c_int, vp, C.POINTER(vp)]
+        L.detint_load_kv.argtypes = [C.c_char_p, C.c_int, C.c_int, C.c_int, vp, C.POINTER(vp)]
         L.detint_prefill.argtypes = [vp, C.c_int, i32p, i32p, vp, vp, vp, vp]
         L.detint_decode_step.argtypes = [vp, C.c_int, i32p, vp, vp, vp, vp]
         L.detint_gemm_i8.argtypes = [vp, vp, vp, C.c_int, C.c_int, C.c_int, vp]
@@ -399,16 +400,18 @@ def chain_hash(rows, prev: bytes | None = None) -> bytes:
 
 
 class Model:
-    """A loaded integer model on the current CUDA device (detint_load)."""
+    """A loaded integer model on the current CUDA device (detint_load; kv_bits 4:
+    detint_load_kv with the 4-bit K/V cache)."""
 
-    def __init__(self, path: str, max_batch: int, max_ctx: int, stream=None):
+    def __init__(self, path: str, max_batch: int, max_ctx: int, stream=None, kv_bits: int = 8):
         import torch
         self.torch = torch
         self.stream = stream if stream is not None else torch.cuda.Stream()
         h = C.c_void_p()
-        _check(lib().detint_load(path.encode(), int(max_batch), int(max_ctx),
-                                 self.stream.cuda_stream, C.byref(h)), "detint_load")
+        _check(lib().detint_load_kv(path.encode(), int(max_batch), int(max_ctx), int(kv_bits),
+                                    self.stream.cuda_stream, C.byref(h)), "detint_load")
         self._h = h
+        self.kv_bits = int(kv_bits)
         info = np.zeros(16, np.int32)
         _check(lib().detint_model_info(self._h, info.ctypes.data_as(C.POINTER(C.c_int32))),
                "detint_model_info")

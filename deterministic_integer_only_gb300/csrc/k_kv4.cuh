@@ -1038,12 +1038,17 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
 
 // ---- the same in two launches, for contexts that keep the whole device busy.
 // k_kv4_scores: a warp takes up to 8 pages of one unit by itself and writes
-// their scores and its maxima to the workspace; nothing waits for another
-// warp. k_kv4_pv: a CTA takes a chunk of pages, settles the maximum from the
-// first launch's, forms probabilities and P V, adds its sums to the unit's by
-// 64-bit integer atomics (exact, so their order does not matter), and the
-// unit's last CTA divides. Scores cost 8 bytes of traffic per key and head,
-// mostly in L2; K and V are read once, with an evict-first policy.
+// their scores and its maxima to the workspace. k_kv4_pv: a warp takes pages
+// again by itself, forms their probabilities in the registers of its own P V
+// operand and runs P V over all channels; the CTA adds its warps' sums in
+// shared memory, then to the unit's by 64-bit integer atomics (exact, so their
+// order does not matter), and the unit's last CTA divides. Nothing waits for
+// another warp in either stream. (With a barrier per tile of 8 pages and a
+// warp per 16 channels the second launch took 115 us instead of the listed
+// 64 x 4k-16k contexts' 67 us of tensor time; handing half of the channels to
+// the dp4a pipe made the barriers longer, 135 us.) Scores cost 8 bytes of
+// traffic per key and head, mostly in L2; K and V are read once, with an
+// evict-first policy.
 template <int D, int GT>
 __global__ void __launch_bounds__(128) k_kv4_scores(Kv4Args a, Kv4Attn p) {
     using C = Kv4Ring<D>;
@@ -1125,18 +1130,17 @@ __global__ void __launch_bounds__(128) k_kv4_scores(Kv4Args a, Kv4Attn p) {
 }
 
 template <int D, int GT>
-__global__ void __launch_bounds__(KV4_DT, GT == 8 ? 2 : 3) k_kv4_pv(Kv4Args a, Kv4Attn p) {
-    constexpr int PG = KV_BLK * D / 2, NST = 2;
-    constexpr int NG = D / 16, WPG = 8 / NG, NV = KV4_TP / WPG, SLOT = NV * 512;
-    constexpr int NT = (2 * GT + 7) / 8, NPASS = (GT + 1) / 2;
-    extern __shared__ __align__(16) unsigned char kv4_raw[];             // 8 warps x 2 slots
-    __shared__ uint32_t wp[2][KV4_TP][2 * GT][16];
-    __shared__ Kv4Row row[GT];
+__global__ void __launch_bounds__(128, GT == 8 ? 2 : 4) k_kv4_pv(Kv4Args a, Kv4Attn p) {
+    using C = Kv4Ring<D>;
+    constexpr int NST = C::NST, NG = D / 16, NT = (2 * GT + 7) / 8;
+    extern __shared__ __align__(16) unsigned char kv4_raw[];
+    __shared__ int num[2][GT][D];                        // low and high limb sums of the CTA
     __shared__ int tmax[GT];
-    __shared__ unsigned se[8][GT], sw[8][GT];
+    __shared__ unsigned sums[2][GT];
+    __shared__ Kv4Row row[GT];
     __shared__ i64 tot[3][GT];
     __shared__ int last;
-    __shared__ unsigned long long full[8][NST];
+    __shared__ unsigned long long full[4][NST];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int t = blockIdx.z + p.t0;
     int g = blockIdx.y, hg = 0;
@@ -1146,150 +1150,167 @@ __global__ void __launch_bounds__(KV4_DT, GT == 8 ? 2 : 3) k_kv4_pv(Kv4Args a, K
     int32_t* orow = p.o + (size_t)t * p.o_stride + (size_t)h0 * D;
     const int32_t* kvp = a.params + (size_t)g * (8 + D);
     if (pos < 0 || pos >= p.max_len || seq < 0 || seq >= a.n_seq || (pos >> 6) >= a.max_blocks) {
-        if (blockIdx.x == 0) {                                           // no key: a zero row
-            for (int i = tid; i < nh * D; i += KV4_DT) orow[i] = 0;
+        if (blockIdx.x == 0) {                           // no key: a zero row
+            for (int i = tid; i < nh * D; i += 128) orow[i] = 0;
             if (pos >= 0 && tid == 0 && a.status) a.status[ST_CTX] = 1;
         }
-        pdl_wait();
+        pdl_wait();                                      // this launch ends after the first, whatever its CTAs do
         return;
     }
     const int j1 = pos + 1, j0 = p.window > 0 ? max(0, j1 - p.window) : 0;
     const int b0 = j0 >> 6, nb = ((j1 + 63) >> 6) - b0;
     const size_t unit = (size_t)blockIdx.z * gridDim.y + blockIdx.y;
-    const int k0 = (int)blockIdx.x << p.lg_cp, np = min(1 << p.lg_cp, nb - k0), ntile = (np + KV4_TP - 1) / KV4_TP;
+    // the CTA's pages k0 .. k0 + 2^lg_cp - 1, this warp's every fourth
+    const int k0 = (int)blockIdx.x << p.lg_cp, np = min(1 << p.lg_cp, nb - k0);
     if (np <= 0) {
-        pdl_wait();                                      // this launch ends after the first, whatever its CTAs do
+        pdl_wait();
         return;
     }
-    if (tid < GT) {
-        const size_t qi = (size_t)t * a.nq + h0 + min(tid, nh - 1);
-        row[tid] = kv4_row(p.mq[qi], p.kq[qi], kvp[6], kvp[7]);
+    const int n = (np - warp + 3) >> 2;
+    int blk_l = -1;
+    if (lane < n) {
+        const int blk = a.block_table[(size_t)seq * a.max_blocks + b0 + k0 + warp + 4 * lane];
+        blk_l = blk < a.n_blocks ? max(blk, -1) : -1;    // (recorded by the first launch)
     }
     if (lane == 0)
         for (int i = 0; i < NST; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
-    const int32_t* bt = a.block_table + (size_t)seq * a.max_blocks + b0 + k0;
-    auto page_of = [&](int i) {                          // -1: past the chunk, or outside the pool
-        const int blk = i < np ? bt[i] : -1;
-        return blk < a.n_blocks ? max(blk, -1) : -1;
-    };
-    const int cg = warp & (NG - 1), ph = warp / NG;
-    unsigned char* ring = kv4_raw + warp * (NST * SLOT);
+    unsigned char* ring = kv4_raw + warp * (NST * C::SLOT);
     const uint64_t pol = l2_evict_first();
-    auto issue = [&](int q) {                            // this warp's slices of tile q
-        if (q >= ntile) return;
-        const uint32_t bar = smem_u32(&full[warp][q & (NST - 1)]), dst = smem_u32(ring + (q & (NST - 1)) * SLOT);
-        const int blk = lane < NV ? page_of(q * KV4_TP + lane * WPG + ph) : -1;
-        const unsigned m = __ballot_sync(0xffffffffu, blk >= 0);
+    auto issue = [&](int q) {
+        if (q >= n) return;
+        const int blk = __shfl_sync(0xffffffffu, blk_l, q);
         if (lane == 0) {
-            if (m) mbar_arrive_expect_tx(bar, 512 * __popc(m));
-            else mbar_arrive(bar);
+            const uint32_t bar = smem_u32(&full[warp][q & (NST - 1)]), dst = smem_u32(ring + (q & (NST - 1)) * C::SLOT);
+            if (blk < 0) {
+                mbar_arrive(bar);
+            } else {
+                const size_t u = (size_t)blk * a.n_kv + g;
+                mbar_arrive_expect_tx(bar, C::PG + KV_BLK);
+                bulk_g2s_hint(dst, a.v + u * C::PG, C::PG, bar, pol);
+                bulk_g2s(dst + C::PG, a.vs + u * KV_BLK, KV_BLK, bar);
+            }
         }
-        __syncwarp();
-        if (blk >= 0) bulk_g2s_hint(dst + lane * 512, a.v + ((size_t)blk * a.n_kv + g) * PG + cg * 512, 512, bar, pol);
     };
-    issue(0);
-    issue(1);
-    const int qd = tid & 127, hh = tid >> 7;             // this thread's four keys of a tile, its heads 2 x + hh
-    uint32_t cv_next = 0;
-    int blk_next = -1;
-    auto load_cv = [&](int tile) {
-        blk_next = page_of(tile * KV4_TP + (qd >> 4));
-        cv_next = blk_next >= 0 ? __ldg((const uint32_t*)(a.vs + ((size_t)blk_next * a.n_kv + g) * KV_BLK) + (qd & 15)) : 0u;
-    };
-    load_cv(0);
+#pragma unroll
+    for (int q = 0; q < NST; ++q) issue(q);
+    for (int i = tid; i < 2 * GT * D; i += 128) (&num[0][0][0])[i] = 0;
+    if (tid < GT) {
+        const size_t qi = (size_t)t * a.nq + h0 + min(tid, nh - 1);
+        row[tid] = kv4_row(p.mq[qi], p.kq[qi], kvp[6], kvp[7]);
+        sums[0][tid] = sums[1][tid] = 0;
+    }
     pdl_wait();                                          // the scores are complete
-    for (int h = warp; h < GT; h += 8) {
+    const int nw = (int)(((u64)(nb + p.pw - 1) * p.pwmul) >> 32);        // ceil(nb / pw) warps wrote maxima
+    for (int h = warp; h < GT; h += 4) {
         int m = KV4_NEG;
-        const int nw = (int)(((u64)(nb + p.pw - 1) * p.pwmul) >> 32);    // ceil(nb / pw) warps wrote maxima
         for (int r = lane; r < nw; r += 32) m = max(m, __ldcg(p.ws_max + (unit * p.n_sw + r) * GT + h));
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) tmax[h] = m;
     }
-    const int* tsrc = p.ws_t + unit * GT * p.ts_pitch + (size_t)k0 * KV_BLK + 4 * qd;
-    int4 t_next[NPASS];
-    auto load_t = [&](int tile) {
-#pragma unroll
-        for (int x = 0; x < NPASS; ++x)
-            if (2 * x + hh < GT && blk_next >= 0) t_next[x] = __ldcg((const int4*)(tsrc + (size_t)(2 * x + hh) * p.ts_pitch + tile * (KV4_TP * KV_BLK)));
-    };
-#pragma unroll
-    for (int x = 0; x < NPASS; ++x) t_next[x] = make_int4(0, 0, 0, 0);
-    load_t(0);
-    int acc[NT][2][4];                                   // low nibbles; high nibbles, times 16
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][0][e] = acc[n][1][e] = 0;
-    unsigned sumE[NPASS], sumW[NPASS];
-#pragma unroll
-    for (int x = 0; x < NPASS; ++x) sumE[x] = sumW[x] = 0;
     __syncthreads();
-    for (int tile = 0; tile < ntile; ++tile) {
-        const int buf = tile & 1;
-        const bool ok = blk_next >= 0;
-        const int jb = ((b0 + k0 + tile * KV4_TP) << 6) + 4 * qd;
-        const bool clear = jb >= j0 && jb + 4 <= j1;
-        uint32_t wl[NPASS], wh[NPASS];
+    // A lane's probabilities: head 4 x + lane / 8, keys 16 tig + 8 limb + 0..7 of
+    // a page; its operand column is that head's byte `limb`, keys 16 tig + 0..15:
+    // the pair of lanes of a head exchanges the bytes it does not need itself.
+    const int tig = lane & 3, limb = (lane >> 2) & 1, koff = 16 * tig + 8 * limb;
+    Kv4Row rw[NT];
+    int T[NT];
+    const int* tsrc[NT];
 #pragma unroll
-        for (int x = 0; x < NPASS; ++x) {
-            const int h = 2 * x + hh;
-            wl[x] = wh[x] = 0;
-            if (h < GT && ok)
-                kv4_probs(row[h], tmax[h], t_next[x], cv_next, clear, j0 - jb, j1 - jb, &wl[x], &wh[x], &sumE[x], &sumW[x]);
-        }
-        load_cv(tile + 1);
-        load_t(tile + 1);
+    for (int x = 0; x < NT; ++x) {
+        const int h = min(4 * x + (lane >> 3), GT - 1);
+        rw[x] = row[h];
+        T[x] = tmax[h];
+        tsrc[x] = p.ws_t + (unit * GT + h) * p.ts_pitch + (size_t)(k0 + warp) * KV_BLK + koff;
+    }
+    const bool mine0 = (lane >> 3) < GT;                 // GT < 4: the other lanes' columns are zero
+    int4 tn[NT][2];
+    auto load_t = [&](int q) {
 #pragma unroll
-        for (int x = 0; x < NPASS; ++x) {
-            const int h = 2 * x + hh;
-            if (h < GT) {
-                wp[buf][qd >> 4][2 * h][qd & 15] = wl[x];
-                wp[buf][qd >> 4][2 * h + 1][qd & 15] = wh[x];
+        for (int x = 0; x < NT; ++x) {
+            tn[x][0] = tn[x][1] = make_int4(0, 0, 0, 0);
+            if (q < n) {
+                tn[x][0] = __ldcg((const int4*)(tsrc[x] + q * (4 * KV_BLK)));
+                tn[x][1] = __ldcg((const int4*)(tsrc[x] + q * (4 * KV_BLK)) + 1);
             }
         }
-        __syncthreads();
-        if (!mbar_wait(smem_u32(&full[warp][tile & (NST - 1)]), (tile / NST) & 1) && a.status) a.status[ST_TIMEOUT] = 1;
-        const unsigned char* vb = ring + (tile & (NST - 1)) * SLOT + lane * 16;
+    };
+    load_t(0);
+    int acc[NG][NT][2][4];                               // low nibbles; high nibbles, times 16
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (tile * KV4_TP + i * WPG + ph >= np) break;               // (a page outside the pool has W = 0)
-            kv4_pv_page<GT, NT>(acc, vb + i * 512, wp[buf][i * WPG + ph]);
+    for (int c = 0; c < NG; ++c)
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[c][x][0][e] = acc[c][x][1][e] = 0;
+    unsigned sumE[NT], sumW[NT];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) sumE[x] = sumW[x] = 0;
+#pragma unroll 1
+    for (int q = 0; q < n; ++q) {
+        const bool ok = __shfl_sync(0xffffffffu, blk_l, q) >= 0;
+        const int jb = ((b0 + k0 + warp + 4 * q) << 6) + koff;
+        const bool clear = jb >= j0 && jb + 8 <= j1;
+        if (!mbar_wait(smem_u32(&full[warp][q & (NST - 1)]), (q / NST) & 1) && a.status) a.status[ST_TIMEOUT] = 1;
+        const unsigned char* base = ring + (q & (NST - 1)) * C::SLOT;
+        const uint2 cv = *(const uint2*)(base + C::PG + koff);
+        int4 b[NT];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            uint32_t l0 = 0, l1 = 0, u0 = 0, u1 = 0;
+            if (ok && mine0) {
+                kv4_probs(rw[x], T[x], tn[x][0], cv.x, clear, j0 - jb, j1 - jb, &l0, &u0, &sumE[x], &sumW[x]);
+                kv4_probs(rw[x], T[x], tn[x][1], cv.y, clear, j0 - jb - 4, j1 - jb - 4, &l1, &u1, &sumE[x], &sumW[x]);
+            }
+            const uint32_t r0 = __shfl_xor_sync(0xffffffffu, limb ? l0 : u0, 4), r1 = __shfl_xor_sync(0xffffffffu, limb ? l1 : u1, 4);
+            b[x] = limb ? make_int4((int)r0, (int)r1, (int)u0, (int)u1) : make_int4((int)l0, (int)l1, (int)r0, (int)r1);
+        }
+        load_t(q + 1);
+        const unsigned char* vb = base + lane * 16;
+#pragma unroll
+        for (int c = 0; c < NG; ++c) {
+            const int4 v = *(const int4*)(vb + c * 512);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                mma_u8u8(acc[c][x][0], kv4_lo(v.x), kv4_lo(v.z), kv4_lo(v.y), kv4_lo(v.w), b[x].x, b[x].z);
+                mma_u8u8(acc[c][x][1], v.x & 0xf0f0f0f0, v.z & 0xf0f0f0f0, v.y & 0xf0f0f0f0, v.w & 0xf0f0f0f0, b[x].y, b[x].w);
+            }
         }
         __syncwarp();
-        issue(tile + NST);
+        issue(q + NST);
     }
-    // ---- add this chunk's sums; the unit's last chunk divides
+    // ---- add up: the CTA's warps, then the unit's CTAs; the last one divides
 #pragma unroll
-    for (int x = 0; x < NPASS; ++x) {
-        const int h = 2 * x + hh;
-        const unsigned e = __reduce_add_sync(0xffffffffu, sumE[x]), w = __reduce_add_sync(0xffffffffu, sumW[x]);
-        if (lane == 0 && h < GT) { se[warp][h] = e; sw[warp][h] = w; }
-    }
-    unsigned long long* un = (unsigned long long*)p.ws_num + unit * (GT * D);
+    for (int x = 0; x < NT; ++x) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int h = 4 * n + (lane & 3);
-        if (h < GT) {
-            int c[4];
+        for (int o = 1; o < 8; o <<= 1) {
+            sumE[x] += __shfl_xor_sync(0xffffffffu, sumE[x], o);
+            sumW[x] += __shfl_xor_sync(0xffffffffu, sumW[x], o);
+        }
+        const int h = 4 * x + (lane >> 3);
+        if ((lane & 7) == 0 && h < GT) {
+            atomicAdd(&sums[0][h], sumE[x]);
+            atomicAdd(&sums[1][h], sumW[x]);
+        }
+        const int hc = 4 * x + tig;                      // the accumulators' head: columns 2 tig, 2 tig + 1
+        if (hc < GT) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = acc[n][0][e] + (acc[n][1][e] >> 4);
-            unsigned long long* d = un + h * D + cg * 16 + (lane >> 2);
-            atomicAdd(d, (unsigned long long)((i64)c[0] + (i64)c[1] * 256));
-            atomicAdd(d + 8, (unsigned long long)((i64)c[2] + (i64)c[3] * 256));
+            for (int c = 0; c < NG; ++c) {
+                const int ch = c * 16 + (lane >> 2);
+                atomicAdd(&num[0][hc][ch], acc[c][x][0][0] + (acc[c][x][1][0] >> 4));
+                atomicAdd(&num[1][hc][ch], acc[c][x][0][1] + (acc[c][x][1][1] >> 4));
+                atomicAdd(&num[0][hc][ch + 8], acc[c][x][0][2] + (acc[c][x][1][2] >> 4));
+                atomicAdd(&num[1][hc][ch + 8], acc[c][x][0][3] + (acc[c][x][1][3] >> 4));
+            }
         }
     }
     __syncthreads();
+    unsigned long long* un = (unsigned long long*)p.ws_num + unit * (GT * D);
     unsigned long long* us = p.ws_sum + unit * (2 * GT);
-    if (tid < GT) {
-        unsigned e = 0, w = 0;
-        const int wbase = (tid & 1) * 4;                                 // head h = 2 x + (warp >= 4)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) { e += se[wbase + k][tid]; w += sw[wbase + k][tid]; }
-        atomicAdd(us + 2 * tid, (unsigned long long)e);
-        atomicAdd(us + 2 * tid + 1, (unsigned long long)w);
-    }
+    for (int i = tid; i < nh * D; i += 128)
+        atomicAdd(un + i, (unsigned long long)((i64)(&num[0][0][0])[i] + (i64)(&num[1][0][0])[i] * 256));
+    if (tid < 2 * GT) atomicAdd(us + tid, (unsigned long long)(&sums[0][0])[tid]);
     __threadfence();
     __syncthreads();
     if (tid == 0) {
@@ -1300,14 +1321,14 @@ __global__ void __launch_bounds__(KV4_DT, GT == 8 ? 2 : 3) k_kv4_pv(Kv4Args a, K
     if (!last) return;
     __threadfence();
     if (tid < GT) {
-        const u64 e = __ldcg(us + 2 * tid), w = __ldcg(us + 2 * tid + 1);
+        const u64 e = __ldcg(us + tid), w = __ldcg(us + GT + tid);
         const int bl = bitlen_u64(e);
         tot[0][tid] = e ? (i64)pow2_recip(e, bl, 1, 23) : 0;
         tot[1][tid] = bl;
         tot[2][tid] = -8 * (i64)w;
     }
     __syncthreads();
-    for (int i = tid; i < nh * D; i += KV4_DT) {
+    for (int i = tid; i < nh * D; i += 128) {
         const int h = i / D;
         orow[i] = kv4_out((i64)__ldcg(un + i) + tot[2][h], tot[0][h], (int)tot[1][h], kvp[4], kvp[5]);
     }

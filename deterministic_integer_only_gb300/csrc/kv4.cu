@@ -15,10 +15,7 @@ namespace detint {
 namespace {
 
 constexpr int KV4_MAX_LEN = 1 << 19;       // keys: the limb sums stay in int32
-#ifndef TWO
-#define TWO 4096
-#endif
-constexpr long long KV4_TWO = TWO;         // pages of all units from which a decode call takes two launches
+constexpr long long KV4_TWO = 4096;         // pages of all units from which a decode call takes two launches
 
 struct DevInfo {
     bool ready = false;
@@ -44,7 +41,6 @@ const DecFn DEC_SCORES[2][4] = {{k_kv4_scores<64, 1>, k_kv4_scores<64, 2>, k_kv4
 const DecFn DEC_PV[2][4] = {{k_kv4_pv<64, 1>, k_kv4_pv<64, 2>, k_kv4_pv<64, 4>, k_kv4_pv<64, 8>},
                             {k_kv4_pv<128, 1>, k_kv4_pv<128, 2>, k_kv4_pv<128, 4>, k_kv4_pv<128, 8>}};
 int scores_smem(int d) { return (d == 128 ? Kv4Ring<128>::BYTES : Kv4Ring<64>::BYTES) / 2; }   // 4 of 8 warps
-int pv_smem(int d) { return 8 * 2 * (d == 128 ? 8 : 4) * 512; }
 
 using AppFn = void (*)(Kv4Args, Kv4Append);
 AppFn append_kernel(int d, bool norm, bool chunk) {
@@ -95,8 +91,8 @@ DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len,
         p.pw = 8;
         while (p.pw > 1 && units * ((mp + p.pw - 1) / p.pw) < 16LL * di.sms) p.pw >>= 1;
         p.n_sw = (mp + p.pw - 1) / p.pw;
-        p.lg_cp = 5;
-        while (p.lg_cp > 3 && units * ((mp + (1 << p.lg_cp) - 1) >> p.lg_cp) < 6LL * di.sms) --p.lg_cp;
+        p.lg_cp = 5;                                                // up to 8 pages a warp
+        while (p.lg_cp > 2 && units * ((mp + (1 << p.lg_cp) - 1) >> p.lg_cp) < 6LL * di.sms) --p.lg_cp;
         p.pitch = ((mp + 7) & ~7) << 6;                             // whole tiles
     }
     return p;
@@ -135,7 +131,7 @@ cudaError_t kv4_init() {
             if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(DEC_SCORES[d == 128][l], cudaFuncAttributeMaxDynamicSharedMemorySize, scores_smem(d));
-            if (e == cudaSuccess) e = cudaFuncSetAttribute(DEC_PV[d == 128][l], cudaFuncAttributeMaxDynamicSharedMemorySize, pv_smem(d));
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(DEC_PV[d == 128][l], cudaFuncAttributeMaxDynamicSharedMemorySize, scores_smem(d));
             if (e != cudaSuccess) continue;
             cudaLaunchConfig_t cfg = {};
             cudaLaunchAttribute at[1];
@@ -267,8 +263,6 @@ cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p0, int d, void* 
             if (e != cudaSuccess) return e;
             // starts while the first launch drains: its V slices travel before it waits
             cfg.gridDim = dim3((pl.pitch / 64 + (1 << pl.lg_cp) - 1) >> pl.lg_cp, a.n_kv * pl.hg, nt);
-            cfg.blockDim = dim3(KV4_DT);
-            cfg.dynamicSmemBytes = pv_smem(d);
             at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
             at[0].val.programmaticStreamSerializationAllowed = 1;
             cfg.numAttrs = 1;
@@ -308,8 +302,7 @@ int check_cache(const char* where, const detint_kv4_t* c, Kv4Args* a) {
     a->gmul = (65536 + c->n_q / c->n_kv - 1) / (c->n_q / c->n_kv);
     a->k = c->k; a->v = c->v; a->ks = c->k_scale; a->vs = c->v_scale;
     a->block_table = c->block_table; a->params = c->params; a->status = c->status;
-    const cudaError_t e = kv4_init();
-    return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
+    return DETINT_OK;
 }
 
 int check_attn(const char* where, const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq,
@@ -360,7 +353,8 @@ int detint_kv4_append(const detint_kv4_t* c, const detint_rope_t* r, const int32
     p.cos = r->cos; p.sin = r->sin; p.max_pos = r->max_pos; p.rot = r->rot_dim; p.inter = r->interleaved;
     p.q_gamma = r->q_gamma; p.k_gamma = r->k_gamma; p.eps = r->eps;
     p.q8 = q8; p.mq = mq; p.kq = kq; p.k_val = k_val; p.v_val = v_val;
-    const cudaError_t e = launch_kv4_append(a, p, d, (cudaStream_t)sp);
+    cudaError_t e = kv4_init();
+    if (e == cudaSuccess) e = launch_kv4_append(a, p, d, (cudaStream_t)sp);
     return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
 }
 
@@ -370,6 +364,8 @@ int detint_kv4_workspace(const detint_kv4_t* c, int n_tok, int max_len, long lon
     if (rc) return rc;
     if (!bytes || n_tok < 1 || max_len < 1 || max_len > KV4_MAX_LEN)
         return set_last_error(DETINT_E_ARG, "detint_kv4_workspace: bad arguments");
+    const cudaError_t e = kv4_init();
+    if (e != cudaSuccess) return cuda_fail("detint_kv4_workspace", e);
     *bytes = (long long)kv4_decode_ws(a, c->head_dim, n_tok, max_len);
     return DETINT_OK;
 }
@@ -382,12 +378,14 @@ int detint_kv4_decode(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq
     Kv4Attn p{};
     const int rc = check_attn(where, c, q8, mq, kq, tok_seq, tok_pos, n_tok, max_len, window, o, o_stride, &a, &p);
     if (rc) return rc;
+    cudaError_t e = kv4_init();
+    if (e != cudaSuccess) return cuda_fail(where, e);
     if (kv4_decode_needs_ws(a, c->head_dim, n_tok, max_len, window)) {
         const size_t need = kv4_decode_ws(a, c->head_dim, n_tok, max_len);
         if (!need || !workspace || workspace_bytes < (long long)need || mis(workspace, 16))
             return failed(DETINT_E_ARG, where, "a 16-byte aligned workspace of detint_kv4_workspace bytes is needed");
     }
-    const cudaError_t e = launch_kv4_decode(a, p, c->head_dim, workspace, (cudaStream_t)sp);
+    e = launch_kv4_decode(a, p, c->head_dim, workspace, (cudaStream_t)sp);
     return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
 }
 
@@ -399,7 +397,8 @@ int detint_kv4_prefill(const detint_kv4_t* c, const int8_t* q8, const int32_t* m
     Kv4Attn p{};
     const int rc = check_attn(where, c, q8, mq, kq, tok_seq, tok_pos, n_tok, max_len, window, o, o_stride, &a, &p);
     if (rc) return rc;
-    const cudaError_t e = launch_kv4_prefill(a, p, c->head_dim, (cudaStream_t)sp);
+    cudaError_t e = kv4_init();
+    if (e == cudaSuccess) e = launch_kv4_prefill(a, p, c->head_dim, (cudaStream_t)sp);
     return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
 }
 

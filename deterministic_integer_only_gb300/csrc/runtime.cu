@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "../../include/detint.h"
+#include "int_device.cuh"
 #include "kernels.h"
 
 using namespace detint;
@@ -175,6 +176,14 @@ struct detint_model {
     size_t gws_elems = 0;
     int* gcnt = nullptr;     // their tile counters (self-resetting)
     int gcnt_n = 0;
+    // 4-bit K/V cache (kv_bits 4): pages and scale codes of every layer, the
+    // layers' parameters in 4-bit units, the decode attention's workspace
+    int kv4 = 0;
+    uint8_t *k4 = nullptr, *v4 = nullptr, *ks4 = nullptr, *vs4 = nullptr;
+    int32_t* kvp4 = nullptr;
+    unsigned char* kv4_ws = nullptr;
+    size_t kv4_ws_bytes = 0;
+    int kv4_len = 0;         // bound of this decode step's context lengths
     int pf_ok = 0;           // the tensor-core prefill attention supports this shape
     CUtensorMap kmap, vmap;  // whole K / V^T caches for the prefill attention
     int32_t* qblk = nullptr; // prefill query blocks [Tcap + max_batch][4]
@@ -297,6 +306,32 @@ static cudaError_t gemm_wide(detint_model* m, const int8_t* X, const int8_t* Whi
     return launch_epi_w16(m->c64, M, N, mode, ep, s);
 }
 
+// The attention of T tokens over the 4-bit cache of layer l: norm, rotation,
+// quantisation and append, then the keys; m->qkv to m->o.
+static int attention_kv4(detint_model* m, int l, int T, int decode, cudaStream_t s) {
+    const int d = m->d, nq = m->nq, nkv = m->nkv;
+    const size_t toks = (size_t)m->nblocks * nkv * KV_BLK;      // token slots of a layer
+    Kv4Args a{};
+    a.nq = nq; a.n_kv = nkv; a.n_blocks = m->nblocks; a.n_seq = m->max_batch; a.max_blocks = m->mbs;
+    a.gmul = 65536 >> m->lg_grp;
+    a.k = m->k4 + l * (toks * d / 2); a.v = m->v4 + l * (toks * d / 2);
+    a.ks = m->ks4 + l * toks; a.vs = m->vs4 + l * toks;
+    a.block_table = m->block_table; a.params = m->kvp4 + (size_t)l * nkv * (8 + d); a.status = m->status;
+    Kv4Append p{};
+    p.qkv = m->qkv; p.qkv_stride = (nq + 2 * nkv) * d; p.tok_seq = m->tok_seq; p.tok_pos = m->tok_pos; p.T = T;
+    p.cos = m->rope_cos; p.sin = m->rope_sin; p.max_pos = m->max_pos; p.rot = d;
+    if (m->qk_norm) { p.q_gamma = m->layers[l].q_gamma; p.k_gamma = m->layers[l].k_gamma; p.eps = m->eps_qk; }
+    p.q8 = m->q8; p.mq = m->mq; p.kq = m->kq;
+    CK(launch_kv4_append(a, p, d, s));
+    Kv4Attn t{};
+    t.q8 = m->q8; t.mq = m->mq; t.kq = m->kq; t.tok_seq = m->tok_seq; t.tok_pos = m->tok_pos;
+    t.o = m->o; t.o_stride = (size_t)nq * d; t.T = T; t.G = 1 << m->lg_grp;
+    t.max_len = decode ? m->kv4_len : m->max_ctx;
+    if (decode) CK(launch_kv4_decode(a, t, d, m->kv4_ws, s));
+    else CK(launch_kv4_prefill(a, t, d, s));
+    return DETINT_OK;
+}
+
 // The forward pass of T tokens whose (sequence, position) are in tok_seq /
 // tok_pos on the device (decode: positions are read from seq_len_dev by the
 // embedding kernel). Produces logits and argmax for the R rows listed in
@@ -332,7 +367,7 @@ static int run_decode_fused(detint_model* m, int T, const int32_t* tokens, int32
     // the staged attention's CTAs (one per token and kv head) need more shared
     // memory than is left beside a GEMV CTA: SMs left free by the QKV GEMV
     // take them early, and they copy the cached K/V while the GEMV runs
-    const int att_ctas = m->dec_staged ? T * nkv : 0;
+    const int att_ctas = m->dec_staged && !m->kv4 ? T * nkv : 0;
     CK(launch_embed(tokens, T, m->tok_seq, m->tok_pos, m->seq_len_dev, 1, m->max_ctx,
                     m->embed, nullptr, m->embed_m, H, m->V, m->h, m->status, s));
     for (int l = 0; l < m->L; ++l) {
@@ -342,20 +377,24 @@ static int run_decode_fused(detint_model* m, int T, const int32_t* tokens, int32
         e.out = m->qkv; e.ldo = nqkv; e.mc = w.m_qkv; e.fout = 12;
         int rc = gemv(w.w_qkv, nqkv, H, m->h, w.attn_gamma, 0, 1, EPI_QKV, e, att_ctas);
         if (rc) return rc;
-        QkvPostArgs qa{};
-        qa.qkv = m->qkv; qa.q_gamma = w.q_gamma; qa.k_gamma = w.k_gamma; qa.qk_norm = m->qk_norm;
-        qa.eps_qk = m->eps_qk; qa.rope_cos = m->rope_cos; qa.rope_sin = m->rope_sin; qa.kvp = w.kvp;
-        qa.tok_seq = m->tok_seq; qa.tok_pos = m->tok_pos; qa.block_table = m->block_table;
-        qa.mbs = m->mbs; qa.kc = m->kcache + (size_t)l * m->kv_layer_elems;
-        qa.vc = m->vcache + (size_t)l * m->kv_layer_elems;
-        qa.T = T; qa.nq = nq; qa.nkv = nkv; qa.d = d; qa.lg_grp = m->lg_grp;
-        AttnArgs aa{};
-        aa.kc = qa.kc; aa.vc = qa.vc; aa.block_table = m->block_table; aa.mbs = m->mbs;
-        aa.tok_seq = m->tok_seq; aa.tok_pos = m->tok_pos; aa.kvp = w.kvp; aa.o = m->o; aa.T = T;
-        aa.nq = nq; aa.nkv = nkv; aa.d = d; aa.lg_grp = m->lg_grp;
-        aa.ctx_cap = m->dec_staged ? m->dec_cap : m->ctx_cap;
-        aa.seq_len = m->seq_len_dev; aa.status = m->status;
-        CK(launch_attn_decode(aa, qa, s, m->dec_staged != 0));
+        if (m->kv4) {
+            if ((rc = attention_kv4(m, l, T, 1, s))) return rc;
+        } else {
+            QkvPostArgs qa{};
+            qa.qkv = m->qkv; qa.q_gamma = w.q_gamma; qa.k_gamma = w.k_gamma; qa.qk_norm = m->qk_norm;
+            qa.eps_qk = m->eps_qk; qa.rope_cos = m->rope_cos; qa.rope_sin = m->rope_sin; qa.kvp = w.kvp;
+            qa.tok_seq = m->tok_seq; qa.tok_pos = m->tok_pos; qa.block_table = m->block_table;
+            qa.mbs = m->mbs; qa.kc = m->kcache + (size_t)l * m->kv_layer_elems;
+            qa.vc = m->vcache + (size_t)l * m->kv_layer_elems;
+            qa.T = T; qa.nq = nq; qa.nkv = nkv; qa.d = d; qa.lg_grp = m->lg_grp;
+            AttnArgs aa{};
+            aa.kc = qa.kc; aa.vc = qa.vc; aa.block_table = m->block_table; aa.mbs = m->mbs;
+            aa.tok_seq = m->tok_seq; aa.tok_pos = m->tok_pos; aa.kvp = w.kvp; aa.o = m->o; aa.T = T;
+            aa.nq = nq; aa.nkv = nkv; aa.d = d; aa.lg_grp = m->lg_grp;
+            aa.ctx_cap = m->dec_staged ? m->dec_cap : m->ctx_cap;
+            aa.seq_len = m->seq_len_dev; aa.status = m->status;
+            CK(launch_attn_decode(aa, qa, s, m->dec_staged != 0));
+        }
         e.out = m->h; e.ldo = H; e.mc = w.m_o; e.fout = 16;
         if ((rc = gemv(w.w_o, H, nq * d, m->o, nullptr, 12, 2, EPI_RESADD, e))) return rc;
         e.out = m->sbuf; e.ldo = F; e.mc = w.m_gu; e.fout = 12;
@@ -412,37 +451,42 @@ static int run_forward(detint_model* m, int T, const int32_t* tokens, int decode
         e.mt = m->mt; e.kt = m->kt;
         e.out = m->qkv; e.ldo = nqkv; e.mc = w.m_qkv; e.fout = 12;
         CK(gemm(w.w_qkv, w.l_qkv, T, nqkv, H, EPI_QKV, e));
-        QkvPostArgs qa{};
-        qa.qkv = m->qkv; qa.q_gamma = w.q_gamma; qa.k_gamma = w.k_gamma; qa.qk_norm = m->qk_norm;
-        qa.eps_qk = m->eps_qk; qa.rope_cos = m->rope_cos; qa.rope_sin = m->rope_sin; qa.kvp = w.kvp;
-        qa.tok_seq = m->tok_seq; qa.tok_pos = m->tok_pos; qa.block_table = m->block_table;
-        qa.mbs = m->mbs; qa.q8 = m->q8; qa.mq = m->mq; qa.kq = m->kq; qa.kc = kc; qa.vc = vc;
-        qa.T = T; qa.nq = nq; qa.nkv = nkv; qa.d = d; qa.lg_grp = m->lg_grp;
-        AttnArgs aa{};
-        aa.q8 = m->q8; aa.mq = m->mq; aa.kq = m->kq; aa.kc = kc; aa.vc = vc;
-        aa.block_table = m->block_table; aa.mbs = m->mbs; aa.tok_seq = m->tok_seq;
-        aa.tok_pos = m->tok_pos; aa.kvp = w.kvp; aa.o = m->o; aa.T = T; aa.nq = nq; aa.nkv = nkv;
-        aa.d = d; aa.lg_grp = m->lg_grp; aa.ctx_cap = m->ctx_cap;
-        if (decode) {
-            // one token per sequence: QKV post-processing fused into the decode
-            // attention, the sequence's K/V staged in shared memory while every
-            // context fits, else read from the cache
-            aa.ctx_cap = m->dec_staged == 1 ? m->dec_cap : m->ctx_cap;
-            aa.seq_len = m->seq_len_dev; aa.status = m->status;
-            CK(launch_attn_decode(aa, qa, s, m->dec_staged == 1));
-        } else if (!decode && m->pf_ok && m->tc_prefill) {
-            CK(launch_qkv_post(qa, s));
-            PfArgs pa{};
-            pa.q8 = m->q8; pa.mq = m->mq; pa.kq = m->kq; pa.block_table = m->block_table;
-            pa.mbs = m->mbs; pa.qblk = m->qblk; pa.nqb = m->nqb; pa.kvp = w.kvp; pa.o = m->o;
-            pa.nq = nq; pa.nkv = nkv; pa.lg_grp = m->lg_grp;
-            pa.krow0 = (int)((long long)l * m->nblocks * nkv * KV_BLK);
-            pa.vrow0 = (int)((long long)l * m->nblocks * nkv * d);
-            pa.status = m->status;
-            CK(launch_attn_prefill(pa, m->kmap, m->vmap, d, s));
+        if (m->kv4) {
+            const int rc = attention_kv4(m, l, T, decode, s);
+            if (rc) return rc;
         } else {
-            CK(launch_qkv_post(qa, s));
-            CK(launch_attention(aa, s));
+            QkvPostArgs qa{};
+            qa.qkv = m->qkv; qa.q_gamma = w.q_gamma; qa.k_gamma = w.k_gamma; qa.qk_norm = m->qk_norm;
+            qa.eps_qk = m->eps_qk; qa.rope_cos = m->rope_cos; qa.rope_sin = m->rope_sin; qa.kvp = w.kvp;
+            qa.tok_seq = m->tok_seq; qa.tok_pos = m->tok_pos; qa.block_table = m->block_table;
+            qa.mbs = m->mbs; qa.q8 = m->q8; qa.mq = m->mq; qa.kq = m->kq; qa.kc = kc; qa.vc = vc;
+            qa.T = T; qa.nq = nq; qa.nkv = nkv; qa.d = d; qa.lg_grp = m->lg_grp;
+            AttnArgs aa{};
+            aa.q8 = m->q8; aa.mq = m->mq; aa.kq = m->kq; aa.kc = kc; aa.vc = vc;
+            aa.block_table = m->block_table; aa.mbs = m->mbs; aa.tok_seq = m->tok_seq;
+            aa.tok_pos = m->tok_pos; aa.kvp = w.kvp; aa.o = m->o; aa.T = T; aa.nq = nq; aa.nkv = nkv;
+            aa.d = d; aa.lg_grp = m->lg_grp; aa.ctx_cap = m->ctx_cap;
+            if (decode) {
+                // one token per sequence: QKV post-processing fused into the decode
+                // attention, the sequence's K/V staged in shared memory while every
+                // context fits, else read from the cache
+                aa.ctx_cap = m->dec_staged == 1 ? m->dec_cap : m->ctx_cap;
+                aa.seq_len = m->seq_len_dev; aa.status = m->status;
+                CK(launch_attn_decode(aa, qa, s, m->dec_staged == 1));
+            } else if (!decode && m->pf_ok && m->tc_prefill) {
+                CK(launch_qkv_post(qa, s));
+                PfArgs pa{};
+                pa.q8 = m->q8; pa.mq = m->mq; pa.kq = m->kq; pa.block_table = m->block_table;
+                pa.mbs = m->mbs; pa.qblk = m->qblk; pa.nqb = m->nqb; pa.kvp = w.kvp; pa.o = m->o;
+                pa.nq = nq; pa.nkv = nkv; pa.lg_grp = m->lg_grp;
+                pa.krow0 = (int)((long long)l * m->nblocks * nkv * KV_BLK);
+                pa.vrow0 = (int)((long long)l * m->nblocks * nkv * d);
+                pa.status = m->status;
+                CK(launch_attn_prefill(pa, m->kmap, m->vmap, d, s));
+            } else {
+                CK(launch_qkv_post(qa, s));
+                CK(launch_attention(aa, s));
+            }
         }
         CK(launch_actquant(m->o, T, nq * d, 12, m->x8, m->mt, m->kt, s));
         e.out = m->h; e.ldo = H; e.mc = w.m_o; e.fout = 16;
@@ -509,8 +553,8 @@ static int sync_block_table(detint_model* m, cudaStream_t s) {
 static int setup_step(detint_model* m) {
     const int H = m->H, d = m->d, G = 1 << m->lg_grp, nqd = m->nq * d, F = m->F, nkv = m->nkv;
     const int nqkv = (m->nq + 2 * nkv) * d;
-    if (m->wide || (H & (H - 1)) || (nkv & (nkv - 1)) || G > 7 || !decode_step_supported(d, G))
-        return DETINT_OK;                           // (16-bit weights: the layer-by-layer path)
+    if (m->wide || m->kv4 || (H & (H - 1)) || (nkv & (nkv - 1)) || G > 7 || !decode_step_supported(d, G))
+        return DETINT_OK;                           // (16-bit weights, 4-bit cache: the layer-by-layer path)
     for (int K : {H, nqd, F})
         if ((K & 15) || K > STEP_SLOT) return DETINT_OK;
     int dev = 0;
@@ -664,6 +708,8 @@ void detint_free(detint_model* m) {
     if (m->wblob) cudaFree(m->wblob);
     if (m->kcache) cudaFree(m->kcache);
     if (m->vcache) cudaFree(m->vcache);
+    for (void* q : {(void*)m->k4, (void*)m->v4, (void*)m->ks4, (void*)m->vs4, (void*)m->kvp4, (void*)m->kv4_ws})
+        if (q) cudaFree(q);
     if (m->block_table) cudaFree(m->block_table);
     if (m->seq_len_dev) cudaFree(m->seq_len_dev);
     if (m->status) cudaFree(m->status);
@@ -680,10 +726,60 @@ void detint_free(detint_model* m) {
 
 static int rd32(const unsigned char* p) { int32_t v; memcpy(&v, p, 4); return v; }
 
+// The artifact's K/V parameters (fixed int8 scales) in units of the 4-bit
+// cache, 1/14 of an int8 step: x = 14 y KQM / 2^KQS = y 7 KQM / 2^(KQS - 1);
+// the score scale divided by 14; the output scale of 128 units. The key
+// exponents of the channel pairs (c, c + d/2) are written out per channel.
+static bool kv4_params(const detint_model* m, const std::vector<const unsigned char*>& src, std::vector<int32_t>* out) {
+    const int d = m->d, in = 8 + d / 2, on = 8 + d;
+    out->assign((size_t)m->L * m->nkv * on, 0);
+    for (int l = 0; l < m->L; ++l)
+        for (int g = 0; g < m->nkv; ++g) {
+            std::vector<int32_t> s(in);
+            memcpy(s.data(), src[l] + (size_t)g * in * 4, (size_t)in * 4);
+            int32_t* o = out->data() + ((size_t)l * m->nkv + g) * on;
+            if (s[0] < 1 || s[2] < 1 || s[4] < 1 || s[6] < 1 || s[1] < 1 || s[3] < 1) return false;
+            int mv, kv, mc, kc;
+            dyadic_fast((u64)s[4] * 64, 7, &mv, &kv);
+            dyadic_fast((u64)s[6], 14, &mc, &kc);
+            o[0] = 7 * s[0]; o[1] = s[1] - 1; o[2] = 7 * s[2]; o[3] = s[3] - 1;
+            o[4] = mv; o[5] = s[5] + kv; o[6] = mc; o[7] = s[7] + kc;
+            for (int c = 0; c < d; ++c) o[8 + c] = s[8 + c % (d / 2)];
+        }
+    return true;
+}
+
+// room for the decode attention of n tokens with contexts up to len
+static int ensure_kv4_ws(detint_model* m, int n, int len) {
+    Kv4Args a{};
+    a.nq = m->nq; a.n_kv = m->nkv;
+    const size_t need = kv4_decode_ws(a, m->d, n, len);
+    if (need <= m->kv4_ws_bytes) return DETINT_OK;
+    CK(cudaDeviceSynchronize());
+    free_graphs(m);
+    if (m->kv4_ws) cudaFree(m->kv4_ws);
+    m->kv4_ws = nullptr;
+    m->kv4_ws_bytes = 0;
+    if (cudaMalloc(&m->kv4_ws, need) != cudaSuccess) {
+        cudaGetLastError();
+        m->kv4_ws = nullptr;
+        return fail(DETINT_E_OOM, "decode attention workspace");
+    }
+    m->kv4_ws_bytes = need;
+    return DETINT_OK;
+}
+
 int detint_load(const char* path, int max_batch, int max_ctx, detint_stream_t stream,
                 detint_model** out) {
+    return detint_load_kv(path, max_batch, max_ctx, 8, stream, out);
+}
+
+int detint_load_kv(const char* path, int max_batch, int max_ctx, int kv_bits, detint_stream_t stream,
+                   detint_model** out) {
     if (!path || !out || max_batch < 1 || max_ctx < 1) return fail(DETINT_E_ARG, "detint_load: bad arguments");
     *out = nullptr;
+    if (kv_bits != 8 && kv_bits != 4) return fail(DETINT_E_ARG, "detint_load_kv: kv_bits must be 8 or 4");
+    const int kv4 = kv_bits == 4;
     (void)stream;
     FILE* f = fopen(path, "rb");
     if (!f) return fail(DETINT_E_ARTIFACT, std::string("cannot open ") + path);
@@ -717,6 +813,7 @@ int detint_load(const char* path, int max_batch, int max_ctx, detint_stream_t st
     const size_t wb = wide ? 2 : 1;                 // bytes per weight
     detint_model* m = new detint_model();
     m->wide = wide;
+    m->kv4 = kv4;
     m->L = rd32(hd + 12); m->H = rd32(hd + 16); m->nq = rd32(hd + 20); m->nkv = rd32(hd + 24);
     m->d = rd32(hd + 28); m->F = rd32(hd + 32); m->V = rd32(hd + 36); m->max_pos = rd32(hd + 40);
     m->qk_norm = rd32(hd + 44); m->eps_h = rd32(hd + 48); m->eps_qk = rd32(hd + 52);
@@ -734,7 +831,9 @@ int detint_load(const char* path, int max_batch, int max_ctx, detint_stream_t st
     m->mbs = (max_ctx + KV_BLK - 1) / KV_BLK;
     m->ctx_cap = m->mbs * KV_BLK;
     m->nblocks = m->mbs * max_batch;
-    if (attention_smem_bytes(grp, d, m->ctx_cap) > 220 * 1024) return bad_shape("max_ctx too large for the attention row");
+    if (kv4 && max_ctx > (1 << 19)) return bad_shape("max_ctx beyond the 4-bit cache's 524288");
+    if (kv4 && (m->eps_qk < 0 || m->eps_qk > 32767)) return bad_shape("eps_qk beyond the 4-bit append's 32767");
+    if (!kv4 && attention_smem_bytes(grp, d, m->ctx_cap) > 220 * 1024) return bad_shape("max_ctx too large for the attention row");
     // section walk (256-byte aligned, file order)
     const int nqkv = (nq + 2 * nkv) * d;
     size_t cur = 256;
@@ -848,10 +947,23 @@ int detint_load(const char* path, int max_batch, int max_ctx, detint_stream_t st
     m->final_gamma = (int16_t*)(m->wblob + secs[s_fg].doff);
     m->rope_cos = (int16_t*)(m->wblob + secs[s_rc].doff);
     m->rope_sin = (int16_t*)(m->wblob + secs[s_rs].doff);
-    // paged int8 KV cache: K [L][NB][nkv][64][d], V [L][NB][nkv][d][64]
+    // paged KV cache: int8 K [L][NB][nkv][64][d], V [L][NB][nkv][d][64], or
+    // 4-bit pages and scale codes (k_kv4.cuh)
     m->kv_layer_elems = (size_t)m->nblocks * nkv * KV_BLK * d;
-    if (cudaMalloc(&m->kcache, m->kv_layer_elems * m->L) != cudaSuccess ||
-        cudaMalloc(&m->vcache, m->kv_layer_elems * m->L) != cudaSuccess) {
+    const size_t toks = (size_t)m->L * m->nblocks * nkv * KV_BLK;
+    std::vector<int32_t> kvp4;
+    std::vector<const unsigned char*> kvp8(m->L);
+    for (int l = 0; l < m->L; ++l) kvp8[l] = secs[ls[l].kvp].src;
+    if (kv4 && !kv4_params(m, kvp8, &kvp4)) {
+        detint_free(m);
+        return fail(DETINT_E_ARTIFACT, "K/V scales that 4 bits cannot refine");
+    }
+    if (kv4 ? (cudaMalloc(&m->k4, toks * d / 2) != cudaSuccess || cudaMalloc(&m->v4, toks * d / 2) != cudaSuccess ||
+               cudaMalloc(&m->ks4, toks) != cudaSuccess || cudaMalloc(&m->vs4, toks) != cudaSuccess ||
+               cudaMalloc(&m->kvp4, kvp4.size() * 4) != cudaSuccess)
+            : (cudaMalloc(&m->kcache, m->kv_layer_elems * m->L) != cudaSuccess ||
+               cudaMalloc(&m->vcache, m->kv_layer_elems * m->L) != cudaSuccess)) {
+        cudaGetLastError();                             // not left for the next launch's check
         detint_free(m);
         return fail(DETINT_E_OOM, "KV cache allocation failed");
     }
@@ -872,18 +984,26 @@ int detint_load(const char* path, int max_batch, int max_ctx, detint_stream_t st
     ce = cudaMemcpy(m->block_table, bt.data(), bt.size() * 4, cudaMemcpyHostToDevice);
     if (ce == cudaSuccess) ce = cudaMemset(m->seq_len_dev, 0, (size_t)max_batch * 4);
     if (ce == cudaSuccess) ce = cudaMemset(m->status, 0, ST_N * 4);
-    if (ce == cudaSuccess) ce = cudaMemset(m->kcache, 0, m->kv_layer_elems * m->L);
-    if (ce == cudaSuccess) ce = cudaMemset(m->vcache, 0, m->kv_layer_elems * m->L);
+    if (kv4) {
+        if (ce == cudaSuccess) ce = cudaMemset(m->k4, 0x88, toks * d / 2);   // value 0
+        if (ce == cudaSuccess) ce = cudaMemset(m->v4, 0x88, toks * d / 2);
+        if (ce == cudaSuccess) ce = cudaMemset(m->ks4, 1, toks);
+        if (ce == cudaSuccess) ce = cudaMemset(m->vs4, 1, toks);
+        if (ce == cudaSuccess) ce = cudaMemcpy(m->kvp4, kvp4.data(), kvp4.size() * 4, cudaMemcpyHostToDevice);
+    } else {
+        if (ce == cudaSuccess) ce = cudaMemset(m->kcache, 0, m->kv_layer_elems * m->L);
+        if (ce == cudaSuccess) ce = cudaMemset(m->vcache, 0, m->kv_layer_elems * m->L);
+    }
     if (ce != cudaSuccess) { detint_free(m); return fail(DETINT_E_CUDA, cudaGetErrorString(ce)); }
     m->seq_len.assign(max_batch, 0);
     // the tensor-core prefill attention takes head_dim 64 or 128 and up to 64 q heads per kv head
-    m->pf_ok = (d == 64 || d == 128) && m->lg_grp <= 6 &&
+    m->pf_ok = !kv4 && (d == 64 || d == 128) && m->lg_grp <= 6 &&
                make_kv_maps(&m->kmap, &m->vmap, m->kcache, m->vcache,
                             (long long)m->L * m->nblocks * nkv, d) == cudaSuccess;
     // staged decode attention: the largest block multiple of keys whose K/V
     // copies and score rows fit the shared-memory budget
     m->dec_cap = 0;
-    if ((d == 64 || d == 128) && m->lg_grp <= 3) {
+    if (!kv4 && (d == 64 || d == 128) && m->lg_grp <= 3) {
         const int want = std::min(m->mbs * KV_BLK, 64 * KV_BLK);
         for (int cap = KV_BLK; cap <= want; cap += KV_BLK)
             if (attn_dec_smem(1 << m->lg_grp, d, cap) <= 220 * 1024) m->dec_cap = cap;
@@ -891,6 +1011,8 @@ int detint_load(const char* path, int max_batch, int max_ctx, detint_stream_t st
     int rc = ensure_scratch(m, std::max(64, max_batch));
     if (rc != DETINT_OK) { detint_free(m); return rc; }
     ce = kernels_init();
+    if (ce != cudaSuccess) { detint_free(m); return fail(DETINT_E_CUDA, cudaGetErrorString(ce)); }
+    ce = kv4 ? kv4_init() : cudaSuccess;
     if (ce != cudaSuccess) { detint_free(m); return fail(DETINT_E_CUDA, cudaGetErrorString(ce)); }
     rc = setup_step(m);
     if (rc != DETINT_OK) { detint_free(m); return rc; }
@@ -1005,6 +1127,15 @@ int detint_decode_step(detint_model* m, int n_seq, const int32_t* seq_ids, const
         m->dec_staged = (m->staged_decode && m->dec_cap > 0 && mx <= m->dec_cap) ? 1 : 0;
         if (m->persistent && n_seq <= 8 && m->st_cfg[n_seq - 1].ok && m->fused_decode && mx <= m->st_scap)
             m->dec_staged = 2;
+        // the context bound of a 4-bit step, a power of two so that a captured
+        // graph is replayed while the contexts grow
+        m->kv4_len = 0;
+        if (m->kv4) {
+            m->kv4_len = 512;
+            while (m->kv4_len < mx) m->kv4_len <<= 1;
+            m->kv4_len = std::min(m->kv4_len, m->max_ctx);
+            if ((rc = ensure_kv4_ws(m, n_seq, m->kv4_len))) return rc;
+        }
     }
     const bool graph = m->use_graph && s != nullptr && s != cudaStreamLegacy && s != cudaStreamPerThread;
     if (!graph) {
@@ -1015,8 +1146,8 @@ int detint_decode_step(detint_model* m, int n_seq, const int32_t* seq_ids, const
         if (rc) return rc;
     } else {
         char key[128];
-        snprintf(key, sizeof key, "%d|%d|%p|%p|%p|", n_seq, m->dec_staged, (const void*)tok, (void*)logits,
-                 (void*)next_tok);
+        snprintf(key, sizeof key, "%d|%d|%d|%p|%p|%p|", n_seq, m->dec_staged, m->kv4_len, (const void*)tok,
+                 (void*)logits, (void*)next_tok);
         std::string k(key);
         for (int i = 0; i < n_seq; ++i) k += std::to_string(seq_ids[i]) + ",";
         auto it = m->graphs.find(k);
@@ -1146,14 +1277,19 @@ int detint_fork_seq(detint_model* m, int src, int dst, int n_tokens, detint_stre
         m->refcnt[b] = 1;
         m->bt_host[(size_t)dst * m->mbs + full] = b;
         db.push_back(b);
-        const size_t blk = (size_t)m->nkv * KV_BLK * m->d;   // bytes of one block of one layer
-        for (int l = 0; l < m->L; ++l) {
-            const size_t base = (size_t)l * m->kv_layer_elems;
-            CK(cudaMemcpyAsync(m->kcache + base + (size_t)b * blk, m->kcache + base + (size_t)sb[full] * blk,
-                               blk, cudaMemcpyDeviceToDevice, s));
-            CK(cudaMemcpyAsync(m->vcache + base + (size_t)b * blk, m->vcache + base + (size_t)sb[full] * blk,
-                               blk, cudaMemcpyDeviceToDevice, s));
-        }
+        // every layer's copy of the block: K and V, and the 4-bit cache's scale codes
+        const size_t slots = (size_t)m->nkv * KV_BLK;              // token slots of one block of one layer
+        struct { uint8_t* base; size_t blk; } parts[4] = {
+            {m->kv4 ? m->k4 : (uint8_t*)m->kcache, m->kv4 ? slots * m->d / 2 : slots * m->d},
+            {m->kv4 ? m->v4 : (uint8_t*)m->vcache, m->kv4 ? slots * m->d / 2 : slots * m->d},
+            {m->ks4, slots},
+            {m->vs4, slots}};
+        for (int l = 0; l < m->L; ++l)
+            for (int i = 0; i < (m->kv4 ? 4 : 2); ++i) {
+                uint8_t* p = parts[i].base + (size_t)l * m->nblocks * parts[i].blk;
+                CK(cudaMemcpyAsync(p + (size_t)b * parts[i].blk, p + (size_t)sb[full] * parts[i].blk, parts[i].blk,
+                                   cudaMemcpyDeviceToDevice, s));
+            }
     }
     m->bt_dirty = true;
     int rc = sync_block_table(m, s);

@@ -62,6 +62,17 @@ enum {
 int detint_load(const char* artifact_path, int max_batch, int max_ctx, detint_stream_t s,
                 detint_model** out);
 
+/* The same with a choice of the K/V cache's width: kv_bits 8 (detint_load) or
+ * 4, the 4-bit paged cache below, at (head_dim + 2) / (2 head_dim) of the
+ * bytes and with contexts up to 524288. The 4-bit cache's units are 1/14 of
+ * the artifact's int8 steps (arithmetic specification, section 16); logits
+ * differ from the 8-bit model's, and are as invariant over batches, splits
+ * and kernels as they are there. Its decode steps run one kernel per phase,
+ * so the one-launch and staged-attention options have no effect.
+ * Errors: as detint_load. */
+int detint_load_kv(const char* artifact_path, int max_batch, int max_ctx, int kv_bits, detint_stream_t s,
+                   detint_model** out);
+
 /* Prefill: append a ragged batch of prompts to the KV caches of `n_seq`
  * distinct sequences and return the logits of each sequence's last new
  * position (DetLLM blog, "DetLLM": prefill and decode see the same cached

@@ -53,6 +53,7 @@ def lib():
         L.or_seq_len.argtypes = [C.c_void_p]
         L.or_seq_feed.argtypes = [C.c_void_p, C.c_void_p, C.c_int, C.POINTER(i32),
                                   C.POINTER(i32), C.POINTER(i32)]
+        L.or_model_set_kv4.argtypes = [C.c_void_p, C.c_int]
         L.or_splitmix64.restype = u64; L.or_splitmix64.argtypes = [u64, u64]
         L.or_sample.restype = C.c_int
         L.or_sample.argtypes = [C.POINTER(i32), C.c_int, i32, i32, i32, u64, u64]
@@ -230,6 +231,41 @@ def attention_row(q8, mq, kq, K8, V8, kvp):
     return o, P, int(sig.value)
 
 
+def quant4(x):
+    """(codes int8 [rows, n], scale codes [rows]) of rows of cached integers."""
+    x = np.ascontiguousarray(np.atleast_2d(x), np.int32)
+    q = np.empty(x.shape, np.int8)
+    c = np.array([lib().or_quant4(_p(x[r], C.c_int32), C.c_int(x.shape[1]), _p(q[r], C.c_int8))
+                  for r in range(x.shape[0])], np.int64)
+    check()
+    return q, c
+
+
+def kv4_params(kvp, d):
+    """An artifact's K/V parameters [8 + d/2] in units of the 4-bit cache [8 + d]."""
+    kvp = np.ascontiguousarray(kvp, np.int32)
+    out = np.empty(8 + d, np.int32)
+    lib().or_kv4_params(_p(kvp, C.c_int32), C.c_int(d), _p(out, C.c_int32))
+    check()
+    return out
+
+
+def attention4_row(q8, mq, kq, K4, ck, V4, cv, prm, first=0):
+    """Attention of one query over keys first.. of 4-bit K/V codes [ctx, d] with
+    scale codes [ctx]; returns (o int32 [d], sum of E)."""
+    q8, K4, V4 = (np.ascontiguousarray(a, np.int8) for a in (q8, K4, V4))
+    ck, cv = (np.ascontiguousarray(a, np.uint8) for a in (ck, cv))
+    prm = np.ascontiguousarray(prm, np.int32)
+    ctx, d = K4.shape
+    o = np.empty(d, np.int32)
+    sig = C.c_int64(0)
+    lib().or_attention4_row(_p(q8, C.c_int8), C.c_int32(int(mq)), C.c_int32(int(kq)), _p(K4, C.c_int8),
+                            _p(ck, C.c_uint8), _p(V4, C.c_int8), _p(cv, C.c_uint8), C.c_int(int(first)),
+                            C.c_int(ctx), C.c_int(d), _p(prm, C.c_int32), _p(o, C.c_int32), C.byref(sig))
+    check()
+    return o, int(sig.value)
+
+
 def argmax(x):
     x = np.ascontiguousarray(x, np.int32)
     return int(lib().or_argmax(_p(x, C.c_int32), C.c_int(x.size)))
@@ -264,14 +300,16 @@ def sample_set(logits, inv_temp: int = 65536, top_k: int = 0, top_p: int = 65536
 
 # --------------------------------------------------------------------- model
 class Model:
-    """A loaded artifact plus per-sequence int8 KV caches, in plain C."""
+    """A loaded artifact plus per-sequence KV caches (int8, or 4-bit with
+    kv_bits 4), in plain C."""
 
-    def __init__(self, path: str):
+    def __init__(self, path: str, kv_bits: int = 8):
         L = lib()
         err = C.c_int(0)
         self._h = L.or_model_load(path.encode(), C.byref(err))
         if not self._h:
             raise OracleError(f"oracle could not load {path} (code {err.value})")
+        L.or_model_set_kv4(self._h, int(kv_bits == 4))
         info = np.zeros(16, np.int32)
         L.or_model_info(self._h, _p(info, C.c_int32))
         (self.n_layers, self.hidden, self.n_q, self.n_kv, self.head_dim, self.ffn,

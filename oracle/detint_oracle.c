@@ -412,6 +412,87 @@ int or_attention_row(const int8_t* q8, int32_t mq, int32_t kq, const int8_t* K8,
     return 0;
 }
 
+/* ---------------------------------------- the 4-bit K/V cache (section 16) */
+/* One head's cached integers x (|x| <= 1785): the scale code and the 4-bit
+ * codes -7..7. */
+int or_quant4(const int32_t* x, int n, int8_t* q) {
+    i64 a = 0;
+    for (int i = 0; i < n; i++) {
+        const i64 m = x[i] < 0 ? -(i64)x[i] : (i64)x[i];
+        CHECK(m <= 1785);
+        if (m > a) a = m;
+    }
+    i64 c = (a + 6) / 7;
+    if (c < 1) c = 1;
+    const int b = bitlen((u64)c);
+    const i64 R = (i64)fdiv((u64)1 << (b + 16), (u64)c);
+    for (int i = 0; i < n; i++) {
+        const i64 v = or_rshr((i64)x[i] * R, b + 16);
+        CHECK(v >= -7 && v <= 7);
+        q[i] = (int8_t)v;
+    }
+    CHECK(c <= 255);
+    return (int)c;
+}
+
+/* An artifact's K/V parameters [8 + d/2] in units of the 4-bit cache [8 + d] */
+void or_kv4_params(const int32_t* in, int d, int32_t* out) {
+    CHECK(in[1] >= 1 && in[3] >= 1);
+    int32_t m, k;
+    out[0] = 7 * in[0];
+    out[1] = in[1] - 1;
+    out[2] = 7 * in[2];
+    out[3] = in[3] - 1;
+    or_dyadic((i64)in[4] * 64, 7, &m, &k);
+    out[4] = m;
+    out[5] = in[5] + k;
+    or_dyadic(in[6], 14, &m, &k);
+    out[6] = m;
+    out[7] = in[7] + k;
+    for (int c = 0; c < d; c++) out[8 + c] = in[8 + c % (d / 2)];
+}
+
+/* Attention of one query over keys first..ctx-1; K4, V4 [ctx][d] codes, ck, cv
+ * [ctx] scale codes, prm in 4-bit units. No key gives zeros. */
+int or_attention4_row(const int8_t* q8, int32_t mq, int32_t kq, const int8_t* K4, const uint8_t* ck,
+                      const int8_t* V4, const uint8_t* cv, int first, int ctx, int d, const int32_t* prm,
+                      int32_t* o, i64* sigma_out) {
+    CHECK(ctx <= (1 << 19) && first >= 0);
+    for (int c = 0; c < d; c++) o[c] = 0;
+    if (sigma_out) *sigma_out = 0;
+    if (first >= ctx) return 0;
+    i64* t = (i64*)malloc(sizeof(i64) * (size_t)ctx);
+    i64 top = 0;
+    for (int j = first; j < ctx; j++) {
+        i64 S = 0;
+        for (int c = 0; c < d; c++) S += (i64)q8[c] * (i64)K4[(size_t)j * d + c];
+        t[j] = S * ck[j];
+        CHECK(t[j] < P2(25) && t[j] > -P2(25));
+        if (j == first || t[j] > top) top = t[j];
+    }
+    int sh = kq + prm[7] - 10;
+    if (sh < 0) sh = 0;
+    if (sh > 62) sh = 62;
+    i64 sigma = 0;
+    for (int j = first; j < ctx; j++) {
+        i64 E = or_exp2q(or_rshr((t[j] - top) * ((i64)mq * prm[6]), sh));
+        if (E > P2(15) - 1) E = P2(15) - 1;
+        sigma += E;
+        t[j] = or_rshr(E * cv[j], 7);
+        CHECK(t[j] < P2(16));
+    }
+    const int bl = bitlen((u64)sigma);
+    const i64 RS = (i64)fdiv((u64)1 << (bl + 23), (u64)sigma);
+    for (int c = 0; c < d; c++) {
+        i64 num = 0;
+        for (int j = first; j < ctx; j++) num += t[j] * (i64)V4[(size_t)j * d + c];
+        o[c] = (int32_t)sat32(or_rshr(or_rshr(num * RS, bl + 7) * prm[4], prm[5] + 16 - 12));
+    }
+    if (sigma_out) *sigma_out = sigma;
+    free(t);
+    return 0;
+}
+
 /* argmax with ties to the lowest index ([BLOG] "DetLLM") */
 int or_argmax(const int32_t* x, int n) {
     int best = 0;
@@ -533,6 +614,7 @@ typedef struct {
 
 typedef struct {
     int L, H, nq, nkv, d, F, V, max_pos, qk_norm, wbits;
+    int kv4;     /* K/V caches in 4 bits (section 16) instead of int8 */
     i64 eps_h, eps_qk;
     const void* embed; const int32_t* embed_m; const int16_t* final_gamma;
     const int16_t *rope_cos, *rope_sin;
@@ -544,6 +626,7 @@ typedef struct {
     int len, max_ctx;
     int8_t* K;   /* [L][nkv][max_ctx][d] */
     int8_t* V;   /* [L][nkv][max_ctx][d] */
+    uint8_t *ck, *cv;  /* 4-bit caches: scale codes [L][nkv][max_ctx] */
 } or_seq;
 
 static int rd32(const uint8_t* p) { int32_t v; memcpy(&v, p, 4); return v; }
@@ -624,6 +707,9 @@ void or_model_info(void* p, int32_t* info) {
     info[5] = m->F; info[6] = m->V; info[7] = m->max_pos; info[8] = m->qk_norm; info[9] = m->wbits;
 }
 
+/* 4-bit (1) or int8 (0) K/V caches for the sequences fed from now on */
+void or_model_set_kv4(void* p, int on) { ((or_model*)p)->kv4 = on; }
+
 void* or_seq_new(void* p, int max_ctx) {
     or_model* m = (or_model*)p;
     or_seq* s = (or_seq*)calloc(1, sizeof(or_seq));
@@ -631,13 +717,15 @@ void* or_seq_new(void* p, int max_ctx) {
     size_t n = (size_t)m->L * m->nkv * max_ctx * m->d;
     s->K = (int8_t*)calloc(n, 1);
     s->V = (int8_t*)calloc(n, 1);
+    s->ck = (uint8_t*)calloc(n / (size_t)m->d, 1);
+    s->cv = (uint8_t*)calloc(n / (size_t)m->d, 1);
     return s;
 }
 
 void or_seq_free(void* p) {
     or_seq* s = (or_seq*)p;
     if (!s) return;
-    free(s->K); free(s->V); free(s);
+    free(s->K); free(s->V); free(s->ck); free(s->cv); free(s);
 }
 
 int or_seq_len(void* p) { return ((or_seq*)p)->len; }
@@ -735,6 +823,20 @@ static void forward_token(or_model* m, or_seq* s, int32_t tok, int32_t* logits, 
                 y[i] = kin[i] * 4;
             }
             or_rope(y, d, cr, sr);
+            if (m->kv4) {
+                /* cached integers in 1/14 of the int8 steps, 4-bit codes, scale codes */
+                int32_t prm[8 + 256];
+                const size_t at = ((size_t)l * nkv + g2) * s->max_ctx + pos;
+                CHECK(d <= 256);
+                or_kv4_params(kvp, d, prm);
+                for (int c = 0; c < d; c++)
+                    y[c] = (int32_t)sat(or_rshr((i64)y[c] * P2(prm[8 + c]) * prm[0], prm[1]), 1785);
+                s->ck[at] = (uint8_t)or_quant4(y, d, Kd);
+                for (int c = 0; c < d; c++)
+                    y[c] = (int32_t)sat(or_rshr((i64)vin[c] * prm[2], prm[3]), 1785);
+                s->cv[at] = (uint8_t)or_quant4(y, d, Vd);
+                continue;
+            }
             for (int c = 0; c < d; c++) {
                 i64 v = (i64)y[c] * P2(kvp[8 + (c % half)]);
                 Kd[c] = (int8_t)sat(or_rshr(v * kvp[0], kvp[1]), 127);
@@ -749,6 +851,14 @@ static void forward_token(or_model* m, or_seq* s, int32_t tok, int32_t* logits, 
             int g2 = hq / grp;
             const int8_t* Kb = s->K + ((size_t)l * nkv + g2) * s->max_ctx * d;
             const int8_t* Vb = s->V + ((size_t)l * nkv + g2) * s->max_ctx * d;
+            if (m->kv4) {
+                int32_t prm[8 + 256];
+                const size_t at = ((size_t)l * nkv + g2) * s->max_ctx;
+                or_kv4_params(ly->kvp + (size_t)g2 * (8 + half), d, prm);
+                or_attention4_row(q8 + hq * d, mq[hq], kq[hq], Kb, s->ck + at, Vb, s->cv + at, 0, pos + 1, d, prm,
+                                  o + hq * d, NULL);
+                continue;
+            }
             or_attention_row(q8 + hq * d, mq[hq], kq[hq], Kb, Vb, pos + 1, d,
                              ly->kvp + (size_t)g2 * (8 + half), o + hq * d, NULL, NULL);
         }

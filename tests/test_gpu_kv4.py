@@ -1,0 +1,472 @@
+"""The 4-bit paged K/V cache operators on the GPU against plain 64-bit forms
+(kv4_plain: the oracle's scalar rows on plain arrays), bit for bit: every
+output, every byte of the pages and everything that must stay as it was."""
+import numpy as np
+import pytest
+
+import kv4_plain as kp
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import deterministic_integer_only_gb300 as pkg
+    pkg.lib()
+    return torch
+
+
+def cuda(torch, a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+class Dev:
+    """Pages, table and parameters on the device."""
+
+    def __init__(self, torch, pages, table, prm, n_q):
+        import deterministic_integer_only_gb300 as pkg
+        k, v = pages.packed()
+        self.k, self.v = cuda(torch, k), cuda(torch, v)
+        self.ck, self.cv = cuda(torch, pages.ck), cuda(torch, pages.cv)
+        self.table, self.prm = cuda(torch, table), cuda(torch, prm)
+        self.status = torch.zeros(8, dtype=torch.int32, device="cuda")
+        self.cache = pkg.KV4Cache(self.k, self.v, self.ck, self.cv, self.table, self.prm, n_q, status=self.status)
+
+    def holds(self, pages):
+        k, v = pages.packed()
+        assert np.array_equal(self.k.cpu().numpy(), k) and np.array_equal(self.v.cpu().numpy(), v)
+        assert np.array_equal(self.ck.cpu().numpy(), pages.ck) and np.array_equal(self.cv.cpu().numpy(), pages.cv)
+
+
+def ragged(spec):
+    """(seq, pos) of runs (sequence, first position, tokens)."""
+    seq = np.concatenate([np.full(n, s) for s, _, n in spec]).astype(np.int32)
+    pos = np.concatenate([np.arange(p, p + n) for _, p, n in spec]).astype(np.int32)
+    return seq, pos
+
+
+def tables(rot, max_pos, stretch=1.0):
+    a = np.arange(max_pos)[:, None] / stretch * 1e4 ** (-2.0 * np.arange(rot // 2) / max(rot, 1))[None]
+    return np.rint(np.cos(a) * 16384).astype(np.int16), np.rint(np.sin(a) * 16384).astype(np.int16)
+
+
+def run_append(torch, pages, dev, prm, n_q, rot, inter, norm, qkv, seq, pos, max_pos, pad=0, tab=None, eps=17):
+    """The GPU's outputs and the plain form's, after checking them and the pages."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(5)
+    n_kv, d, T = pages.n_kv, pages.d, len(pos)
+    cos, sin = tables(rot, max_pos)
+    gq, gk = (rng.integers(-(1 << 13), 1 << 13, d).astype(np.int16) for _ in range(2)) if norm else (None, None)
+    want = kp.append(pages, tab, prm, n_q, cos, sin, inter, (gq, gk), eps if norm else 0, qkv, seq, pos)
+    gam = dict(q_gamma=cuda(torch, gq), k_gamma=cuda(torch, gk), eps=eps) if norm else {}
+    r = pkg.RopeNorm(cuda(torch, cos), cuda(torch, sin), interleaved=inter, **gam) if rot else \
+        pkg.RopeNorm(None, None, max_pos=max_pos, **gam)
+    width = qkv.shape[1]
+    buf = torch.full((T, width + pad), 123456789, dtype=torch.int32, device="cuda")
+    buf[:, :width] = cuda(torch, qkv)
+    outs = [torch.full((T + 2,) + s, 99, dtype=dt, device="cuda") for s, dt in
+            (((n_q, d), torch.int8), ((n_q,), torch.int32), ((n_q,), torch.int32), ((n_kv, d), torch.int16), ((n_kv, d), torch.int16))]
+    pkg.detint_kv4_append(dev.cache, r, buf[:, :width], cuda(torch, seq), cuda(torch, pos), q8=outs[0], mq=outs[1], kq=outs[2],
+                          k_val=outs[3], v_val=outs[4])
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        o = o.cpu().numpy()
+        assert np.array_equal(o[:T], w)
+        assert (o[T:] == 99).all()                      # rows behind the last token are left as they were
+    dev.holds(pages)
+    return want
+
+
+APPENDS = [
+    # n_q, n_kv, d, rot, interleaved, norm, runs (sequence, first position, tokens)
+    (4, 2, 64, 64, False, True, [(0, 0, 1)]),
+    (1, 1, 128, 128, False, False, [(0, 63, 1), (1, 64, 1)]),
+    (3, 1, 64, 32, True, False, [(1, 5, 7), (0, 62, 5)]),
+    (6, 2, 128, 64, True, True, [(0, 3, 66), (1, 0, 1), (2, 127, 2)]),
+    (8, 8, 64, 16, False, True, [(0, 60, 9), (2, 0, 130)]),
+    (5, 1, 128, 0, False, False, [(0, 1, 40)]),
+    (10, 2, 64, 8, True, True, [(0, 0, 3), (1, 7, 2), (2, 120, 17)]),
+    (7, 7, 64, 48, False, False, [(0, 9, 33)]),
+]
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,rot,inter,norm,runs", APPENDS)
+def test_append(torch, n_q, n_kv, d, rot, inter, norm, runs):
+    rng = np.random.default_rng(n_q * d + rot)
+    lens = [max([p + n for s, p, n in runs if s == i], default=1) for i in range(3)]
+    tab = kp.table(lens, 4, 12, rng)
+    prm = kp.params(n_kv, d, rng, inter)
+    pages = kp.Pages(12, n_kv, d, rng)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    seq, pos = ragged(runs)
+    qkv = np.rint(rng.normal(0, 4096, (len(pos), (n_q + 2 * n_kv) * d))).astype(np.int32)
+    qkv[:, ::37] *= 7
+    run_append(torch, pages, dev, prm, n_q, rot, inter, norm, qkv, seq, pos, 200, pad=4 * (n_q % 3), tab=tab)
+    assert not dev.status.any()
+
+
+@pytest.mark.parametrize("d,norm,inter", [(64, True, False), (128, False, True), (128, True, False), (64, False, False)])
+def test_append_chunks_of_rows(torch, d, norm, inter):
+    """Enough tokens that a CTA takes whole chunks of rows, with odd run ends."""
+    rng = np.random.default_rng(d + norm)
+    n_q, n_kv = 2, 1
+    runs = [(0, 5, 1003), (1, 0, 1), (2, 64, 1130), (3, 1, 63), (1, 1, 1200)]
+    lens = [1008, 1201, 1194, 64]
+    tab = kp.table(lens, 19, 60, rng)
+    prm = kp.params(n_kv, d, rng, inter)
+    pages = kp.Pages(60, n_kv, d, rng)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    seq, pos = ragged(runs)
+    pos = np.concatenate([pos, [-1, -1, -5]]).astype(np.int32)     # padding at the end
+    seq = np.concatenate([seq, [0, 9, -1]]).astype(np.int32)
+    qkv = np.rint(rng.normal(0, 4096, (len(pos), (n_q + 2 * n_kv) * d))).astype(np.int32)
+    run_append(torch, pages, dev, prm, n_q, d // 2, inter, norm, qkv, seq, pos, 1300, tab=tab)
+    assert not dev.status.any()
+
+
+@pytest.mark.parametrize("norm", [True, False])
+def test_append_extreme_rows(torch, norm):
+    """Zero rows, single spikes, the largest magnitudes, every exponent."""
+    rng = np.random.default_rng(3)
+    n_q, n_kv, d = 4, 2, 128
+    pages = kp.Pages(4, n_kv, d, rng)
+    tab = kp.table([64], 1, 4, rng)
+    prm = kp.params(n_kv, d, rng)
+    width = (n_q + 2 * n_kv) * d
+    rows = [np.zeros(width), np.eye(width)[5], np.eye(width)[5] * -(2 ** 31 - 1), np.full(width, 2 ** 31 - 1), np.full(width, -(2 ** 31 - 1)),
+            np.tile([2 ** 31 - 1, -(2 ** 31 - 1)], width // 2), np.full(width, 1), np.full(width, -1)]
+    rows += [np.rint(rng.normal(0, 2.0 ** b, width)).clip(-(2 ** 31 - 1), 2 ** 31 - 1) for b in range(0, 31)]
+    rows += [np.full(width, 2 ** 29 - 1), np.full(width, 2 ** 29), np.full(width, -2 ** 29), np.full(width, 2 ** 24), np.full(width, 2 ** 24 - 1)]
+    qkv = np.array(rows).astype(np.int32)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    seq, pos = ragged([(0, 2, len(qkv))])
+    run_append(torch, pages, dev, prm, n_q, 128, False, norm, qkv, seq, pos, 64, tab=tab, eps=32767)
+
+
+def test_append_leaves_out_padding_and_bad_places(torch):
+    rng = np.random.default_rng(8)
+    n_q, n_kv, d = 4, 2, 64
+    pages = kp.Pages(6, n_kv, d, rng)
+    tab = kp.table([128, 70], 2, 6, rng)
+    tab[1, 1] = 6                                       # outside the pool
+    prm = kp.params(n_kv, d, rng)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    # padding, a sequence and a position outside the table, past the rotation rows, a bad page
+    seq = np.array([0, -1, 2, 0, 0, 1, 1, 0], np.int32)
+    pos = np.array([-1, 3, 3, 130, 128, 64, 10, 127], np.int32)
+    qkv = np.rint(rng.normal(0, 4096, (8, 8 * d))).astype(np.int32)
+    run_append(torch, pages, dev, prm, n_q, d, False, False, qkv, seq, pos, 130, tab=tab)
+    assert dev.status.cpu().tolist() == [0, 1, 0, 0, 0, 0, 0, 0]
+
+
+def run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, max_len, window, which, rows=None, want=None, pad=0):
+    import deterministic_integer_only_gb300 as pkg
+    T, width = len(pos), n_q * pages.d
+    if want is None:
+        want = kp.attention(pages, tab, prm, n_q, *q, seq, pos, window, max_len, rows)
+    buf = torch.full((T + 2, width + pad), -77, dtype=torch.int32, device="cuda")
+    out = buf[:T, :width] if pad else buf[:T]
+    args = [cuda(torch, a) for a in q] + [cuda(torch, seq), cuda(torch, pos)]
+    fn = pkg.detint_kv4_decode if which == "decode" else pkg.detint_kv4_prefill
+    fn(dev.cache, *args, max_len, window=window, out=out)
+    torch.cuda.synchronize()
+    got = buf.cpu().numpy()
+    assert (got[T:] == -77).all() and (got[:, width:] == -77).all()
+    got = got[:T, :width]
+    if rows is not None:
+        got_r, want = got[rows], want[rows]
+    else:
+        got_r = got
+    assert np.array_equal(got_r, want), np.argwhere(got_r != want)[:4]
+    return got
+
+
+HEADS = [(1, 1, 64), (2, 1, 128), (3, 1, 64), (8, 2, 128), (5, 1, 128), (16, 2, 64), (12, 1, 64), (4, 4, 128), (10, 5, 64)]
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("n_q,n_kv,d", HEADS)
+def test_attention_of_ragged_tokens(torch, which, n_q, n_kv, d):
+    """Every head layout, lengths around page ends, several tokens of a sequence,
+    padding and empty rows among them."""
+    rng = np.random.default_rng(n_q * 7 + d)
+    lens = [1, 2, 63, 64, 65, 128, 200, 333]
+    tab = kp.table(lens, 7, 24, rng)
+    pages = kp.Pages(24, n_kv, d, rng)
+    prm = kp.params(n_kv, d, rng)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    seq = np.concatenate([np.arange(8), [7, 7, 3, 0, 6, 6]]).astype(np.int32)
+    pos = np.concatenate([np.array(lens) - 1, [0, 300, 5, -1, -9, 199]]).astype(np.int32)
+    q = kp.queries(len(pos), n_q, d, rng)
+    for window in (0, 1, 7, 64, 130):
+        run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 400, window, which, pad=2 * (window % 3))
+    assert not dev.status.any()
+
+
+@pytest.mark.parametrize("n_q,n_kv,d", [(4, 2, 64), (2, 1, 128), (6, 1, 128), (16, 1, 64)])
+def test_prefill_blocks(torch, n_q, n_kv, d):
+    """Runs of one sequence that start and end inside a block of query rows."""
+    rng = np.random.default_rng(n_q + d)
+    runs = [(0, 0, 70), (1, 17, 1), (2, 60, 33), (1, 100, 90), (3, 0, 5), (0, 70, 3)]
+    lens = [73, 190, 93, 5]
+    tab = kp.table(lens, 3, 10, rng)
+    pages = kp.Pages(10, n_kv, d, rng)
+    prm = kp.params(n_kv, d, rng)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    seq, pos = ragged(runs)
+    q = kp.queries(len(pos), n_q, d, rng)
+    for window in (0, 3, 50):
+        a = run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 192, window, "prefill")
+        run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 192, window, "decode", want=a)
+    # any order of the same tokens gives the same rows
+    o = rng.permutation(len(pos))
+    run_attention(torch, dev, pages, prm, tab, n_q, [x[o] for x in q], seq[o], pos[o], 192, 0, "prefill",
+                  want=run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 192, 0, "prefill")[o])
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+def test_attention_extremes(torch, which):
+    """The largest scores of both signs, all keys alike, underflow of all but
+    one key, zero queries, shifts at their ends."""
+    rng = np.random.default_rng(2)
+    n_q, n_kv, d = 8, 1, 128
+    pages = kp.Pages(4, n_kv, d, rng)
+    tab = kp.table([250], 4, 4, rng)
+    pages.k[tab[0, 0], 0, :20], pages.ck[tab[0, 0], 0, :20] = 7, 255
+    pages.k[tab[0, 1], 0, :20], pages.ck[tab[0, 1], 0, :20] = -7, 255
+    pages.v[tab[0, 2], 0], pages.cv[tab[0, 2], 0] = 7, 255
+    prm = kp.params(n_kv, d, rng)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    pos = np.array([249, 249, 100, 63, 0, 249, 20, 249, 249], np.int32)
+    seq = np.zeros(len(pos), np.int32)
+    q8, mq, kq = kp.queries(len(pos), n_q, d, rng)
+    q8[0], q8[1] = 127, -127
+    q8[2], mq[2], kq[2] = 0, 0, 0
+    kq[3], kq[4] = -40, 90                              # shift clamped to 0; everything rounds to nothing
+    mq[5], kq[6] = 1 << 15, 5
+    kq[7], kq[8] = 14, 10 - prm[0, 7] + 2               # far below the maximum; a shift of 2
+    run_attention(torch, dev, pages, prm, tab, n_q, (q8, mq, kq), seq, pos, 250, 0, which)
+    # output scales that saturate 32 bits, and mantissas at their ends
+    prm[0, 4:8] = [1 << 15, 0, 1 << 15, 1]
+    dev = Dev(torch, pages, tab, prm, n_q)
+    run_attention(torch, dev, pages, prm, tab, n_q, (q8, mq, kq), seq, pos, 250, 0, which)
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+def test_bad_pages_and_places_are_masked_and_recorded(torch, which):
+    rng = np.random.default_rng(6)
+    n_q, n_kv, d = 4, 2, 64
+    pages = kp.Pages(8, n_kv, d, rng)
+    tab = kp.table([200, 130, 64], 4, 8, rng)
+    tab[0, 1], tab[1, 0], tab[1, 1], tab[1, 2] = -1, 8, -5, 1 << 30      # one page missing; every page missing
+    prm = kp.params(n_kv, d, rng)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    # the last four: sequences and positions outside the table, and past max_len
+    seq = np.array([0, 0, 1, 2, 3, -1, 2, 0], np.int32)
+    pos = np.array([199, 66, 129, 63, 10, 10, 256, 220], np.int32)
+    q = kp.queries(len(pos), n_q, d, rng)
+    run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 210, 0, which)
+    assert dev.status.cpu().tolist() == [0, 1, 0, 0, 0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,T,hi", [(8, 8, 128, 24, 2300), (32, 4, 64, 40, 1900), (16, 2, 128, 64, 2500), (24, 8, 64, 16, 2100)])
+def test_decode_in_two_launches(torch, n_q, n_kv, d, T, hi):
+    """Batches whose decode takes the two-launch path: against the plain form on
+    some rows and against the block form, bit for bit, on all; twice on one
+    workspace, whose first contents do not matter."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(T)
+    lens = [1 + (hi - 1) * ((i * 7) % T) // (T - 1) for i in range(T)]
+    nb = sum(-(-n // 64) for n in lens)
+    tab = kp.table(lens, -(-hi // 64), nb, rng)
+    pages = kp.Pages(nb, n_kv, d, rng)
+    prm = kp.params(n_kv, d, rng)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    need = pkg.detint_kv4_workspace(dev.cache, T, hi)
+    assert need > 0
+    seq, pos = np.arange(T, dtype=np.int32), np.array(lens, np.int32) - 1
+    pos[3] = -1
+    q = kp.queries(T, n_q, d, rng)
+    rows = [0, 1, 2, 3, T - 1]
+    for window in (0, 700):
+        got = run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, hi, window, "prefill", rows=rows)
+        run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, hi, window, "decode", want=got)
+        ws = torch.full((need,), 0xA5, dtype=torch.uint8, device="cuda")
+        dq = [cuda(torch, a) for a in q] + [cuda(torch, seq), cuda(torch, pos)]
+        for _ in range(2):
+            o = pkg.detint_kv4_decode(dev.cache, *dq, hi, window=window, workspace=ws)
+            assert np.array_equal(o.cpu().numpy(), got)
+    with pytest.raises(pkg.DetintError) as e:
+        pkg.detint_kv4_decode(dev.cache, *dq, hi, workspace=ws[:need - 16])
+    assert e.value.code == 1
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+def test_longest_context(torch, which):
+    """524288 keys: sums past 32 bits, every page index used."""
+    rng = np.random.default_rng(4)
+    n_q, n_kv, d, n = 2, 1, 64, 1 << 19
+    pages = kp.Pages(n // 64, n_kv, d, rng)
+    pages.cv[:] = 255
+    tab = kp.table([n], n // 64, n // 64, rng)
+    prm = kp.params(n_kv, d, rng)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    q8, mq, kq = kp.queries(3, n_q, d, rng)
+    q8[0], mq[0], kq[0] = 0, 0, 0                       # all weights alike: the largest sums there are
+    pos = np.array([n - 1, n - 1, n - 64], np.int32)
+    run_attention(torch, dev, pages, prm, tab, n_q, (q8, mq, kq), np.zeros(3, np.int32), pos, n, 0, which)
+
+
+def test_pages_past_32_bit_offsets(torch):
+    """A pool of more than 4 GB for K and for V: pages at its far end are
+    appended to and read at the right place."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(9)
+    n_q, n_kv, d = 4, 2, 128
+    nb = (1 << 32) // (n_kv * 64 * d // 2) + 70
+    shape = (nb, n_kv, 64, d // 2)
+    k, v = (torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones((nb, n_kv, 64), dtype=torch.uint8, device="cuda") for _ in range(2))
+    small = kp.Pages(3, n_kv, d, rng)
+    far = np.array([nb - 1, nb - 68, 1], np.int32)
+    pk, pv = small.packed()
+    at = cuda(torch, far.astype(np.int64))
+    k[at], v[at], ks[at], vs[at] = cuda(torch, pk), cuda(torch, pv), cuda(torch, small.ck), cuda(torch, small.cv)
+    tab = np.array([[0, 1, 2]], np.int32)
+    prm = kp.params(n_kv, d, rng)
+    dt = cuda(torch, far[tab])
+    cache = pkg.KV4Cache(k, v, ks, vs, dt, cuda(torch, prm), n_q)
+    seq, pos = ragged([(0, 60, 9), (0, 130, 2)])
+    cos, sin = tables(d, 200)
+    qkv = np.rint(rng.normal(0, 4096, (len(pos), 8 * d))).astype(np.int32)
+    want = kp.append(small, tab, prm, n_q, cos, sin, False, (None, None), 0, qkv, seq, pos)
+    q = pkg.detint_kv4_append(cache, pkg.RopeNorm(cuda(torch, cos), cuda(torch, sin)), cuda(torch, qkv), cuda(torch, seq), cuda(torch, pos))
+    for a, b in zip(q, want):
+        assert np.array_equal(a.cpu().numpy(), b)
+    pk, pv = small.packed()
+    for got, exp in ((k, pk), (v, pv), (ks, small.ck), (vs, small.cv)):
+        assert np.array_equal(got[at].cpu().numpy(), exp)
+    want = kp.attention(small, tab, prm, n_q, *want[:3], seq, pos)
+    for fn in (pkg.detint_kv4_decode, pkg.detint_kv4_prefill):
+        assert np.array_equal(fn(cache, *q, cuda(torch, seq), cuda(torch, pos), 192).cpu().numpy(), want)
+
+
+def _step_setup(torch, rng, n_q, n_kv, d, n_seq, max_len):
+    nb = n_seq * -(-max_len // 64)
+    tab = kp.table([max_len] * n_seq, -(-max_len // 64), nb, rng)
+    pages = kp.Pages(nb, n_kv, d, rng)
+    prm = kp.params(n_kv, d, rng)
+    return pages, tab, prm, Dev(torch, pages, tab, prm, n_q)
+
+
+def test_append_then_attention_token_by_token_equals_one_prefill(torch):
+    """The operators as a model uses them: a prompt appended and attended to in
+    one call each, or a token at a time, leaves the same pages and rows."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(12)
+    n_q, n_kv, d, n = 4, 2, 64, 75
+    pages, tab, prm, a = _step_setup(torch, rng, n_q, n_kv, d, 2, 128)
+    b = Dev(torch, pages, tab, prm, n_q)
+    cos, sin = tables(d, 128)
+    r = pkg.RopeNorm(cuda(torch, cos), cuda(torch, sin))
+    qkv = cuda(torch, np.rint(rng.normal(0, 4096, (2 * n, 8 * d))).astype(np.int32))
+    seq, pos = ragged([(0, 0, n), (1, 0, n)])
+    ds, dp = cuda(torch, seq), cuda(torch, pos)
+    q = pkg.detint_kv4_append(a.cache, r, qkv, ds, dp)
+    whole = pkg.detint_kv4_prefill(a.cache, *q, ds, dp, n)
+    for t in range(n):
+        i = torch.tensor([t, n + t], device="cuda")
+        q1 = pkg.detint_kv4_append(b.cache, r, qkv[i], ds[i], dp[i])
+        step = pkg.detint_kv4_decode(b.cache, *q1, ds[i], dp[i], 128)
+        assert torch.equal(step, whole[i]), t
+    for x, y in ((a.k, b.k), (a.v, b.v), (a.ck, b.ck), (a.cv, b.cv)):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("T,hi", [(2, 300), (16, 4200)])
+def test_captured_step_is_replayed_with_new_positions(torch, T, hi):
+    """Append and decode in a CUDA graph (both decode forms): the replay reads
+    the positions that are in memory then."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(T)
+    n_q, n_kv, d = 8, 4, 64
+    pages, tab, prm, dev = _step_setup(torch, rng, n_q, n_kv, d, T, hi)
+    ref = Dev(torch, pages, tab, prm, n_q)
+    cos, sin = tables(d, hi)
+    r = pkg.RopeNorm(cuda(torch, cos), cuda(torch, sin), interleaved=True)
+    qkv = torch.zeros((T, 16 * d), dtype=torch.int32, device="cuda")
+    seq = torch.arange(T, dtype=torch.int32, device="cuda")
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    need = pkg.detint_kv4_workspace(dev.cache, T, hi)
+    assert (need > 0) == (T == 16)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    q8, out = torch.empty((T, n_q, d), dtype=torch.int8, device="cuda"), torch.empty((T, n_q * d), dtype=torch.int32, device="cuda")
+    mq, kq = (torch.empty((T, n_q), dtype=torch.int32, device="cuda") for _ in range(2))
+
+    def step():
+        pkg.detint_kv4_append(dev.cache, r, qkv, seq, pos, q8=q8, mq=mq, kq=kq)
+        pkg.detint_kv4_decode(dev.cache, q8, mq, kq, seq, pos, hi, out=out, workspace=ws)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for p in (0, 63, 64, 200, hi - 1):
+        x = cuda(torch, np.rint(rng.normal(0, 4096, (T, 16 * d))).astype(np.int32))
+        qkv.copy_(x)
+        pos.fill_(p)
+        pos[T - 1] = p // 2
+        g.replay()
+        q = pkg.detint_kv4_append(ref.cache, r, x, seq, pos)
+        assert torch.equal(out, pkg.detint_kv4_prefill(ref.cache, *q, seq, pos, hi)), p
+
+
+def test_two_streams_at_once(torch):
+    """The same cache read by calls on two streams, each with its own outputs
+    and workspace."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(21)
+    n_q, n_kv, d, T, hi = 16, 4, 128, 20, 4000
+    pages, tab, prm, dev = _step_setup(torch, rng, n_q, n_kv, d, T, hi)
+    qs = [[cuda(torch, a) for a in kp.queries(T, n_q, d, rng)] for _ in range(2)]
+    seq = torch.arange(T, dtype=torch.int32, device="cuda")
+    pos = cuda(torch, rng.integers(0, hi, T).astype(np.int32))
+    want = [pkg.detint_kv4_prefill(dev.cache, *q, seq, pos, hi) for q in qs]
+    assert pkg.detint_kv4_workspace(dev.cache, T, hi) > 0
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        got = [pkg.detint_kv4_decode(dev.cache, *q, seq, pos, hi, stream=s) for q, s in zip(qs, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_binding_refusals(torch):
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(1)
+    pages, tab, prm, dev = _step_setup(torch, rng, 4, 2, 64, 1, 64)
+    q8, mq, kq = (cuda(torch, a) for a in kp.queries(3, 4, 64, rng))
+    seq, pos = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    dec = pkg.detint_kv4_decode
+    for bad in ((q8.cpu(), mq, kq, seq, pos), (q8.int(), mq, kq, seq, pos), (q8, mq[:2], kq, seq, pos), (q8, mq, kq.long(), seq, pos),
+                (q8, mq, kq, seq.cpu(), pos), (q8, mq, kq, seq[:1], pos), (q8[:, :, ::2], mq, kq, seq, pos)):
+        with pytest.raises(ValueError):
+            dec(dev.cache, *bad, 64)
+    with pytest.raises(ValueError):
+        dec(dev.cache, q8, mq, kq, seq, pos, 64, out=torch.empty((3, 200), dtype=torch.int32, device="cuda"))
+    for kw in (dict(max_len=0), dict(max_len=(1 << 19) + 1), dict(max_len=64, window=-1)):
+        with pytest.raises(pkg.DetintError):
+            dec(dev.cache, q8, mq, kq, seq, pos, **kw)
+    cos, sin = (cuda(torch, a) for a in tables(64, 64))
+    qkv = torch.zeros((3, 8 * 64), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        pkg.detint_kv4_append(dev.cache, pkg.RopeNorm(cos, sin), qkv.long(), seq, pos)
+    with pytest.raises(ValueError):
+        pkg.detint_kv4_append(dev.cache, pkg.RopeNorm(cos, sin), qkv[:, :500], seq, pos)
+    with pytest.raises(ValueError):                     # gammas of another head width
+        g = torch.ones(128, dtype=torch.int16, device="cuda")
+        pkg.detint_kv4_append(dev.cache, pkg.RopeNorm(cos, sin, q_gamma=g, k_gamma=g), qkv, seq, pos)
+    with pytest.raises(pkg.DetintError):                # one gamma
+        pkg.detint_kv4_append(dev.cache, pkg.RopeNorm(cos, sin, q_gamma=g[:64].contiguous()), qkv, seq, pos)
