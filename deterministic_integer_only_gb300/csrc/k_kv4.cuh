@@ -1338,13 +1338,17 @@ __global__ void __launch_bounds__(128, GT == 8 ? 2 : 4) k_kv4_pv(Kv4Args a, Kv4A
 // A CTA takes 64 query rows (64 / Gp consecutive tokens times the G q heads of
 // one kv head, Gp the power of two >= G) and sweeps its keys twice, as the
 // maximum has to be known first: sweep 1 scores and maxima, sweep 2 scores,
-// probabilities and P V. A warp owns 16 rows, all 64 keys of a page and all
-// channels. Column n of score tile j is key 16 (n / 2) + 2 j + (n & 1), so
-// that the scores a lane holds are the keys of its own P V operand: the
-// probabilities never leave the registers. The tokens of a block may belong
-// to several sequences: each run of one sequence is swept by itself with the
-// other rows masked.
-constexpr int KV4_PT = 128;      // prefill threads
+// probabilities and P V. Two warps share 16 rows: each scores half of a page's
+// keys and sums half of the channels. Column n of score tile j is key
+// 16 (n / 2) + 2 j + (n & 1), so that the scores a lane holds are the keys of
+// its own P V operand for one 32-key step (j / 4, the warp's half); the other
+// step's operand comes from the partner through shared memory. (One warp per
+// 16 rows with all keys and channels needs no exchange, but its accumulators
+// leave 8 warps on an SM: 4 x 4096 tokens of 16 + 8 heads of 128 channels took
+// 4336 us, and 4716 us with sweep 1 on the dp4a pipe.) The tokens of a block may
+// belong to several sequences: each run of one sequence is swept by itself
+// with the other rows masked.
+constexpr int KV4_PT = 256;      // prefill threads
 constexpr int KV4_PROWS = 64;
 constexpr int KV4_PST = 4;       // page stages
 
@@ -1352,18 +1356,21 @@ template <int D>
 struct Kv4Pf {
     static constexpr int PG = KV_BLK * D / 2;            // bytes of a K or V page
     static constexpr int STAGE = 2 * PG + 2 * KV_BLK;    // K, V, key scales, value scales
-    static constexpr int SMEM = KV4_PST * STAGE;
+    static constexpr int O_W = KV4_PST * STAGE;          // probability operands: 2 buffers x 8 warps x 1 KB
+    static constexpr int SMEM = O_W + 2 * 8 * 1024;
 };
 
 template <int D>
 __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p) {
     using C = Kv4Pf<D>;
-    constexpr int KS = D / 32, NC = D / 16;
+    constexpr int KS = D / 32, NC = D / 32;              // 32-channel steps; 16-channel groups of a warp's half
     extern __shared__ __align__(16) unsigned char kv4_raw[];
     __shared__ unsigned long long full[KV4_PST];
     __shared__ int page_ok[KV4_PST];
-    __shared__ int r_pos[KV4_PROWS];
+    __shared__ int r_pos[KV4_PROWS], r_top[2][KV4_PROWS];
+    __shared__ i64 r_sum[2][2][KV4_PROWS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rg = warp >> 1, hf = warp & 1;             // 16-row group; half of the keys and channels
     const int gid = lane >> 2, tig = lane & 3;
     const int g = blockIdx.x;
     const int lgBQ = 6 - p.lgGp, BQ = 1 << lgBQ;
@@ -1375,7 +1382,7 @@ __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // row r: token t0 + (r >> lgGp), q head r & (Gp - 1)
-    const int rA = warp * 16 + gid, rB = rA + 8;
+    const int rA = rg * 16 + gid, rB = rA + 8;
     if (tid < KV4_PROWS) {
         const int i = tid >> p.lgGp, hh = tid & ((1 << p.lgGp) - 1);
         int pos = -1;
@@ -1428,8 +1435,9 @@ __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p)
 #pragma unroll
         for (int e = 0; e < 4; ++e) aL[n][e] = aH[n][e] = 0;
     i64 sumE[2] = {0, 0}, sumW[2] = {0, 0};
+    const int k_lane = 16 * tig + 8 * hf;                // first of this lane's eight keys of a page
 
-    int it = 0;                                          // pages consumed so far (ring position)
+    int it = 0, wbuf = 0;                                // pages consumed so far (ring position); operand buffer
     for (int s0 = 0; s0 < nt;) {
         // a run of one sequence: tokens [s0, s1)
         const int seq = p.tok_seq[t0 + s0];
@@ -1483,12 +1491,14 @@ __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p)
             const int kb = (p0 + (i >= np ? i - np : i)) << 6;
             if (page_ok[st] && kb <= wmax && kb + 63 >= wmin) {
                 const unsigned char* base = kv4_raw + st * C::STAGE;
-                int S[8][4];
+                const bool clear = kb >= cmin && kb + 63 <= cmax;      // no key of the page is masked
+                const uint2 ckv = *(const uint2*)(base + 2 * C::PG + k_lane);
+                int S[4][4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     S[j][0] = S[j][1] = qo[0];
                     S[j][2] = S[j][3] = qo[1];
-                    const unsigned char* kr = base + (16 * (gid >> 1) + 2 * j + (gid & 1)) * (D / 2) + tig * (D / 8);
+                    const unsigned char* kr = base + (16 * (gid >> 1) + 8 * hf + 2 * j + (gid & 1)) * (D / 2) + tig * (D / 8);
                     int w[KS];
                     if (D == 128) {
                         const int4 v = *(const int4*)kr;
@@ -1501,83 +1511,80 @@ __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p)
                     for (int s = 0; s < KS; ++s)
                         mma_s8u8(S[j], qf[s][0], qf[s][1], qf[s][2], qf[s][3], kv4_lo(w[s]), kv4_hi(w[s]));
                 }
-                const uint4 ckv = *(const uint4*)(base + 2 * C::PG + 16 * tig);
-                const unsigned ck[4] = {ckv.x, ckv.y, ckv.z, ckv.w};
-                const bool clear = kb >= cmin && kb + 63 <= cmax;      // no key of the page is masked
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int c = (int)(ck[j >> 1] >> (8 * ((2 * j + e) & 3))) & 255;
-                        const int key = kb + 16 * tig + 2 * j + e;
-                        const bool inA = clear || (key <= hiA && key >= loA), inB = clear || (key <= hiB && key >= loB);
+                        const int c = (int)((j < 2 ? ckv.x : ckv.y) >> (8 * ((2 * j + e) & 3))) & 255;
                         S[j][e] *= c;
                         S[j][2 + e] *= c;
-                        if (i < np) {
-                            T[0] = inA ? max(T[0], S[j][e]) : T[0];
-                            T[1] = inB ? max(T[1], S[j][2 + e]) : T[1];
-                        }
                     }
-                }
-                if (i >= np) {
-                    const uint4 cvv = *(const uint4*)(base + 2 * C::PG + KV_BLK + 16 * tig);
-                    const unsigned cv[4] = {cvv.x, cvv.y, cvv.z, cvv.w};
-                    int wl[2][4], wh[2][4];              // [row][4 keys]
+                if (i < np) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = kb + k_lane + 2 * j + e;
+                            if (clear || (key <= hiA && key >= loA)) T[0] = max(T[0], S[j][e]);
+                            if (clear || (key <= hiB && key >= loB)) T[1] = max(T[1], S[j][2 + e]);
+                        }
+                } else {
+                    const uint2 cv = *(const uint2*)(base + 2 * C::PG + KV_BLK + k_lane);
+                    uint32_t wl[2][2], wh[2][2];         // [row][4 keys]
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        int te = 0, tw = 0;
+                        const int hi = x ? hiB : hiA, lo = x ? loB : loA;
+                        unsigned te = 0, tw = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            int w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int s = S[2 * k + (e >> 1)][2 * x + (e & 1)];
-                                int E = kv4_E(rw[x], s, T[x]);
-                                const int key = kb + 16 * tig + 4 * k + e;
-                                if (!clear && (key > (x ? hiB : hiA) || key < (x ? loB : loA))) E = 0;
-                                w[e] = kv4_W(E, (int)(cv[k] >> (8 * e)) & 255);
-                                te += E;
-                                tw += w[e];
-                            }
-                            const unsigned wa = (unsigned)w[0] | ((unsigned)w[1] << 16), wb = (unsigned)w[2] | ((unsigned)w[3] << 16);
-                            wl[x][k] = (int)__byte_perm(wa, wb, 0x6420);
-                            wh[x][k] = (int)__byte_perm(wa, wb, 0x7531);
-                        }
+                        for (int k = 0; k < 2; ++k)
+                            kv4_probs(rw[x], T[x], make_int4(S[2 * k][2 * x], S[2 * k][2 * x + 1], S[2 * k + 1][2 * x], S[2 * k + 1][2 * x + 1]),
+                                      k ? cv.y : cv.x, clear, lo - (kb + k_lane + 4 * k), hi + 1 - (kb + k_lane + 4 * k),
+                                      &wl[x][k], &wh[x][k], &te, &tw);
                         sumE[x] += te;
                         sumW[x] += tw;
                     }
+                    // this warp's step of the operand, and the partner's
+                    int4* wx = (int4*)(kv4_raw + C::O_W + wbuf * 8192);
+                    wx[(2 * warp) * 32 + lane] = make_int4((int)wl[0][0], (int)wl[1][0], (int)wl[0][1], (int)wl[1][1]);
+                    wx[(2 * warp + 1) * 32 + lane] = make_int4((int)wh[0][0], (int)wh[1][0], (int)wh[0][1], (int)wh[1][1]);
+                    bar_named(1 + rg, 64);
+                    const int4 l0 = wx[(4 * rg) * 32 + lane], u0 = wx[(4 * rg + 1) * 32 + lane];
+                    const int4 l1 = wx[(4 * rg + 2) * 32 + lane], u1 = wx[(4 * rg + 3) * 32 + lane];
+                    wbuf ^= 1;
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        const int4 v = *(const int4*)(base + C::PG + c * 512 + lane * 16);
-                        const int l0 = kv4_lo(v.x), u0 = kv4_hi(v.x), l1 = kv4_lo(v.y), u1 = kv4_hi(v.y);
-                        const int l2 = kv4_lo(v.z), u2 = kv4_hi(v.z), l3 = kv4_lo(v.w), u3 = kv4_hi(v.w);
-                        mma_u8u8(aL[2 * c], wl[0][0], wl[1][0], wl[0][1], wl[1][1], l0, u0);
-                        mma_u8u8(aH[2 * c], wh[0][0], wh[1][0], wh[0][1], wh[1][1], l0, u0);
-                        mma_u8u8(aL[2 * c + 1], wl[0][0], wl[1][0], wl[0][1], wl[1][1], l2, u2);
-                        mma_u8u8(aH[2 * c + 1], wh[0][0], wh[1][0], wh[0][1], wh[1][1], l2, u2);
-                        mma_u8u8(aL[2 * c], wl[0][2], wl[1][2], wl[0][3], wl[1][3], l1, u1);
-                        mma_u8u8(aH[2 * c], wh[0][2], wh[1][2], wh[0][3], wh[1][3], l1, u1);
-                        mma_u8u8(aL[2 * c + 1], wl[0][2], wl[1][2], wl[0][3], wl[1][3], l3, u3);
-                        mma_u8u8(aH[2 * c + 1], wh[0][2], wh[1][2], wh[0][3], wh[1][3], l3, u3);
+                        const int4 v = *(const int4*)(base + C::PG + (hf * NC + c) * 512 + lane * 16);
+                        const int a0 = kv4_lo(v.x), b0 = kv4_hi(v.x), a1 = kv4_lo(v.y), b1 = kv4_hi(v.y);
+                        const int a2 = kv4_lo(v.z), b2 = kv4_hi(v.z), a3 = kv4_lo(v.w), b3 = kv4_hi(v.w);
+                        mma_u8u8(aL[2 * c], l0.x, l0.y, l0.z, l0.w, a0, b0);
+                        mma_u8u8(aH[2 * c], u0.x, u0.y, u0.z, u0.w, a0, b0);
+                        mma_u8u8(aL[2 * c + 1], l0.x, l0.y, l0.z, l0.w, a2, b2);
+                        mma_u8u8(aH[2 * c + 1], u0.x, u0.y, u0.z, u0.w, a2, b2);
+                        mma_u8u8(aL[2 * c], l1.x, l1.y, l1.z, l1.w, a1, b1);
+                        mma_u8u8(aH[2 * c], u1.x, u1.y, u1.z, u1.w, a1, b1);
+                        mma_u8u8(aL[2 * c + 1], l1.x, l1.y, l1.z, l1.w, a3, b3);
+                        mma_u8u8(aH[2 * c + 1], u1.x, u1.y, u1.z, u1.w, a3, b3);
                     }
                 }
             }
             if (i == np - 1) {
-                // the row maxima of this run are complete over the row's four lanes
+                // the row maxima of this run over the row's lanes and both halves
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     T[x] = max(T[x], __shfl_xor_sync(0xffffffffu, T[x], 1));
                     T[x] = max(T[x], __shfl_xor_sync(0xffffffffu, T[x], 2));
+                    if (tig == 0) r_top[hf][x ? rB : rA] = T[x];
                 }
+                bar_named(1 + rg, 64);
+                T[0] = max(T[0], r_top[hf ^ 1][rA]);
+                T[1] = max(T[1], r_top[hf ^ 1][rB]);
             }
             __syncthreads();                             // every warp is done with the stage
             if (tid == 0 && i + KV4_PST < 2 * np) issue(i + KV4_PST);
         }
         it += 2 * np;
     }
-    // ---- one deferred division per row
-    const i64 MV = kvp[4];
-    const int KVS = kvp[5];
+    // ---- the row sums over both halves, then one deferred division per row
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         i64 e = sumE[x], w = sumW[x];
@@ -1585,12 +1592,23 @@ __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p)
         w += __shfl_xor_sync(0xffffffffu, w, 1);
         e += __shfl_xor_sync(0xffffffffu, e, 2);
         w += __shfl_xor_sync(0xffffffffu, w, 2);
+        if (tig == 0) {
+            r_sum[hf][0][x ? rB : rA] = e;
+            r_sum[hf][1][x ? rB : rA] = w;
+        }
+    }
+    bar_named(1 + rg, 64);
+    const i64 MV = kvp[4];
+    const int KVS = kvp[5];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
         const int r = x ? rB : rA;
+        const i64 e = r_sum[0][0][r] + r_sum[1][0][r], w = r_sum[0][1][r] + r_sum[1][1][r];
         const int i = r >> p.lgGp, hh = r & ((1 << p.lgGp) - 1);
         if (i >= nt || hh >= p.G) continue;
         const int bl = bitlen_u64((u64)e);
         const i64 rs = e > 0 ? (i64)pow2_recip((u64)e, bl, 1, 23) : 0;
-        int32_t* orow = p.o + (size_t)(t0 + i) * p.o_stride + (size_t)(g * p.G + hh) * D + 2 * tig;
+        int32_t* orow = p.o + (size_t)(t0 + i) * p.o_stride + (size_t)(g * p.G + hh) * D + hf * (D / 2) + 2 * tig;
 #pragma unroll
         for (int n = 0; n < 2 * NC; ++n) {
             int2 out;
