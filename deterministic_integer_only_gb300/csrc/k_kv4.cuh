@@ -344,17 +344,25 @@ __device__ __forceinline__ void kv4_qk_chunk(const Kv4Args& a, const Kv4Append& 
                 if (__shfl_sync(mask, pos_l, base + 8 * b + i) >= 0) v[i] = __ldg((const int4*)r);
             }
             u64 ss[8];
+            int cl[8], least = 32;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                cl[i] = __clz(seg_max<LPH>(max4(y)));
+                least = min(least, cl[i]);
+                if (lane == i * LPR + b) cl_l = cl[i];
+            }
+            // rows below 2^24 (nearly all there are) only shift left
+            const bool small = __all_sync(0xffffffffu, least >= 8);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 int y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                const int cl = __clz(seg_max<LPH>(max4(y)));
                 ss[i] = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    y[j] = kv4_cut(y[j], cl);
+                    y[j] = small ? y[j] << ((cl[i] - 8) & 31) : kv4_cut(y[j], cl[i]);
                     ss[i] += (u64)((i64)y[j] * y[j]);
                 }
-                if (lane == i * LPR + b) cl_l = cl;
                 *(int4*)(st + (8 * b + i) * D) = make_int4(y[0], y[1], y[2], y[3]);
             }
             const u64 s = rows_sum<LPH>(ss);
@@ -434,9 +442,10 @@ __device__ __forceinline__ void kv4_qk_chunk(const Kv4Args& a, const Kv4Append& 
 // atomics does not matter).
 constexpr int KV4_APT = 128;     // append threads
 constexpr int KV4_VTILE = 64;    // most tokens in a tile
+constexpr int KV4_CH = 16;      // rows of a chunk (at most the lanes of a head)
 
 template <int LPH, bool NORM, bool CHUNK>
-__global__ void __launch_bounds__(KV4_APT) k_kv4_append(Kv4Args a, Kv4Append p) {
+__global__ void __launch_bounds__(KV4_APT, CHUNK ? 6 : 4) k_kv4_append(Kv4Args a, Kv4Append p) {
     constexpr int D = 4 * LPH, HPW = 32 / LPH, HPB = (KV4_APT / 32) * HPW;
     extern __shared__ __align__(16) unsigned char kv4_raw[];
     const int t0 = (int)blockIdx.x * p.tile, nt = min(p.tile, p.T - t0);
@@ -445,14 +454,15 @@ __global__ void __launch_bounds__(KV4_APT) k_kv4_append(Kv4Args a, Kv4Append p) 
         const int slot = (int)blockIdx.y * HPB + hd;
         const bool live = slot < a.nq + a.n_kv;
         if (CHUNK) {
-            for (int i = 0; i < nt; i += LPH)
-                kv4_qk_chunk<LPH, NORM>(a, p, t0 + i, min(LPH, nt - i), live ? slot : 0, live, (int*)kv4_raw + hd * (LPH * D));
+            for (int i = 0; i < nt; i += KV4_CH)
+                kv4_qk_chunk<LPH, NORM>(a, p, t0 + i, min(KV4_CH, nt - i), live ? slot : 0, live, (int*)kv4_raw + hd * (KV4_CH * D));
         } else {
             for (int i = 0; i < nt; ++i) kv4_qk_row<LPH, NORM>(a, p, t0 + i, live ? slot : 0, live);
         }
         return;
     }
     __shared__ int page[KV4_VTILE], offs[KV4_VTILE], code[KV4_VTILE], cinv[KV4_VTILE];
+    __shared__ unsigned lead_m[2];
     short4* xs = (short4*)kv4_raw;                           // [nt][LPH] cached integers before coding
     int* cw = (int*)(xs + p.tile * LPH);                     // [nt][LPH] four codes each
     const int g = (int)blockIdx.y - p.qk_blocks;
@@ -499,11 +509,20 @@ __global__ void __launch_bounds__(KV4_APT) k_kv4_append(Kv4Args a, Kv4Append p) 
                 page[i] < 0 ? make_short4(0, 0, 0, 0) : val4(q, c);
     }
     __syncthreads();
-    // words: a head's lanes take a run of tokens, each its four channels
-    for (int i = hd; i < nt; i += HPB) {
+    // words: a head's lanes take a run of tokens, each its four channels. A run
+    // starts where the word changes or the positions stop ascending.
+    if ((int)threadIdx.x < KV4_VTILE) {
+        const int i = threadIdx.x, blk = i < nt ? page[i] : -1, off = i < nt ? offs[i] : 0;
+        const bool lead = blk >= 0 && !(i > 0 && page[i - 1] == blk && (offs[i - 1] >> 3) == (off >> 3) && offs[i - 1] < off);
+        const unsigned m = __ballot_sync(0xffffffffu, lead);
+        if ((i & 31) == 0) lead_m[i >> 5] = m;
+    }
+    __syncthreads();
+    u64 todo = (u64)lead_m[0] | ((u64)lead_m[1] << 32);
+    for (int k = 0; todo; ++k, todo &= todo - 1) {
+        if ((k & (HPB - 1)) != hd) continue;
+        const int i = __ffsll((i64)todo) - 1;
         const int blk = page[i], off = offs[i];
-        // a run starts where the word changes or the positions stop ascending
-        if (blk < 0 || (i > 0 && page[i - 1] == blk && (offs[i - 1] >> 3) == (off >> 3) && offs[i - 1] < off)) continue;
         int w[8];                                            // codes of the word's keys
 #pragma unroll
         for (int k = 0; k < 8; ++k) w[k] = 0;
@@ -1335,8 +1354,8 @@ __global__ void __launch_bounds__(128, GT == 8 ? 2 : 4) k_kv4_pv(Kv4Args a, Kv4A
 }
 
 // -------------------------------------------- attention of token blocks
-// A CTA takes 64 query rows (64 / Gp consecutive tokens times the G q heads of
-// one kv head, Gp the power of two >= G) and sweeps its keys twice, as the
+// A CTA takes 32 (or 64) query rows (32 / Gp consecutive tokens times the G q
+// heads of one kv head, Gp the power of two >= G) and sweeps its keys twice, as the
 // maximum has to be known first: sweep 1 scores and maxima, sweep 2 scores,
 // probabilities and P V. Two warps share 16 rows: each scores half of a page's
 // keys and sums half of the channels. Column n of score tile j is key
@@ -1348,32 +1367,32 @@ __global__ void __launch_bounds__(128, GT == 8 ? 2 : 4) k_kv4_pv(Kv4Args a, Kv4A
 // 4336 us, and 4716 us with sweep 1 on the dp4a pipe.) The tokens of a block may
 // belong to several sequences: each run of one sequence is swept by itself
 // with the other rows masked.
-constexpr int KV4_PT = 256;      // prefill threads
-constexpr int KV4_PROWS = 64;
 constexpr int KV4_PST = 4;       // page stages
 
-template <int D>
+template <int D, int NW>
 struct Kv4Pf {
+    static constexpr int ROWS = 8 * NW;                  // query rows of a CTA of NW warps
     static constexpr int PG = KV_BLK * D / 2;            // bytes of a K or V page
     static constexpr int STAGE = 2 * PG + 2 * KV_BLK;    // K, V, key scales, value scales
-    static constexpr int O_W = KV4_PST * STAGE;          // probability operands: 2 buffers x 8 warps x 1 KB
-    static constexpr int SMEM = O_W + 2 * 8 * 1024;
+    static constexpr int O_W = KV4_PST * STAGE;          // probability operands: 2 buffers x 1 KB per warp
+    static constexpr int SMEM = O_W + 2 * NW * 1024;
 };
 
-template <int D>
-__global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p) {
-    using C = Kv4Pf<D>;
+template <int D, int NW>
+__global__ void __launch_bounds__(32 * NW, 16 / NW) k_kv4_prefill(Kv4Args a, Kv4Attn p) {
+    using C = Kv4Pf<D, NW>;
+    constexpr int ROWS = C::ROWS;
     constexpr int KS = D / 32, NC = D / 32;              // 32-channel steps; 16-channel groups of a warp's half
     extern __shared__ __align__(16) unsigned char kv4_raw[];
     __shared__ unsigned long long full[KV4_PST];
     __shared__ int page_ok[KV4_PST];
-    __shared__ int r_pos[KV4_PROWS], r_top[2][KV4_PROWS];
-    __shared__ i64 r_sum[2][2][KV4_PROWS];
+    __shared__ int r_pos[ROWS], r_top[2][ROWS];
+    __shared__ i64 r_sum[2][2][ROWS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rg = warp >> 1, hf = warp & 1;             // 16-row group; half of the keys and channels
     const int gid = lane >> 2, tig = lane & 3;
     const int g = blockIdx.x;
-    const int lgBQ = 6 - p.lgGp, BQ = 1 << lgBQ;
+    const int lgBQ = (NW == 8 ? 6 : 5) - p.lgGp, BQ = 1 << lgBQ;
     const int t0 = p.t0 + (int)(gridDim.y - 1 - blockIdx.y) * BQ;    // later tokens tend to have more keys
     const int nt = min(BQ, p.T - t0);
     const int32_t* kvp = a.params + (size_t)g * (8 + D);
@@ -1383,7 +1402,7 @@ __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p)
     }
     // row r: token t0 + (r >> lgGp), q head r & (Gp - 1)
     const int rA = rg * 16 + gid, rB = rA + 8;
-    if (tid < KV4_PROWS) {
+    if (tid < ROWS) {
         const int i = tid >> p.lgGp, hh = tid & ((1 << p.lgGp) - 1);
         int pos = -1;
         if (i < nt && hh < p.G) {
@@ -1434,7 +1453,7 @@ __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p)
     for (int n = 0; n < 2 * NC; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) aL[n][e] = aH[n][e] = 0;
-    i64 sumE[2] = {0, 0}, sumW[2] = {0, 0};
+    unsigned sumE[2] = {0, 0}, sumW[2] = {0, 0};         // an eighth of 2^19 keys: below 2^32
     const int k_lane = 16 * tig + 8 * hf;                // first of this lane's eight keys of a page
 
     int it = 0, wbuf = 0;                                // pages consumed so far (ring position); operand buffer
@@ -1534,17 +1553,14 @@ __global__ void __launch_bounds__(KV4_PT, 2) k_kv4_prefill(Kv4Args a, Kv4Attn p)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int hi = x ? hiB : hiA, lo = x ? loB : loA;
-                        unsigned te = 0, tw = 0;
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             kv4_probs(rw[x], T[x], make_int4(S[2 * k][2 * x], S[2 * k][2 * x + 1], S[2 * k + 1][2 * x], S[2 * k + 1][2 * x + 1]),
                                       k ? cv.y : cv.x, clear, lo - (kb + k_lane + 4 * k), hi + 1 - (kb + k_lane + 4 * k),
-                                      &wl[x][k], &wh[x][k], &te, &tw);
-                        sumE[x] += te;
-                        sumW[x] += tw;
+                                      &wl[x][k], &wh[x][k], &sumE[x], &sumW[x]);
                     }
                     // this warp's step of the operand, and the partner's
-                    int4* wx = (int4*)(kv4_raw + C::O_W + wbuf * 8192);
+                    int4* wx = (int4*)(kv4_raw + C::O_W + wbuf * (NW * 1024));
                     wx[(2 * warp) * 32 + lane] = make_int4((int)wl[0][0], (int)wl[1][0], (int)wl[0][1], (int)wl[1][1]);
                     wx[(2 * warp + 1) * 32 + lane] = make_int4((int)wh[0][0], (int)wh[1][0], (int)wh[0][1], (int)wh[1][1]);
                     bar_named(1 + rg, 64);

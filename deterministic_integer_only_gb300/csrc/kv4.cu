@@ -15,7 +15,6 @@ namespace detint {
 namespace {
 
 constexpr int KV4_MAX_LEN = 1 << 19;       // keys: the limb sums stay in int32
-constexpr long long KV4_TWO = 4096;         // pages of all units from which a decode call takes two launches
 
 struct DevInfo {
     bool ready = false;
@@ -50,6 +49,19 @@ AppFn append_kernel(int d, bool norm, bool chunk) {
     return f[d == 128][norm][chunk];
 }
 
+struct Pf {
+    DecFn fn;
+    int threads, smem;
+};
+const Pf PREFILL[2][2] = {{{k_kv4_prefill<64, 4>, 128, Kv4Pf<64, 4>::SMEM}, {k_kv4_prefill<64, 8>, 256, Kv4Pf<64, 8>::SMEM}},
+                          {{k_kv4_prefill<128, 4>, 128, Kv4Pf<128, 4>::SMEM}, {k_kv4_prefill<128, 8>, 256, Kv4Pf<128, 8>::SMEM}}};
+
+// values: 3 bytes per channel and token; chunks: KV4_CH rows of integers per head
+size_t append_smem(int d, int tile) {
+    const size_t values = (size_t)tile * d * 3, heads = KV4_APT / (d / 4);
+    return tile < 8 ? values : std::max(values, heads * KV4_CH * d * 4);
+}
+
 size_t dec_smem(int d, int gt, int cap) {
     const size_t ring = d == 128 ? Kv4Ring<128>::BYTES : Kv4Ring<64>::BYTES;
     return ring + (size_t)gt * d * 8 + (size_t)(((cap >> 6) + 3) & ~3) * 4 + (size_t)gt * (cap + 8) * 4;
@@ -79,14 +91,19 @@ DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len,
     p.gt = G >= 5 ? 8 : (G >= 3 ? 4 : G);
     p.hg = (G + p.gt - 1) / p.gt;
     const long long units = (long long)T * a.n_kv * p.hg;
-    // one launch: as many CTAs as keep two on every SM busy, at least 2 pages each
+    // One launch: the clusters' CTAs fit the SMs once, two on each, with at
+    // least 2 pages each (32 tokens of 1025..1536 keys, 32 + 8 heads of 64: 12.7
+    // us split so, 19.8 us as two waves of half the size). Where the scores of
+    // such a CTA do not fit its shared memory, two launches (64 tokens of 4 k
+    // to 16 k keys, 32 + 8 heads of 128: 175 us, against 276 us in larger
+    // clusters; at 38 tokens of 4000 keys 50 and 53 us, at 76 of 2000, where
+    // the scores fit, 51 and 48 us).
     int S = 1;
-    while (S < di.max_cluster && units * S < 2 * di.sms && mp >= 4 * S) S <<= 1;
-    while (S < di.max_cluster && dec_smem(d, p.gt, ((mp + S - 1) / S) << 6) > dec_smem2(p.gt)) S <<= 1;
+    while (S < di.max_cluster && units * 2 * S <= 2 * di.sms && mp >= 4 * S) S <<= 1;
     p.S = S;
     p.cap = ((mp + S - 1) / S) << 6;
     p.smem = dec_smem(d, p.gt, p.cap);
-    p.two = p.smem > dec_smem2(p.gt) || units * mp >= KV4_TWO;
+    p.two = p.smem > dec_smem2(p.gt);
     if (p.two) {
         p.pw = 8;
         while (p.pw > 1 && units * ((mp + p.pw - 1) / p.pw) < 16LL * di.sms) p.pw >>= 1;
@@ -152,11 +169,9 @@ cudaError_t kv4_init() {
     for (int d : {64, 128})
         for (int norm = 0; norm < 2; ++norm)
             if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(append_kernel(d, norm, true), cudaFuncAttributeMaxDynamicSharedMemorySize, d * 512);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_kv4_prefill<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Kv4Pf<64>::SMEM);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_kv4_prefill<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Kv4Pf<128>::SMEM);
+                e = cudaFuncSetAttribute(append_kernel(d, norm, true), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)append_smem(d, KV4_VTILE));
+    for (const Pf& f : {PREFILL[0][0], PREFILL[0][1], PREFILL[1][0], PREFILL[1][1]})
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem);
     if (e == cudaSuccess) {
         di->max_cluster = mc;
         di->ready = true;
@@ -177,8 +192,7 @@ cudaError_t launch_kv4_append(const Kv4Args& a, const Kv4Append& p0, int d, cuda
     p.tile = KV4_VTILE;
     while (p.tile > 1 && (long long)((p.T + p.tile - 1) / p.tile) * per_tile < 4LL * di->sms) p.tile >>= 1;
     const dim3 grid((p.T + p.tile - 1) / p.tile, per_tile);
-    // values: 3 bytes per channel and token; chunks: a warp's 32 x 128 (or 2 x 16 x 64) integers
-    const size_t smem = p.tile < 8 ? (size_t)p.tile * d * 3 : (size_t)d * 512;
+    const size_t smem = append_smem(d, p.tile);
     append_kernel(d, p.q_gamma != nullptr, p.tile >= 8)<<<grid, KV4_APT, smem, s>>>(a, p);
     return cudaGetLastError();
 }
@@ -187,14 +201,17 @@ cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p0, int d, cudaS
     Kv4Attn p = p0;
     p.lgGp = 0;
     while ((1 << p.lgGp) < p.G) ++p.lgGp;
-    const int bq = KV4_PROWS >> p.lgGp;
+    // 32 rows per CTA and four CTAs on an SM balance causal blocks better than
+    // 64 rows and two; only a group of more than 32 heads needs 64
+    const bool wide = p.lgGp > 5;
+    const int bq = (wide ? 64 : 32) >> p.lgGp;
     const int tiles = (p.T + bq - 1) / bq;
     for (int b0 = 0; b0 < tiles; b0 += 65535) {
         const int n = std::min(65535, tiles - b0);
         p.t0 = b0 * bq;
         const dim3 grid(a.n_kv, n);
-        if (d == 128) k_kv4_prefill<128><<<grid, KV4_PT, Kv4Pf<128>::SMEM, s>>>(a, p);
-        else k_kv4_prefill<64><<<grid, KV4_PT, Kv4Pf<64>::SMEM, s>>>(a, p);
+        const Pf f = PREFILL[d == 128][wide];
+        f.fn<<<grid, f.threads, f.smem, s>>>(a, p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }

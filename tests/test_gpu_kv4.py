@@ -272,7 +272,8 @@ def test_bad_pages_and_places_are_masked_and_recorded(torch, which):
     assert dev.status.cpu().tolist() == [0, 1, 0, 0, 0, 0, 0, 0]
 
 
-@pytest.mark.parametrize("n_q,n_kv,d,T,hi", [(8, 8, 128, 24, 2300), (32, 4, 64, 40, 1900), (16, 2, 128, 64, 2500), (24, 8, 64, 16, 2100)])
+@pytest.mark.parametrize("n_q,n_kv,d,T,hi", [(32, 8, 128, 40, 2600), (32, 4, 64, 40, 1900), (16, 2, 128, 64, 2500), (24, 8, 64, 40, 3000),
+                                             (16, 8, 128, 40, 5200), (4, 4, 64, 80, 12000)])
 def test_decode_in_two_launches(torch, n_q, n_kv, d, T, hi):
     """Batches whose decode takes the two-launch path: against the plain form on
     some rows and against the block form, bit for bit, on all; twice on one
@@ -386,18 +387,18 @@ def test_append_then_attention_token_by_token_equals_one_prefill(torch):
         assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("T,hi", [(2, 300), (16, 4200)])
-def test_captured_step_is_replayed_with_new_positions(torch, T, hi):
+@pytest.mark.parametrize("T,hi,n_q,n_kv", [(2, 300, 8, 4), (16, 4200, 32, 2)])
+def test_captured_step_is_replayed_with_new_positions(torch, T, hi, n_q, n_kv):
     """Append and decode in a CUDA graph (both decode forms): the replay reads
     the positions that are in memory then."""
     import deterministic_integer_only_gb300 as pkg
     rng = np.random.default_rng(T)
-    n_q, n_kv, d = 8, 4, 64
+    d, width = 64, (n_q + 2 * n_kv) * 64
     pages, tab, prm, dev = _step_setup(torch, rng, n_q, n_kv, d, T, hi)
     ref = Dev(torch, pages, tab, prm, n_q)
     cos, sin = tables(d, hi)
     r = pkg.RopeNorm(cuda(torch, cos), cuda(torch, sin), interleaved=True)
-    qkv = torch.zeros((T, 16 * d), dtype=torch.int32, device="cuda")
+    qkv = torch.zeros((T, width), dtype=torch.int32, device="cuda")
     seq = torch.arange(T, dtype=torch.int32, device="cuda")
     pos = torch.zeros(T, dtype=torch.int32, device="cuda")
     need = pkg.detint_kv4_workspace(dev.cache, T, hi)
@@ -414,7 +415,7 @@ def test_captured_step_is_replayed_with_new_positions(torch, T, hi):
     with torch.cuda.graph(g):
         step()
     for p in (0, 63, 64, 200, hi - 1):
-        x = cuda(torch, np.rint(rng.normal(0, 4096, (T, 16 * d))).astype(np.int32))
+        x = cuda(torch, np.rint(rng.normal(0, 4096, (T, width))).astype(np.int32))
         qkv.copy_(x)
         pos.fill_(p)
         pos[T - 1] = p // 2
@@ -428,7 +429,7 @@ def test_two_streams_at_once(torch):
     and workspace."""
     import deterministic_integer_only_gb300 as pkg
     rng = np.random.default_rng(21)
-    n_q, n_kv, d, T, hi = 16, 4, 128, 20, 4000
+    n_q, n_kv, d, T, hi = 16, 4, 128, 20, 5000
     pages, tab, prm, dev = _step_setup(torch, rng, n_q, n_kv, d, T, hi)
     qs = [[cuda(torch, a) for a in kp.queries(T, n_q, d, rng)] for _ in range(2)]
     seq = torch.arange(T, dtype=torch.int32, device="cuda")

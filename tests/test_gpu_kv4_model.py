@@ -126,10 +126,10 @@ def test_llama_shape_long_batch_equals_one_sequence(torch, llama_artifact):
     """A batch whose decode attention takes the two-launch form gives the rows
     that single sequences (one launch) give."""
     import deterministic_integer_only_gb300 as pkg
-    m = pkg.Model(llama_artifact, max_batch=32, max_ctx=1300, kv_bits=4)
-    prompts = [synth.prompt_ids(0, i, 1040 + i, m.vocab) for i in range(32)]
+    m = pkg.Model(llama_artifact, max_batch=20, max_ctx=2400, kv_bits=4)
+    prompts = [synth.prompt_ids(0, i, 2150 + i, m.vocab) for i in range(20)]
     toks, hashes = m.generate(prompts, 3, keep_logits="hash")
-    m1 = pkg.Model(llama_artifact, max_batch=1, max_ctx=1300, kv_bits=4)
+    m1 = pkg.Model(llama_artifact, max_batch=1, max_ctx=2400, kv_bits=4)
     for b in (0, 17):
         t1, h1 = m1.generate([prompts[b]], 3, keep_logits="hash")
         assert t1[0].tolist() == toks[b].tolist() and h1[0] == hashes[b]
