@@ -1366,7 +1366,9 @@ __global__ void __launch_bounds__(128, GT == 8 ? 2 : 4) k_kv4_pv(Kv4Args a, Kv4A
 // leave 8 warps on an SM: 4 x 4096 tokens of 16 + 8 heads of 128 channels took
 // 4336 us, and 4716 us with sweep 1 on the dp4a pipe.) The tokens of a block may
 // belong to several sequences: each run of one sequence is swept by itself
-// with the other rows masked.
+// with the other rows masked. Where there are few blocks, a thread-block cluster
+// takes one: its CTAs share a run's pages, settle the maxima between the
+// sweeps and add up their sums at the end through distributed shared memory.
 constexpr int KV4_PST = 4;       // page stages
 
 template <int D, int NW>
@@ -1386,12 +1388,12 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) k_kv4_prefill(Kv4Args a, Kv4
     extern __shared__ __align__(16) unsigned char kv4_raw[];
     __shared__ unsigned long long full[KV4_PST];
     __shared__ int page_ok[KV4_PST];
-    __shared__ int r_pos[ROWS], r_top[2][ROWS];
-    __shared__ i64 r_sum[2][2][ROWS];
+    __shared__ int r_pos[ROWS], r_top[2][2][ROWS];       // r_top: by runs in turn, by halves
+    __shared__ i64 r_sum[2][2][ROWS], tot[3][ROWS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rg = warp >> 1, hf = warp & 1;             // 16-row group; half of the keys and channels
     const int gid = lane >> 2, tig = lane & 3;
-    const int g = blockIdx.x;
+    const int g = (int)blockIdx.x >> p.lgC, rank = (int)blockIdx.x & ((1 << p.lgC) - 1);
     const int lgBQ = (NW == 8 ? 6 : 5) - p.lgGp, BQ = 1 << lgBQ;
     const int t0 = p.t0 + (int)(gridDim.y - 1 - blockIdx.y) * BQ;    // later tokens tend to have more keys
     const int nt = min(BQ, p.T - t0);
@@ -1456,7 +1458,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) k_kv4_prefill(Kv4Args a, Kv4
     unsigned sumE[2] = {0, 0}, sumW[2] = {0, 0};         // an eighth of 2^19 keys: below 2^32
     const int k_lane = 16 * tig + 8 * hf;                // first of this lane's eight keys of a page
 
-    int it = 0, wbuf = 0;                                // pages consumed so far (ring position); operand buffer
+    int it = 0, wbuf = 0, run = 0;                       // pages consumed so far (ring position); operand and maxima buffers
     for (int s0 = 0; s0 < nt;) {
         // a run of one sequence: tokens [s0, s1)
         const int seq = p.tok_seq[t0 + s0];
@@ -1479,7 +1481,9 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) k_kv4_prefill(Kv4Args a, Kv4
         const int cmin = __reduce_max_sync(0xffffffffu, max(loA, loB));
         s0 = s1;
         if (kmax < 0) continue;
-        const int p0 = kmin >> 6, np = (kmax >> 6) - p0 + 1;
+        // the run's pages, and this CTA's share of them
+        const int all = (kmax >> 6) - (kmin >> 6) + 1, per = (all + (1 << p.lgC) - 1) >> p.lgC;
+        const int p0 = (kmin >> 6) + rank * per, np = min(per, max(0, all - rank * per));
         const int32_t* bt = a.block_table + (size_t)seq * a.max_blocks + p0;
         auto issue = [&](int i) {                        // i: page of the two sweeps, 0 .. 2 np - 1
             const int st = (it + i) & (KV4_PST - 1), sweep = i >= np;
@@ -1504,7 +1508,29 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) k_kv4_prefill(Kv4Args a, Kv4
         };
         if (tid == 0)
             for (int i = 0; i < min(KV4_PST, 2 * np); ++i) issue(i);
+        // the row maxima of this run over the row's lanes, both halves and every CTA
+        auto settle = [&]() {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                T[x] = max(T[x], __shfl_xor_sync(0xffffffffu, T[x], 1));
+                T[x] = max(T[x], __shfl_xor_sync(0xffffffffu, T[x], 2));
+                if (tig == 0) r_top[run][hf][x ? rB : rA] = T[x];
+            }
+            if (p.lgC) cl_sync();
+            else bar_named(1 + rg, 64);
+            for (int r = 0; r < (1 << p.lgC); ++r)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int row = x ? rB : rA;
+                    const int u = p.lgC ? cl_ld32(&r_top[run][0][row], r) : r_top[run][0][row];
+                    const int v = p.lgC ? cl_ld32(&r_top[run][1][row], r) : r_top[run][1][row];
+                    T[x] = max(T[x], max(u, v));
+                }
+            run ^= 1;
+        };
+        if (np == 0) settle();
         for (int i = 0; i < 2 * np; ++i) {
+            if (i == np) settle();
             const int st = (it + i) & (KV4_PST - 1);
             if (!mbar_wait(smem_u32(&full[st]), ((it + i) / KV4_PST) & 1) && a.status) a.status[ST_TIMEOUT] = 1;
             const int kb = (p0 + (i >= np ? i - np : i)) << 6;
@@ -1583,18 +1609,6 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) k_kv4_prefill(Kv4Args a, Kv4
                     }
                 }
             }
-            if (i == np - 1) {
-                // the row maxima of this run over the row's lanes and both halves
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    T[x] = max(T[x], __shfl_xor_sync(0xffffffffu, T[x], 1));
-                    T[x] = max(T[x], __shfl_xor_sync(0xffffffffu, T[x], 2));
-                    if (tig == 0) r_top[hf][x ? rB : rA] = T[x];
-                }
-                bar_named(1 + rg, 64);
-                T[0] = max(T[0], r_top[hf ^ 1][rA]);
-                T[1] = max(T[1], r_top[hf ^ 1][rB]);
-            }
             __syncthreads();                             // every warp is done with the stage
             if (tid == 0 && i + KV4_PST < 2 * np) issue(i + KV4_PST);
         }
@@ -1613,9 +1627,50 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) k_kv4_prefill(Kv4Args a, Kv4
             r_sum[hf][1][x ? rB : rA] = w;
         }
     }
-    bar_named(1 + rg, 64);
     const i64 MV = kvp[4];
     const int KVS = kvp[5];
+    if (p.lgC) {
+        // limb sums [row][channel] of every CTA where its pages were; each CTA
+        // divides its share of the rows
+        int2* nm = (int2*)kv4_raw;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int n = 0; n < 2 * NC; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    nm[(x ? rB : rA) * D + hf * (D / 2) + 8 * n + 2 * tig + e] = make_int2(aL[n][2 * x + e], aH[n][2 * x + e]);
+        cl_sync();
+        const int share = ROWS >> p.lgC;
+        if (tid < share) {
+            const int r = rank * share + tid;
+            i64 e = 0, w = 0;
+            for (int q = 0; q < (1 << p.lgC); ++q) {
+                e += cl_ld64(&r_sum[0][0][r], q) + cl_ld64(&r_sum[1][0][r], q);
+                w += cl_ld64(&r_sum[0][1][r], q) + cl_ld64(&r_sum[1][1][r], q);
+            }
+            const int bl = bitlen_u64((u64)e);
+            tot[0][tid] = e > 0 ? (i64)pow2_recip((u64)e, bl, 1, 23) : 0;
+            tot[1][tid] = bl;
+            tot[2][tid] = -8 * w;
+        }
+        __syncthreads();
+#pragma unroll 2
+        for (int k = tid; k < share * D; k += 32 * NW) {
+            const int j = k / D, r = rank * share + j, c = k & (D - 1);
+            const int i = r >> p.lgGp, hh = r & ((1 << p.lgGp) - 1);
+            if (i >= nt || hh >= p.G) continue;
+            i64 num = tot[2][j];
+            for (int q = 0; q < (1 << p.lgC); ++q) {
+                const i64 v = cl_ld64((const i64*)(nm + r * D + c), q);
+                num += (i64)(int)v + (v >> 32) * 256;
+            }
+            p.o[(size_t)(t0 + i) * p.o_stride + (size_t)(g * p.G + hh) * D + c] = kv4_out(num, tot[0][j], (int)tot[1][j], MV, KVS);
+        }
+        cl_sync();                                       // no CTA leaves while another reads its shared memory
+        return;
+    }
+    bar_named(1 + rg, 64);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int r = x ? rB : rA;

@@ -260,7 +260,7 @@ struct Kv4Attn {
     int T, t0, G, max_len, window;
     int cap;                      // decode: keys a CTA's shared memory holds
     unsigned long long smul;      // decode: ceil(2^32 / CTAs of a unit)
-    int lgGp;                     // prefill: log2 of the power of two >= G
+    int lgGp, lgC;                // prefill: log2 of the power of two >= G, of the CTAs of a block
     // decode in two launches: pages per warp of the first (and ceil(2^32 / pw)),
     // its warps per unit, log2 pages per CTA of the second; the workspace:
     // scores [unit][heads][ts_pitch], maxima [unit][n_sw][heads], sums

@@ -171,7 +171,9 @@ cudaError_t kv4_init() {
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(append_kernel(d, norm, true), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)append_smem(d, KV4_VTILE));
     for (const Pf& f : {PREFILL[0][0], PREFILL[0][1], PREFILL[1][0], PREFILL[1][1]})
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem);
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+            e = i ? cudaFuncSetAttribute(f.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)
+                  : cudaFuncSetAttribute(f.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem);
     if (e == cudaSuccess) {
         di->max_cluster = mc;
         di->ready = true;
@@ -199,6 +201,13 @@ cudaError_t launch_kv4_append(const Kv4Args& a, const Kv4Append& p0, int d, cuda
 
 cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p0, int d, cudaStream_t s) {
     Kv4Attn p = p0;
+    DevInfo* di = dev_info();
+    if (!di || !di->ready) return cudaErrorInvalidDevice;
+    // so few tokens that the single-token form takes them all in one wave: the
+    // same rows, with every key split over CTAs (3 x 13 tokens after 4000 keys,
+    // 2 + 1 heads of 128: 56 us in blocks)
+    const DecPlan dp = dec_plan(*di, a, d, p.T, p.max_len, p.window);
+    if (!dp.two && (long long)p.T * a.n_kv * dp.hg <= 2LL * di->sms) return launch_kv4_decode(a, p0, d, nullptr, s);
     p.lgGp = 0;
     while ((1 << p.lgGp) < p.G) ++p.lgGp;
     // 32 rows per CTA and four CTAs on an SM balance causal blocks better than
@@ -206,13 +215,28 @@ cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p0, int d, cudaS
     const bool wide = p.lgGp > 5;
     const int bq = (wide ? 64 : 32) >> p.lgGp;
     const int tiles = (p.T + bq - 1) / bq;
+    // few blocks: clusters whose CTAs share a block's pages, while they fit the
+    // SMs once (four CTAs on each) and a CTA keeps 2 pages
+    const int mp = (p.max_len + 63) >> 6;
+    p.lgC = 0;
+    while (!wide && p.lgC < 4 && (1 << (p.lgC + 1)) <= di->max_cluster &&
+           ((long long)tiles * a.n_kv << (p.lgC + 1)) <= 4LL * di->sms && mp >= 4 << p.lgC)
+        ++p.lgC;
+    const Pf f = PREFILL[d == 128][wide];
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1 << p.lgC;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.lgC ? 1 : 0;
+    cfg.blockDim = dim3(f.threads);
+    cfg.dynamicSmemBytes = f.smem;
+    cfg.stream = s;
     for (int b0 = 0; b0 < tiles; b0 += 65535) {
-        const int n = std::min(65535, tiles - b0);
         p.t0 = b0 * bq;
-        const dim3 grid(a.n_kv, n);
-        const Pf f = PREFILL[d == 128][wide];
-        f.fn<<<grid, f.threads, f.smem, s>>>(a, p);
-        const cudaError_t e = cudaGetLastError();
+        cfg.gridDim = dim3(a.n_kv << p.lgC, std::min(65535, tiles - b0));
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, f.fn, a, p);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -183,7 +183,7 @@ struct detint_model {
     int32_t* kvp4 = nullptr;
     unsigned char* kv4_ws = nullptr;
     size_t kv4_ws_bytes = 0;
-    int kv4_len = 0;         // bound of this decode step's context lengths
+    int kv4_len = 0;         // bound of this call's context lengths
     int pf_ok = 0;           // the tensor-core prefill attention supports this shape
     CUtensorMap kmap, vmap;  // whole K / V^T caches for the prefill attention
     int32_t* qblk = nullptr; // prefill query blocks [Tcap + max_batch][4]
@@ -326,7 +326,7 @@ static int attention_kv4(detint_model* m, int l, int T, int decode, cudaStream_t
     Kv4Attn t{};
     t.q8 = m->q8; t.mq = m->mq; t.kq = m->kq; t.tok_seq = m->tok_seq; t.tok_pos = m->tok_pos;
     t.o = m->o; t.o_stride = (size_t)nq * d; t.T = T; t.G = 1 << m->lg_grp;
-    t.max_len = decode ? m->kv4_len : m->max_ctx;
+    t.max_len = m->kv4_len;
     if (decode) CK(launch_kv4_decode(a, t, d, m->kv4_ws, s));
     else CK(launch_kv4_prefill(a, t, d, s));
     return DETINT_OK;
@@ -1072,6 +1072,8 @@ int detint_prefill(detint_model* m, int n_seq, const int32_t* seq_ids, const int
     }
     std::vector<int32_t> newlen(m->seq_len.begin(), m->seq_len.end());
     for (int i = 0; i < n_seq; ++i) newlen[seq_ids[i]] += cu_lens[i + 1] - cu_lens[i];
+    m->kv4_len = 0;
+    for (int i = 0; i < n_seq; ++i) m->kv4_len = std::max(m->kv4_len, newlen[seq_ids[i]]);
     for (int i = 0; i < n_seq; ++i) {
         rc = ensure_blocks(m, seq_ids[i], newlen[seq_ids[i]]);
         if (rc) return rc;

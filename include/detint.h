@@ -329,7 +329,8 @@ int detint_kv4_decode(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq
 /* The same attention with the same result, bit for bit, for many tokens of a
  * sequence: blocks of consecutive tokens of the call share one sweep over
  * their keys on the int8 tensor pipe. Tokens of one sequence should stand
- * together. No workspace. Errors: ARG, SHAPE, CUDA. */
+ * together. No workspace: so few tokens that one wave of the single-token form
+ * takes them are handed to it. Errors: ARG, SHAPE, CUDA. */
 int detint_kv4_prefill(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq,
                        const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int max_len, int window,
                        int32_t* o, long long o_stride, detint_stream_t s);

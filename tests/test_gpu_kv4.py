@@ -163,10 +163,17 @@ def test_append_leaves_out_padding_and_bad_places(torch):
 
 
 def run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, max_len, window, which, rows=None, want=None, pad=0):
+    """which: "decode"; "prefill", which hands few tokens to the single-token
+    form; "blocks": the tokens repeated until they are too many for that."""
     import deterministic_integer_only_gb300 as pkg
     T, width = len(pos), n_q * pages.d
     if want is None:
         want = kp.attention(pages, tab, prm, n_q, *q, seq, pos, window, max_len, rows)
+    if which == "blocks":
+        assert rows is None
+        n = 2 * torch.cuda.get_device_properties(0).multi_processor_count // (T * pages.n_kv) + 1
+        q, seq, pos, want = [np.concatenate([a] * n) for a in q], np.tile(seq, n), np.tile(pos, n), np.tile(want, (n, 1))
+        T *= n
     buf = torch.full((T + 2, width + pad), -77, dtype=torch.int32, device="cuda")
     out = buf[:T, :width] if pad else buf[:T]
     args = [cuda(torch, a) for a in q] + [cuda(torch, seq), cuda(torch, pos)]
@@ -187,7 +194,7 @@ def run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, max_len, window
 HEADS = [(1, 1, 64), (2, 1, 128), (3, 1, 64), (8, 2, 128), (5, 1, 128), (16, 2, 64), (12, 1, 64), (4, 4, 128), (10, 5, 64)]
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", ["decode", "prefill", "blocks"])
 @pytest.mark.parametrize("n_q,n_kv,d", HEADS)
 def test_attention_of_ragged_tokens(torch, which, n_q, n_kv, d):
     """Every head layout, lengths around page ends, several tokens of a sequence,
@@ -206,28 +213,28 @@ def test_attention_of_ragged_tokens(torch, which, n_q, n_kv, d):
     assert not dev.status.any()
 
 
-@pytest.mark.parametrize("n_q,n_kv,d", [(4, 2, 64), (2, 1, 128), (6, 1, 128), (16, 1, 64)])
+@pytest.mark.parametrize("n_q,n_kv,d", [(4, 2, 64), (2, 1, 128), (6, 1, 128), (16, 1, 64), (40, 1, 64), (64, 1, 128)])
 def test_prefill_blocks(torch, n_q, n_kv, d):
     """Runs of one sequence that start and end inside a block of query rows."""
     rng = np.random.default_rng(n_q + d)
-    runs = [(0, 0, 70), (1, 17, 1), (2, 60, 33), (1, 100, 90), (3, 0, 5), (0, 70, 3)]
-    lens = [73, 190, 93, 5]
-    tab = kp.table(lens, 3, 10, rng)
-    pages = kp.Pages(10, n_kv, d, rng)
+    runs = [(0, 0, 70), (1, 17, 1), (2, 60, 33), (1, 100, 90), (3, 0, 5), (0, 70, 3), (4, 3, 280)]
+    lens = [73, 190, 93, 5, 283]
+    tab = kp.table(lens, 5, 16, rng)
+    pages = kp.Pages(16, n_kv, d, rng)
     prm = kp.params(n_kv, d, rng)
     dev = Dev(torch, pages, tab, prm, n_q)
     seq, pos = ragged(runs)
     q = kp.queries(len(pos), n_q, d, rng)
     for window in (0, 3, 50):
-        a = run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 192, window, "prefill")
-        run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 192, window, "decode", want=a)
+        a = run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 283, window, "prefill")
+        run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 283, window, "decode", want=a)
     # any order of the same tokens gives the same rows
     o = rng.permutation(len(pos))
-    run_attention(torch, dev, pages, prm, tab, n_q, [x[o] for x in q], seq[o], pos[o], 192, 0, "prefill",
-                  want=run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 192, 0, "prefill")[o])
+    run_attention(torch, dev, pages, prm, tab, n_q, [x[o] for x in q], seq[o], pos[o], 283, 0, "prefill",
+                  want=run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, 283, 0, "prefill")[o])
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", ["decode", "prefill", "blocks"])
 def test_attention_extremes(torch, which):
     """The largest scores of both signs, all keys alike, underflow of all but
     one key, zero queries, shifts at their ends."""
@@ -255,7 +262,7 @@ def test_attention_extremes(torch, which):
     run_attention(torch, dev, pages, prm, tab, n_q, (q8, mq, kq), seq, pos, 250, 0, which)
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", ["decode", "prefill", "blocks"])
 def test_bad_pages_and_places_are_masked_and_recorded(torch, which):
     rng = np.random.default_rng(6)
     n_q, n_kv, d = 4, 2, 64
@@ -305,7 +312,7 @@ def test_decode_in_two_launches(torch, n_q, n_kv, d, T, hi):
     assert e.value.code == 1
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", ["decode", "prefill", "blocks"])
 def test_longest_context(torch, which):
     """524288 keys: sums past 32 bits, every page index used."""
     rng = np.random.default_rng(4)
