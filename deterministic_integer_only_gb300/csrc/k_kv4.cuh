@@ -562,6 +562,15 @@ __global__ void __launch_bounds__(KV4_APT, CHUNK ? 6 : 4) k_kv4_append(Kv4Args a
 }
 
 // ------------------------------------------------------------ attention
+// a bounded wait for a phase of a bulk copy's barrier, recorded when it runs
+// out (the polls come as an argument: as an immediate, ptxas moves the number
+// with an fp16 instruction, and these kernels execute none)
+__device__ __forceinline__ void kv4_wait(unsigned long long* bar, int parity, int polls, int32_t* status) {
+    const uint32_t b = smem_u32(bar);
+    for (int i = polls; i > 0; --i)
+        if (mbar_try_wait(b, (uint32_t)parity)) return;
+    if (status) status[ST_TIMEOUT] = 1;
+}
 // What a query row's scores become: E = exp2q(rshr(d M, sh)) with d = t - T
 // <= 0. M is brought to [2^29, 2^30] (and sh with it), and d to a multiple
 // that makes the shift at least 33, so that the shifted sum is the high word
@@ -894,7 +903,7 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
         }
     };
     auto wait = [&](int q) {
-        if (!mbar_wait(smem_u32(&full[warp][q & (C::NST - 1)]), (q / C::NST) & 1) && a.status) a.status[ST_TIMEOUT] = 1;
+        kv4_wait(&full[warp][q & (C::NST - 1)], (q / C::NST) & 1, p.polls, a.status);
     };
 #pragma unroll
     for (int q = 0; q < C::NST; ++q) issue(q);
@@ -1128,13 +1137,13 @@ __global__ void __launch_bounds__(128) k_kv4_scores(Kv4Args a, Kv4Attn p) {
     qr.load(p.q8 + ((size_t)t * a.nq + h0) * D, nh);
     int tm[HPL];
 #pragma unroll
-    for (int x = 0; x < HPL; ++x) tm[x] = KV4_NEG;
+    for (int x = 0; x < HPL; ++x) tm[x] = p.none;
     const int sub = lane & (LPK - 1), hb = sub / Q::LPG * HPL;
     int* out = p.ws_t + (unit * GT + hb) * p.ts_pitch + (size_t)k0 * KV_BLK + lane / LPK;
     for (int q = 0; q < n; ++q, out += KV_BLK) {
         const bool ok = __shfl_sync(0xffffffffu, blk_l, q) >= 0;
         const int jb = (b0 + k0 + q) << 6;
-        if (!mbar_wait(smem_u32(&full[warp][q & (NST - 1)]), (q / NST) & 1) && a.status) a.status[ST_TIMEOUT] = 1;
+        kv4_wait(&full[warp][q & (NST - 1)], (q / NST) & 1, p.polls, a.status);
         qr.page(ring + (q & (NST - 1)) * C::SLOT, out, p.ts_pitch, ok && jb >= j0 && jb + 64 <= j1, j0 - jb,
                 ok ? j1 - jb : -1, tm);
         __syncwarp();
@@ -1271,7 +1280,7 @@ __global__ void __launch_bounds__(128, GT == 8 ? 2 : 4) k_kv4_pv(Kv4Args a, Kv4A
         const bool ok = __shfl_sync(0xffffffffu, blk_l, q) >= 0;
         const int jb = ((b0 + k0 + warp + 4 * q) << 6) + koff;
         const bool clear = jb >= j0 && jb + 8 <= j1;
-        if (!mbar_wait(smem_u32(&full[warp][q & (NST - 1)]), (q / NST) & 1) && a.status) a.status[ST_TIMEOUT] = 1;
+        kv4_wait(&full[warp][q & (NST - 1)], (q / NST) & 1, p.polls, a.status);
         const unsigned char* base = ring + (q & (NST - 1)) * C::SLOT;
         const uint2 cv = *(const uint2*)(base + C::PG + koff);
         int4 b[NT];
@@ -1532,7 +1541,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW) k_kv4_prefill(Kv4Args a, Kv4
         for (int i = 0; i < 2 * np; ++i) {
             if (i == np) settle();
             const int st = (it + i) & (KV4_PST - 1);
-            if (!mbar_wait(smem_u32(&full[st]), ((it + i) / KV4_PST) & 1) && a.status) a.status[ST_TIMEOUT] = 1;
+            kv4_wait(&full[st], ((it + i) / KV4_PST) & 1, p.polls, a.status);
             const int kb = (p0 + (i >= np ? i - np : i)) << 6;
             if (page_ok[st] && kb <= wmax && kb + 63 >= wmin) {
                 const unsigned char* base = kv4_raw + st * C::STAGE;

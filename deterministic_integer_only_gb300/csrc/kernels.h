@@ -258,6 +258,7 @@ struct Kv4Attn {
     int32_t* o;
     size_t o_stride;
     int T, t0, G, max_len, window;
+    int polls, none;              // bound of a wait for a copy; the maximum of no key
     int cap;                      // decode: keys a CTA's shared memory holds
     unsigned long long smul;      // decode: ceil(2^32 / CTAs of a unit)
     int lgGp, lgC;                // prefill: log2 of the power of two >= G, of the CTAs of a block

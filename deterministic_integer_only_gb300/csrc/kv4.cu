@@ -201,6 +201,8 @@ cudaError_t launch_kv4_append(const Kv4Args& a, const Kv4Append& p0, int d, cuda
 
 cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p0, int d, cudaStream_t s) {
     Kv4Attn p = p0;
+    p.polls = SG_SPIN;
+    p.none = KV4_NEG;
     DevInfo* di = dev_info();
     if (!di || !di->ready) return cudaErrorInvalidDevice;
     // so few tokens that the single-token form takes them all in one wave: the
@@ -262,6 +264,8 @@ cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p0, int d, void* 
     DevInfo* di = dev_info();
     if (!di || !di->ready) return cudaErrorInvalidDevice;
     Kv4Attn p = p0;
+    p.polls = SG_SPIN;
+    p.none = KV4_NEG;
     const DecPlan pl = dec_plan(*di, a, d, std::min(p.T, 65535), p.max_len, p.window);
     const int d128 = d == 128, l = lg2(pl.gt);
     cudaLaunchConfig_t cfg = {};
