@@ -273,7 +273,7 @@ def _row_stride(where, name, t, dtype, rows, width, index) -> int:
         if t.numel() == rows * width and t.is_contiguous():
             return width
         if t.dim() == 2 and t.size(0) >= rows and t.size(1) >= width and t.stride(1) == 1:
-            return t.stride(0) if t.size(0) > 1 else t.size(1)
+            return t.stride(0) if t.size(0) > 1 else width
     raise ValueError(f"{where}: {name}: {dtype} rows [{rows}, {width}] on cuda:{index} expected, got {t.dtype} "
                      f"{tuple(t.shape)} on {t.device}")
 
@@ -345,8 +345,10 @@ def detint_kv4_workspace(cache, n_tok: int, max_len: int) -> int:
     return int(n.value)
 
 
-def _kv4_out(w, cache, n, out, stream):
+def _kv4_out(w, cache, n, max_len, window, out, stream):
     torch, width = cache._torch, cache.n_q * cache.head_dim
+    if max_len >> 31 or window >> 31:                    # (would be cut to 32 bits on the way)
+        raise DetintError(1, w, f"max_len {max_len} or window {window} out of range")
     if out is None:
         return _new(stream, (n, width), torch.int32, cache.device), width
     return out, _row_stride(w, "out", out, torch.int32, n, width, cache._index)
@@ -359,7 +361,7 @@ def detint_kv4_decode(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, window:
     detint_kv4_workspace bytes (made here when it is needed and not given)."""
     w = "detint_kv4_decode"
     n, raw = _kv4_call(w, cache, q8, mq, kq, tok_seq, tok_pos, stream)
-    out, stride = _kv4_out(w, cache, n, out, stream)
+    out, stride = _kv4_out(w, cache, n, max_len, window, out, stream)
     ws = size = 0
     if workspace is not None:
         if workspace.get_device() != cache._index or not workspace.is_contiguous():
@@ -382,7 +384,7 @@ def detint_kv4_prefill(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, window
     the same sequence (tokens of a sequence stand together)."""
     w = "detint_kv4_prefill"
     n, raw = _kv4_call(w, cache, q8, mq, kq, tok_seq, tok_pos, stream)
-    out, stride = _kv4_out(w, cache, n, out, stream)
+    out, stride = _kv4_out(w, cache, n, max_len, window, out, stream)
     rc = lib().detint_kv4_prefill(cache._ref, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), tok_seq.data_ptr(),
                                   tok_pos.data_ptr(), n, max_len, window, out.data_ptr(), stride, raw)
     if rc:

@@ -1,6 +1,11 @@
 """The 4-bit paged K/V cache operators on the GPU against plain 64-bit forms
 (kv4_plain: the oracle's scalar rows on plain arrays), bit for bit: every
 output, every byte of the pages and everything that must stay as it was."""
+import os
+import subprocess
+import sys
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 
@@ -431,6 +436,98 @@ def test_captured_step_is_replayed_with_new_positions(torch, T, hi, n_q, n_kv):
         assert torch.equal(out, pkg.detint_kv4_prefill(ref.cache, *q, seq, pos, hi)), p
 
 
+FIRST_CALL = """
+import sys
+sys.path[:0] = [%(root)r, %(tests)r]
+import numpy as np, torch
+import deterministic_integer_only_gb300 as pkg
+import test_gpu_kv4 as t
+rng = np.random.default_rng(2)
+pages, tab, prm, dev = t._step_setup(torch, rng, 8, 2, 64, 3, 200)
+q = [t.cuda(torch, a) for a in t.kp.queries(3, 8, 64, rng)]
+seq, pos = torch.arange(3, dtype=torch.int32, device="cuda"), t.cuda(torch, np.array([199, 0, 64], np.int32))
+out = torch.zeros((3, 512), dtype=torch.int32, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    pkg.detint_kv4_%(which)s(dev.cache, *q, seq, pos, 200, out=out)
+g.replay()
+torch.cuda.synchronize()
+want = t.kp.attention(pages, tab, prm, 8, *[a.cpu().numpy() for a in q], seq.cpu().numpy(), pos.cpu().numpy())
+assert np.array_equal(out.cpu().numpy(), want)
+"""
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+def test_first_call_of_a_process_may_be_captured(torch, which):
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL % dict(root=os.path.dirname(here), tests=here, which=which)
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
+
+
+def test_host_threads_at_once(torch):
+    """Calls of two host threads, each on a stream of its own."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(31)
+    n_q, n_kv, d, T, hi = 8, 2, 128, 6, 700
+    sets = []
+    for _ in range(2):
+        pages, tab, prm, dev = _step_setup(torch, rng, n_q, n_kv, d, T, hi)
+        q = kp.queries(T, n_q, d, rng)
+        pos = rng.integers(0, hi, T).astype(np.int32)
+        want = kp.attention(pages, tab, prm, n_q, *q, np.arange(T), pos)
+        sets.append((dev, [cuda(torch, a) for a in q], cuda(torch, np.arange(T, dtype=np.int32)), cuda(torch, pos), want))
+    torch.cuda.synchronize()
+
+    def work(x):
+        dev, q, seq, pos, want = x
+        s = torch.cuda.Stream()
+        got = [fn(dev.cache, *q, seq, pos, hi, stream=s) for _ in range(20) for fn in (pkg.detint_kv4_decode, pkg.detint_kv4_prefill)]
+        s.synchronize()
+        return all(np.array_equal(g.cpu().numpy(), want) for g in got)
+
+    with ThreadPoolExecutor(2) as ex:
+        assert all(ex.map(work, sets))
+
+
+@pytest.mark.parametrize("n_q,d,hi", [(1, 64, 100), (8, 64, 1300)])
+def test_more_tokens_than_a_launch_takes(torch, n_q, d, hi):
+    """65600 tokens: past a launch's 65535 for the single-token form, in one
+    launch of clusters and in two with a workspace."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(hi)
+    T = 65600
+    pages, tab, prm, dev = _step_setup(torch, rng, n_q, 1, d, 3, hi)
+    q = kp.queries(T, n_q, d, rng)
+    seq = np.sort(rng.integers(0, 3, T)).astype(np.int32)
+    pos = rng.integers(-2, hi, T).astype(np.int32)
+    args = [cuda(torch, a) for a in (*q, seq, pos)]
+    assert (pkg.detint_kv4_workspace(dev.cache, T, hi) > 0) == (hi > 1000)
+    dec = pkg.detint_kv4_decode(dev.cache, *args, hi)
+    pre = pkg.detint_kv4_prefill(dev.cache, *args, hi)
+    assert torch.equal(dec, pre)
+    rows = np.array([0, 1, 32767, 65533, 65534, 65535, 65536, 65537, T - 1])
+    want = kp.attention(pages, tab, prm, n_q, *[a[rows] for a in q], seq[rows], pos[rows])
+    assert np.array_equal(dec.cpu().numpy()[rows], want)
+    assert not dev.status.any()
+
+
+def test_one_row_of_a_wider_buffer(torch):
+    """A single row's stride does not matter, whatever its buffer's width."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(14)
+    pages, tab, prm, dev = _step_setup(torch, rng, 4, 2, 64, 1, 64)
+    ref = Dev(torch, pages, tab, prm, 4)
+    qkv = cuda(torch, np.rint(rng.normal(0, 4096, (1, 8 * 64 + 3))).astype(np.int32))
+    rope = pkg.RopeNorm(*(cuda(torch, a) for a in tables(64, 64)))
+    seq, pos = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    q = pkg.detint_kv4_append(dev.cache, rope, qkv, seq, pos)
+    w = pkg.detint_kv4_append(ref.cache, rope, qkv[:, :512].contiguous(), seq, pos)
+    assert all(torch.equal(a, b) for a, b in zip(q, w)) and torch.equal(dev.k, ref.k) and torch.equal(dev.v, ref.v)
+    out = torch.full((1, 4 * 64 + 1), -5, dtype=torch.int32, device="cuda")
+    pkg.detint_kv4_decode(dev.cache, *q, seq, pos, 64, out=out)
+    assert torch.equal(out[:, :256], pkg.detint_kv4_decode(dev.cache, *q, seq, pos, 64)) and int(out[0, 256]) == -5
+
+
 def test_two_streams_at_once(torch):
     """The same cache read by calls on two streams, each with its own outputs
     and workspace."""
@@ -464,7 +561,8 @@ def test_binding_refusals(torch):
             dec(dev.cache, *bad, 64)
     with pytest.raises(ValueError):
         dec(dev.cache, q8, mq, kq, seq, pos, 64, out=torch.empty((3, 200), dtype=torch.int32, device="cuda"))
-    for kw in (dict(max_len=0), dict(max_len=(1 << 19) + 1), dict(max_len=64, window=-1)):
+    for kw in (dict(max_len=0), dict(max_len=(1 << 19) + 1), dict(max_len=64, window=-1), dict(max_len=64, window=(1 << 32) + 1),
+               dict(max_len=(1 << 32) + 64)):
         with pytest.raises(pkg.DetintError):
             dec(dev.cache, q8, mq, kq, seq, pos, **kw)
     cos, sin = (cuda(torch, a) for a in tables(64, 64))
