@@ -64,7 +64,8 @@ __device__ __forceinline__ int kv4_slot(const Kv4Args& a, int seq, int pos, int*
 }
 
 __device__ __forceinline__ unsigned max4(const int (&x)[4]) {
-    return max(max(uabs32(x[0]), uabs32(x[1])), max(uabs32(x[2]), uabs32(x[3])));
+    const int hi = max(max(x[0], x[1]), max(x[2], x[3])), lo = min(min(x[0], x[1]), min(x[2], x[3]));
+    return max((unsigned)max(hi, 0), 0u - (unsigned)min(lo, 0));
 }
 __device__ __forceinline__ int pack4(const int (&q)[4]) { return q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24); }
 __device__ __forceinline__ short4 val4(const int (&q)[4], int c) {
@@ -354,16 +355,21 @@ __device__ __forceinline__ void kv4_qk_chunk(const Kv4Args& a, const Kv4Append& 
             }
             // rows below 2^24 (nearly all there are) only shift left
             const bool small = __all_sync(0xffffffffu, least >= 8);
+            if (small) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int s = (cl[i] - 8) & 31;
+                    v[i] = make_int4(v[i].x << s, v[i].y << s, v[i].z << s, v[i].w << s);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = make_int4(kv4_cut(v[i].x, cl[i]), kv4_cut(v[i].y, cl[i]), kv4_cut(v[i].z, cl[i]), kv4_cut(v[i].w, cl[i]));
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                int y[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                ss[i] = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    y[j] = small ? y[j] << ((cl[i] - 8) & 31) : kv4_cut(y[j], cl[i]);
-                    ss[i] += (u64)((i64)y[j] * y[j]);
-                }
-                *(int4*)(st + (8 * b + i) * D) = make_int4(y[0], y[1], y[2], y[3]);
+                ss[i] = (u64)((i64)v[i].x * v[i].x) + (u64)((i64)v[i].y * v[i].y) + (u64)((i64)v[i].z * v[i].z) + (u64)((i64)v[i].w * v[i].w);
+                *(int4*)(st + (8 * b + i) * D) = v[i];
             }
             const u64 s = rows_sum<LPH>(ss);
             if ((lane & (LPR - 1)) == b) ss_l = s;
