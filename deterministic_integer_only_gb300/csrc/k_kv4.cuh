@@ -446,9 +446,16 @@ __device__ __forceinline__ void kv4_qk_chunk(const Kv4Args& a, const Kv4Append& 
 // run changes its own nibbles with two atomics, so that another CTA's tokens
 // in the same word are kept (the nibbles are distinct, so the order of the
 // atomics does not matter).
+// Bound: single tokens by latency (one warp's dependent chain, 3.7 us with the
+// launch); many by integer instructions, 65 per channel: 4 x 4096 tokens of 16 +
+// 8 + 8 heads of 128 channels take 201 us, 1.9 TB/s of the 389 MB they move, at
+// 51 % of the ALU pipe and 0.57 instructions per cycle and scheduler. Chunks
+// of 16 rows and 6 CTAs per SM: 32 rows took 332 us, 8 or 4 rows held in
+// registers 334 and 248 us, 7 CTAs (fewer registers) 212 us; bringing the next
+// chunk to L2 ahead changed nothing.
 constexpr int KV4_APT = 128;     // append threads
-constexpr int KV4_VTILE = 64;    // most tokens in a tile
-constexpr int KV4_CH = 16;      // rows of a chunk (at most the lanes of a head)
+constexpr int KV4_VTILE = 32;    // most tokens in a tile: a lane each
+constexpr int KV4_CH = 16;       // rows of a chunk (at most the lanes of a head)
 
 template <int LPH, bool NORM, bool CHUNK>
 __global__ void __launch_bounds__(KV4_APT, CHUNK ? 6 : 4) k_kv4_append(Kv4Args a, Kv4Append p) {
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(KV4_APT, CHUNK ? 6 : 4) k_kv4_append(Kv4Args a
         return;
     }
     __shared__ int page[KV4_VTILE], offs[KV4_VTILE], code[KV4_VTILE], cinv[KV4_VTILE];
-    __shared__ unsigned lead_m[2];
+    __shared__ unsigned lead_m;
     short4* xs = (short4*)kv4_raw;                           // [nt][LPH] cached integers before coding
     int* cw = (int*)(xs + p.tile * LPH);                     // [nt][LPH] four codes each
     const int g = (int)blockIdx.y - p.qk_blocks;
@@ -521,13 +528,13 @@ __global__ void __launch_bounds__(KV4_APT, CHUNK ? 6 : 4) k_kv4_append(Kv4Args a
         const int i = threadIdx.x, blk = i < nt ? page[i] : -1, off = i < nt ? offs[i] : 0;
         const bool lead = blk >= 0 && !(i > 0 && page[i - 1] == blk && (offs[i - 1] >> 3) == (off >> 3) && offs[i - 1] < off);
         const unsigned m = __ballot_sync(0xffffffffu, lead);
-        if ((i & 31) == 0) lead_m[i >> 5] = m;
+        if (i == 0) lead_m = m;
     }
     __syncthreads();
-    u64 todo = (u64)lead_m[0] | ((u64)lead_m[1] << 32);
+    unsigned todo = lead_m;
     for (int k = 0; todo; ++k, todo &= todo - 1) {
         if ((k & (HPB - 1)) != hd) continue;
-        const int i = __ffsll((i64)todo) - 1;
+        const int i = __ffs((int)todo) - 1;
         const int blk = page[i], off = offs[i];
         int w[8];                                            // codes of the word's keys
 #pragma unroll
@@ -658,6 +665,9 @@ __device__ __forceinline__ int kv4_out(i64 num, i64 RS, int bl, i64 MV, int KVS)
 // between warps while scores are formed, and the first V slices travel while
 // the unit settles its maximum. dp4a and mma.sync run on different pipes (a
 // loop of one does not slow the other).
+// Bound: latency, of the launch, the table, one page and two exchanges in the
+// cluster (1 token of 65 keys 5.7 us, 8 of 17..767 8.2 us, 16 + 8 heads of 128; 32
+// of 1025..1536 keys, 32 + 8 heads of 64, 13 us or 1.7 TB/s of K and V).
 constexpr int KV4_DT = 256;      // decode threads
 constexpr int KV4_TP = 8;        // pages per probability tile
 
@@ -1080,9 +1090,15 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
 // another warp in either stream. (With a barrier per tile of 8 pages and a
 // warp per 16 channels the second launch took 115 us instead of the listed
 // 64 x 4k-16k contexts' 67 us of tensor time; handing half of the channels to
-// the dp4a pipe made the barriers longer, 135 us.) Scores cost 8 bytes of
+// the dp4a pipe made the barriers longer, 135 us. One cooperative launch drawing
+// both kinds of work from a counter took 67 and 180 us where the two take 48
+// and 176: 1 token of 131071 keys, and the 64 above.) Scores cost 8 bytes of
 // traffic per key and head, mostly in L2; K and V are read once, with an
 // evict-first policy.
+// Bound: at 64 x 4k-16k the score launch takes 66 us, 5.2 TB/s of K with the ALU
+// pipe (which runs dp4a's nibble masks and the maxima) half busy; P V takes 117
+// us, the tensor pipe 66 % busy, the rest the sums at a chunk's end and the last
+// wave. Chunks of 8 pages per warp: 4 and 16 pages were slower.
 template <int D, int GT>
 __global__ void __launch_bounds__(128) k_kv4_scores(Kv4Args a, Kv4Attn p) {
     using C = Kv4Ring<D>;
@@ -1379,7 +1395,10 @@ __global__ void __launch_bounds__(128, GT == 8 ? 2 : 4) k_kv4_pv(Kv4Args a, Kv4A
 // step's operand comes from the partner through shared memory. (One warp per
 // 16 rows with all keys and channels needs no exchange, but its accumulators
 // leave 8 warps on an SM: 4 x 4096 tokens of 16 + 8 heads of 128 channels took
-// 4336 us, and 4716 us with sweep 1 on the dp4a pipe.) The tokens of a block may
+// 4336 us, and 4716 us with sweep 1 on the dp4a pipe.) Bound: the int8 tensor
+// pipe, 92 % busy over those 4 x 4096 tokens (3840 us; 3480 us would be its
+// measured rate for two score sweeps and two limbs), 71 % over 1 x 1024 (99 us),
+// where the SMs' causal blocks do not come out even. The tokens of a block may
 // belong to several sequences: each run of one sequence is swept by itself
 // with the other rows masked. Where there are few blocks, a thread-block cluster
 // takes one: its CTAs share a run's pages, settle the maxima between the

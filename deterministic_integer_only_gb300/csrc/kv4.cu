@@ -15,6 +15,7 @@ namespace detint {
 namespace {
 
 constexpr int KV4_MAX_LEN = 1 << 19;       // keys: the limb sums stay in int32
+constexpr int KV4_CHUNK_MIN = 4;           // tokens of a tile from which append takes chunks
 
 struct DevInfo {
     bool ready = false;
@@ -59,7 +60,7 @@ const Pf PREFILL[2][2] = {{{k_kv4_prefill<64, 4>, 128, Kv4Pf<64, 4>::SMEM}, {k_k
 // values: 3 bytes per channel and token; chunks: KV4_CH rows of integers per head
 size_t append_smem(int d, int tile) {
     const size_t values = (size_t)tile * d * 3, heads = KV4_APT / (d / 4);
-    return tile < 8 ? values : std::max(values, heads * KV4_CH * d * 4);
+    return tile < KV4_CHUNK_MIN ? values : std::max(values, heads * KV4_CH * d * 4);
 }
 
 size_t dec_smem(int d, int gt, int cap) {
@@ -187,15 +188,18 @@ cudaError_t launch_kv4_append(const Kv4Args& a, const Kv4Append& p0, int d, cuda
     if (!di || !di->ready) return cudaErrorInvalidDevice;
     const int hpb = d == 128 ? 4 : 8;
     p.qk_blocks = (a.nq + a.n_kv + hpb - 1) / hpb;
-    // Tokens per CTA: as many as a page where that still makes 4 CTAs per SM;
-    // below 8 the chunk's three passes have too few rows (T = 32 tokens of
-    // 32 + 8 + 8 heads: one row at a time)
+    // Tokens per CTA: up to 32 (of 64, 10000 tokens of 16 + 8 + 8 heads of 128 made
+    // 2.4 waves and took 170 us, not 131), as many as still make 6 CTAs per SM
+    // (with 4, 1400 and 2800 tokens took 31 and 75 us, not 22 and 44; with 8, 300
+    // took 11.5, not 8.8). Below 4 each row's lanes repeat what the row needs once:
+    // the chunk's three passes have too few rows (300 tokens in tiles of 2: 12.6
+    // us in chunks, 11.5 us by rows; in tiles of 4: 8.9 and 13.6 us).
     const int per_tile = p.qk_blocks + a.n_kv;
     p.tile = KV4_VTILE;
-    while (p.tile > 1 && (long long)((p.T + p.tile - 1) / p.tile) * per_tile < 4LL * di->sms) p.tile >>= 1;
+    while (p.tile > 1 && (long long)((p.T + p.tile - 1) / p.tile) * per_tile < 6LL * di->sms) p.tile >>= 1;
     const dim3 grid((p.T + p.tile - 1) / p.tile, per_tile);
     const size_t smem = append_smem(d, p.tile);
-    append_kernel(d, p.q_gamma != nullptr, p.tile >= 8)<<<grid, KV4_APT, smem, s>>>(a, p);
+    append_kernel(d, p.q_gamma != nullptr, p.tile >= KV4_CHUNK_MIN)<<<grid, KV4_APT, smem, s>>>(a, p);
     return cudaGetLastError();
 }
 
@@ -207,18 +211,22 @@ cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p0, int d, cudaS
     if (!di || !di->ready) return cudaErrorInvalidDevice;
     // so few tokens that the single-token form takes them all in one wave: the
     // same rows, with every key split over CTAs (3 x 13 tokens after 4000 keys,
-    // 2 + 1 heads of 128: 56 us in blocks)
+    // 2 + 1 heads of 128: 14.5 us, 53 us in blocks; 20 after 1000, 16 + 8 heads: 13
+    // and 22 us)
     const DecPlan dp = dec_plan(*di, a, d, p.T, p.max_len, p.window);
     if (!dp.two && (long long)p.T * a.n_kv * dp.hg <= 2LL * di->sms) return launch_kv4_decode(a, p0, d, nullptr, s);
     p.lgGp = 0;
     while ((1 << p.lgGp) < p.G) ++p.lgGp;
     // 32 rows per CTA and four CTAs on an SM balance causal blocks better than
-    // 64 rows and two; only a group of more than 32 heads needs 64
+    // 64 rows and two (4 x 4096 tokens 3840 us, not 3951; 1 x 1024 99 us, not 117);
+    // only a group of more than 32 heads needs 64
     const bool wide = p.lgGp > 5;
     const int bq = (wide ? 64 : 32) >> p.lgGp;
     const int tiles = (p.T + bq - 1) / bq;
     // few blocks: clusters whose CTAs share a block's pages, while they fit the
-    // SMs once (four CTAs on each) and a CTA keeps 2 pages
+    // SMs once (four CTAs on each) and a CTA keeps 2 pages (60 tokens after 4000
+    // keys, 16 + 8 heads of 128: 52 us, one CTA per block 302 us; 1 x 512: 38 and
+    // 47 us)
     const int mp = (p.max_len + 63) >> 6;
     p.lgC = 0;
     while (!wide && p.lgC < 4 && (1 << (p.lgC + 1)) <= di->max_cluster &&

@@ -132,6 +132,25 @@ def test_append_chunks_of_rows(torch, d, norm, inter):
     assert not dev.status.any()
 
 
+@pytest.mark.parametrize("T", [171, 333, 700, 1403, 3001])
+@pytest.mark.parametrize("d,norm,inter", [(64, False, True), (128, True, False)])
+def test_append_tiles_of_every_size(torch, d, norm, inter, T):
+    """Tiles of 2 to 32 tokens on a GPU of 152 SMs, the last one cut short."""
+    rng = np.random.default_rng(T + d)
+    n_q, n_kv = 16, 8
+    lens = [T // 3 + 5, T - T // 3 - 1]
+    tab = kp.table(lens, 40, 70, rng)
+    prm = kp.params(n_kv, d, rng, inter)
+    pages = kp.Pages(70, n_kv, d, rng)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    seq, pos = ragged([(0, 5, T // 3), (1, 0, T - T // 3 - 1)])
+    pos = np.concatenate([pos, [-1]]).astype(np.int32)
+    seq = np.concatenate([seq, [0]]).astype(np.int32)
+    qkv = np.rint(rng.normal(0, 4096, (T, (n_q + 2 * n_kv) * d))).astype(np.int32)
+    run_append(torch, pages, dev, prm, n_q, d, inter, norm, qkv, seq, pos, 2100, tab=tab)
+    assert not dev.status.any()
+
+
 @pytest.mark.parametrize("norm", [True, False])
 def test_append_extreme_rows(torch, norm):
     """Zero rows, single spikes, the largest magnitudes, every exponent."""
