@@ -93,22 +93,27 @@ DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len,
     p.hg = (G + p.gt - 1) / p.gt;
     const long long units = (long long)T * a.n_kv * p.hg;
     // One launch: the clusters' CTAs fit the SMs once, two on each, with at
-    // least 2 pages each (32 tokens of 1025..1536 keys, 32 + 8 heads of 64: 12.7
-    // us split so, 19.8 us as two waves of half the size). Where the scores of
+    // least 4 pages each (32 tokens of 1025..1536 keys, 32 + 8 heads of 64: 12.8
+    // us split so, 19.8 us as two waves of half the size; 3 tokens of 300 keys, 16
+    // + 8 heads of 128: 6.3 us, 7.6 with 2 pages each; 1 of 2000: 8.2 and 7.8). Where the scores of
     // such a CTA do not fit its shared memory, two launches (64 tokens of 4 k
     // to 16 k keys, 32 + 8 heads of 128: 175 us, against 276 us in larger
     // clusters; at 38 tokens of 4000 keys 50 and 53 us, at 76 of 2000, where
     // the scores fit, 51 and 48 us).
     int S = 1;
-    while (S < di.max_cluster && units * 2 * S <= 2 * di.sms && mp >= 4 * S) S <<= 1;
+    while (S < di.max_cluster && units * 2 * S <= 2 * di.sms && mp >= 8 * S) S <<= 1;
     p.S = S;
     p.cap = ((mp + S - 1) / S) << 6;
     p.smem = dec_smem(d, p.gt, p.cap);
     p.two = p.smem > dec_smem2(p.gt);
     if (p.two) {
+        // pages of a score warp: 32 warps per SM (16 tokens of 12000 keys, 32 + 8
+        // heads of 128: 55 us; with 16 warps 58, with 48 55)
         p.pw = 8;
-        while (p.pw > 1 && units * ((mp + p.pw - 1) / p.pw) < 16LL * di.sms) p.pw >>= 1;
+        while (p.pw > 1 && units * ((mp + p.pw - 1) / p.pw) < 32LL * di.sms) p.pw >>= 1;
         p.n_sw = (mp + p.pw - 1) / p.pw;
+        // pages of a P V CTA: 6 CTAs per SM (3 tokens of 20000 keys, 32 + 8 heads of
+        // 128: 28 us; with 10 32; 40 of 4000, heads of 64: 34, 40; with 4 as with 6)
         p.lg_cp = 5;                                                // up to 8 pages a warp
         while (p.lg_cp > 2 && units * ((mp + (1 << p.lg_cp) - 1) >> p.lg_cp) < 6LL * di.sms) --p.lg_cp;
         p.pitch = ((mp + 7) & ~7) << 6;                             // whole tiles

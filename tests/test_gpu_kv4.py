@@ -303,6 +303,18 @@ def test_bad_pages_and_places_are_masked_and_recorded(torch, which):
     assert dev.status.cpu().tolist() == [0, 1, 0, 0, 0, 0, 0, 0]
 
 
+@pytest.mark.parametrize("n_q,n_kv,d,hi", [(2, 1, 64, 600), (8, 2, 128, 1100), (4, 1, 128, 2500), (3, 1, 64, 4800), (16, 2, 64, 4500), (5, 1, 128, 4200)])
+def test_decode_split_over_a_cluster(torch, n_q, n_kv, d, hi):
+    """Few tokens of 600 to 4800 keys: 2 to 16 CTAs share one, some without a page."""
+    rng = np.random.default_rng(hi)
+    pages, tab, prm, dev = _step_setup(torch, rng, n_q, n_kv, d, 3, hi)
+    q = kp.queries(3, n_q, d, rng)
+    seq, pos = np.arange(3, dtype=np.int32), np.array([hi - 1, hi // 3, 64], np.int32)
+    for window in (0, 65, 900):
+        run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, hi, window, "decode")
+    assert not dev.status.any()
+
+
 @pytest.mark.parametrize("n_q,n_kv,d,T,hi", [(32, 8, 128, 40, 2600), (32, 4, 64, 40, 1900), (16, 2, 128, 64, 2500), (24, 8, 64, 40, 3000),
                                              (16, 8, 128, 40, 5200), (4, 4, 64, 80, 12000)])
 def test_decode_in_two_launches(torch, n_q, n_kv, d, T, hi):
