@@ -447,9 +447,9 @@ __device__ __forceinline__ void kv4_qk_chunk(const Kv4Args& a, const Kv4Append& 
 // in the same word are kept (the nibbles are distinct, so the order of the
 // atomics does not matter).
 // Bound: single tokens by latency (one warp's dependent chain, 3.7 us with the
-// launch); many by integer instructions, 65 per channel: 4 x 4096 tokens of 16 +
-// 8 + 8 heads of 128 channels take 201 us, 1.9 TB/s of the 389 MB they move, at
-// 51 % of the ALU pipe and 0.57 instructions per cycle and scheduler. Chunks
+// launch); many by integer instructions, 67 per channel: 4 x 4096 tokens of 16 +
+// 8 + 8 heads of 128 channels take 199 us, 2.0 TB/s of the 389 MB they move, at
+// 52 % of the ALU pipe and 0.58 instructions per cycle and scheduler. Chunks
 // of 16 rows and 6 CTAs per SM: 32 rows took 332 us, 8 or 4 rows held in
 // registers 334 and 248 us, 7 CTAs (fewer registers) 212 us; bringing the next
 // chunk to L2 ahead changed nothing.
