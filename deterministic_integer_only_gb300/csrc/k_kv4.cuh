@@ -1096,9 +1096,11 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
 // traffic per key and head, mostly in L2; K and V are read once, with an
 // evict-first policy.
 // Bound: at 64 x 4k-16k the score launch takes 66 us, 5.2 TB/s of K with the ALU
-// pipe (which runs dp4a's nibble masks and the maxima) half busy; P V takes 117
-// us, the tensor pipe 66 % busy, the rest the sums at a chunk's end and the last
-// wave. Chunks of 8 pages per warp: 4 and 16 pages were slower.
+// pipe (which runs dp4a's nibble masks and the maxima) half busy; P V takes 110
+// us, its tensor work 67, the rest the sums at a chunk's end and the last wave.
+// Chunks of 8 pages per warp: 4 and 16 pages were slower. CTAs per SM of P V: 5 (3
+// or 4 with 8 heads) cost a few spilled registers and hide a chunk's ends (64 x
+// 4k-16k 171 us, with 4 176; with 6, 64 tokens of 8000 keys took 134 us, not 119).
 template <int D, int GT>
 __global__ void __launch_bounds__(128) k_kv4_scores(Kv4Args a, Kv4Attn p) {
     using C = Kv4Ring<D>;
@@ -1180,7 +1182,7 @@ __global__ void __launch_bounds__(128) k_kv4_scores(Kv4Args a, Kv4Attn p) {
 }
 
 template <int D, int GT>
-__global__ void __launch_bounds__(128, GT == 8 ? 2 : 4) k_kv4_pv(Kv4Args a, Kv4Attn p) {
+__global__ void __launch_bounds__(128, GT == 8 ? (D == 64 ? 4 : 3) : 5) k_kv4_pv(Kv4Args a, Kv4Attn p) {
     using C = Kv4Ring<D>;
     constexpr int NST = C::NST, NG = D / 16, NT = (2 * GT + 7) / 8;
     extern __shared__ __align__(16) unsigned char kv4_raw[];
@@ -1361,9 +1363,9 @@ __global__ void __launch_bounds__(128, GT == 8 ? 2 : 4) k_kv4_pv(Kv4Args a, Kv4A
     for (int i = tid; i < nh * D; i += 128)
         atomicAdd(un + i, (unsigned long long)((i64)(&num[0][0][0])[i] + (i64)(&num[1][0][0])[i] * 256));
     if (tid < 2 * GT) atomicAdd(us + tid, (unsigned long long)(&sums[0][0])[tid]);
-    __threadfence();
     __syncthreads();
     if (tid == 0) {
+        __threadfence();
         const unsigned chunks = (unsigned)((nb + (1 << p.lg_cp) - 1) >> p.lg_cp);
         last = atomicAdd(p.ws_cnt + unit, 1u) == chunks - 1;
     }
