@@ -84,7 +84,8 @@ struct DecPlan {
     int pw, n_sw, lg_cp, pitch;
 };
 
-DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len, int window) {
+// no_ws: one launch wherever it fits
+DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len, int window, bool no_ws) {
     DecPlan p{};
     const int G = a.nq / a.n_kv;
     int mp = (max_len + 63) >> 6;                                   // pages a token can have
@@ -106,6 +107,12 @@ DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len,
     p.cap = ((mp + S - 1) / S) << 6;
     p.smem = dec_smem(d, p.gt, p.cap);
     p.two = p.smem > dec_smem2(p.gt);
+    // Two as well where CTAs of more than 32 pages leave over a quarter of their
+    // places on the SMs empty (16 + 8 heads of 128: 1 token of 120000 keys 33 us,
+    // 49 in one launch, 40 of 4000 45 and 50; 100 of 3000, which fill 88 % of
+    // them, 78 and 73 us).
+    const long long n = units * S, places = 2 * di.sms, waves = (n + places - 1) / places;
+    if (!no_ws && p.cap > 32 * KV_BLK && 4 * n < 3 * waves * places) p.two = true;
     if (p.two) {
         // pages of a score warp: 32 warps per SM (16 tokens of 12000 keys, 32 + 8
         // heads of 128: 55 us; with 16 warps 58, with 48 55)
@@ -218,7 +225,7 @@ cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p0, int d, cudaS
     // same rows, with every key split over CTAs (3 x 13 tokens after 4000 keys,
     // 2 + 1 heads of 128: 14.5 us, 53 us in blocks; 20 after 1000, 16 + 8 heads: 13
     // and 22 us)
-    const DecPlan dp = dec_plan(*di, a, d, p.T, p.max_len, p.window);
+    const DecPlan dp = dec_plan(*di, a, d, p.T, p.max_len, p.window, true);
     if (!dp.two && (long long)p.T * a.n_kv * dp.hg <= 2LL * di->sms) return launch_kv4_decode(a, p0, d, nullptr, s);
     p.lgGp = 0;
     while ((1 << p.lgGp) < p.G) ++p.lgGp;
@@ -263,14 +270,14 @@ size_t kv4_decode_ws(const Kv4Args& a, int d, int T, int max_len) {
     DevInfo* di = dev_info();
     if (!di || !di->ready) return 0;
     const int Tc = std::min(T, 65535);
-    DecPlan pl = dec_plan(*di, a, d, Tc, max_len, 0);
+    DecPlan pl = dec_plan(*di, a, d, Tc, max_len, 0, false);
     if (!pl.two) return 0;
     pl.n_sw = (max_len + 63) >> 6;
     return ws_layout(pl, (long long)Tc * a.n_kv * pl.hg, d).total;
 }
 bool kv4_decode_needs_ws(const Kv4Args& a, int d, int T, int max_len, int window) {
     DevInfo* di = dev_info();
-    return di && di->ready && dec_plan(*di, a, d, std::min(T, 65535), max_len, window).two;
+    return di && di->ready && dec_plan(*di, a, d, std::min(T, 65535), max_len, window, false).two;
 }
 
 cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p0, int d, void* ws, cudaStream_t s) {
@@ -279,7 +286,7 @@ cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p0, int d, void* 
     Kv4Attn p = p0;
     p.polls = SG_SPIN;
     p.none = KV4_NEG;
-    const DecPlan pl = dec_plan(*di, a, d, std::min(p.T, 65535), p.max_len, p.window);
+    const DecPlan pl = dec_plan(*di, a, d, std::min(p.T, 65535), p.max_len, p.window, !ws);
     const int d128 = d == 128, l = lg2(pl.gt);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];

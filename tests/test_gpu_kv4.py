@@ -315,6 +315,22 @@ def test_decode_split_over_a_cluster(torch, n_q, n_kv, d, hi):
     assert not dev.status.any()
 
 
+@pytest.mark.parametrize("n_q,n_kv,d,hi", [(2, 1, 64, 34000), (3, 1, 128, 40001)])
+def test_few_tokens_of_long_contexts(torch, n_q, n_kv, d, hi):
+    """More than 32 pages for each of 16 CTAs: two launches with a workspace as
+    single tokens, one where a block of few tokens, which has none, goes there."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(hi)
+    pages, tab, prm, dev = _step_setup(torch, rng, n_q, n_kv, d, 2, hi)
+    assert pkg.detint_kv4_workspace(dev.cache, 2, hi) > 0
+    q = kp.queries(2, n_q, d, rng)
+    seq, pos = np.arange(2, dtype=np.int32), np.array([hi - 1, hi // 2], np.int32)
+    for window in (0, 33000):
+        for which in ("decode", "prefill"):
+            run_attention(torch, dev, pages, prm, tab, n_q, q, seq, pos, hi, window, which)
+    assert not dev.status.any()
+
+
 @pytest.mark.parametrize("n_q,n_kv,d,T,hi", [(32, 8, 128, 40, 2600), (32, 4, 64, 40, 1900), (16, 2, 128, 64, 2500), (24, 8, 64, 40, 3000),
                                              (16, 8, 128, 40, 5200), (4, 4, 64, 80, 12000)])
 def test_decode_in_two_launches(torch, n_q, n_kv, d, T, hi):
