@@ -14,7 +14,7 @@
 //     mma.sync fragment of two channels and two 32-key steps, and a warp's
 //     load is 512 contiguous bytes.
 //
-// Attention of a query row over its keys (docs: section 16):
+// Attention of a query row over its keys (arithmetic specification, section 16):
 //   t_j = c_j sum q8 k4_j, T = max t, delta_j = rshr((t_j - T) m_q CSTM, sh),
 //   E_j = min(32767, exp2q(delta_j)), W_j = rshr(E_j cv_j, 7) (16 bits),
 //   num = sum W_j v4_j, o = one deferred division by sum E_j.
@@ -576,8 +576,8 @@ __global__ void __launch_bounds__(KV4_APT, CHUNK ? 6 : 4) k_kv4_append(Kv4Args a
 
 // ------------------------------------------------------------ attention
 // a bounded wait for a phase of a bulk copy's barrier, recorded when it runs
-// out (the polls come as an argument: as an immediate, ptxas moves the number
-// with an fp16 instruction, and these kernels execute none)
+// out (the polls come as an argument: as an immediate, the compiler moves the
+// number with an fp16 instruction in some of the kernels)
 __device__ __forceinline__ void kv4_wait(unsigned long long* bar, int parity, int polls, int32_t* status) {
     const uint32_t b = smem_u32(bar);
     for (int i = polls; i > 0; --i)
