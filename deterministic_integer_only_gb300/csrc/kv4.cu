@@ -384,7 +384,8 @@ int check_attn(const char* where, const detint_kv4_t* c, const int8_t* q8, const
     if (o_stride < (long long)c->n_q * c->head_dim || (o_stride & 1)) return err(DETINT_E_ARG, "o_stride must be even and hold a row");
     *p = Kv4Attn{};
     p->q8 = q8; p->mq = mq; p->kq = kq; p->tok_seq = tok_seq; p->tok_pos = tok_pos; p->o = o; p->o_stride = (size_t)o_stride;
-    p->T = n_tok; p->G = c->n_q / c->n_kv; p->max_len = max_len; p->window = window;
+    p->T = n_tok; p->G = c->n_q / c->n_kv; p->max_len = max_len;
+    p->window = window < max_len ? window : 0;      // a window that every key is in: none (any int, so no sum with it may overflow)
     return DETINT_OK;
 }
 
@@ -445,7 +446,7 @@ int detint_kv4_decode(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq
     if (rc) return rc;
     cudaError_t e = kv4_init();
     if (e != cudaSuccess) return cuda_fail(where, e);
-    if (kv4_decode_needs_ws(a, c->head_dim, n_tok, max_len, window)) {
+    if (kv4_decode_needs_ws(a, c->head_dim, n_tok, max_len, p.window)) {
         const size_t need = kv4_decode_ws(a, c->head_dim, n_tok, max_len);
         if (!need || !workspace || workspace_bytes < (long long)need || mis(workspace, 16))
             return failed(DETINT_E_ARG, where, "a 16-byte aligned workspace of detint_kv4_workspace bytes is needed");

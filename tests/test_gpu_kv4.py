@@ -623,3 +623,28 @@ def test_binding_refusals(torch):
         pkg.detint_kv4_append(dev.cache, pkg.RopeNorm(cos, sin, q_gamma=g, k_gamma=g), qkv, seq, pos)
     with pytest.raises(pkg.DetintError):                # one gamma
         pkg.detint_kv4_append(dev.cache, pkg.RopeNorm(cos, sin, q_gamma=g[:64].contiguous()), qkv, seq, pos)
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,T,hi", [(16, 8, 128, 1, 300), (4, 1, 64, 3, 700), (32, 4, 64, 40, 1900)])
+def test_windows_past_every_key(torch, n_q, n_kv, d, T, hi):
+    """A window of max_len or more sees every key, up to the largest int: both
+    forms give what no window gives, with the workspace that was asked for."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(hi + T)
+    pages, tab, prm, dev = _step_setup(torch, rng, n_q, n_kv, d, T, hi)
+    q = [cuda(torch, a) for a in kp.queries(T, n_q, d, rng)]
+    seq = torch.arange(T, dtype=torch.int32, device="cuda")
+    pos = cuda(torch, rng.integers(hi // 2, hi, T).astype(np.int32))
+    need = pkg.detint_kv4_workspace(dev.cache, T, hi)
+    assert (need > 0) == (T == 40)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    want = pkg.detint_kv4_decode(dev.cache, *q, seq, pos, hi, workspace=ws)
+    rows = np.array([0, T - 1])
+    assert np.array_equal(want.cpu().numpy()[rows], kp.attention(pages, tab, prm, n_q, *[a.cpu().numpy()[rows] for a in q],
+                                                                 rows, pos.cpu().numpy()[rows]))
+    for window in (hi - 1, hi, hi + 1, (1 << 31) - 63, (1 << 31) - 1):
+        got = pkg.detint_kv4_prefill(dev.cache, *q, seq, pos, hi, window=window)
+        if window >= hi:
+            assert torch.equal(got, want), window
+        assert torch.equal(pkg.detint_kv4_decode(dev.cache, *q, seq, pos, hi, window=window, workspace=ws), got), window
+    assert not dev.status.any()
