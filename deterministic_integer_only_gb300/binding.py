@@ -339,7 +339,8 @@ def detint_kv4_append(cache, rope, qkv, tok_seq, tok_pos, q8=None, mq=None, kq=N
 
 
 def detint_kv4_workspace(cache, n_tok: int, max_len: int) -> int:
-    """Bytes of workspace of detint_kv4_decode; 0 for most sizes."""
+    """Bytes of workspace for every detint_kv4_decode of up to n_tok tokens and
+    max_len keys; 0 for most sizes."""
     n = C.c_longlong(0)
     _check(lib().detint_kv4_workspace(cache._ref, int(n_tok), int(max_len), C.byref(n)), "detint_kv4_workspace")
     return int(n.value)
@@ -357,8 +358,9 @@ def _kv4_out(w, cache, n, max_len, window, out, stream):
 def detint_kv4_decode(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, window: int = 0, out=None,
                       workspace=None, stream=None):
     """Attention of single tokens over the cache (detint_kv4_decode): int32 Q12
-    rows [n_tok, n_q head_dim]. workspace: a cuda uint8 tensor of
-    detint_kv4_workspace bytes (made here when it is needed and not given)."""
+    rows [n_tok, n_q head_dim]. workspace: a cuda uint8 tensor of the bytes that
+    detint_kv4_workspace gives for these or larger sizes (made here when it is
+    needed and not given)."""
     w = "detint_kv4_decode"
     n, raw = _kv4_call(w, cache, q8, mq, kq, tok_seq, tok_pos, stream)
     out, stride = _kv4_out(w, cache, n, max_len, window, out, stream)

@@ -275,9 +275,10 @@ struct Kv4Attn {
 };
 cudaError_t launch_kv4_append(const Kv4Args& a, const Kv4Append& p, int d, cudaStream_t s);
 cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p, int d, cudaStream_t s);
-// bytes of workspace the decode attention of T tokens needs (0: none)
+// bytes of workspace for every decode attention of up to T tokens and max_len
+// keys (0: none); and for one call of T tokens
 size_t kv4_decode_ws(const Kv4Args& a, int d, int T, int max_len);
-bool kv4_decode_needs_ws(const Kv4Args& a, int d, int T, int max_len, int window);
+size_t kv4_decode_need(const Kv4Args& a, int d, int T, int max_len, int window);
 cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p, int d, void* ws, cudaStream_t s);
 cudaError_t kv4_init();           // once per device, outside any stream capture
 

@@ -264,20 +264,35 @@ cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p0, int d, cudaS
     return cudaSuccess;
 }
 
-// Enough for every window: fewer keys take less of each array, but may need
-// more warps and CTAs per page, which only the maxima depend on.
+// Bytes for a call of two launches, whatever its window: fewer keys take less
+// of each array, but may need more warps and CTAs per page, which only the
+// maxima depend on. Fewer tokens or keys take less.
+static size_t ws_bytes(const Kv4Args& a, int d, int T, int max_len, DecPlan pl) {
+    pl.n_sw = (max_len + 63) >> 6;
+    return ws_layout(pl, (long long)T * a.n_kv * pl.hg, d).total;
+}
+// The most that a call of T tokens or fewer may ask for. Two launches depend on
+// how the CTAs fill the SMs, so fewer tokens may take them where T take one (16 +
+// 8 heads of 128, 3000 keys: 20 and 40 tokens do, 38, 64 and 100 do not); for a
+// number of tokens, more keys never turn two launches into one. Past three waves
+// of one CTA per unit a wave is never a quarter empty and shared memory alone
+// decides, for every number of tokens alike.
 size_t kv4_decode_ws(const Kv4Args& a, int d, int T, int max_len) {
     DevInfo* di = dev_info();
     if (!di || !di->ready) return 0;
-    const int Tc = std::min(T, 65535);
-    DecPlan pl = dec_plan(*di, a, d, Tc, max_len, 0, false);
-    if (!pl.two) return 0;
-    pl.n_sw = (max_len + 63) >> 6;
-    return ws_layout(pl, (long long)Tc * a.n_kv * pl.hg, d).total;
+    for (int n = std::min(T, 65535); n > 0; --n) {
+        const DecPlan pl = dec_plan(*di, a, d, n, max_len, 0, false);
+        if (pl.two) return ws_bytes(a, d, n, max_len, pl);
+        n = std::min(n, 6 * di->sms / (a.n_kv * pl.hg) + 1);
+    }
+    return 0;
 }
-bool kv4_decode_needs_ws(const Kv4Args& a, int d, int T, int max_len, int window) {
+size_t kv4_decode_need(const Kv4Args& a, int d, int T, int max_len, int window) {
     DevInfo* di = dev_info();
-    return di && di->ready && dec_plan(*di, a, d, std::min(T, 65535), max_len, window, false).two;
+    if (!di || !di->ready) return 0;
+    const int Tc = std::min(T, 65535);
+    if (!dec_plan(*di, a, d, Tc, max_len, window, false).two) return 0;
+    return ws_bytes(a, d, Tc, max_len, dec_plan(*di, a, d, Tc, max_len, 0, false));
 }
 
 cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p0, int d, void* ws, cudaStream_t s) {
@@ -446,11 +461,9 @@ int detint_kv4_decode(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq
     if (rc) return rc;
     cudaError_t e = kv4_init();
     if (e != cudaSuccess) return cuda_fail(where, e);
-    if (kv4_decode_needs_ws(a, c->head_dim, n_tok, max_len, p.window)) {
-        const size_t need = kv4_decode_ws(a, c->head_dim, n_tok, max_len);
-        if (!need || !workspace || workspace_bytes < (long long)need || mis(workspace, 16))
-            return failed(DETINT_E_ARG, where, "a 16-byte aligned workspace of detint_kv4_workspace bytes is needed");
-    }
+    const size_t need = kv4_decode_need(a, c->head_dim, n_tok, max_len, p.window);
+    if (need && (!workspace || workspace_bytes < (long long)need || mis(workspace, 16)))
+        return failed(DETINT_E_ARG, where, "a 16-byte aligned workspace of detint_kv4_workspace bytes is needed");
     e = launch_kv4_decode(a, p, c->head_dim, workspace, (cudaStream_t)sp);
     return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
 }

@@ -183,6 +183,7 @@ struct detint_model {
     int32_t* kvp4 = nullptr;
     unsigned char* kv4_ws = nullptr;
     size_t kv4_ws_bytes = 0;
+    int kv4_ws_tok = 0, kv4_ws_len = 0;   // tokens and context it is enough for, and all below
     int kv4_len = 0;         // bound of this call's context lengths
     int pf_ok = 0;           // the tensor-core prefill attention supports this shape
     CUtensorMap kmap, vmap;  // whole K / V^T caches for the prefill attention
@@ -749,23 +750,29 @@ static bool kv4_params(const detint_model* m, const std::vector<const unsigned c
     return true;
 }
 
-// room for the decode attention of n tokens with contexts up to len
+// room for the decode attention of up to n tokens with contexts up to len: a
+// batch or context that shrinks finds it there and keeps the captured graphs
 static int ensure_kv4_ws(detint_model* m, int n, int len) {
+    if (n <= m->kv4_ws_tok && len <= m->kv4_ws_len) return DETINT_OK;
     Kv4Args a{};
     a.nq = m->nq; a.n_kv = m->nkv;
     const size_t need = kv4_decode_ws(a, m->d, n, len);
-    if (need <= m->kv4_ws_bytes) return DETINT_OK;
-    CK(cudaDeviceSynchronize());
-    free_graphs(m);
-    if (m->kv4_ws) cudaFree(m->kv4_ws);
-    m->kv4_ws = nullptr;
-    m->kv4_ws_bytes = 0;
-    if (cudaMalloc(&m->kv4_ws, need) != cudaSuccess) {
-        cudaGetLastError();
+    if (need > m->kv4_ws_bytes) {
+        CK(cudaDeviceSynchronize());
+        free_graphs(m);
+        if (m->kv4_ws) cudaFree(m->kv4_ws);
         m->kv4_ws = nullptr;
-        return fail(DETINT_E_OOM, "decode attention workspace");
+        m->kv4_ws_bytes = 0;
+        m->kv4_ws_tok = m->kv4_ws_len = 0;
+        if (cudaMalloc(&m->kv4_ws, need) != cudaSuccess) {
+            cudaGetLastError();
+            m->kv4_ws = nullptr;
+            return fail(DETINT_E_OOM, "decode attention workspace");
+        }
+        m->kv4_ws_bytes = need;
     }
-    m->kv4_ws_bytes = need;
+    m->kv4_ws_tok = n;
+    m->kv4_ws_len = len;
     return DETINT_OK;
 }
 

@@ -308,8 +308,10 @@ int detint_kv4_append(const detint_kv4_t* c, const detint_rope_t* r, const int32
                       const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int8_t* q8, int32_t* mq,
                       int32_t* kq, int16_t* k_val, int16_t* v_val, detint_stream_t s);
 
-/* Bytes of workspace (16-byte aligned) that detint_kv4_decode of n_tok tokens
- * with contexts up to max_len needs; 0 for most sizes. Two calls that may
+/* Bytes of workspace (16-byte aligned) that are enough for every
+ * detint_kv4_decode of up to n_tok tokens with a max_len up to this one, with
+ * any window; 0 for most sizes. A buffer sized for the largest batch and
+ * context serves all calls below them. Two calls that may
  * overlap on the GPU, captured ones included, need a workspace each.
  * Errors: ARG, SHAPE, CUDA. */
 int detint_kv4_workspace(const detint_kv4_t* c, int n_tok, int max_len, long long* bytes);

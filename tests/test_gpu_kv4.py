@@ -648,3 +648,35 @@ def test_windows_past_every_key(torch, n_q, n_kv, d, T, hi):
             assert torch.equal(got, want), window
         assert torch.equal(pkg.detint_kv4_decode(dev.cache, *q, seq, pos, hi, window=window, workspace=ws), got), window
     assert not dev.status.any()
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,T,hi", [(16, 8, 128, 100, 3000), (8, 8, 64, 160, 2300)])
+def test_a_workspace_serves_smaller_calls(torch, n_q, n_kv, d, T, hi):
+    """A buffer sized once, for the largest batch and context, is enough for
+    every smaller call, also where the largest takes one launch and a smaller
+    one two."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(hi)
+    pages, tab, prm, dev = _step_setup(torch, rng, n_q, n_kv, d, T, hi)
+    need = pkg.detint_kv4_workspace(dev.cache, T, hi)
+    for n in [*range(1, T + 1), 2 * T, 5 * T]:
+        smaller = [pkg.detint_kv4_workspace(dev.cache, n, m) for m in (1, 64, 700, 2100, hi)]
+        assert smaller == sorted(smaller)
+        assert smaller[-1] <= need if n <= T else smaller[-1] >= need
+    buf = torch.full((need + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+    ws = buf[:need]
+    q = kp.queries(T, n_q, d, rng)
+    pos = rng.integers(hi // 2, hi, T).astype(np.int32)
+    dq, dp = [cuda(torch, a) for a in q], cuda(torch, pos)
+    seq = torch.arange(T, dtype=torch.int32, device="cuda")
+    want = pkg.detint_kv4_prefill(dev.cache, *dq, seq, dp, hi)
+    row = kp.attention(pages, tab, prm, n_q, *[a[:1] for a in q], np.zeros(1, np.int32), pos[:1])
+    assert np.array_equal(want[:1].cpu().numpy(), row)
+    for n in (T, T // 2, 40, 38, 20, 7, 1):
+        for window in (0, hi - 10, 2200):
+            exp = want if not window else pkg.detint_kv4_prefill(dev.cache, *dq, seq, dp, hi, window=window)
+            args = [a[:n] for a in dq] + [seq[:n], dp[:n]]
+            got = pkg.detint_kv4_decode(dev.cache, *args, hi, window=window, workspace=ws if need else None)
+            assert torch.equal(got, exp[:n]), (n, window)
+    assert (buf[need:] == 0x5A).all()
+    assert not dev.status.any()
