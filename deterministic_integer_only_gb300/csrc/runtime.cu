@@ -731,6 +731,8 @@ static int rd32(const unsigned char* p) { int32_t v; memcpy(&v, p, 4); return v;
 // cache, 1/14 of an int8 step: x = 14 y KQM / 2^KQS = y 7 KQM / 2^(KQS - 1);
 // the score scale divided by 14; the output scale of 128 units. The key
 // exponents of the channel pairs (c, c + d/2) are written out per channel.
+// False for parameters outside the 4-bit cache's domain (arithmetic
+// specification, section 16), whose results it does not define.
 static bool kv4_params(const detint_model* m, const std::vector<const unsigned char*>& src, std::vector<int32_t>* out) {
     const int d = m->d, in = 8 + d / 2, on = 8 + d;
     out->assign((size_t)m->L * m->nkv * on, 0);
@@ -740,12 +742,18 @@ static bool kv4_params(const detint_model* m, const std::vector<const unsigned c
             memcpy(s.data(), src[l] + (size_t)g * in * 4, (size_t)in * 4);
             int32_t* o = out->data() + ((size_t)l * m->nkv + g) * on;
             if (s[0] < 1 || s[2] < 1 || s[4] < 1 || s[6] < 1 || s[1] < 1 || s[3] < 1) return false;
+            if (s[0] > ((1 << 27) - 1) / 7 || s[2] > ((1 << 27) - 1) / 7 || s[1] > 63 || s[3] > 63) return false;
             int mv, kv, mc, kc;
             dyadic_fast((u64)s[4] * 64, 7, &mv, &kv);
             dyadic_fast((u64)s[6], 14, &mc, &kc);
+            const i64 so = (i64)s[5] + kv, sc = (i64)s[7] + kc;
+            if (so < 0 || so > 62 || sc < 0 || sc > 62) return false;
             o[0] = 7 * s[0]; o[1] = s[1] - 1; o[2] = 7 * s[2]; o[3] = s[3] - 1;
-            o[4] = mv; o[5] = s[5] + kv; o[6] = mc; o[7] = s[7] + kc;
-            for (int c = 0; c < d; ++c) o[8 + c] = s[8 + c % (d / 2)];
+            o[4] = mv; o[5] = (int)so; o[6] = mc; o[7] = (int)sc;
+            for (int c = 0; c < d; ++c) {
+                o[8 + c] = s[8 + c % (d / 2)];
+                if (o[8 + c] < 0 || o[8 + c] > 3) return false;
+            }
         }
     return true;
 }
@@ -885,6 +893,13 @@ int detint_load_kv(const char* path, int max_batch, int max_ctx, int kv_bits, de
         x.kvp = add((size_t)nkv * (8 + d / 2) * 4);
     }
     if (!ok) { delete m; return fail(DETINT_E_ARTIFACT, "artifact truncated"); }
+    std::vector<int32_t> kvp4;
+    std::vector<const unsigned char*> kvp8(m->L);
+    for (int l = 0; l < m->L; ++l) kvp8[l] = secs[ls[l].kvp].src;
+    if (kv4 && !kv4_params(m, kvp8, &kvp4)) {
+        delete m;
+        return fail(DETINT_E_ARTIFACT, "K/V scales that 4 bits cannot refine");
+    }
     cudaError_t ce = cudaMalloc(&m->wblob, dsz);
     if (ce != cudaSuccess) { m->wblob = nullptr; detint_free(m); return fail(DETINT_E_OOM, "weight allocation failed"); }
     // 16-bit weights pass through a device staging buffer and are split there
@@ -958,13 +973,6 @@ int detint_load_kv(const char* path, int max_batch, int max_ctx, int kv_bits, de
     // 4-bit pages and scale codes (k_kv4.cuh)
     m->kv_layer_elems = (size_t)m->nblocks * nkv * KV_BLK * d;
     const size_t toks = (size_t)m->L * m->nblocks * nkv * KV_BLK;
-    std::vector<int32_t> kvp4;
-    std::vector<const unsigned char*> kvp8(m->L);
-    for (int l = 0; l < m->L; ++l) kvp8[l] = secs[ls[l].kvp].src;
-    if (kv4 && !kv4_params(m, kvp8, &kvp4)) {
-        detint_free(m);
-        return fail(DETINT_E_ARTIFACT, "K/V scales that 4 bits cannot refine");
-    }
     if (kv4 ? (cudaMalloc(&m->k4, toks * d / 2) != cudaSuccess || cudaMalloc(&m->v4, toks * d / 2) != cudaSuccess ||
                cudaMalloc(&m->ks4, toks) != cudaSuccess || cudaMalloc(&m->vs4, toks) != cudaSuccess ||
                cudaMalloc(&m->kvp4, kvp4.size() * 4) != cudaSuccess)

@@ -110,3 +110,29 @@ def test_views_refuse_cpu_tensors():
         pkg.KV4Cache(u8(4, 2, 64, 32), u8(4, 2, 64, 32), u8(4, 2, 64), u8(4, 2, 64), i32(1, 4), i32(2, 72), 8)
     with pytest.raises(ValueError):
         pkg.RopeNorm(None, None)
+
+
+@pytest.mark.parametrize("change", [{0: (1 << 27) // 7 + 1}, {2: 1 << 28}, {2: (1 << 31) - 1}, {0: 0}, {2: -3}, {4: 0}, {6: -1},
+                                    {1: 0}, {3: 64}, {1: (1 << 31) - 1}, {5: -40}, {5: 90}, {5: (1 << 31) - 1}, {7: 70},
+                                    {7: -(1 << 31)}, {8: 4}, {9: -1}, {8 + 31: 1 << 20}])
+def test_load_refuses_artifact_scales_outside_the_domain(L, tiny_artifact, tmp_path, change):
+    """K/V parameters of the last layer's last kv head that the 4-bit cache's
+    arithmetic does not define: refused before anything is sent to a GPU."""
+    import hashlib
+
+    import numpy as np
+
+    import float_model
+    data = bytearray(open(tiny_artifact, "rb").read())
+    kvp = np.array(float_model.load(tiny_artifact)["layers"][-1]["kvp"], np.int32)
+    at = data.rfind(kvp.tobytes())
+    assert at > 0 and kvp.shape[1] == 40
+    for i, x in change.items():
+        kvp[-1, i] = x
+    data[at:at + kvp.nbytes] = kvp.tobytes()
+    path = tmp_path / "changed.detint"
+    path.write_bytes(data)
+    (tmp_path / "changed.detint.sha256").write_text(hashlib.sha256(data).hexdigest())
+    h = C.c_void_p()
+    assert L.detint_load_kv(str(path).encode(), 1, 16, 4, None, C.byref(h)) == 5 and not h.value
+    assert b"4 bits" in L.detint_last_error()
