@@ -247,6 +247,9 @@ class RopeNorm:
             self.device = cos.device
             _expect("RopeNorm", "cos", cos, torch.int16, max_pos * rot // 2, cos.device)
             _expect("RopeNorm", "sin", sin, torch.int16, max_pos * rot // 2, cos.device)
+        for name, t in (("cos", cos), ("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+            if t is not None and not t.is_cuda:              # the others have to be where these are
+                raise ValueError(f"RopeNorm: {name}: a cuda tensor expected, got one on {t.device}")
         self._gammas = 0 if q_gamma is None else q_gamma.numel()
         for name, t in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
             if t is not None:

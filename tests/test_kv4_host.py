@@ -136,3 +136,16 @@ def test_load_refuses_artifact_scales_outside_the_domain(L, tiny_artifact, tmp_p
     h = C.c_void_p()
     assert L.detint_load_kv(str(path).encode(), 1, 16, 4, None, C.byref(h)) == 5 and not h.value
     assert b"4 bits" in L.detint_last_error()
+
+
+def test_rotation_tables_and_gammas_in_host_memory_are_refused():
+    """The kernels read them: a view of cpu tensors may not reach a launch."""
+    torch = pytest.importorskip("torch")
+    import deterministic_integer_only_gb300 as pkg
+    i16 = lambda *s: torch.zeros(*s, dtype=torch.int16)  # noqa: E731
+    with pytest.raises(ValueError, match="cuda"):
+        pkg.RopeNorm(i16(16, 32), i16(16, 32))
+    with pytest.raises(ValueError, match="cuda"):
+        pkg.RopeNorm(None, None, max_pos=16, q_gamma=i16(64), k_gamma=i16(64))
+    with pytest.raises(ValueError, match="cuda"):
+        pkg.RopeNorm(None, None, max_pos=16, k_gamma=i16(64))
