@@ -256,6 +256,8 @@ class RopeNorm:
                 self.device = self.device or t.device
                 _expect("RopeNorm", name, t, torch.int16, self._gammas, self.device)
         self._index = None if self.device is None else self.device.index
+        if not (abs(max_pos) < 1 << 31 and abs(eps) < 1 << 31):          # (would be cut to 32 bits on the way)
+            raise ValueError(f"RopeNorm: max_pos {max_pos} or eps {eps} out of range")
         self._keep = (cos, sin, q_gamma, k_gamma)
         self._c = _Rope(_ptr(cos), _ptr(sin), int(max_pos), rot, int(bool(interleaved)), int(eps), _ptr(q_gamma),
                         _ptr(k_gamma))
@@ -344,8 +346,10 @@ def detint_kv4_append(cache, rope, qkv, tok_seq, tok_pos, q8=None, mq=None, kq=N
 def detint_kv4_workspace(cache, n_tok: int, max_len: int) -> int:
     """Bytes of workspace for every detint_kv4_decode of up to n_tok tokens and
     max_len keys; 0 for most sizes."""
-    n = C.c_longlong(0)
-    _check(lib().detint_kv4_workspace(cache._ref, int(n_tok), int(max_len), C.byref(n)), "detint_kv4_workspace")
+    w, n = "detint_kv4_workspace", C.c_longlong(0)
+    if n_tok >> 31 or max_len >> 31:                     # (would be cut to 32 bits on the way)
+        raise DetintError(1, w, f"n_tok {n_tok} or max_len {max_len} out of range")
+    _check(lib().detint_kv4_workspace(cache._ref, int(n_tok), int(max_len), C.byref(n)), w)
     return int(n.value)
 
 

@@ -149,3 +149,23 @@ def test_rotation_tables_and_gammas_in_host_memory_are_refused():
         pkg.RopeNorm(None, None, max_pos=16, q_gamma=i16(64), k_gamma=i16(64))
     with pytest.raises(ValueError, match="cuda"):
         pkg.RopeNorm(None, None, max_pos=16, k_gamma=i16(64))
+
+
+def test_integers_past_32_bits_are_refused(L):
+    """They were cut to their low 32 bits on the way to the library: 2^32 + 1
+    tokens asked for the workspace of one."""
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+
+    import deterministic_integer_only_gb300 as pkg
+    c = _cache()
+    cache = SimpleNamespace(_ref=C.addressof(c), _index=0, device="cuda:0",
+                            _torch=SimpleNamespace(_C=SimpleNamespace(_cuda_getDevice=lambda: 0)))
+    for n_tok, max_len in (((1 << 32) + 1, 64), (1, (1 << 32) + 64), (1 << 31, 64), (1, -(1 << 32) + 64)):
+        with pytest.raises(pkg.DetintError) as e:
+            pkg.detint_kv4_workspace(cache, n_tok, max_len)
+        assert e.value.code == 1
+    for kw in (dict(max_pos=(1 << 32) + 16), dict(max_pos=16, eps=(1 << 32) + 17), dict(max_pos=16, eps=-(1 << 32))):
+        with pytest.raises(ValueError):
+            pkg.RopeNorm(None, None, **kw)
+    assert pkg.RopeNorm(None, None, max_pos=(1 << 31) - 1, eps=17)._c.eps == 17
