@@ -283,13 +283,17 @@ def _row_stride(where, name, t, dtype, rows, width, index) -> int:
                      f"{tuple(t.shape)} on {t.device}")
 
 
+def _kv4_current(where, cache):
+    if cache._torch._C._cuda_getDevice() != cache._index:
+        raise ValueError(f"{where}: the cache is on {cache.device}, which is not the current device")
+
+
 def _kv4_call(where, cache, q8, mq, kq, tok_seq, tok_pos, stream):
     """The checks the kv4 operators share: tokens and query buffers (None:
     to be made). Returns (tokens, raw stream)."""
     index, torch, n = cache._index, cache._torch, tok_pos.numel()
     i32 = torch.int32
-    if torch._C._cuda_getDevice() != index:
-        raise ValueError(f"{where}: the cache is on {cache.device}, which is not the current device")
+    _kv4_current(where, cache)
     rows = n * cache.n_q
     if _unfit(tok_pos, i32, n, index) or _unfit(tok_seq, i32, n, index) or \
             mq is not None and _unfit(mq, i32, rows, index) or kq is not None and _unfit(kq, i32, rows, index) or \
@@ -349,6 +353,7 @@ def detint_kv4_workspace(cache, n_tok: int, max_len: int) -> int:
     w, n = "detint_kv4_workspace", C.c_longlong(0)
     if n_tok >> 31 or max_len >> 31:                     # (would be cut to 32 bits on the way)
         raise DetintError(1, w, f"n_tok {n_tok} or max_len {max_len} out of range")
+    _kv4_current(w, cache)
     _check(lib().detint_kv4_workspace(cache._ref, int(n_tok), int(max_len), C.byref(n)), w)
     return int(n.value)
 

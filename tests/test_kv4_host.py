@@ -169,3 +169,16 @@ def test_integers_past_32_bits_are_refused(L):
         with pytest.raises(ValueError):
             pkg.RopeNorm(None, None, **kw)
     assert pkg.RopeNorm(None, None, max_pos=(1 << 31) - 1, eps=17)._c.eps == 17
+
+
+def test_workspace_query_wants_the_caches_device(L):
+    """The split depends on the device's SMs: a query on another current device
+    is refused, as the calls it is for are."""
+    from types import SimpleNamespace
+
+    import deterministic_integer_only_gb300 as pkg
+    c = _cache()
+    cache = SimpleNamespace(_ref=C.addressof(c), _index=1, device="cuda:1",
+                            _torch=SimpleNamespace(_C=SimpleNamespace(_cuda_getDevice=lambda: 0)))
+    with pytest.raises(ValueError, match="current device"):
+        pkg.detint_kv4_workspace(cache, 1, 64)
