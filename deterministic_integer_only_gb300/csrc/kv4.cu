@@ -378,6 +378,7 @@ int check_cache(const char* where, const detint_kv4_t* c, Kv4Args* a) {
     if (c->n_blocks < 1 || c->n_seq < 1 || c->max_blocks < 1) return err(DETINT_E_ARG, "n_blocks, n_seq and max_blocks must be positive");
     if (mis(c->k, 16) || mis(c->v, 16) || mis(c->k_scale, 16) || mis(c->v_scale, 16) || mis(c->params, 16))
         return err(DETINT_E_ARG, "pages, scale codes and parameters must be 16-byte aligned");
+    if (mis(c->block_table, 4) || mis(c->status, 4)) return err(DETINT_E_ARG, "block_table and status must be 4-byte aligned");
     a->nq = c->n_q; a->n_kv = c->n_kv; a->n_blocks = c->n_blocks; a->n_seq = c->n_seq; a->max_blocks = c->max_blocks;
     a->gmul = (65536 + c->n_q / c->n_kv - 1) / (c->n_q / c->n_kv);
     a->k = c->k; a->v = c->v; a->ks = c->k_scale; a->vs = c->v_scale;
@@ -395,6 +396,7 @@ int check_attn(const char* where, const detint_kv4_t* c, const int8_t* q8, const
     if (n_tok < 1) return err(DETINT_E_ARG, "n_tok must be positive");
     if (max_len < 1 || max_len > KV4_MAX_LEN) return err(DETINT_E_ARG, "max_len must be in 1..524288");
     if (window < 0) return err(DETINT_E_ARG, "window must not be negative");
+    if (mis(tok_seq, 4) || mis(tok_pos, 4) || mis(mq, 4) || mis(kq, 4)) return err(DETINT_E_ARG, "tokens and scales must be 4-byte aligned");
     if (mis(q8, 16) || mis(o, 8)) return err(DETINT_E_ARG, "q8 must be 16-byte and o 8-byte aligned");
     if (o_stride < (long long)c->n_q * c->head_dim || (o_stride & 1)) return err(DETINT_E_ARG, "o_stride must be even and hold a row");
     *p = Kv4Attn{};
@@ -428,6 +430,7 @@ int detint_kv4_append(const detint_kv4_t* c, const detint_rope_t* r, const int32
     if ((long long)r->max_pos * r->rot_dim > 0x7fffffffLL) return err(DETINT_E_SHAPE, "rotation tables too large");
     if (qkv_stride < (long long)(c->n_q + 2 * c->n_kv) * d || (qkv_stride & 3) || mis(qkv, 16))
         return err(DETINT_E_ARG, "qkv rows must be 16-byte aligned and hold every head");
+    if (mis(tok_seq, 4) || mis(tok_pos, 4) || mis(mq, 4) || mis(kq, 4)) return err(DETINT_E_ARG, "tokens and scales must be 4-byte aligned");
     if (mis(q8, 16) || mis(k_val, 8) || mis(v_val, 8)) return err(DETINT_E_ARG, "outputs misaligned");
     Kv4Append p{};
     p.qkv = qkv; p.qkv_stride = (size_t)qkv_stride; p.tok_seq = tok_seq; p.tok_pos = tok_pos; p.T = n_tok;

@@ -182,3 +182,18 @@ def test_workspace_query_wants_the_caches_device(L):
                             _torch=SimpleNamespace(_C=SimpleNamespace(_cuda_getDevice=lambda: 0)))
     with pytest.raises(ValueError, match="current device"):
         pkg.detint_kv4_workspace(cache, 1, 64)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_misaligned_integers_are_refused(L, off):
+    """Int arrays off their natural boundary would be a misaligned access on the
+    GPU: an error code on the host instead."""
+    n = C.c_longlong(0)
+    for name in ("block_table", "status"):
+        c = _cache(**{name: P + off})
+        assert _append(L, c) == 1 and _attn(L, "decode", c) == 1 and _attn(L, "prefill", c) == 1
+        assert L.detint_kv4_workspace(C.addressof(c), 1, 100, C.byref(n)) == 1
+    for name in ("seq", "pos", "mq", "kq"):
+        assert _append(L, **{name: P + off}) == 1
+        assert _attn(L, "decode", **{name: P + off}) == 1 and _attn(L, "prefill", **{name: P + off}) == 1
+        assert b"aligned" in L.detint_last_error()
