@@ -260,8 +260,12 @@ int detint_model_info(detint_model* m, int32_t* info);
  * replayed after they changed: tok_seq[t] is a row of the block table,
  * tok_pos[t] the token's position in its sequence. A negative position marks
  * a padding token: nothing is appended for it, its query codes are zero and
- * its attention output is a zero row. A position or a block outside its range
- * sets slot 1 of `status`; the token is then treated as padding, the page as
+ * its attention output is a zero row. What is outside its range sets slot 1
+ * of `status`: for a position past the rotation's max_pos append does as for
+ * padding; where the sequence, the position or the page is outside the block
+ * table or the pool it leaves the token's keys and values out and quantises
+ * its query all the same. Attention gives a zero row for a token outside the
+ * table or past max_len; the keys of a page outside the pool are
  * masked. All three operators are exact integer arithmetic: the same inputs
  * give the same bits whatever the batch, the split or the kernel. */
 typedef struct {
