@@ -364,7 +364,11 @@ int failed(int code, const char* where, const char* what) {
     snprintf(msg, sizeof msg, "%s: %s", where, what);
     return set_last_error(code, msg);
 }
-int cuda_fail(const char* where, cudaError_t e) { return failed(DETINT_E_CUDA, where, cudaGetErrorString(e)); }
+// (the error is reported here and not left for the check of the next launch)
+int cuda_fail(const char* where, cudaError_t e) {
+    cudaGetLastError();
+    return failed(DETINT_E_CUDA, where, cudaGetErrorString(e));
+}
 bool mis(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) != 0; }
 
 // the checks every entry point shares; fills the kernels' view of the cache

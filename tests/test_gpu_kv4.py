@@ -680,3 +680,48 @@ def test_a_workspace_serves_smaller_calls(torch, n_q, n_kv, d, T, hi):
             assert torch.equal(got, exp[:n]), (n, window)
     assert (buf[need:] == 0x5A).all()
     assert not dev.status.any()
+
+
+REFUSED_LAUNCH = """
+import ctypes, sys
+sys.path[:0] = [%(root)r, %(tests)r]
+import numpy as np, torch
+import deterministic_integer_only_gb300 as pkg
+import test_gpu_kv4 as t
+rng = np.random.default_rng(17)
+pages, tab, prm, dev = t._step_setup(torch, rng, 4, 2, 64, 1, 64)
+ref = t.Dev(torch, pages, tab, prm, 4)
+q = [t.cuda(torch, a) for a in t.kp.queries(1, 4, 64, rng)]
+seq, pos = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.full((1,), 5, dtype=torch.int32, device="cuda")
+qkv = t.cuda(torch, np.rint(rng.normal(0, 4096, (1, 8 * 64))).astype(np.int32))
+rope = pkg.RopeNorm(*(t.cuda(torch, a) for a in t.tables(64, 64)))
+out, q2 = torch.zeros((1, 256), dtype=torch.int32, device="cuda"), [torch.empty_like(a) for a in q]
+want = pkg.detint_kv4_append(ref.cache, rope, qkv, seq, pos)
+pkg.detint_kv4_decode(dev.cache, *q, seq, pos, 64, out=out)
+torch.cuda.synchronize()
+legacy, other, codes, raw = torch.cuda.default_stream(), torch.cuda.Stream(), [], ctypes.c_void_p()
+torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(raw))     # one that the legacy stream would wait for
+calls = (lambda: pkg.detint_kv4_decode(dev.cache, *q, seq, pos, 64, out=out, stream=legacy),
+         lambda: pkg.detint_kv4_append(dev.cache, rope, qkv, seq, pos, *q2, stream=other))
+try:
+    with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=torch.cuda.ExternalStream(raw.value)):
+        for call in calls:
+            try:
+                call()
+                codes.append(0)
+            except pkg.DetintError as e:
+                codes.append(e.code)
+except RuntimeError:                # the refused launch ended the capture
+    pass
+other.synchronize()
+assert codes == [7, 0], codes
+assert all(torch.equal(a, b) for a, b in zip(q2, want)) and torch.equal(dev.k, ref.k) and torch.equal(dev.v, ref.v)
+"""
+
+
+def test_a_refused_launch_does_not_fail_the_next_call(torch):
+    """A launch that CUDA refuses on the host (on the legacy stream while another
+    is being captured) is that call's error and not the next one's."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = REFUSED_LAUNCH % dict(root=os.path.dirname(here), tests=here)
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
