@@ -293,7 +293,8 @@ def _kv4_call(where, cache, q8, mq, kq, tok_seq, tok_pos, stream):
     to be made). Returns (tokens, raw stream)."""
     index, torch, n = cache._index, cache._torch, tok_pos.numel()
     i32 = torch.int32
-    _kv4_current(where, cache)
+    if torch._C._cuda_getDevice() != index:
+        _kv4_current(where, cache)                       # words the error
     rows = n * cache.n_q
     if _unfit(tok_pos, i32, n, index) or _unfit(tok_seq, i32, n, index) or \
             mq is not None and _unfit(mq, i32, rows, index) or kq is not None and _unfit(kq, i32, rows, index) or \
