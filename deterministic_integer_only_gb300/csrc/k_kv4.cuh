@@ -576,8 +576,8 @@ __global__ void __launch_bounds__(KV4_APT, CHUNK ? 6 : 4) k_kv4_append(Kv4Args a
 
 // ------------------------------------------------------------ attention
 // a bounded wait for a phase of a bulk copy's barrier, recorded when it runs
-// out (the polls come as an argument: as an immediate, the compiler moves the
-// number with an fp16 instruction in some of the kernels)
+// out (the polls come as an argument: with an immediate, some of the kernels
+// counted fp16-class instructions)
 __device__ __forceinline__ void kv4_wait(unsigned long long* bar, int parity, int polls, int32_t* status) {
     const uint32_t b = smem_u32(bar);
     for (int i = polls; i > 0; --i)
@@ -1088,11 +1088,11 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_decode(Kv4Args a, Kv4Attn p) 
 // shared memory, then to the unit's by 64-bit integer atomics (exact, so their
 // order does not matter), and the unit's last CTA divides. Nothing waits for
 // another warp in either stream. (With a barrier per tile of 8 pages and a
-// warp per 16 channels the second launch took 115 us instead of the listed
-// 64 x 4k-16k contexts' 67 us of tensor time; handing half of the channels to
-// the dp4a pipe made the barriers longer, 135 us. One cooperative launch drawing
-// both kinds of work from a counter took 67 and 180 us where the two take 48
-// and 176: 1 token of 131071 keys, and the 64 above.) Scores cost 8 bytes of
+// warp per 16 channels the second launch took 115 us over 64 contexts of 4 k to
+// 16 k keys, 32 + 8 heads of 128, whose tensor time is 67 us; handing half of the
+// channels to the dp4a pipe made the barriers longer, 135 us. One cooperative
+// launch drawing both kinds of work from a counter took 67 and 180 us where the
+// two took 48 and 176: 1 token of 131071 keys, and those 64.) Scores cost 8 bytes of
 // traffic per key and head, mostly in L2; K and V are read once, with an
 // evict-first policy.
 // Bound: at 64 x 4k-16k the score launch takes 66 us, 5.2 TB/s of K with the ALU

@@ -280,7 +280,9 @@ cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p, int d, cudaSt
 size_t kv4_decode_ws(const Kv4Args& a, int d, int T, int max_len);
 size_t kv4_decode_need(const Kv4Args& a, int d, int T, int max_len, int window);
 cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p, int d, void* ws, cudaStream_t s);
-cudaError_t kv4_init();           // once per device, outside any stream capture
+// called by every entry point: sets the kernels' attributes once per device, and
+// makes no call that a stream capture forbids
+cudaError_t kv4_init();
 
 // records the detail that detint_last_error reports; returns code
 int set_last_error(int code, const char* what);

@@ -98,7 +98,7 @@ DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len,
     // us split so, 19.8 us as two waves of half the size; 3 tokens of 300 keys, 16
     // + 8 heads of 128: 6.3 us, 7.6 with 2 pages each; 1 of 2000: 8.2 and 7.8). Where the scores of
     // such a CTA do not fit its shared memory, two launches (64 tokens of 4 k
-    // to 16 k keys, 32 + 8 heads of 128: 175 us, against 276 us in larger
+    // to 16 k keys, 32 + 8 heads of 128: 171 us, against 276 us in larger
     // clusters; at 38 tokens of 4000 keys 50 and 53 us, at 76 of 2000, where
     // the scores fit, 51 and 48 us).
     int S = 1;
@@ -114,8 +114,9 @@ DecPlan dec_plan(const DevInfo& di, const Kv4Args& a, int d, int T, int max_len,
     const long long n = units * S, places = 2 * di.sms, waves = (n + places - 1) / places;
     if (!no_ws && p.cap > 32 * KV_BLK && 4 * n < 3 * waves * places) p.two = true;
     if (p.two) {
-        // pages of a score warp: 32 warps per SM (16 tokens of 12000 keys, 32 + 8
-        // heads of 128: 55 us; with 16 warps 58, with 48 55)
+        // pages of a score warp: 32 warps per SM, of which 6 CTAs of 4 fit at a
+        // time (16 tokens of 12000 keys, 32 + 8 heads of 128: 55 us; with 16 warps
+        // 58, with 48 55)
         p.pw = 8;
         while (p.pw > 1 && units * ((mp + p.pw - 1) / p.pw) < 32LL * di.sms) p.pw >>= 1;
         p.n_sw = (mp + p.pw - 1) / p.pw;

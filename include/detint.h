@@ -69,7 +69,8 @@ int detint_load(const char* artifact_path, int max_batch, int max_ctx, detint_st
  * differ from the 8-bit model's, and are as invariant over batches, splits
  * and kernels as they are there. Its decode steps run one kernel per phase,
  * so the one-launch and staged-attention options have no effect.
- * Errors: as detint_load. */
+ * Errors: as detint_load, and ARTIFACT for K/V parameters outside that
+ * section's domain. */
 int detint_load_kv(const char* artifact_path, int max_batch, int max_ctx, int kv_bits, detint_stream_t s,
                    detint_model** out);
 
