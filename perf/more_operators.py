@@ -626,8 +626,8 @@ def run(state):
         return [s["q8"], s["mq"], s["kq"], s["kv"], s["k"], s["v"], s["ks"], s["vs"]]
     if case["op"] == "weigh":
         s["w"].zero_()
-        return detint.detint_kv4_weigh(cache, s["q8"], s["mq"], s["kq"], s["seq"], s["pos"], s["max_len"], s["w"],
-                                       window=case["window"])
+        weigh = detint.detint_kv4_weigh if case["new"] == 1 else detint.detint_kv4_weigh_block
+        return weigh(cache, s["q8"], s["mq"], s["kq"], s["seq"], s["pos"], s["max_len"], s["w"], window=case["window"])
     detint.detint_kv4_evict(cache, s["w"], s["seq"], s["lens"], s["max_len"], case["keep"], s["new_table"], sinks=case["sinks"],
                             recent=case["recent"], kept=s["kept"])
     return [s["kept"], s["k"], s["v"], s["ks"], s["vs"], s["w"]]
