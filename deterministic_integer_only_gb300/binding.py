@@ -27,7 +27,9 @@ SYMBOLS = ["detint_load", "detint_load_kv", "detint_prefill", "detint_decode_ste
            "detint_reset_seq", "detint_seq_len", "detint_status", "detint_set_graph",
            "detint_set_option", "detint_argmax_noalloc", "detint_sample", "detint_fork_seq", "detint_gemm_w16", "detint_split_w16",
            "detint_int8_peak_loop", "detint_kv4_append", "detint_kv4_workspace", "detint_kv4_decode",
-           "detint_kv4_prefill", "detint_model_info", "detint_free", "detint_strerror", "detint_last_error"]
+           "detint_kv4_prefill", "detint_kv4_append_axes", "detint_kv4_weigh", "detint_kv4_weigh_block",
+           "detint_kv4_evict", "detint_kv4_copy", "detint_beam_select", "detint_beam_workspace",
+           "detint_beam_reorder", "detint_model_info", "detint_free", "detint_strerror", "detint_last_error"]
 
 
 class DetintError(RuntimeError):
@@ -67,6 +69,15 @@ def lib():
         L.detint_kv4_workspace.argtypes = [vp, C.c_int, C.c_int, C.POINTER(ll)]
         L.detint_kv4_decode.argtypes = [vp, vp, vp, vp, vp, vp, C.c_int, C.c_int, C.c_int, vp, ll, vp, ll, vp]
         L.detint_kv4_prefill.argtypes = [vp, vp, vp, vp, vp, vp, C.c_int, C.c_int, C.c_int, vp, ll, vp]
+        L.detint_kv4_append_axes.argtypes = [vp, vp, vp, vp, C.c_int, vp, ll, vp, vp, C.c_int, vp, vp, vp, vp, vp, vp]
+        L.detint_kv4_weigh.argtypes = [vp, vp, vp, vp, vp, vp, C.c_int, C.c_int, C.c_int, vp, vp]
+        L.detint_kv4_weigh_block.argtypes = [vp, vp, vp, vp, vp, vp, C.c_int, C.c_int, C.c_int, vp, vp]
+        L.detint_kv4_evict.argtypes = [vp, vp, vp, vp, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, vp, vp, vp]
+        L.detint_kv4_copy.argtypes = [vp, vp, vp, C.c_int, vp, vp]
+        L.detint_beam_select.argtypes = [vp, ll, C.c_int, vp, vp, C.c_int, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp, vp,
+                                         ll, vp]
+        L.detint_beam_workspace.argtypes = [C.c_int, C.c_int, C.c_int, C.POINTER(ll)]
+        L.detint_beam_reorder.argtypes = [vp, vp, C.c_int, vp, vp, C.c_int, C.c_int, vp, vp, vp]
         L.detint_model_info.argtypes = [vp, i32p]
         L.detint_free.argtypes = [vp]
         L.detint_free.restype = None
@@ -223,6 +234,7 @@ class KV4Cache:
         if status is not None:
             _expect("KV4Cache", "status", status, torch.int32, 8, dev)
         self.n_q, self.n_kv, self.head_dim, self.device = int(n_q), n_kv, d, dev
+        self.n_blocks = n_blocks
         self._index, self._torch = dev.index, torch
         self._keep = (k, v, k_scale, v_scale, block_table, params, status)
         self._c = _Kv4(int(n_q), n_kv, d, n_blocks, n_seq, max_blocks, _ptr(k), _ptr(v), _ptr(k_scale),
@@ -317,13 +329,8 @@ def _new(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def detint_kv4_append(cache, rope, qkv, tok_seq, tok_pos, q8=None, mq=None, kq=None, k_val=None, v_val=None,
-                      stream=None):
-    """Norm, rotate and quantise the Q12 projections qkv [n_tok, (n_q + 2 n_kv)
-    head_dim] (int32, rows may be strided) and append keys and values to the
-    cache; returns (q8, mq, kq). k_val, v_val (int16 [n_tok, n_kv, head_dim])
-    receive the cached integers where given."""
-    w, torch, dev, index = "detint_kv4_append", cache._torch, cache.device, cache._index
+def _kv4_append(w, cache, rope, qkv, tok_seq, tok_pos, axes, q8, mq, kq, k_val, v_val, stream):
+    torch, dev, index = cache._torch, cache.device, cache._index
     n, raw = _kv4_call(w, cache, q8, mq, kq, tok_seq, tok_pos, stream)
     nq, d = cache.n_q, cache.head_dim
     stride = _row_stride(w, "qkv", qkv, torch.int32, n, (nq + 2 * cache.n_kv) * d, index)
@@ -341,11 +348,44 @@ def detint_kv4_append(cache, rope, qkv, tok_seq, tok_pos, q8=None, mq=None, kq=N
         if _unfit(v_val, torch.int16, n * cache.n_kv * d, index):
             _expect(w, "v_val", v_val, torch.int16, n * cache.n_kv * d, dev)
         vp = v_val.data_ptr()
-    rc = lib().detint_kv4_append(cache._ref, rope._ref, qkv.data_ptr(), stride, tok_seq.data_ptr(),
-                                 tok_pos.data_ptr(), n, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), kp, vp, raw)
+    if axes is None:
+        rc = lib().detint_kv4_append(cache._ref, rope._ref, qkv.data_ptr(), stride, tok_seq.data_ptr(),
+                                     tok_pos.data_ptr(), n, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), kp, vp, raw)
+    else:
+        rope_pos, axis = axes
+        n_axes = rope_pos.size(0) if rope_pos.dim() == 2 else 1
+        if _unfit(rope_pos, torch.int32, n_axes * n, index) or rope_pos.numel() != n_axes * n:
+            raise ValueError(f"{w}: rope_pos: a contiguous int32 tensor [axes, {n}] on {dev} expected, got "
+                             f"{rope_pos.dtype} {tuple(rope_pos.shape)} on {rope_pos.device}")
+        ap = 0
+        if axis is not None:
+            if _unfit(axis, torch.uint8, rope._c.rot_dim // 2, index):
+                _expect(w, "axis", axis, torch.uint8, rope._c.rot_dim // 2, dev)
+            ap = axis.data_ptr()
+        rc = lib().detint_kv4_append_axes(cache._ref, rope._ref, rope_pos.data_ptr(), ap, n_axes, qkv.data_ptr(), stride,
+                                          tok_seq.data_ptr(), tok_pos.data_ptr(), n, q8.data_ptr(), mq.data_ptr(),
+                                          kq.data_ptr(), kp, vp, raw)
     if rc:
         _check(rc, w)
     return q8, mq, kq
+
+
+def detint_kv4_append(cache, rope, qkv, tok_seq, tok_pos, q8=None, mq=None, kq=None, k_val=None, v_val=None,
+                      stream=None):
+    """Norm, rotate and quantise the Q12 projections qkv [n_tok, (n_q + 2 n_kv)
+    head_dim] (int32, rows may be strided) and append keys and values to the
+    cache; returns (q8, mq, kq). k_val, v_val (int16 [n_tok, n_kv, head_dim])
+    receive the cached integers where given."""
+    return _kv4_append("detint_kv4_append", cache, rope, qkv, tok_seq, tok_pos, None, q8, mq, kq, k_val, v_val, stream)
+
+
+def detint_kv4_append_axes(cache, rope, qkv, tok_seq, tok_pos, rope_pos, axis=None, q8=None, mq=None, kq=None,
+                           k_val=None, v_val=None, stream=None):
+    """detint_kv4_append with rotary positions rope_pos (int32 [n_tok] or [axes,
+    n_tok], 1 to 4 axes) beside the places tok_pos in the cache; axis (uint8
+    [rot_dim // 2]) names the axis of each rotated pair."""
+    return _kv4_append("detint_kv4_append_axes", cache, rope, qkv, tok_seq, tok_pos, (rope_pos, axis), q8, mq, kq, k_val,
+                       v_val, stream)
 
 
 def detint_kv4_workspace(cache, n_tok: int, max_len: int) -> int:
@@ -405,6 +445,174 @@ def detint_kv4_prefill(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, window
     if rc:
         _check(rc, w)
     return out
+
+
+def _kv4_weight(w, cache, weight):
+    need = cache.n_blocks * cache.n_kv * 64
+    if _unfit(weight, cache._torch.int64, need, cache._index):
+        _expect(w, "weight", weight, cache._torch.int64, need, cache.device)
+    return weight.data_ptr()
+
+
+def _kv4_weigh(w, fn, cache, q8, mq, kq, tok_seq, tok_pos, max_len, weight, window, stream):
+    n, raw = _kv4_call(w, cache, q8, mq, kq, tok_seq, tok_pos, stream)
+    if max_len >> 31 or window >> 31:                    # (would be cut to 32 bits on the way)
+        raise DetintError(1, w, f"max_len {max_len} or window {window} out of range")
+    wp = _kv4_weight(w, cache, weight)
+    rc = fn(cache._ref, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), tok_seq.data_ptr(), tok_pos.data_ptr(), n, max_len,
+            window, wp, raw)
+    if rc:
+        _check(rc, w)
+    return weight
+
+
+def detint_kv4_weigh(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, weight, window: int = 0, stream=None):
+    """Add the attention probabilities (Q24) of single tokens to the weights
+    (int64 [n_blocks, n_kv, 64]) of the keys that they see; returns weight."""
+    return _kv4_weigh("detint_kv4_weigh", lib().detint_kv4_weigh, cache, q8, mq, kq, tok_seq, tok_pos, max_len, weight,
+                      window, stream)
+
+
+def detint_kv4_weigh_block(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, weight, window: int = 0, stream=None):
+    """The weights of detint_kv4_weigh, bit for bit, for blocks of tokens of the
+    same sequence (tokens of a sequence stand together)."""
+    return _kv4_weigh("detint_kv4_weigh_block", lib().detint_kv4_weigh_block, cache, q8, mq, kq, tok_seq, tok_pos,
+                      max_len, weight, window, stream)
+
+
+def _ints(w, name, t, numel, index, dev):
+    if _unfit(t, _i32_type(), numel, index):
+        _expect(w, name, t, _i32_type(), numel, dev)
+    return t.data_ptr()
+
+
+def _i32_type():
+    import torch
+    return torch.int32
+
+
+def _raw(index, stream):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def detint_kv4_evict(cache, weight, seq, lens, max_len: int, keep: int, new_table, sinks: int = 0, recent: int = 0,
+                     kept=None, stream=None):
+    """Move the `keep` tokens of the largest weights (the first `sinks` and last
+    `recent` ones always) of every kv head of sequences seq (int32 [n], rows of
+    the block table) with lens (int32 [n]) tokens to the pages new_table (int32
+    [n, ceil(keep / 64)]); returns their old places, int32 [n, n_kv, keep] with -1
+    behind the last."""
+    w, n = "detint_kv4_evict", seq.numel()
+    _kv4_current(w, cache)
+    if any(x >> 31 for x in (max_len, keep, sinks, recent)):
+        raise DetintError(1, w, "max_len, keep, sinks or recent out of range")
+    wp = _kv4_weight(w, cache, weight)
+    sp, lp = (_ints(w, m, t, n, cache._index, cache.device) for m, t in (("seq", seq), ("lens", lens)))
+    tp = _ints(w, "new_table", new_table, n * ((max(keep, 1) + 63) // 64), cache._index, cache.device)
+    if kept is None:
+        kept = _new(stream, (n, cache.n_kv, max(keep, 0)), cache._torch.int32, cache.device)
+    kp = _ints(w, "kept", kept, n * cache.n_kv * keep, cache._index, cache.device)
+    rc = lib().detint_kv4_evict(cache._ref, wp, sp, lp, n, max_len, keep, sinks, recent, tp, kp, _raw(cache._index, stream))
+    if rc:
+        _check(rc, w)
+    return kept
+
+
+def detint_kv4_copy(cache, src, dst, weight=None, stream=None):
+    """Copy whole pages src[i] to dst[i] (int32 lists, a negative entry: none),
+    with their weights where given."""
+    w, n = "detint_kv4_copy", src.numel()
+    _kv4_current(w, cache)
+    sp, dp = (_ints(w, m, t, n, cache._index, cache.device) for m, t in (("src", src), ("dst", dst)))
+    wp = 0 if weight is None else _kv4_weight(w, cache, weight)
+    rc = lib().detint_kv4_copy(cache._ref, sp, dp, n, wp, _raw(cache._index, stream))
+    if rc:
+        _check(rc, w)
+
+
+# ---------------------------------------------------------------- beam search
+def _current(w, t):
+    """The index of a cuda tensor's device, which has to be the current one."""
+    import torch
+    index = t.get_device()
+    if index < 0 or torch._C._cuda_getDevice() != index:
+        raise ValueError(f"{w}: cuda tensors on the current device expected, got one on {t.device}")
+    return index
+
+
+def detint_beam_workspace(rows: int, n: int, n_out: int) -> int:
+    """Bytes of workspace for detint_beam_select of up to `rows` rows (groups
+    times beams) of n logits and n_out continuations."""
+    w, v = "detint_beam_workspace", C.c_longlong(0)
+    if rows >> 31 or n >> 31 or n_out >> 31:             # (would be cut to 32 bits on the way)
+        raise DetintError(1, w, f"rows {rows}, n {n} or n_out {n_out} out of range")
+    _check(lib().detint_beam_workspace(int(rows), int(n), int(n_out), C.byref(v)), w)
+    return int(v.value)
+
+
+def detint_beam_select(logits, scores, n_out: int, done=None, end_id: int = -1, out=None, workspace=None, stream=None):
+    """The n_out best continuations of each group of beams, best first: (parent,
+    token, score, done), int32 and for the scores int64 tensors [groups, n_out].
+    logits: int32 Q16 [groups * beams, n] (rows may be strided), -2^31 masks a
+    token; scores: int64 [groups, beams], Q16 (-2^63: no beam); done: int32
+    [groups, beams] or None. out: the four tensors, workspace: a uint8 tensor of
+    detint_beam_workspace bytes (made here where they are not given)."""
+    import torch
+    w, index, dev = "detint_beam_select", _current("detint_beam_select", logits), logits.device
+    if scores.dim() != 2 or logits.dim() != 2:
+        raise ValueError(f"{w}: logits [rows, n] and scores [groups, beams] expected")
+    groups, beams = scores.shape
+    n = logits.size(1)
+    if logits.size(0) != groups * beams:
+        raise ValueError(f"{w}: {groups} x {beams} beams, but {logits.size(0)} rows of logits")
+    stride = _row_stride(w, "logits", logits, torch.int32, groups * beams, n, index)
+    if n_out >> 31 or not -(1 << 31) <= end_id < 1 << 31:
+        raise DetintError(1, w, f"n_out {n_out} or end_id {end_id} out of range")
+    rows = groups * beams
+    if _unfit(scores, torch.int64, rows, index):
+        _expect(w, "scores", scores, torch.int64, rows, dev)
+    dp = 0 if done is None else _ints(w, "done", done, rows, index, dev)
+    if out is None:
+        shape = (groups, max(n_out, 0))
+        out = tuple(_new(stream, shape, torch.int64 if i == 2 else torch.int32, dev) for i in range(4))
+    parent, token, score, end = out
+    m = groups * n_out
+    pp, tp, ep = (_ints(w, k, t, m, index, dev) for k, t in (("parent", parent), ("token", token), ("done", end)))
+    if _unfit(score, torch.int64, m, index):
+        _expect(w, "score", score, torch.int64, m, dev)
+    if workspace is None:
+        workspace = _new(stream, detint_beam_workspace(rows, n, n_out), torch.uint8, dev)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"{w}: workspace: a contiguous tensor on {dev} expected")
+    rc = lib().detint_beam_select(logits.data_ptr(), stride, n, scores.data_ptr(), dp, groups, beams, end_id, n_out, pp, tp,
+                                  score.data_ptr(), ep, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                  _raw(index, stream))
+    if rc:
+        _check(rc, w)
+    return parent, token, score, end
+
+
+def detint_beam_reorder(block_table, parent, lens, out=None, src=None, dst=None, stream=None):
+    """Give every beam its parent's pages: block_table int32 [groups * beams,
+    max_blocks], parent int32 [groups, beams], lens int32 [groups]; out: another
+    table, or None for block_table itself. Returns (src, dst), int32 [groups,
+    beams]: the pages that detint_kv4_copy has to copy in every layer."""
+    import torch
+    w, index, dev = "detint_beam_reorder", _current("detint_beam_reorder", block_table), block_table.device
+    if parent.dim() != 2 or block_table.dim() != 2 or block_table.size(0) != parent.numel():
+        raise ValueError(f"{w}: parent [groups, beams] and block_table [groups * beams, max_blocks] expected")
+    groups, beams = parent.shape
+    rows, out = groups * beams, block_table if out is None else out
+    bp = _ints(w, "block_table", block_table, block_table.numel(), index, dev)
+    op = _ints(w, "out", out, block_table.numel(), index, dev)
+    pp, lp = _ints(w, "parent", parent, rows, index, dev), _ints(w, "lens", lens, groups, index, dev)
+    src, dst = (_new(stream, (groups, beams), torch.int32, dev) if t is None else t for t in (src, dst))
+    sp, dp = (_ints(w, m, t, rows, index, dev) for m, t in (("src", src), ("dst", dst)))
+    rc = lib().detint_beam_reorder(bp, op, block_table.size(1), pp, lp, groups, beams, sp, dp, _raw(index, stream))
+    if rc:
+        _check(rc, w)
+    return src, dst
 
 
 def chain_hash(rows, prev: bytes | None = None) -> bytes:

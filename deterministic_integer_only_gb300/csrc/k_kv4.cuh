@@ -24,6 +24,7 @@
 #pragma once
 #include "kernels.h"
 #include "ptx.cuh"
+#include "cluster.cuh"
 #include "int_device.cuh"
 
 namespace detint {
@@ -116,14 +117,40 @@ __device__ __forceinline__ int kv4_turn(int x0, int c0, int x1, int c1) {
     const int top = hi >> 13;                                // 0 or -1 when the result fits
     return max((unsigned)(top + 1) > 1u ? (hi < 0 ? -2147483647 : 2147483647) : r, -2147483647);
 }
+// Rotary positions of their own (AXES): the tile's places in the cache (-1 for
+// padding) and positions [axis][token] in shared memory, and the axes of this
+// lane's pairs, one to a byte
+constexpr int KV4_VTILE = 32;    // most tokens in a tile: a lane each
+constexpr int KV4_AXES = 4;      // axes of rotary positions
+struct Kv4Places {
+    const int *pos, *rp;
+    unsigned ax;
+    __device__ __forceinline__ int row(int j) const { return rp[(ax >> (8 * j) & 255) * KV4_VTILE]; }
+    __device__ __forceinline__ Kv4Places from(int i) const { return {pos + i, rp + i, ax}; }
+};
+// this lane's pairs as kv4_rotate deals them out; an axis that is not there counts as the last
+template <int LPH>
+__device__ __forceinline__ unsigned kv4_pair_axes(const Kv4Append& p) {
+    const int lane = threadIdx.x & (LPH - 1), R2 = p.rot >> 1, sh = R2 >> 2;
+    const int n = p.inter ? 2 : 4, i0 = p.inter ? 2 * lane : 4 * (lane < sh ? lane : lane - sh);
+    unsigned ax = 0;
+    if (p.axis && 4 * lane < p.rot)
+        for (int j = 0; j < n; ++j) ax |= (unsigned)min((int)__ldg(p.axis + i0 + j), p.n_axes - 1) << (8 * j);
+    return ax;
+}
 // the rotation of a head held as four consecutive channels per lane
-template <int LPH, bool NORM>
-__device__ __forceinline__ void kv4_rotate(const Kv4Append& p, int pos, int (&y)[4]) {
+template <int LPH, bool NORM, bool AXES>
+__device__ __forceinline__ void kv4_rotate(const Kv4Append& p, int pos, int (&y)[4], const Kv4Places& pl) {
     const int lane = threadIdx.x & (LPH - 1), R2 = p.rot >> 1;
     if (p.inter) {
         if (4 * lane < p.rot) {
-            const unsigned at = (unsigned)max(pos, 0) * R2 + 2 * lane;
-            const short2 c = __ldg((const short2*)(p.cos + at)), s = __ldg((const short2*)(p.sin + at));
+            const unsigned at = (unsigned)max(AXES ? pl.row(0) : pos, 0) * R2 + 2 * lane;
+            short2 c = __ldg((const short2*)(p.cos + at)), s = __ldg((const short2*)(p.sin + at));
+            if (AXES && (pl.ax >> 8) != (pl.ax & 255)) {
+                const unsigned a1 = (unsigned)pl.row(1) * R2 + 2 * lane + 1;
+                c.y = __ldg(p.cos + a1);
+                s.y = __ldg(p.sin + a1);
+            }
             const int a0 = y[0], a1 = y[1], a2 = y[2], a3 = y[3];
             y[0] = kv4_turn<NORM>(a0, c.x, a1, -s.x);
             y[1] = kv4_turn<NORM>(a1, c.x, a0, s.x);
@@ -134,8 +161,15 @@ __device__ __forceinline__ void kv4_rotate(const Kv4Append& p, int pos, int (&y)
         const int sh = R2 >> 2;                              // lanes between a pair's halves
         const bool first = lane < sh, in = lane < 2 * sh;
         const int src = (threadIdx.x & 31) + (first ? sh : (in ? -sh : 0));
-        const unsigned at = (unsigned)max(pos, 0) * R2 + 4 * (first ? lane : (in ? lane - sh : 0));
-        const short4 c = __ldg((const short4*)(p.cos + at)), s = __ldg((const short4*)(p.sin + at));
+        const int i0 = 4 * (first ? lane : (in ? lane - sh : 0));
+        const unsigned at = (unsigned)max(AXES ? pl.row(0) : pos, 0) * R2 + i0;
+        short4 c = __ldg((const short4*)(p.cos + at)), s = __ldg((const short4*)(p.sin + at));
+        if (AXES && pl.ax != (pl.ax & 255) * 0x01010101u) {
+            const unsigned a1 = (unsigned)pl.row(1) * R2 + i0 + 1, a2 = (unsigned)pl.row(2) * R2 + i0 + 2;
+            const unsigned a3 = (unsigned)pl.row(3) * R2 + i0 + 3;
+            c = make_short4(c.x, __ldg(p.cos + a1), __ldg(p.cos + a2), __ldg(p.cos + a3));
+            s = make_short4(s.x, __ldg(p.sin + a1), __ldg(p.sin + a2), __ldg(p.sin + a3));
+        }
         const int c4[4] = {c.x, c.y, c.z, c.w};
         const int s4[4] = {first ? -s.x : s.x, first ? -s.y : s.y, first ? -s.z : s.z, first ? -s.w : s.w};
 #pragma unroll
@@ -209,21 +243,22 @@ __device__ __forceinline__ void kv4_put_k(const Kv4Args& a, const Kv4Append& p, 
         *(short4*)(p.k_val + ((size_t)t * a.n_kv + kvh) * D + 4 * lane) = blk < 0 ? make_short4(0, 0, 0, 0) : val4(q, c);
 }
 // the page of a token of the call, -1 where nothing is appended
+template <bool AXES>
 __device__ __forceinline__ int kv4_page_of(const Kv4Args& a, const Kv4Append& p, int t, int pos, int* off) {
     *off = 0;
-    return pos >= 0 && pos < p.max_pos ? kv4_slot(a, p.tok_seq[t], pos, off) : -1;
+    return pos >= 0 && (AXES || pos < p.max_pos) ? kv4_slot(a, p.tok_seq[t], pos, off) : -1;
 }
 
 // Single tokens: q or k head `slot` of token t, every lane of the head
 // repeating what the row needs once (the latency of one row is all there is).
-template <int LPH, bool NORM>
-__device__ __forceinline__ void kv4_qk_row(const Kv4Args& a, const Kv4Append& p, int t, int slot, bool live) {
+template <int LPH, bool NORM, bool AXES>
+__device__ __forceinline__ void kv4_qk_row(const Kv4Args& a, const Kv4Append& p, int t, int slot, bool live, const Kv4Places& pl) {
     constexpr int D = 4 * LPH;
     const int lane = threadIdx.x & (LPH - 1);
     const bool isq = slot < a.nq;
     const int kvh = isq ? (slot * a.gmul) >> 16 : slot - a.nq;
-    int pos = live ? p.tok_pos[t] : -1;
-    if (pos >= p.max_pos) {
+    int pos = live ? (AXES ? pl.pos[0] : p.tok_pos[t]) : -1;
+    if (!AXES && pos >= p.max_pos) {
         if (lane == 0 && a.status) a.status[ST_CTX] = 1;
         pos = -1;
     }
@@ -252,7 +287,7 @@ __device__ __forceinline__ void kv4_qk_row(const Kv4Args& a, const Kv4Append& p,
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = kv4_x4(y[j]);
     }
-    kv4_rotate<LPH, NORM>(p, pos, y);
+    kv4_rotate<LPH, NORM, AXES>(p, pos, y, pl);
     if (isq) {
         const int E = (int)seg_max<LPH>((unsigned)max(max(e4[0], e4[1]), max(e4[2], e4[3])));
 #pragma unroll
@@ -274,7 +309,7 @@ __device__ __forceinline__ void kv4_qk_row(const Kv4Args& a, const Kv4Append& p,
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = kv4_code(y[j], R, c);
         int off;
-        const int blk = kv4_page_of(a, p, t, pos, &off);
+        const int blk = kv4_page_of<AXES>(a, p, t, pos, &off);
         kv4_put_k<LPH>(a, p, t, kvh, blk, off, y, c, live);
     }
 }
@@ -308,9 +343,9 @@ __device__ __forceinline__ u64 rows_sum(u64 (&v)[8]) {
     return v[0];
 }
 
-template <int LPH, bool NORM>
+template <int LPH, bool NORM, bool AXES>
 __device__ __forceinline__ void kv4_qk_chunk(const Kv4Args& a, const Kv4Append& p, int t0, int n, int slot, bool live,
-                                             int* st) {
+                                             int* st, const Kv4Places& pl) {
     constexpr int D = 4 * LPH, LPR = LPH / 8;
     const unsigned mask = seg_mask<LPH>();
     const int lane = threadIdx.x & (LPH - 1), base = threadIdx.x & 31 & ~(LPH - 1);
@@ -318,8 +353,8 @@ __device__ __forceinline__ void kv4_qk_chunk(const Kv4Args& a, const Kv4Append& 
     const int kvh = isq ? (slot * a.gmul) >> 16 : slot - a.nq;
     st += 4 * lane;                                          // row r at st + r D
     // lane l: position (and for keys the page) of token t0 + l
-    int pos_l = lane < n ? p.tok_pos[t0 + lane] : -1;
-    if (pos_l >= p.max_pos) {
+    int pos_l = lane < n ? (AXES ? pl.pos[lane] : p.tok_pos[t0 + lane]) : -1;
+    if (!AXES && pos_l >= p.max_pos) {
         if (a.status) a.status[ST_CTX] = 1;
         pos_l = -1;
     }
@@ -392,7 +427,7 @@ __device__ __forceinline__ void kv4_qk_chunk(const Kv4Args& a, const Kv4Append& 
         const int bl = NORM ? __shfl_sync(mask, inv.bl, base + own) : 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = NORM ? kv4_scale(y[j], g4[j], R, bl) : kv4_x4(y[j]);
-        kv4_rotate<LPH, NORM>(p, pos, y);
+        kv4_rotate<LPH, NORM, AXES>(p, pos, y, pl.from(i));
         if (isq) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[j] = NORM ? y[j] << (E - e4[j]) : sat32((i64)y[j] << (E - e4[j]));
@@ -454,23 +489,43 @@ __device__ __forceinline__ void kv4_qk_chunk(const Kv4Args& a, const Kv4Append& 
 // registers 334 and 248 us, 7 CTAs (fewer registers) 212 us; bringing the next
 // chunk to L2 ahead changed nothing.
 constexpr int KV4_APT = 128;     // append threads
-constexpr int KV4_VTILE = 32;    // most tokens in a tile: a lane each
 constexpr int KV4_CH = 16;       // rows of a chunk (at most the lanes of a head)
 
-template <int LPH, bool NORM, bool CHUNK>
+template <int LPH, bool NORM, bool CHUNK, bool AXES>
 __global__ void __launch_bounds__(KV4_APT, CHUNK ? 6 : 4) k_kv4_append(Kv4Args a, Kv4Append p) {
     constexpr int D = 4 * LPH, HPW = 32 / LPH, HPB = (KV4_APT / 32) * HPW;
     extern __shared__ __align__(16) unsigned char kv4_raw[];
     const int t0 = (int)blockIdx.x * p.tile, nt = min(p.tile, p.T - t0);
     const int lane = threadIdx.x & (LPH - 1), hd = (int)threadIdx.x / LPH;
+    __shared__ int place[AXES ? KV4_VTILE : 1], rpos[AXES ? KV4_AXES * KV4_VTILE : 1];
+    Kv4Places pl = {place, rpos, 0};
+    if (AXES) {
+        // a position outside the tables makes its token padding, and is recorded
+        if ((int)threadIdx.x < nt) {
+            const int t = t0 + (int)threadIdx.x;
+            int at = p.tok_pos[t];
+            for (int x = 0; x < p.n_axes; ++x) {
+                int v = p.rope_pos[(size_t)x * p.T + t];
+                if (at >= 0 && (v < 0 || v >= p.max_pos)) {
+                    at = -1;
+                    if (a.status) a.status[ST_CTX] = 1;
+                }
+                rpos[x * KV4_VTILE + threadIdx.x] = v < 0 || v >= p.max_pos ? 0 : v;
+            }
+            place[threadIdx.x] = at;
+        }
+        pl.ax = kv4_pair_axes<LPH>(p);
+        __syncthreads();
+    }
     if ((int)blockIdx.y < p.qk_blocks) {
         const int slot = (int)blockIdx.y * HPB + hd;
         const bool live = slot < a.nq + a.n_kv;
         if (CHUNK) {
             for (int i = 0; i < nt; i += KV4_CH)
-                kv4_qk_chunk<LPH, NORM>(a, p, t0 + i, min(KV4_CH, nt - i), live ? slot : 0, live, (int*)kv4_raw + hd * (KV4_CH * D));
+                kv4_qk_chunk<LPH, NORM, AXES>(a, p, t0 + i, min(KV4_CH, nt - i), live ? slot : 0, live, (int*)kv4_raw + hd * (KV4_CH * D),
+                                              pl.from(i));
         } else {
-            for (int i = 0; i < nt; ++i) kv4_qk_row<LPH, NORM>(a, p, t0 + i, live ? slot : 0, live);
+            for (int i = 0; i < nt; ++i) kv4_qk_row<LPH, NORM, AXES>(a, p, t0 + i, live ? slot : 0, live, pl.from(i));
         }
         return;
     }
@@ -483,7 +538,7 @@ __global__ void __launch_bounds__(KV4_APT, CHUNK ? 6 : 4) k_kv4_append(Kv4Args a
     const Kv4Fix f = kv4_fix(kvp[2], kvp[3]);
     if ((int)threadIdx.x < nt) {
         int off;
-        page[threadIdx.x] = kv4_page_of(a, p, t0 + (int)threadIdx.x, p.tok_pos[t0 + threadIdx.x], &off);
+        page[threadIdx.x] = kv4_page_of<AXES>(a, p, t0 + (int)threadIdx.x, AXES ? place[threadIdx.x] : p.tok_pos[t0 + threadIdx.x], &off);
         offs[threadIdx.x] = off;
     }
     __syncthreads();
@@ -690,30 +745,6 @@ struct Kv4DecSm {
     i64 tot[3][GT];              // RS, bl, -8 sum W
     Kv4Row row[GT];
 };
-
-__device__ __forceinline__ unsigned cl_rank() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cl_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cl_addr(const void* p, unsigned rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-    return r;
-}
-__device__ __forceinline__ int cl_ld32(const int* p, unsigned rank) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cl_addr(p, rank)) : "memory");
-    return v;
-}
-__device__ __forceinline__ i64 cl_ld64(const i64* p, unsigned rank) {
-    i64 v;
-    asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(cl_addr(p, rank)) : "memory");
-    return v;
-}
 
 // q heads of a lane: register head i is head HPL (i / HPL ^ subh) + i % HPL,
 // subh the lane's place among the lanes that keep heads apart

@@ -251,6 +251,11 @@ struct Kv4Append {
     int8_t* q8;
     int32_t *mq, *kq;
     int16_t *k_val, *v_val;       // or null
+    // rotary positions of their own (rope_pos not null): [n_axes][T], and the
+    // axis of each pair [rot / 2] (null: one axis)
+    const int32_t* rope_pos;
+    const uint8_t* axis;
+    int n_axes;
 };
 struct Kv4Attn {
     const int8_t* q8;

@@ -2,19 +2,18 @@
 // the C entry points detint_kv4_*. Kernel code lives in k_kv4.cuh.
 #include <cuda_runtime.h>
 #include <stdint.h>
-#include <stdio.h>
 
 #include <algorithm>
 #include <mutex>
 
 #include "../../include/detint.h"
 #include "k_kv4.cuh"
+#include "kv4_check.h"
 
 namespace detint {
 
 namespace {
 
-constexpr int KV4_MAX_LEN = 1 << 19;       // keys: the limb sums stay in int32
 constexpr int KV4_CHUNK_MIN = 4;           // tokens of a tile from which append takes chunks
 
 struct DevInfo {
@@ -43,12 +42,16 @@ const DecFn DEC_PV[2][4] = {{k_kv4_pv<64, 1>, k_kv4_pv<64, 2>, k_kv4_pv<64, 4>, 
 int scores_smem(int d) { return (d == 128 ? Kv4Ring<128>::BYTES : Kv4Ring<64>::BYTES) / 2; }   // 4 of 8 warps
 
 using AppFn = void (*)(Kv4Args, Kv4Append);
-AppFn append_kernel(int d, bool norm, bool chunk) {
+template <bool AXES>
+AppFn append_of(int d, bool norm, bool chunk) {
     static const AppFn f[2][2][2] = {
-        {{k_kv4_append<16, false, false>, k_kv4_append<16, false, true>}, {k_kv4_append<16, true, false>, k_kv4_append<16, true, true>}},
-        {{k_kv4_append<32, false, false>, k_kv4_append<32, false, true>}, {k_kv4_append<32, true, false>, k_kv4_append<32, true, true>}}};
+        {{k_kv4_append<16, false, false, AXES>, k_kv4_append<16, false, true, AXES>},
+         {k_kv4_append<16, true, false, AXES>, k_kv4_append<16, true, true, AXES>}},
+        {{k_kv4_append<32, false, false, AXES>, k_kv4_append<32, false, true, AXES>},
+         {k_kv4_append<32, true, false, AXES>, k_kv4_append<32, true, true, AXES>}}};
     return f[d == 128][norm][chunk];
 }
+AppFn append_kernel(int d, bool norm, bool chunk, bool axes) { return axes ? append_of<true>(d, norm, chunk) : append_of<false>(d, norm, chunk); }
 
 struct Pf {
     DecFn fn;
@@ -182,8 +185,9 @@ cudaError_t kv4_init() {
         }
     for (int d : {64, 128})
         for (int norm = 0; norm < 2; ++norm)
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(append_kernel(d, norm, true), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)append_smem(d, KV4_VTILE));
+            for (int axes = 0; axes < 2; ++axes)
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(append_kernel(d, norm, true, axes), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)append_smem(d, KV4_VTILE));
     for (const Pf& f : {PREFILL[0][0], PREFILL[0][1], PREFILL[1][0], PREFILL[1][1]})
         for (int i = 0; i < 2 && e == cudaSuccess; ++i)
             e = i ? cudaFuncSetAttribute(f.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)
@@ -212,7 +216,7 @@ cudaError_t launch_kv4_append(const Kv4Args& a, const Kv4Append& p0, int d, cuda
     while (p.tile > 1 && (long long)((p.T + p.tile - 1) / p.tile) * per_tile < 6LL * di->sms) p.tile >>= 1;
     const dim3 grid((p.T + p.tile - 1) / p.tile, per_tile);
     const size_t smem = append_smem(d, p.tile);
-    append_kernel(d, p.q_gamma != nullptr, p.tile >= KV4_CHUNK_MIN)<<<grid, KV4_APT, smem, s>>>(a, p);
+    append_kernel(d, p.q_gamma != nullptr, p.tile >= KV4_CHUNK_MIN, p.rope_pos != nullptr)<<<grid, KV4_APT, smem, s>>>(a, p);
     return cudaGetLastError();
 }
 
@@ -360,65 +364,10 @@ using namespace detint;
 
 namespace {
 
-int failed(int code, const char* where, const char* what) {
-    char msg[160];
-    snprintf(msg, sizeof msg, "%s: %s", where, what);
-    return set_last_error(code, msg);
-}
-// (the error is reported here and not left for the check of the next launch)
-int cuda_fail(const char* where, cudaError_t e) {
-    cudaGetLastError();
-    return failed(DETINT_E_CUDA, where, cudaGetErrorString(e));
-}
-bool mis(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) != 0; }
-
-// the checks every entry point shares; fills the kernels' view of the cache
-int check_cache(const char* where, const detint_kv4_t* c, Kv4Args* a) {
-    auto err = [&](int code, const char* what) { return failed(code, where, what); };
-    if (!c) return err(DETINT_E_ARG, "null cache");
-    if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->block_table || !c->params) return err(DETINT_E_ARG, "null pointer in the cache");
-    if (c->head_dim != 64 && c->head_dim != 128) return err(DETINT_E_SHAPE, "head_dim must be 64 or 128");
-    if (c->n_kv < 1 || c->n_q < 1 || c->n_q > 1024 || c->n_q % c->n_kv || c->n_q / c->n_kv > 64)
-        return err(DETINT_E_SHAPE, "n_q must be n_kv times 1..64, at most 1024");
-    if (c->n_blocks < 1 || c->n_seq < 1 || c->max_blocks < 1) return err(DETINT_E_ARG, "n_blocks, n_seq and max_blocks must be positive");
-    if (mis(c->k, 16) || mis(c->v, 16) || mis(c->k_scale, 16) || mis(c->v_scale, 16) || mis(c->params, 16))
-        return err(DETINT_E_ARG, "pages, scale codes and parameters must be 16-byte aligned");
-    if (mis(c->block_table, 4) || mis(c->status, 4)) return err(DETINT_E_ARG, "block_table and status must be 4-byte aligned");
-    a->nq = c->n_q; a->n_kv = c->n_kv; a->n_blocks = c->n_blocks; a->n_seq = c->n_seq; a->max_blocks = c->max_blocks;
-    a->gmul = (65536 + c->n_q / c->n_kv - 1) / (c->n_q / c->n_kv);
-    a->k = c->k; a->v = c->v; a->ks = c->k_scale; a->vs = c->v_scale;
-    a->block_table = c->block_table; a->params = c->params; a->status = c->status;
-    return DETINT_OK;
-}
-
-int check_attn(const char* where, const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq,
-               const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int max_len, int window, int32_t* o,
-               long long o_stride, Kv4Args* a, Kv4Attn* p) {
-    auto err = [&](int code, const char* what) { return failed(code, where, what); };
-    const int rc = check_cache(where, c, a);
-    if (rc) return rc;
-    if (!q8 || !mq || !kq || !tok_seq || !tok_pos || !o) return err(DETINT_E_ARG, "null pointer");
-    if (n_tok < 1) return err(DETINT_E_ARG, "n_tok must be positive");
-    if (max_len < 1 || max_len > KV4_MAX_LEN) return err(DETINT_E_ARG, "max_len must be in 1..524288");
-    if (window < 0) return err(DETINT_E_ARG, "window must not be negative");
-    if (mis(tok_seq, 4) || mis(tok_pos, 4) || mis(mq, 4) || mis(kq, 4)) return err(DETINT_E_ARG, "tokens and scales must be 4-byte aligned");
-    if (mis(q8, 16) || mis(o, 8)) return err(DETINT_E_ARG, "q8 must be 16-byte and o 8-byte aligned");
-    if (o_stride < (long long)c->n_q * c->head_dim || (o_stride & 1)) return err(DETINT_E_ARG, "o_stride must be even and hold a row");
-    *p = Kv4Attn{};
-    p->q8 = q8; p->mq = mq; p->kq = kq; p->tok_seq = tok_seq; p->tok_pos = tok_pos; p->o = o; p->o_stride = (size_t)o_stride;
-    p->T = n_tok; p->G = c->n_q / c->n_kv; p->max_len = max_len;
-    p->window = window < max_len ? window : 0;      // a window that every key is in: none (any int, so no sum with it may overflow)
-    return DETINT_OK;
-}
-
-}  // namespace
-
-extern "C" {
-
-int detint_kv4_append(const detint_kv4_t* c, const detint_rope_t* r, const int32_t* qkv, long long qkv_stride,
-                      const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int8_t* q8, int32_t* mq, int32_t* kq,
-                      int16_t* k_val, int16_t* v_val, detint_stream_t sp) {
-    const char* where = "detint_kv4_append";
+// both appends; p holds the rotary positions where they are given
+int append(const char* where, const detint_kv4_t* c, const detint_rope_t* r, const int32_t* qkv, long long qkv_stride,
+           const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int8_t* q8, int32_t* mq, int32_t* kq, int16_t* k_val,
+           int16_t* v_val, Kv4Append p, detint_stream_t sp) {
     auto err = [&](int code, const char* what) { return failed(code, where, what); };
     Kv4Args a{};
     const int rc = check_cache(where, c, &a);
@@ -437,7 +386,6 @@ int detint_kv4_append(const detint_kv4_t* c, const detint_rope_t* r, const int32
         return err(DETINT_E_ARG, "qkv rows must be 16-byte aligned and hold every head");
     if (mis(tok_seq, 4) || mis(tok_pos, 4) || mis(mq, 4) || mis(kq, 4)) return err(DETINT_E_ARG, "tokens and scales must be 4-byte aligned");
     if (mis(q8, 16) || mis(k_val, 8) || mis(v_val, 8)) return err(DETINT_E_ARG, "outputs misaligned");
-    Kv4Append p{};
     p.qkv = qkv; p.qkv_stride = (size_t)qkv_stride; p.tok_seq = tok_seq; p.tok_pos = tok_pos; p.T = n_tok;
     p.cos = r->cos; p.sin = r->sin; p.max_pos = r->max_pos; p.rot = r->rot_dim; p.inter = r->interleaved;
     p.q_gamma = r->q_gamma; p.k_gamma = r->k_gamma; p.eps = r->eps;
@@ -445,6 +393,30 @@ int detint_kv4_append(const detint_kv4_t* c, const detint_rope_t* r, const int32
     cudaError_t e = kv4_init();
     if (e == cudaSuccess) e = launch_kv4_append(a, p, d, (cudaStream_t)sp);
     return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int detint_kv4_append(const detint_kv4_t* c, const detint_rope_t* r, const int32_t* qkv, long long qkv_stride,
+                      const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int8_t* q8, int32_t* mq, int32_t* kq,
+                      int16_t* k_val, int16_t* v_val, detint_stream_t sp) {
+    return append("detint_kv4_append", c, r, qkv, qkv_stride, tok_seq, tok_pos, n_tok, q8, mq, kq, k_val, v_val, Kv4Append{}, sp);
+}
+
+int detint_kv4_append_axes(const detint_kv4_t* c, const detint_rope_t* r, const int32_t* rope_pos, const uint8_t* axis,
+                           int n_axes, const int32_t* qkv, long long qkv_stride, const int32_t* tok_seq,
+                           const int32_t* tok_pos, int n_tok, int8_t* q8, int32_t* mq, int32_t* kq, int16_t* k_val,
+                           int16_t* v_val, detint_stream_t sp) {
+    const char* where = "detint_kv4_append_axes";
+    if (!rope_pos) return failed(DETINT_E_ARG, where, "null pointer");
+    if (n_axes < 1 || n_axes > KV4_AXES) return failed(DETINT_E_ARG, where, "n_axes must be in 1..4");
+    if (n_axes > 1 && !axis) return failed(DETINT_E_ARG, where, "several axes need the axis of each pair");
+    if (mis(rope_pos, 4)) return failed(DETINT_E_ARG, where, "rope_pos must be 4-byte aligned");
+    Kv4Append p{};
+    p.rope_pos = rope_pos; p.axis = axis; p.n_axes = n_axes;
+    return append(where, c, r, qkv, qkv_stride, tok_seq, tok_pos, n_tok, q8, mq, kq, k_val, v_val, p, sp);
 }
 
 int detint_kv4_workspace(const detint_kv4_t* c, int n_tok, int max_len, long long* bytes) {

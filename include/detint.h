@@ -342,6 +342,108 @@ int detint_kv4_prefill(const detint_kv4_t* c, const int8_t* q8, const int32_t* m
                        const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int max_len, int window,
                        int32_t* o, long long o_stride, detint_stream_t s);
 
+/* Append with rotary positions of their own: tok_pos[t] is the token's place in
+ * the cache, as everywhere, and rope_pos [n_axes][n_tok] (device int32) the rows
+ * of the rotation tables, one for each axis. axis [rot_dim / 2] (device uint8,
+ * values 0..n_axes - 1, larger ones count as the last) names the axis of each
+ * pair; NULL for a single axis. n_axes is 1..4: time, height and width of a
+ * picture's patches, in sections of the head or interleaved, or one axis for a
+ * token whose place is not its position any more because keys before it were
+ * evicted. A token with a rope_pos outside [0, max_pos) is treated as padding
+ * and sets slot 1 of `status`; everything else is detint_kv4_append's.
+ * Errors: ARG, SHAPE, CUDA. */
+int detint_kv4_append_axes(const detint_kv4_t* c, const detint_rope_t* r, const int32_t* rope_pos, const uint8_t* axis,
+                           int n_axes, const int32_t* qkv, long long qkv_stride, const int32_t* tok_seq,
+                           const int32_t* tok_pos, int n_tok, int8_t* q8, int32_t* mq, int32_t* kq, int16_t* k_val,
+                           int16_t* v_val, detint_stream_t s);
+
+/* ---- What a context's keys are worth, and eviction (arithmetic specification,
+ * sections 18 and 19). No passage of the pages: they keep every key. */
+
+/* Add to the weight of every key that a token sees the probabilities (Q24) that
+ * the q heads of the key's kv head give it: weight is device int64
+ * [n_blocks][n_kv][64], in the order of the scale codes, 16-byte aligned and
+ * owned by the caller, who clears it. Tokens, max_len and window are
+ * detint_kv4_decode's; a token without keys adds nothing. Sums are exact, so
+ * neither the order of the tokens nor pages that sequences share change them.
+ * Each token is a unit of its own whose keys are split over CTAs. No
+ * workspace. Errors: ARG, SHAPE, CUDA. */
+int detint_kv4_weigh(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq, const int32_t* tok_seq,
+                     const int32_t* tok_pos, int n_tok, int max_len, int window, int64_t* weight, detint_stream_t s);
+
+/* The same weights, bit for bit, for many tokens of a sequence, which should
+ * stand together: blocks of consecutive tokens of the call share a sweep over
+ * their keys on the int8 tensor pipe. Errors: ARG, SHAPE, CUDA. */
+int detint_kv4_weigh_block(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq,
+                           const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int max_len, int window,
+                           int64_t* weight, detint_stream_t s);
+
+/* Keep `keep` tokens of each of n sequences and move them to new pages. seq,
+ * lens: device int32 [n], rows of the block table and the tokens that they hold
+ * now, at most max_len. For every kv head by itself the first `sinks` and the
+ * last `recent` tokens stay, and of those between them the keep - sinks -
+ * recent of the largest weights (the lower place first among equal ones). They
+ * go, in their order, to places 0, 1, ... of the pages new_table [n][ceil(keep /
+ * 64)] (device int32), with codes, scale codes and weights; a sequence of keep
+ * tokens or fewer is moved whole. kept: device int32 [n][n_kv][keep], the old
+ * places, -1 behind the last. The new pages must be in no sequence's use;
+ * places behind the last kept token are left as they were. The caller puts the
+ * new pages into the block table, appends from place min(lens, keep) on with
+ * detint_kv4_append_axes, and may free the old pages. A token on a page outside
+ * the pool weighs 0 and moves as a zero key and value; it, a sequence outside
+ * the table, a length outside 0..max_len and a new page outside the pool (which
+ * is skipped) set slot 1 of `status`. Errors: ARG, SHAPE, CUDA. */
+int detint_kv4_evict(const detint_kv4_t* c, int64_t* weight, const int32_t* seq, const int32_t* lens, int n, int max_len,
+                     int keep, int sinks, int recent, const int32_t* new_table, int32_t* kept, detint_stream_t s);
+
+/* Copy whole pages of every kv head, src[i] to dst[i] (device int32 [n]): codes,
+ * scale codes and, where weight is given, weights. A negative entry copies
+ * nothing; one past the pool sets slot 1 of `status`. No page may be copied to
+ * twice or be both copied from and to in a call. Errors: ARG, SHAPE, CUDA. */
+int detint_kv4_copy(const detint_kv4_t* c, const int32_t* src, const int32_t* dst, int n, int64_t* weight,
+                    detint_stream_t s);
+
+/* ---- Beam search (arithmetic specification, section 17). The pages decode
+ * greedily (DetLLM blog, "DetLLM"); no passage of them defines beams. */
+
+/* The n_out (1..64) best continuations of each group of `beams` (1..64) rows.
+ * logits: device int32 Q16 rows of n elements, `stride` apart, group after
+ * group; -2^31 masks a token. scores: device int64 [groups][beams], the beams'
+ * log-probabilities in Q16; below -2^62 the beam is not there (the first step of
+ * a group has one beam). done: device int32 [groups][beams] or NULL: a beam with
+ * a nonzero entry is finished and continues with end_id alone at its score.
+ * Continuation i of a row scores score + l_i - lse(l), in whole units of Q16;
+ * the larger score comes first, then the lower beam, then the lower token.
+ * Outputs [groups][n_out], best first: parent (the beam in its group), token,
+ * score, and done_out (1 where the parent was finished or the token is end_id);
+ * where there are fewer continuations, parent and token -1, score -2^63 and
+ * done 0. scores and done may be the outputs of the call before but not of this
+ * one. end_id -1: no token ends a beam. workspace: detint_beam_workspace bytes,
+ * 16-byte aligned; calls that may overlap on the GPU, captured ones included,
+ * need one each. Up to 2^20 rows of up to 2^24 logits.
+ * Errors: ARG, SHAPE, CUDA. */
+int detint_beam_select(const int32_t* logits, long long stride, int n, const int64_t* scores, const int32_t* done,
+                       int groups, int beams, int end_id, int n_out, int32_t* parent, int32_t* token, int64_t* score,
+                       int32_t* done_out, void* workspace, long long workspace_bytes, detint_stream_t s);
+
+/* Bytes of workspace for detint_beam_select of `rows` rows (groups times beams)
+ * of n logits; enough for fewer rows and a smaller n_out. Errors: ARG. */
+int detint_beam_workspace(int rows, int n, int n_out, long long* bytes);
+
+/* The block tables of the chosen beams. block_table: device int32 [groups *
+ * beams][max_blocks]; parent: device int32 [groups][beams], as detint_beam_select
+ * gives it (outside 0..beams - 1: the beam keeps its own pages); lens: device
+ * int32 [groups], the tokens that every beam of the group holds. Row b of out
+ * (which may be block_table itself) gets its parent's whole pages, shared. Of
+ * the page that is still being filled, a beam's first child becomes the owner;
+ * each other child gets the page of a beam that has no child, and an entry of
+ * src and dst (device int32 [groups][beams], -1: none) that detint_kv4_copy
+ * takes, once per layer, before the next append. So a group needs no page that it
+ * does not have; its beams' growing pages and the entries behind them must be
+ * distinct from the start. Later columns stay. Errors: ARG, CUDA. */
+int detint_beam_reorder(const int32_t* block_table, int32_t* out, int max_blocks, const int32_t* parent, const int32_t* lens,
+                        int groups, int beams, int32_t* src, int32_t* dst, detint_stream_t s);
+
 /* Release everything the model owns. NULL is a no-op. No passage of the
  * pages: library housekeeping. */
 void detint_free(detint_model* m);
