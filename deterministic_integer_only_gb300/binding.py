@@ -458,9 +458,8 @@ def _kv4_weigh(w, fn, cache, q8, mq, kq, tok_seq, tok_pos, max_len, weight, wind
     n, raw = _kv4_call(w, cache, q8, mq, kq, tok_seq, tok_pos, stream)
     if max_len >> 31 or window >> 31:                    # (would be cut to 32 bits on the way)
         raise DetintError(1, w, f"max_len {max_len} or window {window} out of range")
-    wp = _kv4_weight(w, cache, weight)
     rc = fn(cache._ref, q8.data_ptr(), mq.data_ptr(), kq.data_ptr(), tok_seq.data_ptr(), tok_pos.data_ptr(), n, max_len,
-            window, wp, raw)
+            window, _kv4_weight(w, cache, weight), raw)
     if rc:
         _check(rc, w)
     return weight
@@ -480,20 +479,11 @@ def detint_kv4_weigh_block(cache, q8, mq, kq, tok_seq, tok_pos, max_len: int, we
                       max_len, weight, window, stream)
 
 
-def _ints(w, name, t, numel, index, dev):
-    if _unfit(t, _i32_type(), numel, index):
-        _expect(w, name, t, _i32_type(), numel, dev)
-    return t.data_ptr()
-
-
-def _i32_type():
-    import torch
-    return torch.int32
-
-
-def _raw(index, stream):
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+def _fit_all(w, named, index, device):
+    """Words the error of the first tensor that does not fit: (name, tensor, type, elements)."""
+    for name, t, dtype, numel in named:
+        if t is not None and _unfit(t, dtype, numel, index):
+            _expect(w, name, t, dtype, numel, device)
 
 
 def detint_kv4_evict(cache, weight, seq, lens, max_len: int, keep: int, new_table, sinks: int = 0, recent: int = 0,
@@ -503,17 +493,22 @@ def detint_kv4_evict(cache, weight, seq, lens, max_len: int, keep: int, new_tabl
     the block table) with lens (int32 [n]) tokens to the pages new_table (int32
     [n, ceil(keep / 64)]); returns their old places, int32 [n, n_kv, keep] with -1
     behind the last."""
-    w, n = "detint_kv4_evict", seq.numel()
-    _kv4_current(w, cache)
-    if any(x >> 31 for x in (max_len, keep, sinks, recent)):
+    w, n, index, torch = "detint_kv4_evict", seq.numel(), cache._index, cache._torch
+    i32 = torch.int32
+    if torch._C._cuda_getDevice() != index:
+        _kv4_current(w, cache)                           # words the error
+    if max_len >> 31 or keep >> 31 or sinks >> 31 or recent >> 31 or keep < 1:
         raise DetintError(1, w, "max_len, keep, sinks or recent out of range")
-    wp = _kv4_weight(w, cache, weight)
-    sp, lp = (_ints(w, m, t, n, cache._index, cache.device) for m, t in (("seq", seq), ("lens", lens)))
-    tp = _ints(w, "new_table", new_table, n * ((max(keep, 1) + 63) // 64), cache._index, cache.device)
     if kept is None:
-        kept = _new(stream, (n, cache.n_kv, max(keep, 0)), cache._torch.int32, cache.device)
-    kp = _ints(w, "kept", kept, n * cache.n_kv * keep, cache._index, cache.device)
-    rc = lib().detint_kv4_evict(cache._ref, wp, sp, lp, n, max_len, keep, sinks, recent, tp, kp, _raw(cache._index, stream))
+        kept = _new(stream, (n, cache.n_kv, keep), i32, cache.device)
+    room, places = n * ((keep + 63) >> 6), n * cache.n_kv * keep
+    if _unfit(seq, i32, n, index) or _unfit(lens, i32, n, index) or _unfit(new_table, i32, room, index) or \
+            _unfit(kept, i32, places, index):
+        _fit_all(w, (("seq", seq, i32, n), ("lens", lens, i32, n), ("new_table", new_table, i32, room),
+                     ("kept", kept, i32, places)), index, cache.device)
+    rc = lib().detint_kv4_evict(cache._ref, _kv4_weight(w, cache, weight), seq.data_ptr(), lens.data_ptr(), n, max_len, keep,
+                                sinks, recent, new_table.data_ptr(), kept.data_ptr(),
+                                torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, w)
     return kept
@@ -522,19 +517,22 @@ def detint_kv4_evict(cache, weight, seq, lens, max_len: int, keep: int, new_tabl
 def detint_kv4_copy(cache, src, dst, weight=None, stream=None):
     """Copy whole pages src[i] to dst[i] (int32 lists, a negative entry: none),
     with their weights where given."""
-    w, n = "detint_kv4_copy", src.numel()
-    _kv4_current(w, cache)
-    sp, dp = (_ints(w, m, t, n, cache._index, cache.device) for m, t in (("src", src), ("dst", dst)))
-    wp = 0 if weight is None else _kv4_weight(w, cache, weight)
-    rc = lib().detint_kv4_copy(cache._ref, sp, dp, n, wp, _raw(cache._index, stream))
+    w, n, index, torch = "detint_kv4_copy", src.numel(), cache._index, cache._torch
+    i32 = torch.int32
+    if torch._C._cuda_getDevice() != index:
+        _kv4_current(w, cache)                           # words the error
+    if _unfit(src, i32, n, index) or _unfit(dst, i32, n, index):
+        _fit_all(w, (("src", src, i32, n), ("dst", dst, i32, n)), index, cache.device)
+    rc = lib().detint_kv4_copy(cache._ref, src.data_ptr(), dst.data_ptr(), n,
+                               0 if weight is None else _kv4_weight(w, cache, weight),
+                               torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, w)
 
 
 # ---------------------------------------------------------------- beam search
-def _current(w, t):
+def _beam_device(w, torch, t):
     """The index of a cuda tensor's device, which has to be the current one."""
-    import torch
     index = t.get_device()
     if index < 0 or torch._C._cuda_getDevice() != index:
         raise ValueError(f"{w}: cuda tensors on the current device expected, got one on {t.device}")
@@ -559,35 +557,35 @@ def detint_beam_select(logits, scores, n_out: int, done=None, end_id: int = -1, 
     [groups, beams] or None. out: the four tensors, workspace: a uint8 tensor of
     detint_beam_workspace bytes (made here where they are not given)."""
     import torch
-    w, index, dev = "detint_beam_select", _current("detint_beam_select", logits), logits.device
-    if scores.dim() != 2 or logits.dim() != 2:
-        raise ValueError(f"{w}: logits [rows, n] and scores [groups, beams] expected")
+    w, i32, i64 = "detint_beam_select", torch.int32, torch.int64
+    index = _beam_device(w, torch, logits)
+    if scores.dim() != 2 or logits.dim() != 2 or logits.size(0) != scores.numel():
+        raise ValueError(f"{w}: logits [groups * beams, n] and scores [groups, beams] expected, got "
+                         f"{tuple(logits.shape)} and {tuple(scores.shape)}")
     groups, beams = scores.shape
-    n = logits.size(1)
-    if logits.size(0) != groups * beams:
-        raise ValueError(f"{w}: {groups} x {beams} beams, but {logits.size(0)} rows of logits")
-    stride = _row_stride(w, "logits", logits, torch.int32, groups * beams, n, index)
+    rows, n = logits.shape
+    stride = _row_stride(w, "logits", logits, i32, rows, n, index)
     if n_out >> 31 or not -(1 << 31) <= end_id < 1 << 31:
         raise DetintError(1, w, f"n_out {n_out} or end_id {end_id} out of range")
-    rows = groups * beams
-    if _unfit(scores, torch.int64, rows, index):
-        _expect(w, "scores", scores, torch.int64, rows, dev)
-    dp = 0 if done is None else _ints(w, "done", done, rows, index, dev)
-    if out is None:
-        shape = (groups, max(n_out, 0))
-        out = tuple(_new(stream, shape, torch.int64 if i == 2 else torch.int32, dev) for i in range(4))
-    parent, token, score, end = out
     m = groups * n_out
-    pp, tp, ep = (_ints(w, k, t, m, index, dev) for k, t in (("parent", parent), ("token", token), ("done", end)))
-    if _unfit(score, torch.int64, m, index):
-        _expect(w, "score", score, torch.int64, m, dev)
+    if out is None:
+        parent, token, end = _new(stream, (3, groups, n_out), i32, logits.device).unbind(0)
+        score = _new(stream, (groups, n_out), i64, logits.device)
+    else:
+        parent, token, score, end = out
     if workspace is None:
-        workspace = _new(stream, detint_beam_workspace(rows, n, n_out), torch.uint8, dev)
+        workspace = _new(stream, detint_beam_workspace(rows, n, n_out), torch.uint8, logits.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"{w}: workspace: a contiguous tensor on {dev} expected")
-    rc = lib().detint_beam_select(logits.data_ptr(), stride, n, scores.data_ptr(), dp, groups, beams, end_id, n_out, pp, tp,
-                                  score.data_ptr(), ep, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                  _raw(index, stream))
+        raise ValueError(f"{w}: workspace: a contiguous tensor on {logits.device} expected")
+    if _unfit(scores, i64, rows, index) or done is not None and _unfit(done, i32, rows, index) or \
+            out is not None and (_unfit(parent, i32, m, index) or _unfit(token, i32, m, index) or
+                                 _unfit(score, i64, m, index) or _unfit(end, i32, m, index)):
+        _fit_all(w, (("scores", scores, i64, rows), ("done", done, i32, rows), ("parent", parent, i32, m),
+                     ("token", token, i32, m), ("score", score, i64, m), ("done", end, i32, m)), index, logits.device)
+    rc = lib().detint_beam_select(logits.data_ptr(), stride, n, scores.data_ptr(), 0 if done is None else done.data_ptr(), groups,
+                                  beams, end_id, n_out, parent.data_ptr(), token.data_ptr(), score.data_ptr(), end.data_ptr(),
+                                  workspace.data_ptr(), workspace.nbytes,
+                                  torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, w)
     return parent, token, score, end
@@ -599,17 +597,22 @@ def detint_beam_reorder(block_table, parent, lens, out=None, src=None, dst=None,
     table, or None for block_table itself. Returns (src, dst), int32 [groups,
     beams]: the pages that detint_kv4_copy has to copy in every layer."""
     import torch
-    w, index, dev = "detint_beam_reorder", _current("detint_beam_reorder", block_table), block_table.device
+    w, i32 = "detint_beam_reorder", torch.int32
+    index = _beam_device(w, torch, block_table)
     if parent.dim() != 2 or block_table.dim() != 2 or block_table.size(0) != parent.numel():
-        raise ValueError(f"{w}: parent [groups, beams] and block_table [groups * beams, max_blocks] expected")
+        raise ValueError(f"{w}: parent [groups, beams] and block_table [groups * beams, max_blocks] expected, got "
+                         f"{tuple(parent.shape)} and {tuple(block_table.shape)}")
     groups, beams = parent.shape
-    rows, out = groups * beams, block_table if out is None else out
-    bp = _ints(w, "block_table", block_table, block_table.numel(), index, dev)
-    op = _ints(w, "out", out, block_table.numel(), index, dev)
-    pp, lp = _ints(w, "parent", parent, rows, index, dev), _ints(w, "lens", lens, groups, index, dev)
-    src, dst = (_new(stream, (groups, beams), torch.int32, dev) if t is None else t for t in (src, dst))
-    sp, dp = (_ints(w, m, t, rows, index, dev) for m, t in (("src", src), ("dst", dst)))
-    rc = lib().detint_beam_reorder(bp, op, block_table.size(1), pp, lp, groups, beams, sp, dp, _raw(index, stream))
+    rows, size, out = groups * beams, block_table.numel(), block_table if out is None else out
+    src = _new(stream, (groups, beams), i32, block_table.device) if src is None else src
+    dst = _new(stream, (groups, beams), i32, block_table.device) if dst is None else dst
+    if _unfit(block_table, i32, size, index) or _unfit(out, i32, size, index) or _unfit(parent, i32, rows, index) or \
+            _unfit(lens, i32, groups, index) or _unfit(src, i32, rows, index) or _unfit(dst, i32, rows, index):
+        _fit_all(w, (("block_table", block_table, i32, size), ("out", out, i32, size), ("parent", parent, i32, rows),
+                     ("lens", lens, i32, groups), ("src", src, i32, rows), ("dst", dst, i32, rows)), index, block_table.device)
+    rc = lib().detint_beam_reorder(block_table.data_ptr(), out.data_ptr(), block_table.size(1), parent.data_ptr(), lens.data_ptr(),
+                                   groups, beams, src.data_ptr(), dst.data_ptr(),
+                                   torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, w)
     return src, dst

@@ -14,99 +14,80 @@ namespace detint {
 
 namespace {
 
-struct DevInfo {
-    bool ready = false;
-    int sms = 0;
-    int lg_max = 3;                      // log2 of the CTAs of the largest cluster
-};
-DevInfo g_dev[64];
+int g_sms[64];                               // 0: not set up yet
 std::mutex g_mu;
 
-using RowsFn = void (*)(BeamArgs);
-constexpr int NQ = 6;
-constexpr int QUADS[NQ] = {1, 2, 4, 5, 8, 10};
-template <bool VEC>
-RowsFn rows_of(int i) {
-    static const RowsFn f[NQ + 1] = {k_beam_rows<1, true, VEC>, k_beam_rows<2, true, VEC>, k_beam_rows<4, true, VEC>,
-                                     k_beam_rows<5, true, VEC>, k_beam_rows<8, true, VEC>, k_beam_rows<10, true, VEC>,
-                                     k_beam_rows<8, false, VEC>};
-    return f[i];
-}
+// scores and tokens of the beams' lists, then a list per warp
+size_t merge_smem(int beams, int n_out) { return (((size_t)beams * n_out * 12 + 15) & ~(size_t)15) + (size_t)std::min(beams, BM_MERGE_NW) * BM_CAP * 8; }
 
-cudaError_t init(DevInfo** out) {
+// sets the kernels' attributes once per device (no call that a stream capture forbids)
+cudaError_t init(int* sms) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    DevInfo* di = *out = &g_dev[dev];
     std::lock_guard<std::mutex> lk(g_mu);
-    if (di->ready) return cudaSuccess;
-    e = cudaDeviceGetAttribute(&di->sms, cudaDevAttrMultiProcessorCount, dev);
-    int lg = 4;
-    for (int i = 0; i <= NQ; ++i)
-        for (int v = 0; v < 2 && e == cudaSuccess; ++v) {
-            const RowsFn f = v ? rows_of<true>(i) : rows_of<false>(i);
-            e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            cudaLaunchConfig_t cfg = {};
-            cudaLaunchAttribute at[1];
-            at[0].id = cudaLaunchAttributeClusterDimension;
-            at[0].val.clusterDim.x = 16;
-            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-            cfg.gridDim = dim3(16);
-            cfg.blockDim = dim3(BM_THREADS);
-            cfg.attrs = at;
-            cfg.numAttrs = 1;
-            int n = 0;
-            if (e == cudaSuccess && (cudaOccupancyMaxActiveClusters(&n, f, &cfg) != cudaSuccess || n < 1)) {
-                cudaGetLastError();
-                lg = 3;
-            }
-        }
-    if (e == cudaSuccess) {
-        di->lg_max = lg;
-        di->ready = true;
-    }
+    if ((*sms = g_sms[dev])) return cudaSuccess;
+    int n = 0;
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_beam_merge, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)merge_smem(BM_MAX_OUT, BM_MAX_OUT));
+    if (e == cudaSuccess) *sms = g_sms[dev] = n;
     return e;
 }
 
 size_t a256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-cudaError_t launch_select(const DevInfo& di, BeamArgs a, int groups, cudaStream_t s) {
-    const int quads = (a.n + 3) / 4;
-    int lg = 0;
-    while (lg < di.lg_max && quads > BM_THREADS << lg && ((long long)a.rows << (lg + 1)) <= 4LL * di.sms) ++lg;
-    while (lg < di.lg_max && quads > (QUADS[NQ - 1] * BM_THREADS) << lg) ++lg;
-    int i = 0;
-    while (i < NQ && quads > (QUADS[i] * BM_THREADS) << lg) ++i;
-    const int entries = BM_WARPS << lg;
-    a.lg_cl = lg;
-    a.lg_groups = 0;
-    while ((1 << a.lg_groups) < a.n_out && (1 << a.lg_groups) < entries) ++a.lg_groups;
-    a.per_warp = (a.n_out + entries - 1) / entries;
+struct WsLayout { size_t part_key, key, sum, list, top, most, count, total; };
+WsLayout ws_layout(size_t rows) {
+    // (of the most parts that a row can have: enough for shorter rows too)
+    WsLayout w{};
+    size_t o = 0;
+    w.part_key = o; o += a256(rows * BM_PARTS * 8);
+    w.key = o; o += a256(rows * BM_PARTS * BM_NW * 8);
+    w.sum = o; o += a256(rows * BM_PARTS * 8);
+    w.list = o; o += a256(rows * BM_CAP * 8);
+    w.top = o; o += a256(rows * BM_PARTS * 4);
+    w.most = o; o += a256(rows * 4);
+    w.count = o; o += a256(rows * 4);
+    w.total = o;
+    return w;
+}
+
+cudaError_t launch_select(BeamArgs a, int groups, int sms, cudaStream_t s) {
+    const int all = (a.n + BM_ROUND - 1) / BM_ROUND;
+    // parts: up to 6 CTAs per SM, of which 4 of k_beam_sum run at a time, so that
+    // what a CTA does once is not done too often (24 x 5 rows of 128256 logits:
+    // 28.7 us, with 12 30.6, with 24 39; with 4 29.7)
+    int most = BM_PARTS;
+    while (most > 1 && (long long)groups * a.beams * std::min(most, all) > 6LL * sms) --most;
+    a.rounds = (all + most - 1) / most;
+    a.parts = (all + a.rounds - 1) / a.rounds;
+    // entries that the n_out-th largest value is looked for among: twice as many
+    // as continuations, so that the bound is well above their least
+    a.per_part = a.parts >= 2 * a.n_out ? a.n_out : 0;
+    a.lanes = std::min(32, (2 * a.n_out + a.parts * BM_NW - 1) / (a.parts * BM_NW));
+    a.per_warp = (a.n_out + a.lanes - 1) / a.lanes;
     const bool vec = !(a.stride & 3) && !mis(a.logits, 16);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
-    cfg.attrs = at;
-    cfg.stream = s;
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1 << lg;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3(a.rows << lg);
-    cfg.blockDim = dim3(BM_THREADS);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, vec ? rows_of<true>(i) : rows_of<false>(i), a);
-    if (e != cudaSuccess) return e;
-    // starts while the rows' launch drains
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.stream = s;
+    cfg.gridDim = dim3(a.parts, groups * a.beams);
+    cfg.blockDim = dim3(BM_NT);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, vec ? k_beam_top<true> : k_beam_top<false>, a);
+    cfg.numAttrs = 1;                                    // the others start while the one before drains
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, vec ? k_beam_sum<true> : k_beam_sum<false>, a);
     cfg.gridDim = dim3(groups);
-    cfg.blockDim = dim3(BM_MERGE_THREADS);
-    cfg.dynamicSmemBytes = (size_t)a.beams * a.n_out * 8;
-    return cudaLaunchKernelEx(&cfg, k_beam_merge, a);
+    cfg.blockDim = dim3(BM_MERGE);
+    cfg.dynamicSmemBytes = merge_smem(a.beams, a.n_out);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k_beam_merge, a);
+    return e;
 }
 
 constexpr int MAX_VOCAB = 1 << 24;           // the sum of a row's exponentials stays below 2^55
-constexpr int MAX_ROWS = 1 << 20;
+constexpr int MAX_ROWS = 65535;
 
 }  // namespace
 }  // namespace detint
@@ -118,7 +99,7 @@ extern "C" {
 int detint_beam_workspace(int rows, int n, int n_out, long long* bytes) {
     if (!bytes || rows < 1 || rows > MAX_ROWS || n < 1 || n > MAX_VOCAB || n_out < 1 || n_out > BM_MAX_OUT)
         return failed(DETINT_E_ARG, "detint_beam_workspace", "bad arguments");
-    *bytes = (long long)(a256((size_t)rows * n_out * 8) + a256((size_t)rows * n_out * 4));
+    *bytes = (long long)ws_layout((size_t)rows).total;
     return DETINT_OK;
 }
 
@@ -130,7 +111,7 @@ int detint_beam_select(const int32_t* logits, long long stride, int n, const int
     if (!logits || !scores || !parent || !token || !score || !done_out) return err(DETINT_E_ARG, "null pointer");
     if (groups < 1 || beams < 1 || beams > BM_MAX_OUT) return err(DETINT_E_ARG, "groups must be positive, beams in 1..64");
     if (n_out < 1 || n_out > BM_MAX_OUT) return err(DETINT_E_ARG, "n_out must be in 1..64");
-    if ((long long)groups * beams > MAX_ROWS) return err(DETINT_E_ARG, "more than 2^20 rows");
+    if ((long long)groups * beams > MAX_ROWS) return err(DETINT_E_ARG, "more than 65535 rows");
     if (n < 1 || n > MAX_VOCAB) return err(DETINT_E_SHAPE, "a row must have 1..2^24 logits");
     if (stride < n) return err(DETINT_E_ARG, "the stride must hold a row");
     if (end_id < -1 || end_id >= n || (done && end_id < 0)) return err(DETINT_E_ARG, "end_id must be a token, or -1 without done");
@@ -143,13 +124,20 @@ int detint_beam_select(const int32_t* logits, long long stride, int n, const int
         return err(DETINT_E_ARG, "a 16-byte aligned workspace of detint_beam_workspace bytes is needed");
     BeamArgs a{};
     a.logits = logits; a.stride = (size_t)stride; a.scores = (const long long*)scores; a.done = done;
-    a.rows = groups * beams; a.n = n; a.n_out = n_out; a.end_id = end_id; a.beams = beams;
-    a.ws_score = (long long*)workspace;
-    a.ws_tok = (int32_t*)((unsigned char*)workspace + a256((size_t)a.rows * n_out * 8));
+    a.n = n; a.n_out = n_out; a.end_id = end_id; a.beams = beams;
+    unsigned char* ws = (unsigned char*)workspace;
+    const WsLayout w = ws_layout((size_t)groups * beams);
+    a.part_key = (unsigned long long*)(ws + w.part_key);
+    a.key = (unsigned long long*)(ws + w.key);
+    a.sum = (unsigned long long*)(ws + w.sum);
+    a.list = (unsigned long long*)(ws + w.list);
+    a.top = (int32_t*)(ws + w.top);
+    a.most = (int32_t*)(ws + w.most);
+    a.count = (unsigned*)(ws + w.count);
     a.parent = parent; a.token = token; a.done_out = done_out; a.score_out = (long long*)score;
-    DevInfo* di = nullptr;
-    cudaError_t e = init(&di);
-    if (e == cudaSuccess) e = launch_select(*di, a, groups, (cudaStream_t)sp);
+    int sms = 0;
+    cudaError_t e = init(&sms);
+    if (e == cudaSuccess) e = launch_select(a, groups, sms, (cudaStream_t)sp);
     return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
 }
 

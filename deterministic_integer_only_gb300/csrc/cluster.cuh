@@ -16,6 +16,8 @@ __device__ __forceinline__ unsigned cl_rank() {
 __device__ __forceinline__ void cl_sync() {
     asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
+__device__ __forceinline__ void cl_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cl_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cl_addr(const void* p, unsigned rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
@@ -39,6 +41,9 @@ __device__ __forceinline__ unsigned cl_size() {
 __device__ __forceinline__ unsigned cl_ld32u(const unsigned* p, unsigned rank) { return (unsigned)cl_ld32((const int*)p, rank); }
 __device__ __forceinline__ void cl_st64(u64* p, unsigned rank, u64 v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cl_addr(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void cl_st32(int* p, unsigned rank, int v) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(cl_addr(p, rank)), "r"(v) : "memory");
 }
 __device__ __forceinline__ unsigned cl_add32(unsigned* p, unsigned rank, unsigned v) {
     unsigned old;

@@ -7,25 +7,29 @@
 // so the maximum is settled over the whole row first; within a row the order
 // is that of the logits, so a row's best n need no lse.
 //
-// One thread-block cluster per row, its values in registers between the
-// passes: one read of the logits. Pass 1 takes maxima; the cluster's warps are
-// put into at least n groups, and the smallest of the groups' maxima is a
-// bound that n values or more reach and few more do (about g ln g of g
-// groups, whatever the row's distribution, as every group samples the whole
-// row). Pass 2 sums the exponentials and hands what reaches the bound to the
-// cluster's first CTA, which ranks it by counting. Values carry their index
-// as the low half of a 64-bit key, so that equal logits do not all pass.
+// Three launches, each starting while the one before drains. k_beam_top: the
+// largest values of the row's parts, a part per CTA, and of their warps. Where n
+// of these entries or more reach a bound, so do n values; the n-th largest entry
+// is such a bound, and few more values reach it, as most lie in warps of their
+// own. (The least of n groups' maxima, which is cheaper to find, lets n ln n
+// through, and whatever there is where a group is short.) k_beam_sum: the same
+// parts again, from L2, now that the maximum is known: the exponentials' sum,
+// and what reaches the bound goes to the row's list. k_beam_merge: a warp per
+// row ranks the list by counting, then the beams' lists are merged. Values
+// carry their index (in the bound, their quad's) as the low half of a 64-bit
+// key, so that equal logits do not all pass.
 #pragma once
 #include "kernels.h"
 #include "ptx.cuh"
-#include "cluster.cuh"
 #include "int_device.cuh"
 
 namespace detint {
 
-constexpr int BM_THREADS = 512, BM_WARPS = BM_THREADS / 32;
-constexpr int BM_MAX_CL = 16;            // CTAs of a row
-constexpr int BM_CAP = 1024;             // values over the bound that are ranked by counting
+constexpr int BM_NT = 256, BM_NW = BM_NT / 32;   // threads, warps of a part
+constexpr int BM_Q = 4;                  // quads of a thread and round
+constexpr int BM_ROUND = BM_NT * BM_Q * 4;
+constexpr int BM_PARTS = 64;             // parts of a row, at most
+constexpr int BM_CAP = 512;              // values of a row over the bound that are listed
 constexpr int BM_MAX_OUT = 64;           // continuations of a group; beams
 constexpr int BM_MASKED = -2147483647 - 1;
 
@@ -34,14 +38,21 @@ struct BeamArgs {
     size_t stride;                       // elements between rows
     const long long* scores;             // [rows]
     const int32_t* done;                 // [rows] or null
-    int rows, n, n_out, end_id, beams;
-    int lg_cl;                           // log2 of the CTAs of a row
-    int lg_groups, per_warp;             // log2 of the groups of warps; values of a warp that count for the bound
-    long long* ws_score;                       // [rows][n_out], best first
-    int32_t* ws_tok;                     // [rows][n_out], -1 behind the last
+    int n, n_out, end_id, beams;
+    int parts, rounds;                   // of a row; of a part
+    int per_part, per_warp;              // place of the bound among the parts' entries (0: not taken), and the warps'
+    int lanes;                           // a warp's entry is the lanes-th largest of its lanes' maxima
+    unsigned long long *part_key, *key;  // [rows][parts], [rows][parts BM_NW]: the entries
+    unsigned long long *sum, *list;      // [rows][parts], [rows][BM_CAP]
+    int32_t *top, *most;                 // [rows][parts] maxima, [rows]: the row's
+    unsigned* count;                     // [rows]
     int32_t *parent, *token, *done_out;  // [groups][n_out]
     long long* score_out;
 };
+// whether a row has continuations of its own (k_beam_merge gives a finished beam its one)
+__device__ __forceinline__ bool bm_open(const BeamArgs& a, int r) {
+    return a.scores[r] >= -(1ll << 62) && !(a.done && a.done[r]);
+}
 
 // a value and its index as one key: larger values, then smaller indexes, are
 // larger (0 is no value's key, and neither are all ones)
@@ -51,31 +62,45 @@ __device__ __forceinline__ int bm_index(u64 key) { return 0x7fffffff - (int)(uns
 __device__ __forceinline__ u64 umax64(u64 a, u64 b) { return a > b ? a : b; }
 __device__ __forceinline__ u64 umin64(u64 a, u64 b) { return a < b ? a : b; }
 
-// exp(l - M) in Q30 of Q16 logits l <= M: delta in Q10 octaves, exp2q's cubic on
-// its fraction; zero from 31 octaves down, where the difference is clamped
-__device__ __forceinline__ unsigned bm_exp(int l, int M) {
-    const int d = -(int)min((unsigned)M - (unsigned)l, 1u << 22);
-    const int delta = (int)(((i64)d * 47274 + (1 << 20)) >> 21);
-    const int f = delta & 1023;
+// exp(l - M) in Q30 of Q16 logits l <= M: with d = M - l, -delta = (d L2E + 2^20 -
+// 1) >> 21 octaves in Q10, which is the high word of d (L2E 2^11) + (2^20 - 1)
+// 2^11; here m = -delta - 1, so that the fraction is ~m and the octaves down
+// are (m >> 10) + 1. exp2q's cubic p of the fraction comes from a table of the
+// CTA's (2^16 p; computing it took 25 instructions a value in place of 17); then
+// rshr(2^15 p, sh) = (((2^16 p) >> sh) + 1) >> 1. Zero from 31 octaves down:
+// below `least` (what it is there is not used, but computed: a branch for each
+// value cost more).
+constexpr int BM_TABLE = 1024;
+__device__ __forceinline__ unsigned bm_octave(int f) {
     const int v1 = (2562 * f + (512 + (7419 << 10))) >> 10;
     const int v2 = (f * v1 + (512 + (22787 << 10))) >> 10;
-    const unsigned p = (unsigned)((f * v2 + (512 + (32768 << 10))) >> 10) << 15;
-    const int sh = -(delta >> 10);
-    return sh >= 31 ? 0u : (p + ((1u << sh) >> 1)) >> sh;
+    return (unsigned)((f * v2 + (512 + (32768 << 10))) >> 10) << 16;
 }
+__device__ __forceinline__ unsigned bm_exp(const unsigned* table, int l, int M, int least) {
+    const u64 w = (u64)((unsigned)M - (unsigned)l) * (47274u << 11) + (((1ull << 20) - 1) << 11) - (1ull << 32);
+    const int m = (int)(w >> 32);
+    unsigned e;
+    asm("shr.u32 %0, %1, %2;" : "=r"(e) : "r"(table[~m & (BM_TABLE - 1)]), "r"((m + 1024) >> 10));
+    e = (e + 1) >> 1;
+    return l >= least ? e : 0u;
+}
+// -delta <= 30 2^10, that is d L2E + 2^20 - 1 < 30721 2^21
+constexpr int BM_FAR = (int)(((30721ull << 21) - (1ull << 20)) / 47274);
+__device__ __forceinline__ int bm_least(int M) { return (int)max((i64)M - BM_FAR, (i64)BM_MASKED + 1); }
 // ln(S / 2^30) in Q16, S >= 2^30: log2 to 20 bits below the point, a bit per
 // squaring of the 32-bit mantissa, times ln 2
 __device__ __forceinline__ i64 bm_ln(u64 S) {
     const int b = bitlen_u64(S);
-    u64 y = b <= 32 ? S << (32 - b) : S >> (b - 32);
-    i64 lg = b - 31;
+    unsigned y = (unsigned)(b <= 32 ? S << (32 - b) : S >> (b - 32));
+    int lg = b - 31;                                     // (at most 24 2^20)
+#pragma unroll 4
     for (int i = 0; i < 20; ++i) {
-        const u64 z = y * y;
-        const int bit = (int)(z >> 63);
-        y = z >> (31 + bit);
-        lg = 2 * lg + bit;
+        const u64 z = (u64)y * y;
+        const unsigned hi = (unsigned)(z >> 32);
+        lg = 2 * lg + (int)(hi >> 31);
+        y = (int)hi < 0 ? hi : (unsigned)(z >> 31);
     }
-    return rshr(lg * 726817, 24);
+    return rshr((i64)lg * 726817, 24);
 }
 
 // four consecutive logits of a row (VEC: one aligned load), masked ones past the end
@@ -90,214 +115,247 @@ __device__ __forceinline__ int4 bm_load(const int32_t* row, int at, int n) {
     return v;
 }
 
-// Q quads of a row per thread and round. HELD: one round, kept in registers
-// for the second pass; otherwise rounds over the row, read again by it.
-template <int Q, bool HELD, bool VEC>
-__global__ void __launch_bounds__(BM_THREADS) k_beam_rows(BeamArgs a) {
-    constexpr int NL = BM_MAX_CL * BM_WARPS / 32;        // warps of a cluster per lane
-    __shared__ u64 wkey[BM_WARPS], wsum[BM_WARPS], cand[BM_CAP], sums[BM_MAX_CL], best, tau_s;
-    __shared__ int wtop[BM_WARPS], max_s;
-    __shared__ i64 base_s;
-    __shared__ unsigned count;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int CL = (int)cl_size(), rank = (int)cl_rank(), r = (int)(blockIdx.x >> a.lg_cl);
-    pdl_launch();
-    long long* const ws_score = a.ws_score + (size_t)r * a.n_out;
-    int32_t* const ws_tok = a.ws_tok + (size_t)r * a.n_out;
-    const i64 score = min((i64)a.scores[r], 1ll << 62);
-    const bool dead = score < -(1ll << 62);
-    if (dead || (a.done && a.done[r])) {                 // (the whole cluster takes this way out)
-        if (rank == 0)
-            for (int i = tid; i < a.n_out; i += BM_THREADS) {
-                ws_tok[i] = i == 0 && !dead ? a.end_id : -1;
-                ws_score[i] = score;
-            }
-        return;
-    }
-    const int32_t* row = a.logits + (size_t)r * a.stride;
-    const int step = CL * BM_THREADS * 4, first = (rank * BM_THREADS + tid) * 4;
-    int4 x[Q];
-    auto load = [&](int base) {
+// a round of a part: BM_Q quads per thread, from `base` on
+template <bool VEC>
+struct BmRound {
+    int4 x[BM_Q];
+    __device__ __forceinline__ void load(const int32_t* row, int base, int n) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) x[q] = bm_load<VEC>(row, base + q * step, a.n);
-    };
-    auto each = [&](int base, auto f) {
+        for (int q = 0; q < BM_Q; ++q) x[q] = bm_load<VEC>(row, base + (q * BM_NT + (int)threadIdx.x) * 4, n);
+    }
+    template <class F>
+    __device__ __forceinline__ void each(int base, F f) const {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            f(x[q].x, base + q * step);
-            f(x[q].y, base + q * step + 1);
-            f(x[q].z, base + q * step + 2);
-            f(x[q].w, base + q * step + 3);
+        for (int q = 0; q < BM_Q; ++q) {
+            const int i = base + (q * BM_NT + (int)threadIdx.x) * 4;
+            f(x[q].x, i);
+            f(x[q].y, i + 1);
+            f(x[q].z, i + 2);
+            f(x[q].w, i + 3);
         }
-    };
-    // ---- pass 1: this thread's largest value, the first of equal ones
-    int top = BM_MASKED, at = 0;
-    for (int base = first; base < a.n; base += Q * step) {
-        load(base);
-        each(base, [&](int v, int i) {
-            if (v > top) { top = v; at = i; }
-        });
-        if (HELD) break;
     }
-    {
-        u64 k = top == BM_MASKED ? 0 : bm_key(top, at), wk = redux_max_u64(k);
-        if (lane == 0) wtop[warp] = wk ? bm_value(wk) : BM_MASKED;
-        for (int i = 1; i < a.per_warp; ++i) {           // the per_warp-th largest of the warp's
-            if (k == wk) k = 0;
-            wk = redux_max_u64(k);
-        }
-        if (lane == 0) wkey[warp] = wk;
-        if (tid == 0) count = 0;
-    }
-    cl_sync();
-    // ---- the row's maximum, and the bound: entry e (a warp) is in group e mod 2^lg_groups
-    if (warp == 0) {
-        const int NE = CL * BM_WARPS, NG = 1 << a.lg_groups;
-        u64 g[NL], tau = ~0ull;
+    __device__ __forceinline__ int most() const {        // the largest value
         int m = BM_MASKED;
 #pragma unroll
-        for (int j = 0; j < NL; ++j) {
-            const int e = lane + 32 * j;
-            g[j] = 0;
-            if (e < NE) {
-                g[j] = (u64)cl_ld64((const i64*)&wkey[e & (BM_WARPS - 1)], e / BM_WARPS);
-                m = max(m, cl_ld32(&wtop[e & (BM_WARPS - 1)], e / BM_WARPS));
-            }
-        }
+        for (int q = 0; q < BM_Q; ++q) m = max(m, max(max(x[q].x, x[q].y), max(x[q].z, x[q].w)));
+        return m;
+    }
+};
+
+template <bool VEC>
+__global__ void __launch_bounds__(BM_NT) k_beam_top(BeamArgs a) {
+    __shared__ u64 best[BM_NW];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = blockIdx.x, r = blockIdx.y;
+    pdl_launch();
+    const int32_t* row = a.logits + (size_t)r * a.stride;
+    const int first = part * a.rounds * BM_ROUND;
+    BmRound<VEC> x, y;
+    y.load(row, first, a.n);                             // (on its way while the beam is looked at)
+    if (!bm_open(a, r)) return;
+    int top = BM_MASKED, at = 0;                         // this thread's largest value, the first quad that holds it
+    for (int i = 0; i < a.rounds; ++i) {
+        const int base = first + i * BM_ROUND;
+        x = y;
+        if (i + 1 < a.rounds) y.load(row, base + BM_ROUND, a.n);
 #pragma unroll
-        for (int h = NL / 2; h; h >>= 1)
-            if (32 * h >= NG)
-#pragma unroll
-                for (int j = 0; j < h; ++j) g[j] = umax64(g[j], g[j + h]);
-#pragma unroll
-        for (int j = 0; j < NL; ++j)
-            if (j == 0 || 32 * j < NG) tau = umin64(tau, g[j]);
-        for (int o = 16; o >= NG; o >>= 1) tau = umax64(tau, __shfl_xor_sync(0xffffffffu, tau, o));
-        for (int o = 16; o; o >>= 1) tau = umin64(tau, __shfl_xor_sync(0xffffffffu, tau, o));
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) {
-            tau_s = umax64(tau, 1);                      // (a masked value has no key)
-            max_s = m;
+        for (int q = 0; q < BM_Q; ++q) {
+            const int m = max(max(x.x[q].x, x.x[q].y), max(x.x[q].z, x.x[q].w));
+            if (m > top) { top = m; at = base + (q * BM_NT + (int)threadIdx.x) * 4; }
         }
     }
+    u64 k = top == BM_MASKED ? 0 : bm_key(top, at), wk = redux_max_u64(k);
+    if (lane == 0) best[warp] = wk;
+    for (int i = 1; i < a.lanes; ++i) {                  // the lanes-th largest of the warp's lanes
+        if (k == wk) k = 0;
+        wk = redux_max_u64(k);
+    }
+    const size_t e = (size_t)r * a.parts + part;
+    if (lane == 0) a.key[e * BM_NW + warp] = wk;
     __syncthreads();
-    const int M = max_s;
-    const u64 tau = tau_s;
-    const int tau_v = tau > 1 ? bm_value(tau) : BM_MASKED + 1;
-    // ---- pass 2: the sum, and what reaches the bound (nothing of a row without candidates)
+    if (threadIdx.x == 0) {
+        u64 m = 0;
+#pragma unroll
+        for (int w = 0; w < BM_NW; ++w) m = umax64(m, best[w]);
+        a.part_key[e] = m;
+        a.top[e] = m ? bm_value(m) : BM_MASKED;
+        if (part == 0) a.count[r] = 0;
+    }
+}
+
+// the want-th largest of n entries (0 where fewer have a value): the rank of each
+// by counting; entries that have a value differ
+__device__ __forceinline__ void bm_nth(const u64* key, int n, int want, u64* out) {
+    for (int e = threadIdx.x; e < n; e += BM_NT) {
+        const u64 k = key[e];
+        int better = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; j += 2) {                 // (an entry of 0 behind an odd end)
+            const ulonglong2 o = *(const ulonglong2*)(key + j);
+            better += (o.x > k) + (o.y > k);
+        }
+        if (better == want - 1) *out = k;
+    }
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(BM_NT, 4) k_beam_sum(BeamArgs a) {
+    __shared__ __align__(16) u64 key[BM_PARTS * BM_NW + 2];
+    __shared__ u64 wsum[BM_NW], tau_s;
+    __shared__ unsigned table[BM_TABLE];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, part = blockIdx.x, r = blockIdx.y;
+    pdl_launch();
+    const int32_t* row = a.logits + (size_t)r * a.stride;
+    const int first = part * a.rounds * BM_ROUND;
+    BmRound<VEC> x, y;
+    y.load(row, first, a.n);
+    const bool open = bm_open(a, r);
+    if (tid == 0) tau_s = 0;
+#pragma unroll
+    for (int i = 0; i < BM_TABLE; i += BM_NT) table[i + tid] = bm_octave(i + tid);
+    pdl_wait();                                          // (every CTA, so that this launch ends after the one before)
+    if (!open) return;
+    int m = max(lane < a.parts ? __ldcg(a.top + (size_t)r * a.parts + lane) : BM_MASKED,
+                lane + 32 < a.parts ? __ldcg(a.top + (size_t)r * a.parts + lane + 32) : BM_MASKED);
+    for (int fine = a.per_part ? 0 : 1; fine < 2; ++fine) {
+        // the parts' entries, and the warps' where too few of those have a value
+        const int n = fine ? a.parts * BM_NW : a.parts, per = fine ? a.per_warp : a.per_part;
+        const unsigned long long* src = (fine ? a.key : a.part_key) + (size_t)r * n;
+        for (int e = tid; e < n + (n & 1); e += BM_NT) key[e] = e < n ? __ldcg(src + e) : 0;
+        __syncthreads();
+        bm_nth(key, n, per, &tau_s);
+        __syncthreads();
+        if (tau_s) break;
+    }
+    const int M = __reduce_max_sync(0xffffffffu, m);
+    if (part == 0 && tid == 0) a.most[r] = M;
+    // the bound names a quad: equal values up to its last element reach it; a masked value has no key
+    const u64 tau = tau_s ? tau_s - 3 : 1;
+    const int tau_v = tau_s ? bm_value(tau_s) : BM_MASKED + 1, least = bm_least(M);
     u64 sum = 0;
-    for (int base = first; base < a.n; base += Q * step) {
-        if (!HELD) load(base);
-        each(base, [&](int v, int i) {
-            if (v != BM_MASKED) sum += bm_exp(v, M);
-            if (v >= tau_v) {
-                const u64 k = bm_key(v, i);
-                if (k >= tau) {
-                    const unsigned to = cl_add32(&count, 0, 1);
-                    if (to < BM_CAP) cl_st64(&cand[to], 0, k);
+    for (int i = 0; i < a.rounds; ++i) {
+        const int base = first + i * BM_ROUND;
+        x = y;
+        if (i + 1 < a.rounds) y.load(row, base + BM_ROUND, a.n);
+#pragma unroll
+        for (int q = 0; q < BM_Q; ++q) {
+            // (two exponentials stay below 2^32)
+            sum += bm_exp(table, x.x[q].x, M, least) + bm_exp(table, x.x[q].y, M, least);
+            sum += bm_exp(table, x.x[q].z, M, least) + bm_exp(table, x.x[q].w, M, least);
+        }
+        if (x.most() >= tau_v)
+            x.each(base, [&](int v, int j) {
+                if (v >= tau_v && bm_key(v, j) >= tau) {
+                    const unsigned to = atomicAdd(a.count + r, 1u);
+                    if (to < BM_CAP) a.list[(size_t)r * BM_CAP + to] = bm_key(v, j);
                 }
-            }
-        });
-        if (HELD) break;
+            });
     }
     sum = redux_sum_u64(sum);
     if (lane == 0) wsum[warp] = sum;
     __syncthreads();
     if (tid == 0) {
         u64 t = 0;
-        for (int w = 0; w < BM_WARPS; ++w) t += wsum[w];
-        cl_st64(&sums[rank], 0, t);
+#pragma unroll
+        for (int w = 0; w < BM_NW; ++w) t += wsum[w];
+        a.sum[(size_t)r * a.parts + part] = t;
     }
-    cl_sync();
-    const unsigned c = cl_ld32u(&count, 0);
-    if (c > BM_CAP) {                                    // too many: n_out times the best one below the last
-        u64 last = ~0ull;
-        for (int i = 0; i < a.n_out; ++i) {
-            u64 k = 0;
-            for (int base = first; base < a.n; base += Q * step) {
-                if (!HELD) load(base);
-                each(base, [&](int v, int j) {
-                    const u64 y = v == BM_MASKED ? 0 : bm_key(v, j);
-                    if (y < last) k = umax64(k, y);
-                });
-                if (HELD) break;
-            }
-            k = redux_max_u64(k);
-            if (lane == 0) wkey[warp] = k;
-            __syncthreads();
-            if (tid == 0) {
-                u64 t = 0;
-                for (int w = 0; w < BM_WARPS; ++w) t = umax64(t, wkey[w]);
-                best = t;
-            }
-            cl_sync();
-            k = 0;
-            for (int q = 0; q < CL; ++q) k = umax64(k, (u64)cl_ld64((const i64*)&best, q));
-            cl_sync();
-            last = k;
-            if (rank == 0 && tid == 0) cand[i] = k;
-        }
-    }
-    if (rank == 0) {
-        if (tid == BM_THREADS - 1) {
-            u64 t = 0;
-            for (int q = 0; q < CL; ++q) t += sums[q];
-            base_s = t ? score - M - bm_ln(t) : 0;
-        }
-        __syncthreads();
-        const int m = c > BM_CAP ? a.n_out : (int)c;
-        for (int i = tid; i < m; i += BM_THREADS) {
-            const u64 k = cand[i];
-            int better = 0;
-            for (int j = 0; j < m; ++j) better += cand[j] > k;
-            if (better < a.n_out) {
-                ws_tok[better] = bm_index(k);
-                ws_score[better] = base_s + bm_value(k);
-            }
-        }
-        for (int i = m + tid; i < a.n_out; i += BM_THREADS) {
-            ws_tok[i] = -1;
-            ws_score[i] = 0;
-        }
-    }
-    cl_sync();                                           // no CTA leaves while another reads its shared memory
 }
 
-// The best n_out of a group: a candidate's place is the number of better ones,
-// found in every other beam's sorted list by halving.
-constexpr int BM_MERGE_THREADS = 256;
-__global__ void __launch_bounds__(BM_MERGE_THREADS) k_beam_merge(BeamArgs a) {
+// A group's rows, a warp each: the sum's logarithm, and the list ranked by
+// counting. A list that ran over is found again by n_out sweeps of the row.
+// Then the best n_out of the group: a candidate's place is the number of
+// better ones, found in every other beam's sorted list by halving.
+constexpr int BM_MERGE = 512, BM_MERGE_NW = BM_MERGE / 32;
+__global__ void __launch_bounds__(BM_MERGE) k_beam_merge(BeamArgs a) {
     extern __shared__ __align__(16) unsigned char bm_raw[];
-    __shared__ int len[BM_MAX_OUT], ended[BM_MAX_OUT];
-    const int W = a.beams, n = a.n_out, tid = threadIdx.x, r0 = (int)blockIdx.x * W;
-    i64* sc = (i64*)bm_raw;                              // [W][n]
-    if (tid < W) ended[tid] = a.done && a.done[r0 + tid];
+    __shared__ int len[BM_MAX_OUT], ended[BM_MAX_OUT], over[BM_MAX_OUT];
+    __shared__ u64 best[BM_MERGE_NW];
+    const int W = a.beams, n = a.n_out, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r0 = (int)blockIdx.x * W;
+    constexpr int NT = BM_MERGE, NW = BM_MERGE_NW;
+    i64* sc = (i64*)bm_raw;                              // [W][n] scores, best first
+    int* tk = (int*)(sc + W * n);                        // [W][n] tokens
+    u64* buf = (u64*)(bm_raw + ((W * n * 12 + 15) & ~15)) + min(warp, W - 1) * BM_CAP;
     pdl_wait();
-    const long long* ws = a.ws_score + (size_t)r0 * n;
-    const int32_t* wt = a.ws_tok + (size_t)r0 * n;
-    for (int i = tid; i < W * n; i += BM_MERGE_THREADS) sc[i] = __ldcg(ws + i);
-    if (tid < W) {
-        int lo = 0, hi = n;                              // entries of the beam: the tokens before the first -1
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (__ldcg(wt + tid * n + mid) >= 0) lo = mid + 1;
-            else hi = mid;
+    for (int b = warp; b < W; b += NW) {
+        const int r = r0 + b;
+        // (one trip to memory: what follows the list's end is not looked at)
+        const size_t e0 = (size_t)r * a.parts;
+        const u64 l0 = __ldcg(a.list + (size_t)r * BM_CAP + lane), l1 = __ldcg(a.list + (size_t)r * BM_CAP + 32 + lane);
+        u64 t = lane < a.parts ? __ldcg(a.sum + e0 + lane) : 0;
+        const u64 t1 = lane + 32 < a.parts ? __ldcg(a.sum + e0 + 32 + lane) : 0;
+        int c = (int)__ldcg(a.count + r);
+        const int m = __ldcg(a.most + r);
+        const i64 score = min((i64)a.scores[r], 1ll << 62);
+        const bool dead = score < -(1ll << 62), end = !dead && a.done && a.done[r];
+        if (dead || end) {
+            if (lane == 0 && end) { sc[b * n] = score; tk[b * n] = a.end_id; }
+            c = end;
+        } else {
+            buf[lane] = l0;
+            buf[lane + 32] = l1;
+            for (int i = 64 + lane; i < min(c, BM_CAP); i += 32) buf[i] = __ldcg(a.list + (size_t)r * BM_CAP + i);
+            t = redux_sum_u64(t + t1);
+            const i64 base = t ? score - m - bm_ln(t) : 0;
+            __syncwarp();
+            if (c <= BM_CAP) {
+                for (int i = lane; i < c; i += 32) {
+                    const u64 k = buf[i];
+                    int better = 0;
+#pragma unroll 8
+                    for (int j = 0; j < c; ++j) better += buf[j] > k;
+                    if (better < n) {
+                        sc[b * n + better] = base + bm_value(k);
+                        tk[b * n + better] = bm_index(k);
+                    }
+                }
+            } else if (lane == 0) {
+                sc[b * n] = base;
+            }
+            __syncwarp();
         }
-        len[tid] = lo;
+        if (lane == 0) {
+            len[b] = min(c, n);
+            ended[b] = end;
+            over[b] = c > BM_CAP;
+        }
     }
     __syncthreads();
+    for (int b = 0; b < W; ++b) {
+        if (!over[b]) continue;
+        const int32_t* row = a.logits + (size_t)(r0 + b) * a.stride;
+        const i64 base = sc[b * n];
+        u64 last = ~0ull;
+        for (int i = 0; i < n; ++i) {                    // the best one below the last
+            u64 k = 0;
+            for (int j = tid; j < a.n; j += NT) {
+                const int v = __ldg(row + j);
+                const u64 y = v == BM_MASKED ? 0 : bm_key(v, j);
+                if (y < last) k = umax64(k, y);
+            }
+            k = redux_max_u64(k);
+            __syncthreads();
+            if (lane == 0) best[warp] = k;
+            __syncthreads();
+            k = 0;
+            for (int w = 0; w < NW; ++w) k = umax64(k, best[w]);
+            last = k;
+            if (tid == 0) {
+                sc[b * n + i] = base + bm_value(k);
+                tk[b * n + i] = bm_index(k);
+            }
+        }
+        __syncthreads();
+    }
     const size_t out = (size_t)blockIdx.x * n;
     int total = 0;
     for (int q = 0; q < W; ++q) total += len[q];
-    for (int i = tid; i < n; i += BM_MERGE_THREADS)
-        if (i >= total) {
-            a.parent[out + i] = a.token[out + i] = -1;
-            a.score_out[out + i] = (long long)(1ull << 63);
-            a.done_out[out + i] = 0;
-        }
-    // (a thread per beam and place, the places side by side)
-    for (int b = 0; b < W; ++b)
-        for (int i = tid; i < len[b]; i += BM_MERGE_THREADS) {
+    for (int i = total + tid; i < n; i += NT) {
+        a.parent[out + i] = a.token[out + i] = -1;
+        a.score_out[out + i] = (long long)(1ull << 63);
+        a.done_out[out + i] = 0;
+    }
+    for (int b = warp; b < W; b += NW)
+        for (int i = lane; i < len[b]; i += 32) {
             const i64 s = sc[b * n + i];
             int place = i;
             for (int q = 0; q < W && place < n; ++q) {
@@ -313,7 +371,7 @@ __global__ void __launch_bounds__(BM_MERGE_THREADS) k_beam_merge(BeamArgs a) {
                 place += lo;
             }
             if (place < n) {
-                const int tok = __ldcg(wt + b * n + i);
+                const int tok = tk[b * n + i];
                 a.parent[out + place] = b;
                 a.token[out + place] = tok;
                 a.score_out[out + place] = s;

@@ -420,14 +420,14 @@ int detint_kv4_copy(const detint_kv4_t* c, const int32_t* src, const int32_t* ds
  * done 0. scores and done may be the outputs of the call before but not of this
  * one. end_id -1: no token ends a beam. workspace: detint_beam_workspace bytes,
  * 16-byte aligned; calls that may overlap on the GPU, captured ones included,
- * need one each. Up to 2^20 rows of up to 2^24 logits.
+ * need one each. Up to 65535 rows of up to 2^24 logits.
  * Errors: ARG, SHAPE, CUDA. */
 int detint_beam_select(const int32_t* logits, long long stride, int n, const int64_t* scores, const int32_t* done,
                        int groups, int beams, int end_id, int n_out, int32_t* parent, int32_t* token, int64_t* score,
                        int32_t* done_out, void* workspace, long long workspace_bytes, detint_stream_t s);
 
 /* Bytes of workspace for detint_beam_select of `rows` rows (groups times beams)
- * of n logits; enough for fewer rows and a smaller n_out. Errors: ARG. */
+ * of n logits; enough for fewer rows and any n and n_out. Errors: ARG. */
 int detint_beam_workspace(int rows, int n, int n_out, long long* bytes);
 
 /* The block tables of the chosen beams. block_table: device int32 [groups *

@@ -67,7 +67,7 @@ def _select(L, **kw):
 @pytest.mark.parametrize("code,change", [
     (1, dict(logits=None)), (1, dict(scores=None)), (1, dict(parent=None)), (1, dict(token=None)), (1, dict(score=None)),
     (1, dict(done_out=None)), (1, dict(ws=None)), (1, dict(size=100)), (1, dict(ws=P + 8)), (1, dict(groups=0)),
-    (1, dict(beams=0)), (1, dict(beams=65)), (1, dict(n_out=0)), (1, dict(n_out=65)), (1, dict(groups=1 << 20)),
+    (1, dict(beams=0)), (1, dict(beams=65)), (1, dict(n_out=0)), (1, dict(n_out=65)), (1, dict(groups=21846)),
     (2, dict(n=0)), (2, dict(n=(1 << 24) + 1, stride=1 << 25)), (1, dict(stride=99)), (1, dict(end=100)), (1, dict(end=-2)),
     (1, dict(done=P)), (1, dict(done=P + 2, end=3)), (1, dict(logits=P + 1)), (1, dict(scores=P + 4)), (1, dict(score=P + 4)),
     (1, dict(token=P + 2)), (1, dict(groups=-1)), (1, dict(stride=-100))])
@@ -76,7 +76,7 @@ def test_bad_select_arguments_are_refused(L, code, change):
     assert b"detint_beam" in L.detint_last_error()
 
 
-@pytest.mark.parametrize("args", [(0, 10, 1), (1, 0, 1), (1, 10, 0), (1, 10, 65), ((1 << 20) + 1, 10, 1), (1, (1 << 24) + 1, 1)])
+@pytest.mark.parametrize("args", [(0, 10, 1), (1, 0, 1), (1, 10, 0), (1, 10, 65), (65536, 10, 1), (1, (1 << 24) + 1, 1)])
 def test_bad_workspace_queries_are_refused(L, args):
     assert L.detint_beam_workspace(*args, C.byref(C.c_longlong())) == 1
     assert L.detint_beam_workspace(1, 10, 1, None) == 1
