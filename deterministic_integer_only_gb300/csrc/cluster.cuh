@@ -50,5 +50,8 @@ __device__ __forceinline__ unsigned cl_add32(unsigned* p, unsigned rank, unsigne
     asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(cl_addr(p, rank)), "r"(v) : "memory");
     return old;
 }
+__device__ __forceinline__ void cl_red32(unsigned* p, unsigned rank, unsigned v) {
+    asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(cl_addr(p, rank)), "r"(v) : "memory");
+}
 
 }  // namespace detint

@@ -209,38 +209,50 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_weigh(Kv4Args a, Kv4Attn p, K
 // ------------------------------------------------------------------ eviction
 // The kept places of one sequence and kv head, ascending: the first `sinks`
 // and last `recent` ones and, between them, those of the largest weights, the
-// lower place first among equal ones. A cluster per sequence and kv head, a
-// run of whole pages per CTA, the weights in shared memory as order-preserving
-// keys. The least kept key is found from its leading bits: a histogram of the
-// next 11 bits of the keys that agree so far, until its bin is taken whole or
-// the bits run out. Then a prefix sum over the places deals the kept ones out.
+// lower place first among equal ones. A cluster per sequence and kv head, a run
+// of whole pages per CTA, the weights in shared memory as order-preserving
+// keys. The least kept key is found in a histogram of the distances from the
+// least key, 32 bins to an octave (attention weights are heavy-tailed: in even
+// bins most would share one), whose few keys in the bin in question are then
+// ranked by counting; where that bin is too full, its keys are split by 11 bits
+// at a time first. Then every warp deals the kept places of its run out.
 constexpr int EV_THREADS = 512, EV_WARPS = EV_THREADS / 32;
 constexpr int EV_BITS = 11, EV_BINS = 1 << EV_BITS;
+constexpr int EV_LIST = 512;             // keys that are ranked by counting
+constexpr int EV_PAGES = EV_BINS / 4;    // pages of a CTA
 
 struct Kv4Evict {
-    const long long* weight_in;          // = weight
     long long* weight;
     const int32_t *seq, *lens;           // [n]
     const int32_t* new_table;            // [n][pages of keep]
     int32_t* kept;                       // [n][n_kv][keep]
     int max_len, keep, sinks, recent;
     int new_blocks;                      // pages of keep
-    int lg_s, cap;                       // log2 of the CTAs of a cluster; keys of a CTA (whole pages)
+    int lg_s;                            // log2 of the CTAs of a cluster
     int held;                            // the keys fit shared memory
 };
 
 __device__ __forceinline__ u64 ev_key(long long w) { return (u64)w ^ (1ull << 63); }
+// bin of a distance, and the open bits of the distances in it
+__device__ __forceinline__ int ev_bin(u64 d) {
+    const int e = bitlen_u64(d);
+    return e <= 5 ? (int)d : ((e - 5) << 5) + (int)(d >> (e - 6) & 31);
+}
+__device__ __forceinline__ int ev_open(int bin) { return bin < 32 ? 0 : (bin >> 5) - 1; }
+__device__ __forceinline__ u64 ev_least(int bin) { return bin < 32 ? (u64)bin : (u64)(32 + (bin & 31)) << ev_open(bin); }
 
 __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4Evict p) {
     extern __shared__ __align__(16) unsigned char ev_raw[];
-    u64* keys = (u64*)ev_raw;                            // [cap] where they are held
+    u64* keys = (u64*)ev_raw;                            // the CTA's, where they are held
     __shared__ unsigned hist[EV_BINS];
-    __shared__ u64 red[2][EV_WARPS], range[2];           // largest key, smallest key (complemented)
-    __shared__ unsigned scan[2][EV_WARPS], mine[2], pick[3];
+    __shared__ u64 list[EV_LIST], red[EV_WARPS], least_s, found;
+    __shared__ unsigned scan[2][EV_WARPS], mine[2], pick[3], count;
+    __shared__ int page[EV_PAGES];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = 1 << p.lg_s, rank = (int)blockIdx.x & (S - 1), i = (int)blockIdx.x >> p.lg_s, g = blockIdx.y;
     const int seq = p.seq[i], max_len = min(p.max_len, a.max_blocks * KV_BLK);
     int len = p.lens[i];
+    pdl_launch();
     int32_t* out = p.kept + ((size_t)i * a.n_kv + g) * p.keep;
     if (seq < 0 || seq >= a.n_seq || len < 0 || len > max_len) {
         if (tid == 0 && a.status) a.status[ST_CTX] = 1;
@@ -252,69 +264,86 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
     }
     const int lo = p.sinks, hi = len - p.recent;         // the places that are weighed
     unsigned want = (unsigned)(p.keep - p.sinks - p.recent);
-    const int j0 = rank * p.cap, j1 = min(len, j0 + p.cap);
-    const int32_t* row = a.block_table + (size_t)seq * a.max_blocks;
-    auto fetch = [&](int j) -> u64 {
-        const int blk = row[j >> 6];
+    // this CTA's pages
+    const int all = (len + KV_BLK - 1) >> 6, per = (all + S - 1) >> p.lg_s;
+    const int b0 = rank * per, nb = max(0, min(per, all - b0)), j0 = b0 << 6;
+    for (int b = tid; b < nb; b += EV_THREADS) {
+        int blk = a.block_table[(size_t)seq * a.max_blocks + b0 + b];
         if (blk < 0 || blk >= a.n_blocks) {
+            blk = -1;
             if (a.status) a.status[ST_CTX] = 1;
-            return ev_key(0);
         }
-        return ev_key(p.weight_in[((size_t)blk * a.n_kv + g) * KV_BLK + (j & 63)]);
-    };
-    auto key = [&](int j) -> u64 { return p.held ? keys[j - j0] : fetch(j); };
-    u64 top = 0, bot = 0;                                // of the keys, and of their complements
-    for (int j = j0 + tid; j < j1; j += EV_THREADS) {
-        const u64 k = fetch(j);
-        if (p.held) keys[j - j0] = k;
-        if (j >= lo && j < hi) {
-            top = k > top ? k : top;
-            bot = ~k > bot ? ~k : bot;
-        }
-    }
-    top = redux_max_u64(top);
-    bot = redux_max_u64(bot);
-    if (lane == 0) { red[0][warp] = top; red[1][warp] = bot; }
-    __syncthreads();
-    if (tid < 2) {
-        u64 m = 0;
-        for (int w = 0; w < EV_WARPS; ++w) m = red[tid][w] > m ? red[tid][w] : m;
-        range[tid] = m;
+        page[b] = blk;
     }
     for (int b = tid; b < EV_BINS; b += EV_THREADS) hist[b] = 0;
-    cl_sync();
-    top = bot = 0;
-    for (int r = 0; r < S; ++r) {
-        const u64 x = (u64)cl_ld64((const i64*)&range[0], r), y = (u64)cl_ld64((const i64*)&range[1], r);
-        top = x > top ? x : top;
-        bot = y > bot ? y : bot;
-    }
-    bot = ~bot;
-    // ---- the want-th largest key: `left` low bits are open, the others agree with `top`
-    int left = want ? bitlen_u64(top ^ bot) : 0;
-    u64 cut = want ? top : ~0ull;                        // its open bits are yet to be found
-    bool whole = false;                                  // every key that agrees with cut's closed bits is kept
-    while (left > 0 && !whole) {
-        const int sh = max(left - EV_BITS, 0);
-        const u64 agree = left >= 64 ? 0 : cut >> left, bins = (1ull << (left - sh)) - 1;
-        for (int j = max(j0, lo) + tid; j < min(j1, hi); j += EV_THREADS) {
-            const u64 k = key(j);
-            if (left >= 64 || k >> left == agree) atomicAdd(&hist[(k >> sh) & bins], 1u);
+    if (tid == 0) count = 0;
+    __syncthreads();
+    // a warp takes pages; a lane two neighbouring places of a page
+    auto fetch = [&](int b) -> ulonglong2 {
+        const int blk = page[b];
+        if (blk < 0) return make_ulonglong2(ev_key(0), ev_key(0));
+        const longlong2 w = *((const longlong2*)(p.weight + ((size_t)blk * a.n_kv + g) * KV_BLK) + lane);
+        return make_ulonglong2(ev_key(w.x), ev_key(w.y));
+    };
+    auto each = [&](auto f) {                            // f(key) of every key that is weighed
+        for (int b = warp; b < nb; b += EV_WARPS) {
+            const ulonglong2 k = p.held ? *((const ulonglong2*)(keys + (b << 6)) + lane) : fetch(b);
+            const int j = j0 + (b << 6) + 2 * lane;
+            if (j >= lo && j < hi) f(k.x);
+            if (j + 1 >= lo && j + 1 < hi) f(k.y);
         }
+    };
+    u64 least = ~0ull;
+#pragma unroll 4
+    for (int b = warp; b < nb; b += EV_WARPS) {
+        const ulonglong2 k = fetch(b);
+        if (p.held) *((ulonglong2*)(keys + (b << 6)) + lane) = k;
+        const int j = j0 + (b << 6) + 2 * lane;
+        if (j >= lo && j < hi) least = k.x < least ? k.x : least;
+        if (j + 1 >= lo && j + 1 < hi) least = k.y < least ? k.y : least;
+    }
+    least = ~redux_max_u64(~least);
+    if (lane == 0) red[warp] = least;
+    __syncthreads();
+    if (warp == 0) {
+        least = ~redux_max_u64(~red[lane & (EV_WARPS - 1)]);
+        if (lane == 0) least_s = least;
+    }
+    cl_sync();
+    least = ~0ull;
+    for (int r = 0; r < S; ++r) {
+        const u64 x = (u64)cl_ld64((const i64*)&least_s, r);
+        least = x < least ? x : least;
+    }
+    // ---- the want-th largest distance: cut, whose `open` low bits are yet to be found
+    int open = 64;
+    u64 cut = 0;
+    const bool any = want > 0;
+    bool whole = !any;                                   // every key that agrees with cut's closed bits is kept
+    if (!any) open = 0;
+    while (open > 0 && !whole) {
+        const int sh = max(open - EV_BITS, 0);
+        const u64 agree = open >= 64 ? 0 : cut >> open, bins = (1ull << (open - sh)) - 1;
+        each([&](u64 k) {
+            const u64 d = k - least;
+            if (open >= 64) atomicAdd(&hist[ev_bin(d)], 1u);
+            else if (d >> open == agree) atomicAdd(&hist[(d >> sh) & bins], 1u);
+        });
         __syncthreads();
         if (rank)                                        // the first CTA's bins become the cluster's
             for (int b = tid; b < EV_BINS; b += EV_THREADS)
                 if (hist[b]) {
-                    cl_add32(&hist[b], 0, hist[b]);
+                    cl_red32(&hist[b], 0, hist[b]);
                     hist[b] = 0;
                 }
         cl_sync();
         if (rank == 0) {
             // from the highest bin down: the bin in which `want` is reached
-            unsigned c[EV_BINS / EV_THREADS], sum = 0;
+            constexpr int BPT = EV_BINS / EV_THREADS;
+            unsigned c[BPT], sum = 0;
 #pragma unroll
-            for (int x = 0; x < EV_BINS / EV_THREADS; ++x) {
-                c[x] = hist[EV_BINS - 1 - (tid * (EV_BINS / EV_THREADS) + x)];
+            for (int x = 0; x < BPT; ++x) {
+                c[x] = hist[EV_BINS - 1 - (tid * BPT + x)];
                 sum += c[x];
             }
             unsigned inc = sum;
@@ -328,59 +357,84 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
             unsigned before = inc - sum;
             for (int w = 0; w < warp; ++w) before += scan[0][w];
             if (before < want && want <= before + sum) {
-                int x = 0;
 #pragma unroll
-                for (; x < EV_BINS / EV_THREADS - 1; ++x) {
-                    if (want <= before + c[x]) break;
+                for (int x = 0; x < BPT; ++x) {
+                    if (before < want && want <= before + c[x]) {
+                        pick[0] = (unsigned)(EV_BINS - 1 - (tid * BPT + x));
+                        pick[1] = want - before;         // of the bin's keys
+                        pick[2] = c[x];
+                    }
                     before += c[x];
                 }
-                unsigned n = 0;
-#pragma unroll
-                for (int y = 0; y < EV_BINS / EV_THREADS; ++y)
-                    if (y == x) n = c[y];
-                pick[0] = (unsigned)(EV_BINS - 1 - (tid * (EV_BINS / EV_THREADS) + x));
-                pick[1] = want - before;                 // of the bin's n keys
-                pick[2] = n;
             }
-            __syncthreads();
             for (int b = tid; b < EV_BINS; b += EV_THREADS) hist[b] = 0;
         }
         cl_sync();
         const unsigned bin = cl_ld32u(&pick[0], 0), n = cl_ld32u(&pick[2], 0);
         want = cl_ld32u(&pick[1], 0);
-        cut = (agree << (left - sh) | bin) << sh;
-        left = sh;
+        if (open >= 64) {
+            open = ev_open((int)bin);
+            cut = ev_least((int)bin);
+        } else {
+            cut = (agree << (open - sh) | bin) << sh;
+            open = sh;
+        }
         whole = want == n;
-        cl_sync();                                       // pick is read before it is written again
+        if (!whole && open > 0 && n <= EV_LIST) {        // few: ranked by the first CTA
+            const u64 near = cut >> open;
+            each([&](u64 k) {
+                const u64 d = k - least;
+                if (d >> open == near) cl_st64(&list[cl_add32(&count, 0, 1)], 0, d);
+            });
+            cl_sync();
+            if (rank == 0) {
+                for (int x = tid; x < (int)n; x += EV_THREADS) {
+                    const u64 d = list[x];
+                    unsigned above = 0, same = 0;
+#pragma unroll 4
+                    for (int y = 0; y < (int)n; ++y) {
+                        above += list[y] > d;
+                        same += list[y] == d;
+                    }
+                    if (above < want && want <= above + same) {      // (equal keys write the same)
+                        found = d;
+                        pick[1] = want - above;
+                    }
+                }
+            }
+            cl_sync();
+            cut = (u64)cl_ld64((const i64*)&found, 0);
+            want = cl_ld32u(&pick[1], 0);
+            open = 0;
+        }
+        cl_sync();                                       // what was read is not written again before all have read it
     }
-    // kept: places outside [lo, hi), keys past the bits of cut (all that agree with
-    // them too when whole), and the first `want` of those equal to it
-    const u64 edge = cut >> left;
+    // ---- kept: places outside [lo, hi), distances past the closed bits of cut (all
+    // that agree with them too when whole), and the first `want` of those equal to it
+    const u64 edge = cut >> open;
+    const int bpw = (nb + EV_WARPS - 1) / EV_WARPS, w0 = min(nb, warp * bpw), w1 = min(nb, w0 + bpw);   // this warp's pages
+    unsigned* mask = hist;                               // [page][half][kept, equal to the cut] of 32 places (the bins are done)
     unsigned take = 0, ties = 0;
-    // a thread's run of places, so that the places ascend with the threads
-    const int span = (p.cap + EV_THREADS - 1) / EV_THREADS, a0 = j0 + tid * span, a1 = min(j1, a0 + span);
-    auto kind = [&](int j) -> int {                      // 2 kept, 1 equal to the cut, 0 not kept
-        if (j < lo || j >= hi) return 2;
-        if (!want) return 0;
-        const u64 k = key(j) >> left;
-        return k > edge || (whole && k == edge) ? 2 : (k == edge ? 1 : 0);
-    };
-    for (int j = a0; j < a1; ++j) {
-        const int t = kind(j);
-        take += t == 2;
-        ties += t == 1;
-    }
-    unsigned it = take, ie = ties;
+    for (int b = w0; b < w1; ++b)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_up_sync(0xffffffffu, it, o), z = __shfl_up_sync(0xffffffffu, ie, o);
-        if (lane >= o) { it += y; ie += z; }
-    }
-    if (lane == 31) { scan[0][warp] = it; scan[1][warp] = ie; }
+        for (int half = 0; half < 2; ++half) {
+            const int x = 32 * half + lane, j = j0 + (b << 6) + x;
+            u64 k = ev_key(0);
+            if (p.held) k = keys[(b << 6) + x];
+            else if (page[b] >= 0) k = ev_key(p.weight[((size_t)page[b] * a.n_kv + g) * KV_BLK + x]);
+            const u64 d = (k - least) >> open;
+            const bool in = j >= lo && j < hi;
+            const unsigned mk = __ballot_sync(0xffffffffu, j < len && (!in || (any && (d > edge || (whole && d == edge)))));
+            const unsigned mt = __ballot_sync(0xffffffffu, in && !whole && d == edge);
+            if (lane < 2) mask[4 * b + 2 * half + lane] = lane ? mt : mk;
+            take += __popc(mk);
+            ties += __popc(mt);
+        }
+    if (lane == 0) { scan[0][warp] = take; scan[1][warp] = ties; }
     __syncthreads();
-    unsigned bt = it - take, be = ie - ties, nt = 0, ne = 0;
+    unsigned bt = 0, be = 0, nt = 0, ne = 0;
     for (int w = 0; w < EV_WARPS; ++w) {
-        if (w == warp) { bt += nt; be += ne; }
+        if (w == warp) { bt = nt; be = ne; }
         nt += scan[0][w];
         ne += scan[1][w];
     }
@@ -390,78 +444,133 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
         bt += cl_ld32u(&mine[0], r);
         be += cl_ld32u(&mine[1], r);
     }
-    for (int j = a0; j < a1; ++j) {
-        const int t = kind(j);
-        if (t == 2 || (t == 1 && be < want)) out[bt + min(be, want)] = j;
-        bt += t == 2;
-        be += t == 1;
-    }
+    for (int b = w0; b < w1; ++b)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const unsigned mk = mask[4 * b + 2 * half], mt = mask[4 * b + 2 * half + 1], lt = (1u << lane) - 1;
+            const unsigned e = be + __popc(mt & lt);
+            if ((mk >> lane & 1) || ((mt >> lane & 1) && e < want)) out[bt + __popc(mk & lt) + min(e, want)] = j0 + (b << 6) + 32 * half + lane;
+            bt += __popc(mk);
+            be += __popc(mt);
+        }
     cl_sync();                                           // no CTA leaves while another reads its shared memory
 }
 
-// The kept tokens of 64 new places (a page of one kv head), a CTA each: rows
-// of keys, scale codes and weights by gathers; the values' codes, packed by
-// channel, by one thread per channel that walks the kept places in order,
-// takes a source word's kept codes out of it and fills the new words. Places
-// behind the last kept token are left as they were. The new pages may not be
-// among the sequences' own.
+// The kept tokens of 64 new places (a page of one kv head), a CTA each. Rows
+// of keys, scale codes and weights are gathered. A thread of the values takes
+// two channels that share 16 bytes of every 16 places of a page, and walks the
+// kept places in order: one load for those that lie in the same 16, a nibble
+// out of it for each, one store for 16 new places. Places behind the last kept
+// token are left as they were. The new pages may not be among the sequences'
+// own.
 constexpr int KV4_ZEROS = -0x77777778;   // eight codes of zero (8 each)
 template <int D>
 __global__ void __launch_bounds__(128) k_kv4_evict_move(Kv4Args a, Kv4Evict p) {
+    constexpr int PW = D * KV_BLK / 8;                   // words of a page of values
     __shared__ int from[KV_BLK], page[KV_BLK];           // places in their pages, and those pages (-1: outside the pool)
+    __shared__ int run[KV_BLK + 1], runs;                // first kept places of the same 16 places of a page
+    __shared__ int2 move[KV_BLK];                        // shift of a place's code in its word (negative: the second of two); what brings it to its new one
     const int tid = threadIdx.x, b = blockIdx.x, g = blockIdx.y, i = blockIdx.z;
-    const int seq = p.seq[i];
+    const int seq = p.seq[i], to = p.new_table[(size_t)i * p.new_blocks + b];
     const int32_t* kept = p.kept + ((size_t)i * a.n_kv + g) * p.keep;
-    int n = 0;
+    pdl_wait();
     if (tid < KV_BLK) {
         const int s = b * KV_BLK + tid, j = s < p.keep ? __ldcg(kept + s) : -1;
         int blk = -1;
         if (j >= 0) blk = a.block_table[(size_t)seq * a.max_blocks + (j >> 6)];
         from[tid] = j < 0 ? -1 : j & 63;
         page[tid] = blk >= 0 && blk < a.n_blocks ? blk : -1;
+        move[tid] = make_int2((8 * (j & 3) + (j & 4)) | (j & 8 ? (int)0x80000000 : 0), 1 << (8 * (tid & 3) + (tid & 4)));
     }
-    n = __syncthreads_count(tid < KV_BLK && from[tid & 63] >= 0);        // the kept ones come first
+    const int n = __syncthreads_count(tid < KV_BLK && from[tid & 63] >= 0);      // the kept ones come first
     if (!n) return;
-    const int to = p.new_table[(size_t)i * p.new_blocks + b];
     if (to < 0 || to >= a.n_blocks) {
         if (tid == 0 && a.status) a.status[ST_CTX] = 1;
         return;
     }
     const size_t u = (size_t)to * a.n_kv + g;
+    if (tid < 32) {
+        int at = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int s = 32 * h + tid;
+            const bool lead = s < n && (s == 0 || page[s] != page[s - 1] || from[s] >> 4 != from[s - 1] >> 4);
+            const unsigned m = __ballot_sync(0xffffffffu, lead);
+            if (lead) run[at + __popc(m & ((1u << tid) - 1))] = s;
+            at += __popc(m);
+        }
+        if (tid == 0) { runs = at; run[at] = n; }
+    }
+    __syncthreads();
+    if (tid < D / 2) {
+        // values: row tid of 16 words holds channels 16 (tid / 8) + tid % 8 and 8 more
+        const int4* vin = (const int4*)(a.v + (size_t)g * PW * 4) + tid * 4;
+        int4* vout = (int4*)(a.v + u * PW * 4) + tid * 4;
+        auto load = [&](int r) -> int4 {
+            const int s = run[r], blk = page[s];
+            return blk >= 0 ? vin[(size_t)blk * a.n_kv * (PW / 4) + (from[s] >> 4)] : make_int4(KV4_ZEROS, KV4_ZEROS, KV4_ZEROS, KV4_ZEROS);
+        };
+        constexpr int AHEAD = 4;
+        int4 next[AHEAD];
+#pragma unroll
+        for (int r = 0; r < AHEAD; ++r)
+            if (r < runs) next[r] = load(r);
+        unsigned w0 = 0, w1 = 0, lo0 = 0, lo1 = 0;       // eight places of both channels; the eight before them
+        for (int r0 = 0; r0 < runs; r0 += AHEAD) {
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) {
+                if (r0 + x >= runs) break;
+                const int4 v = next[x];
+                if (r0 + x + AHEAD < runs) next[x] = load(r0 + x + AHEAD);
+                const int s1 = run[r0 + x + 1];
+                for (int s = run[r0 + x]; s < s1; ++s) {
+                    const int2 f = move[s];
+                    const unsigned c0 = f.x < 0 ? v.y : v.x, c1 = f.x < 0 ? v.w : v.z;
+                    w0 += (__funnelshift_r(c0, 0, f.x) & 15) * f.y;      // (the shift is taken mod 32)
+                    w1 += (__funnelshift_r(c1, 0, f.x) & 15) * f.y;
+                    if ((s & 7) == 7) {
+                        if (s & 8) vout[s >> 4] = make_int4((int)lo0, (int)w0, (int)lo1, (int)w1);
+                        lo0 = w0;
+                        lo1 = w1;
+                        w0 = w1 = 0;
+                    }
+                }
+            }
+        }
+        if (n & 15) {                                    // the last 16 places are not all taken
+            auto rest = [](int k) -> unsigned {          // nibbles of places k and up of a word of eight
+                unsigned m = 0;
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    if (x >= k) m |= 15u << (8 * (x & 3) + (x & 4));
+                return m;
+            };
+            const int4 old = vout[n >> 4];
+            const unsigned m0 = rest(n & 15), m1 = rest((n & 15) - 8);
+            if (!(n & 8)) { lo0 = w0; lo1 = w1; w0 = w1 = 0; }
+            vout[n >> 4] = make_int4((int)(lo0 | ((unsigned)old.x & m0)), (int)(w0 | ((unsigned)old.y & m1)),
+                                     (int)(lo1 | ((unsigned)old.z & m0)), (int)(w1 | ((unsigned)old.w & m1)));
+        }
+        return;
+    }
     // keys: rows of D / 2 bytes
-    constexpr int V = D / 32;                            // 16-byte pieces of a row
-    for (int x = tid; x < n * V; x += 128) {
+    constexpr int V = D / 32, NK = 128 - D / 2;          // 16-byte pieces of a row; threads
+    const int kt = tid - D / 2;
+#pragma unroll 4
+    for (int x = kt; x < n * V; x += NK) {
         const int s = x / V, c = x & (V - 1), blk = page[s];
         int4 v = make_int4(KV4_ZEROS, KV4_ZEROS, KV4_ZEROS, KV4_ZEROS);
         if (blk >= 0) v = *((const int4*)(a.k + (((size_t)blk * a.n_kv + g) * KV_BLK + from[s]) * (D / 2)) + c);
         *((int4*)(a.k + (u * KV_BLK + s) * (D / 2)) + c) = v;
     }
-    if (tid < n) {
-        const int blk = page[tid];
-        const size_t o = ((size_t)max(blk, 0) * a.n_kv + g) * KV_BLK + from[tid];
-        a.ks[u * KV_BLK + tid] = blk >= 0 ? a.ks[o] : 1;
-        a.vs[u * KV_BLK + tid] = blk >= 0 ? a.vs[o] : 1;
-        p.weight[u * KV_BLK + tid] = blk >= 0 ? p.weight[o] : 0;
-    }
-    if (tid >= D) return;
-    // values: word [key / 16][channel / 8 mod 2][key / 8 mod 2] of a channel's row of 16
-    const size_t ch = (size_t)(tid >> 4) * 128 + (tid & 7) * 16 + ((tid >> 3) & 1) * 2;
-    const uint32_t* vin = (const uint32_t*)a.v;
-    uint32_t* vout = (uint32_t*)a.v + u * (D * KV_BLK / 8) + ch;
-    unsigned w = 0;
-    for (int s = 0; s < n; ++s) {
-        const int blk = page[s], j = from[s];
-        unsigned code = 8;
-        if (blk >= 0)
-            code = vin[((size_t)blk * a.n_kv + g) * (D * KV_BLK / 8) + ch + (j >> 4) * 4 + ((j >> 3) & 1)] >> (8 * (j & 3) + (j & 4)) & 15;
-        w |= code << (8 * (s & 3) + (s & 4));
-        if ((s & 7) == 7 || s == n - 1) {
-            uint32_t* d = vout + (s >> 4) * 4 + ((s >> 3) & 1);
-            unsigned keep = 0;                           // codes behind the last kept token
-            for (int k = (s & 7) + 1; k < 8; ++k) keep |= 15u << (8 * (k & 3) + (k & 4));
-            *d = w | (keep ? *d & keep : 0u);
-            w = 0;
-        }
+    if (kt < n) {
+        const int blk = page[kt];
+        const size_t o = ((size_t)max(blk, 0) * a.n_kv + g) * KV_BLK + from[kt];
+        const uint8_t ck = a.ks[o], cv = a.vs[o];
+        const long long w = p.weight[o];
+        a.ks[u * KV_BLK + kt] = blk >= 0 ? ck : 1;
+        a.vs[u * KV_BLK + kt] = blk >= 0 ? cv : 1;
+        p.weight[u * KV_BLK + kt] = blk >= 0 ? w : 0;
     }
 }
 

@@ -118,11 +118,18 @@ cudaError_t launch_weigh(const DevInfo& di, const Kv4Args& a, Kv4Attn p, const K
 cudaError_t launch_evict(const DevInfo& di, const Kv4Args& a, Kv4Evict p, int n, int d, cudaStream_t s) {
     const int mp = (p.max_len + 63) >> 6;
     int lg = 0;
-    while ((2 << lg) <= di.max_cluster && mp > 16 << lg && ((long long)n * a.n_kv << (lg + 1)) <= 2LL * di.sms) ++lg;
-    while ((2 << lg) <= di.max_cluster && ((((mp + (1 << lg) - 1) >> lg) << 6) * 8LL) > EV_HELD) ++lg;
+    auto pages = [&]() { return (mp + (1 << lg) - 1) >> lg; };
+    // CTAs of 32 pages or less while there are few of them (4 sequences of 8192
+    // keys, 8 kv heads: 23.6 us, with one CTA 26.3, with 8 27.1; 16 of up to 32768
+    // 105.7 with 4, with 2 117.6, with 8 124; 64 of 2048 50 with one, with two 67),
+    // 16 of them only for long contexts (1 of 32768: 27.8 with 8, with 16 32)
+    while ((2 << lg) <= di.max_cluster &&
+           (pages() > EV_PAGES || (pages() > (lg < 3 ? 32 : 128) && ((long long)n * a.n_kv << (lg + 1)) * 2 <= 7LL * di.sms)))
+        ++lg;
     p.lg_s = lg;
-    p.cap = ((mp + (1 << lg) - 1) >> lg) << 6;
-    p.held = p.cap * 8LL <= EV_HELD;
+    const size_t bytes = (size_t)pages() * KV_BLK * 8;
+    p.held = bytes <= EV_HELD;
+    if (pages() > EV_PAGES) return cudaErrorNotSupported;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -133,13 +140,16 @@ cudaError_t launch_evict(const DevInfo& di, const Kv4Args& a, Kv4Evict p, int n,
     cfg.stream = s;
     cfg.gridDim = dim3(n << lg, a.n_kv);
     cfg.blockDim = dim3(EV_THREADS);
-    cfg.dynamicSmemBytes = p.held ? (size_t)p.cap * 8 : 0;
+    cfg.dynamicSmemBytes = p.held ? bytes : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_evict_select, a, p);
     if (e != cudaSuccess) return e;
-    const dim3 grid(p.new_blocks, a.n_kv, n);
-    if (d == 128) k_kv4_evict_move<128><<<grid, 128, 0, s>>>(a, p);
-    else k_kv4_evict_move<64><<<grid, 128, 0, s>>>(a, p);
-    return cudaGetLastError();
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(p.new_blocks, a.n_kv, n);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, d == 128 ? k_kv4_evict_move<128> : k_kv4_evict_move<64>, a, p);
 }
 
 }  // namespace
@@ -195,7 +205,7 @@ int detint_kv4_evict(const detint_kv4_t* c, int64_t* weight, const int32_t* seq,
     if (mis(weight, 16) || mis(seq, 4) || mis(lens, 4) || mis(new_table, 4) || mis(kept, 4))
         return err(DETINT_E_ARG, "weights must be 16-byte, the other arrays 4-byte aligned");
     Kv4Evict p{};
-    p.weight_in = p.weight = (long long*)weight;
+    p.weight = (long long*)weight;
     p.seq = seq; p.lens = lens; p.new_table = new_table; p.kept = kept;
     p.max_len = max_len; p.keep = keep; p.sinks = sinks; p.recent = recent;
     p.new_blocks = (keep + KV_BLK - 1) / KV_BLK;
