@@ -781,11 +781,14 @@ struct Kv4Q {
         const int lane = threadIdx.x & 31, sub = lane & (LPK - 1), kl = lane / LPK;
         const unsigned char* kr = base + kl * (D / 2) + sub * 16;
         const unsigned char* cr = base + KV_BLK * D / 2 + kl;
-        const bool writer = (sub & (LPG - 1)) == 0;
 #pragma unroll 4
-        for (int i = 0; i < KV_BLK / KPL; ++i) {
-            const int4 kv = *(const int4*)(kr + i * (KPL * D / 2));
-            const int ck = cr[i * KPL];
+        for (int i = 0; i < KV_BLK / KPL; ++i) keys(*(const int4*)(kr + i * (KPL * D / 2)), cr[i * KPL], i, out, pitch, clear, lo, hi, tm);
+    }
+    // key i KPL + lane / LPK of a page
+    __device__ __forceinline__ void keys(const int4& kv, int ck, int i, int* out, int pitch, bool clear, int lo, int hi, int (&tm)[HPL]) const {
+        const int lane = threadIdx.x & 31, sub = lane & (LPK - 1), kl = lane / LPK;
+        const bool writer = (sub & (LPG - 1)) == 0;
+        {
             const int ww[4] = {kv.x, kv.y, kv.z, kv.w};
             int acc[GT];
 #pragma unroll

@@ -14,13 +14,15 @@ struct Kv4Weigh {
 // p = rshr(E RS, bl - 1) with RS = floor(2^(bl + 23) / sum E), bl = bitlen(sum E)
 // >= 15: the probability in Q24. E RS < 2^39; p <= 2^24 and a rounding.
 __device__ __forceinline__ unsigned kv4_p24(int E, unsigned RS, int bl) {
-    return (unsigned)(((u64)((i64)E * RS) + (1ull << (bl - 2))) >> (bl - 1));
+    return (unsigned)(((u64)(unsigned)E * RS + (1ull << (bl - 2))) >> (bl - 1));
 }
 
 // ------------------------------------------------- weights, single tokens
 // A unit is a token, a kv head and up to GT of its q heads; its pages are
 // split over a cluster of CTAs that keep their scores in shared memory, as in
-// k_kv4_decode: scores (dp4a, a page per warp), the maximum over the cluster,
+// k_kv4_decode: scores (dp4a, a page per warp, whose codes go straight to
+// registers: without a ring there is room for twice the scores, and half as many
+// CTAs exchange), the maximum over the cluster,
 // exponentials in the scores' places and their sum over the cluster, then the
 // heads' probabilities of a key are added and sent to the key's weight by one
 // 64-bit integer atomic (exact, so the order does not matter; tokens of
@@ -36,14 +38,13 @@ struct Kv4WeighSm {
 };
 
 template <int D, int GT>
-__global__ void __launch_bounds__(KV4_DT, 2) k_kv4_weigh(Kv4Args a, Kv4Attn p, Kv4Weigh wg) {
-    using C = Kv4Ring<D>;
+__global__ void __launch_bounds__(KV4_DT, 3) k_kv4_weigh(Kv4Args a, Kv4Attn p, Kv4Weigh wg) {
     using Q = Kv4Q<D, GT>;
     constexpr int LPK = Q::LPK, HPL = Q::HPL, NPASS = (GT + 1) / 2;
+    constexpr int PG = KV_BLK * D / 2, N = KV_BLK / Q::KPL;             // loads of a lane for a page
     extern __shared__ __align__(16) unsigned char kv4_raw[];
     __shared__ Kv4WeighSm<GT> sm;
-    __shared__ unsigned long long full[8][C::NST];
-    int* pg = (int*)(kv4_raw + C::BYTES);                // [cap / 64]
+    int* pg = (int*)kv4_raw;                             // [cap / 64]
     const int pitch = p.cap + 8;                         // 8 banks between heads
     int* ts = pg + (((p.cap >> 6) + 3) & ~3);            // [GT][pitch]
 
@@ -77,43 +78,35 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_weigh(Kv4Args a, Kv4Attn p, K
         const size_t qi = (size_t)t * a.nq + h0 + min(tid, nh - 1);
         sm.row[tid] = kv4_row(p.mq[qi], p.kq[qi], kvp[6], kvp[7]);
     }
-    if (lane == 0)
-        for (int i = 0; i < C::NST; ++i) mbar_init(smem_u32(&full[warp][i]), 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     Q qr;
     qr.load(p.q8 + ((size_t)t * a.nq + h0) * D, nh);
     __syncthreads();
 
-    // ---- scores: this warp's pages warp, warp + 8, ... through its ring
+    // ---- scores: this warp's pages warp, warp + 8, ...
     const int nk = np > warp ? (np - warp + 7) >> 3 : 0;
-    unsigned char* ring = kv4_raw + warp * (C::NST * C::SLOT);
-    auto issue = [&](int q) {
-        if (q >= nk || lane) return;
-        const int st = q & (C::NST - 1), blk = pg[warp + 8 * q];
-        const uint32_t bar = smem_u32(&full[warp][st]), dst = smem_u32(ring + st * C::SLOT);
-        if (blk < 0) {
-            mbar_arrive(bar);
-        } else {
-            const size_t u = (size_t)blk * a.n_kv + g;
-            mbar_arrive_expect_tx(bar, C::PG + KV_BLK);
-            bulk_g2s(dst, a.k + u * C::PG, C::PG, bar);
-            bulk_g2s(dst + C::PG, a.ks + u * KV_BLK, KV_BLK, bar);
-        }
-    };
-#pragma unroll
-    for (int q = 0; q < C::NST; ++q) issue(q);
     int tm[HPL];
 #pragma unroll
     for (int x = 0; x < HPL; ++x) tm[x] = p.none;
-    const int sub = lane & (LPK - 1), hb = sub / Q::LPG * HPL;
+    const int sub = lane & (LPK - 1), kl = lane / LPK, hb = sub / Q::LPG * HPL;
     for (int q = 0; q < nk; ++q) {
-        const int pi = warp + 8 * q, jb = (pg0 + pi) << 6;
-        const bool ok = pg[pi] >= 0;
-        kv4_wait(&full[warp][q & (C::NST - 1)], (q / C::NST) & 1, p.polls, a.status);
-        qr.page(ring + (q & (C::NST - 1)) * C::SLOT, ts + hb * pitch + pi * KV_BLK + lane / LPK, pitch,
-                ok && jb >= j0 && jb + 64 <= j1, j0 - jb, ok ? j1 - jb : -1, tm);
-        __syncwarp();
-        issue(q + C::NST);
+        const int pi = warp + 8 * q, jb = (pg0 + pi) << 6, blk = pg[pi];
+        if (blk < 0) continue;                           // (its scores are not looked at)
+        const size_t u = (size_t)blk * a.n_kv + g;
+        const unsigned char *kr = a.k + u * PG + kl * (D / 2) + sub * 16, *cr = a.ks + u * KV_BLK + kl;
+        const bool clear = jb >= j0 && jb + 64 <= j1;
+        int* out = ts + hb * pitch + pi * KV_BLK + kl;
+#pragma unroll
+        for (int i0 = 0; i0 < N; i0 += 4) {
+            int4 kv[4];
+            int cv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                kv[i] = __ldg((const int4*)(kr + (i0 + i) * (Q::KPL * D / 2)));
+                cv[i] = __ldg(cr + (i0 + i) * Q::KPL);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qr.keys(kv[i], cv[i], i0 + i, out, pitch, clear, j0 - jb, j1 - jb, tm);
+        }
     }
 #pragma unroll
     for (int x = 0; x < HPL; ++x) {
@@ -151,14 +144,16 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_weigh(Kv4Args a, Kv4Attn p, K
             for (int k = 4 * (tid & 127); k < np * KV_BLK; k += 512) {
                 int4* at = (int4*)(ts + h * pitch + k);
                 const int jb = (pg0 << 6) + k;
-                const bool ok = pg[k >> 6] >= 0;
                 int4 v = make_int4(0, 0, 0, 0);
-                if (ok) {
+                if (pg[k >> 6] >= 0) {
                     v = *at;
-                    v.x = jb >= j0 && jb < j1 ? kv4_E(rw, v.x, T) : 0;
-                    v.y = jb + 1 >= j0 && jb + 1 < j1 ? kv4_E(rw, v.y, T) : 0;
-                    v.z = jb + 2 >= j0 && jb + 2 < j1 ? kv4_E(rw, v.z, T) : 0;
-                    v.w = jb + 3 >= j0 && jb + 3 < j1 ? kv4_E(rw, v.w, T) : 0;
+                    v = make_int4(kv4_E(rw, v.x, T), kv4_E(rw, v.y, T), kv4_E(rw, v.z, T), kv4_E(rw, v.w, T));
+                    if (jb < j0 || jb + 4 > j1) {
+                        if (jb < j0 || jb >= j1) v.x = 0;
+                        if (jb + 1 < j0 || jb + 1 >= j1) v.y = 0;
+                        if (jb + 2 < j0 || jb + 2 >= j1) v.z = 0;
+                        if (jb + 3 < j0 || jb + 3 >= j1) v.w = 0;
+                    }
                 }
                 *at = v;
                 sumE[x] += (unsigned)(v.x + v.y + v.z + v.w);
@@ -204,6 +199,305 @@ __global__ void __launch_bounds__(KV4_DT, 2) k_kv4_weigh(Kv4Args a, Kv4Attn p, K
         for (int h = 0; h < GT; ++h) s += kv4_p24(ts[h * pitch + k], RS[h], bl[h]);
         if (s) atomicAdd((unsigned long long*)wg.weight + ((size_t)pg[k >> 6] * a.n_kv + g) * KV_BLK + (k & 63), (unsigned long long)s);
     }
+}
+
+// ------------------------------------------------- weights, blocks of tokens
+// A cluster of CTAs takes 16 query rows (16 / Gp consecutive tokens times up to
+// 16 q heads of one kv head, Gp a power of two) and all their keys at once: a
+// warp scores up to 4 pages of 64 keys on the int8 tensor pipe and keeps the
+// scores, of one page in its registers, of the others in shared memory, so that
+// each is computed once (three sweeps, for the maxima, the sums and the weights,
+// would take the tensor pipe three times).
+// Two exchanges settle the rows' maxima and sums over the warps and CTAs; then
+// the 16 rows' probabilities of a key are added over the lanes and go to the
+// key's weight by one 64-bit atomic. Column n of score tile j is key 16 (n / 2)
+// + 2 j + (n & 1), so that a lane's scores are 16 neighbouring keys. K fragments
+// come straight from the pages: a warp's load is eight whole rows. A block's
+// tokens may belong to several sequences: each run of one sequence whose pages
+// fit the cluster is a round of its own with the other rows masked.
+constexpr int WB_NW = 8;                 // warps of a CTA
+constexpr int WB_ROWS = 16;
+constexpr int WB_PG = 4;                 // pages of a warp
+constexpr int WB_SMEM = WB_NW * (WB_PG - 1) * 4096;
+
+template <int D>
+__global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv4Attn p, Kv4Weigh wg) {
+    constexpr int KS = D / 32, PG = KV_BLK * D / 2;
+    extern __shared__ __align__(16) unsigned char kv4_raw[];
+    __shared__ int r_pos[WB_ROWS], w_top[WB_NW][WB_ROWS];
+    __shared__ unsigned w_sum[WB_NW][WB_ROWS];
+    __shared__ int c_top[2][16][WB_ROWS];                // by rounds in turn: [CTA][row]
+    __shared__ unsigned c_sum[2][16][WB_ROWS];
+    __shared__ unsigned r_RS[WB_ROWS];
+    __shared__ int r_bl[WB_ROWS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
+    const int S = 1 << p.lgC, rank = (int)blockIdx.x;
+    int g = blockIdx.y, hg = 0;
+    while (g >= a.n_kv) { g -= a.n_kv; ++hg; }
+    const int BQ = WB_ROWS >> p.lgGp, Gp = 1 << p.lgGp, h0 = g * p.G + hg * Gp, nh = min(Gp, p.G - hg * Gp);
+    const int t0 = p.t0 + (int)(gridDim.z - 1 - blockIdx.z) * BQ;    // later tokens tend to have more keys
+    const int nt = min(BQ, p.T - t0);
+    const int32_t* kvp = a.params + (size_t)g * (8 + D);
+    if (S > 1) cl_arrive();
+    if (tid < WB_ROWS) {
+        const int i = tid >> p.lgGp, hh = tid & (Gp - 1);
+        int pos = -1;
+        if (i < nt && hh < nh) {
+            pos = p.tok_pos[t0 + i];
+            const int seq = p.tok_seq[t0 + i];
+            if (pos >= 0 && (pos >= p.max_len || seq < 0 || seq >= a.n_seq || (pos >> 6) >= a.max_blocks)) {
+                pos = -1;
+                if (a.status) a.status[ST_CTX] = 1;
+            }
+        }
+        r_pos[tid] = pos;
+    }
+    const int rA = gid, rB = gid + 8;
+    Kv4Row rw[2];
+    int qf[KS][4], qo[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int r = x ? rB : rA, i = r >> p.lgGp, hh = r & (Gp - 1);
+        int w[2 * KS];
+#pragma unroll
+        for (int j = 0; j < 2 * KS; ++j) w[j] = 0;
+        int mq = 0, kq = 0;
+        if (i < nt && hh < nh) {
+            const size_t qi = (size_t)(t0 + i) * a.nq + h0 + hh;
+            const int* qp = (const int*)(p.q8 + qi * D + tig * (D / 4));
+#pragma unroll
+            for (int j = 0; j < 2 * KS; ++j) w[j] = __ldg(qp + j);
+            mq = p.mq[qi];
+            kq = p.kq[qi];
+        }
+        rw[x] = kv4_row(mq, kq, kvp[6], kvp[7]);
+        int sq = 0;
+#pragma unroll
+        for (int j = 0; j < 2 * KS; ++j) sq = __dp4a(w[j], 0x01010101, sq);
+        sq += __shfl_xor_sync(0xffffffffu, sq, 1);
+        sq += __shfl_xor_sync(0xffffffffu, sq, 2);
+        qo[x] = -8 * sq;                                 // the codes are values + 8
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            qf[s][x] = w[2 * s];
+            qf[s][2 + x] = w[2 * s + 1];
+        }
+    }
+    __syncthreads();
+    if (S > 1) cl_wait();                                // every CTA runs: its shared memory may be written
+    int round = 0;
+    for (int s0 = 0; s0 < nt;) {
+        // tokens [s0, s1) of one sequence whose pages fit the cluster (one token's always do)
+        const int seq = p.tok_seq[t0 + s0];
+        int s1 = s0, kmax = -1, kmin = 0x7fffffff;
+        for (; s1 < nt && p.tok_seq[t0 + s1] == seq; ++s1) {
+            const int pos = r_pos[s1 << p.lgGp];
+            if (pos < 0) continue;
+            const int hi = max(kmax, pos), lo = min(kmin, p.window > 0 ? max(0, pos + 1 - p.window) : 0);
+            if (kmax >= 0 && (hi >> 6) - (lo >> 6) >= S * WB_NW * WB_PG) break;
+            kmax = hi;
+            kmin = lo;
+        }
+        const int iA = rA >> p.lgGp, iB = rB >> p.lgGp;
+        const int hiA = iA >= s0 && iA < s1 ? r_pos[rA] : -1, hiB = iB >= s0 && iB < s1 ? r_pos[rB] : -1;
+        const int loA = p.window > 0 ? max(0, hiA + 1 - p.window) : 0, loB = p.window > 0 ? max(0, hiB + 1 - p.window) : 0;
+        // the keys that every row takes
+        const int cmax = __reduce_min_sync(0xffffffffu, min(hiA, hiB)), cmin = __reduce_max_sync(0xffffffffu, max(loA, loB));
+        s0 = s1;
+        if (kmax < 0) continue;
+        const int p0 = kmin >> 6, np = (kmax >> 6) - p0 + 1, buf = round & 1;
+        ++round;
+        // ---- scores of this warp's pages rank WB_NW + warp, + S WB_NW, ...; the first one's stay in registers
+        const int first = rank * WB_NW + warp, mine = np > first ? ((np - first - 1) >> (p.lgC + 3)) + 1 : 0;
+        int4* const store = (int4*)kv4_raw + warp * ((WB_PG - 1) * 256) + lane - 256;      // page q from [256 q]
+        int t[8][4], T[2] = {p.none, p.none}, blk_l = -1;
+        if (lane < mine) {
+            blk_l = a.block_table[(size_t)seq * a.max_blocks + p0 + first + (lane << (p.lgC + 3))];
+            if (blk_l < 0 || blk_l >= a.n_blocks) {
+                blk_l = -1;
+                if (a.status) a.status[ST_CTX] = 1;
+            }
+        }
+        auto page_of = [&](int q) { return __shfl_sync(0xffffffffu, blk_l, q); };          // -1: its scores are not looked at
+        auto key_of = [&](int q) { return (p0 + first + (q << (p.lgC + 3))) << 6; };
+#pragma unroll 1
+        for (int q = mine - 1; q >= 0; --q) {
+            const int blk = page_of(q);
+            if (blk < 0) continue;
+            const size_t u = (size_t)blk * a.n_kv + g;
+            const unsigned char* kr = a.k + u * PG + (16 * (gid >> 1) + (gid & 1)) * (D / 2) + tig * (D / 8);
+            const int4 cv = __ldg((const int4*)(a.ks + u * KV_BLK) + tig);
+            const int cw[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                int w[4][KS];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const unsigned char* at = kr + 2 * (4 * half + j) * (D / 2);
+                    if (D == 128) {
+                        const int4 v = __ldg((const int4*)at);
+                        w[j][0] = v.x; w[j][1] = v.y; w[j][KS - 2] = v.z; w[j][KS - 1] = v.w;
+                    } else {
+                        const int2 v = __ldg((const int2*)at);
+                        w[j][0] = v.x; w[j][1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    int (&c)[4] = t[4 * half + j];
+                    c[0] = c[1] = qo[0];
+                    c[2] = c[3] = qo[1];
+#pragma unroll
+                    for (int s = 0; s < KS; ++s)
+                        mma_s8u8(c, qf[s][0], qf[s][1], qf[s][2], qf[s][3], kv4_lo(w[j][s]), kv4_hi(w[j][s]));
+                }
+            }
+            const int kb = key_of(q), k0 = kb + 16 * tig;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int sc = cw[j >> 1] >> (8 * (2 * (j & 1) + e)) & 255;
+                    t[j][e] *= sc;
+                    t[j][2 + e] *= sc;
+                }
+            if (kb >= cmin && kb + 63 <= cmax) {         // no key of the page is masked
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    T[0] = max(T[0], max(t[j][0], t[j][1]));
+                    T[1] = max(T[1], max(t[j][2], t[j][3]));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = k0 + 2 * j + e;
+                        if (key <= hiA && key >= loA) T[0] = max(T[0], t[j][e]);
+                        if (key <= hiB && key >= loB) T[1] = max(T[1], t[j][2 + e]);
+                    }
+            }
+            if (q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) store[256 * q + 32 * j] = make_int4(t[j][0], t[j][1], t[j][2], t[j][3]);
+        }
+        // ---- the rows' maxima over the warps and CTAs
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            T[x] = max(T[x], __shfl_xor_sync(0xffffffffu, T[x], 1));
+            T[x] = max(T[x], __shfl_xor_sync(0xffffffffu, T[x], 2));
+            if (tig == 0) w_top[warp][x ? rB : rA] = T[x];
+        }
+        __syncthreads();
+        if (tid < 16 * S) {                              // every CTA of the cluster gets this one's
+            const int r = tid & 15;
+            int m = w_top[0][r];
+#pragma unroll
+            for (int w = 1; w < WB_NW; ++w) m = max(m, w_top[w][r]);
+            cl_st32(&c_top[buf][rank][r], tid >> 4, m);
+        }
+        if (S > 1) cl_sync();
+        else __syncthreads();
+#pragma unroll 4
+        for (int c = 0; c < S; ++c) {
+            T[0] = max(T[0], c_top[buf][c][rA]);
+            T[1] = max(T[1], c_top[buf][c][rB]);
+        }
+        // ---- exponentials in the scores' places, and their sums
+        unsigned sum[2] = {0, 0};
+        auto exps = [&](int (&v)[4]) {
+            v[0] = kv4_E(rw[0], v[0], T[0]);
+            v[1] = kv4_E(rw[0], v[1], T[0]);
+            v[2] = kv4_E(rw[1], v[2], T[1]);
+            v[3] = kv4_E(rw[1], v[3], T[1]);
+        };
+        auto mask = [&](int (&v)[4], int k) {            // keys k, k + 1
+            if (k > hiA || k < loA) v[0] = 0;
+            if (k + 1 > hiA || k + 1 < loA) v[1] = 0;
+            if (k > hiB || k < loB) v[2] = 0;
+            if (k + 1 > hiB || k + 1 < loB) v[3] = 0;
+        };
+#pragma unroll 1
+        for (int q = 0; q < mine; ++q) {
+            if (page_of(q) < 0) continue;
+            const int kb = key_of(q), k0 = kb + 16 * tig;
+            const bool clear = kb >= cmin && kb + 63 <= cmax;
+            if (q == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    exps(t[j]);
+                    if (!clear) mask(t[j], k0 + 2 * j);
+                    sum[0] += (unsigned)(t[j][0] + t[j][1]);
+                    sum[1] += (unsigned)(t[j][2] + t[j][3]);
+                }
+            } else {
+#pragma unroll 4
+                for (int j = 0; j < 8; ++j) {
+                    const int4 s = store[256 * q + 32 * j];
+                    int v[4] = {s.x, s.y, s.z, s.w};
+                    exps(v);
+                    if (!clear) mask(v, k0 + 2 * j);
+                    sum[0] += (unsigned)(v[0] + v[1]);
+                    sum[1] += (unsigned)(v[2] + v[3]);
+                    store[256 * q + 32 * j] = make_int4(v[0], v[1], v[2], v[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
+            sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
+            if (tig == 0) w_sum[warp][x ? rB : rA] = sum[x];
+        }
+        __syncthreads();
+        if (tid < 16 * S) {
+            const int r = tid & 15;
+            unsigned m = 0;
+#pragma unroll
+            for (int w = 0; w < WB_NW; ++w) m += w_sum[w][r];        // 2^11 keys: below 2^26
+            cl_st32((int*)&c_sum[buf][rank][r], tid >> 4, (int)m);
+        }
+        if (S > 1) cl_sync();
+        else __syncthreads();
+        if (tid < WB_ROWS) {
+            unsigned m = 0;                              // at most 2^15 keys: below 2^30
+            for (int c = 0; c < S; ++c) m += c_sum[buf][c][tid];
+            const int bl = 32 - __clz(m);
+            r_RS[tid] = m ? (unsigned)pow2_recip(m, bl, 1, 23) : 0;
+            r_bl[tid] = max(bl, 2);
+        }
+        __syncthreads();
+        // ---- the rows' probabilities of each key, added over the lanes: lane gid ends with keys 2 gid, 2 gid + 1 of its 16
+        const unsigned RSa = r_RS[rA], RSb = r_RS[rB];
+        const int bla = r_bl[rA], blb = r_bl[rB];
+#pragma unroll 1
+        for (int q = 0; q < mine; ++q) {
+            const int blk = page_of(q);
+            if (blk < 0) continue;
+            unsigned v[16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                int4 s = make_int4(t[j][0], t[j][1], t[j][2], t[j][3]);
+                if (q) s = store[256 * q + 32 * j];
+                v[2 * j] = kv4_p24(s.x, RSa, bla) + kv4_p24(s.z, RSb, blb);
+                v[2 * j + 1] = kv4_p24(s.y, RSa, bla) + kv4_p24(s.w, RSb, blb);
+            }
+#pragma unroll
+            for (int n = 8, o = 16; o >= 4; n >>= 1, o >>= 1) {
+                const bool up = (lane & o) != 0;
+#pragma unroll
+                for (int h = 0; h < 8; ++h)
+                    if (h < n) {
+                        const unsigned keep = up ? v[h + n] : v[h], give = up ? v[h] : v[h + n];
+                        v[h] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+            }
+            unsigned long long* w = (unsigned long long*)wg.weight + ((size_t)blk * a.n_kv + g) * KV_BLK + 16 * tig + 2 * gid;
+            if (v[0]) atomicAdd(w, (unsigned long long)v[0]);
+            if (v[1]) atomicAdd(w + 1, (unsigned long long)v[1]);
+        }
+    }
+    if (S > 1) cl_sync();                                // no CTA leaves while another writes to it
 }
 
 // ------------------------------------------------------------------ eviction

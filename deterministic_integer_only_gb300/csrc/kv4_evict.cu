@@ -26,13 +26,14 @@ constexpr int SMEM_MAX = 227 * 1024;
 constexpr int EV_HELD = 192 * 1024;          // bytes of keys that select holds in shared memory
 
 using WeighFn = void (*)(Kv4Args, Kv4Attn, Kv4Weigh);
-const WeighFn WEIGH[2][4] = {{k_kv4_weigh<64, 1>, k_kv4_weigh<64, 2>, k_kv4_weigh<64, 4>, k_kv4_weigh<64, 8>},
-                             {k_kv4_weigh<128, 1>, k_kv4_weigh<128, 2>, k_kv4_weigh<128, 4>, k_kv4_weigh<128, 8>}};
-int lg2(int n) { return n >= 8 ? 3 : n >= 4 ? 2 : n >= 2 ? 1 : 0; }
-size_t weigh_fixed(int gt) { return gt == 8 ? sizeof(Kv4WeighSm<8>) : gt == 4 ? sizeof(Kv4WeighSm<4>) : gt == 2 ? sizeof(Kv4WeighSm<2>) : sizeof(Kv4WeighSm<1>); }
-size_t weigh_smem(int d, int gt, int cap) {
-    const size_t ring = d == 128 ? Kv4Ring<128>::BYTES : Kv4Ring<64>::BYTES;
-    return ring + (size_t)(((cap >> 6) + 3) & ~3) * 4 + (size_t)gt * (cap + 8) * 4;
+constexpr int NGT = 3;                       // 1, 2 or 4 heads of a CTA
+const WeighFn WEIGH[2][NGT] = {{k_kv4_weigh<64, 1>, k_kv4_weigh<64, 2>, k_kv4_weigh<64, 4>},
+                               {k_kv4_weigh<128, 1>, k_kv4_weigh<128, 2>, k_kv4_weigh<128, 4>}};
+const WeighFn WEIGH_BLOCK[2] = {k_kv4_weigh_block<64>, k_kv4_weigh_block<128>};
+int lg2(int n) { return n >= 4 ? 2 : n >= 2 ? 1 : 0; }
+size_t weigh_fixed(int gt) { return gt == 4 ? sizeof(Kv4WeighSm<4>) : gt == 2 ? sizeof(Kv4WeighSm<2>) : sizeof(Kv4WeighSm<1>); }
+size_t weigh_smem(int gt, int cap) {
+    return (size_t)(((cap >> 6) + 3) & ~3) * 4 + (size_t)gt * (cap + 8) * 4;
 }
 // dynamic shared memory of one CTA on an SM, and of two
 size_t weigh_room(int gt, int ctas) { return (ctas == 1 ? SMEM_MAX : 113 * 1024) - 1024 - weigh_fixed(gt); }
@@ -67,12 +68,17 @@ cudaError_t init(DevInfo** out) {
     e = cudaDeviceGetAttribute(&di->sms, cudaDevAttrMultiProcessorCount, dev);
     int mc = 16;
     for (int d : {0, 1})
-        for (int l = 0; l < 4 && e == cudaSuccess; ++l) {
+        for (int l = 0; l < NGT && e == cudaSuccess; ++l) {
             const size_t room = weigh_room(1 << l, 1);
             e = cudaFuncSetAttribute(WEIGH[d][l], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)room);
             if (e == cudaSuccess) e = cudaFuncSetAttribute(WEIGH[d][l], cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e == cudaSuccess) mc = std::min(mc, cluster_of((const void*)WEIGH[d][l], KV4_DT, room));
         }
+    for (int d : {0, 1}) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(WEIGH_BLOCK[d], cudaFuncAttributeMaxDynamicSharedMemorySize, WB_SMEM);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(WEIGH_BLOCK[d], cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) mc = std::min(mc, cluster_of((const void*)WEIGH_BLOCK[d], 32 * WB_NW, WB_SMEM));
+    }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv4_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_HELD);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv4_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) {
@@ -87,15 +93,15 @@ cudaError_t launch_weigh(const DevInfo& di, const Kv4Args& a, Kv4Attn p, const K
     p.none = KV4_NEG;
     int mp = (p.max_len + 63) >> 6;                                 // pages a token can have
     if (p.window > 0) mp = std::min(mp, ((p.window + 62) >> 6) + 1);
-    int gt = p.G >= 5 ? 8 : (p.G >= 3 ? 4 : p.G), S = 1;
+    int gt = p.G >= 3 ? 4 : p.G, S = 1;
     const int Tc = std::min(p.T, 65535);
     auto units = [&]() { return (long long)Tc * a.n_kv * ((p.G + gt - 1) / gt); };
     auto cap = [&]() { return ((mp + S - 1) / S) << 6; };
     while (S < di.max_cluster && units() * 2 * S <= 2 * di.sms && mp >= 8 * S) S <<= 1;
-    while (S < di.max_cluster && weigh_smem(d, gt, cap()) > weigh_room(gt, 2)) S <<= 1;
-    while (gt > 1 && weigh_smem(d, gt, cap()) > weigh_room(gt, 1)) gt >>= 1;
+    while (S < di.max_cluster && weigh_smem(gt, cap()) > weigh_room(gt, 2)) S <<= 1;
+    while (gt > 1 && weigh_smem(gt, cap()) > weigh_room(gt, 1)) gt >>= 1;
     p.cap = cap();
-    if (weigh_smem(d, gt, p.cap) > weigh_room(gt, 1)) return cudaErrorNotSupported;
+    if (weigh_smem(gt, p.cap) > weigh_room(gt, 1)) return cudaErrorNotSupported;
     p.smul = ((1ull << 32) + S - 1) / S;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
@@ -106,10 +112,39 @@ cudaError_t launch_weigh(const DevInfo& di, const Kv4Args& a, Kv4Attn p, const K
     cfg.numAttrs = S > 1 ? 1 : 0;
     cfg.stream = s;
     cfg.blockDim = dim3(KV4_DT);
-    cfg.dynamicSmemBytes = weigh_smem(d, gt, p.cap);
+    cfg.dynamicSmemBytes = weigh_smem(gt, p.cap);
     for (p.t0 = 0; p.t0 < p.T; p.t0 += 65535) {
         cfg.gridDim = dim3(S, a.n_kv * ((p.G + gt - 1) / gt), std::min(65535, p.T - p.t0));
         const cudaError_t e = cudaLaunchKernelEx(&cfg, WEIGH[d == 128][lg2(gt)], a, p, w);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_weigh_block(const DevInfo& di, const Kv4Args& a, Kv4Attn p, const Kv4Weigh& w, int d, cudaStream_t s) {
+    p.none = KV4_NEG;
+    int mp = (p.max_len + 63) >> 6;                                 // pages a token can have, and one for its neighbours
+    if (p.window > 0) mp = std::min(mp, ((p.window + 62) >> 6) + 2);
+    p.lgC = 0;
+    while (mp > (WB_NW * WB_PG) << p.lgC && (2 << p.lgC) <= di.max_cluster) ++p.lgC;
+    if (mp > (WB_NW * WB_PG) << p.lgC) return launch_weigh(di, a, p, w, d, s);   // too long to be kept at once
+    p.lgGp = 0;
+    while (p.lgGp < 4 && (1 << p.lgGp) < p.G) ++p.lgGp;
+    const int bq = WB_ROWS >> p.lgGp, hg = (p.G + (1 << p.lgGp) - 1) >> p.lgGp, tiles = (p.T + bq - 1) / bq;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1 << p.lgC;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.lgC ? 1 : 0;
+    cfg.stream = s;
+    cfg.blockDim = dim3(32 * WB_NW);
+    cfg.dynamicSmemBytes = mp > WB_NW ? WB_SMEM : 0;
+    for (int b0 = 0; b0 < tiles; b0 += 65535) {
+        p.t0 = b0 * bq;
+        cfg.gridDim = dim3(1 << p.lgC, a.n_kv * hg, std::min(65535, tiles - b0));
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, WEIGH_BLOCK[d == 128], a, p, w);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -172,7 +207,7 @@ int weigh(const char* where, bool block, const detint_kv4_t* c, const int8_t* q8
     w.weight = (long long*)weight;
     DevInfo* di = nullptr;
     cudaError_t e = init(&di);
-    if (e == cudaSuccess) e = launch_weigh(*di, a, p, w, c->head_dim, (cudaStream_t)sp);
+    if (e == cudaSuccess) e = (block ? launch_weigh_block : launch_weigh)(*di, a, p, w, c->head_dim, (cudaStream_t)sp);
     return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
 }
 
