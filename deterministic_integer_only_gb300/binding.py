@@ -25,7 +25,7 @@ ERRORS = {0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "token id o
 # every entry point of include/detint.h
 SYMBOLS = ["detint_load", "detint_load_kv", "detint_prefill", "detint_decode_step", "detint_gemm_i8",
            "detint_reset_seq", "detint_seq_len", "detint_status", "detint_set_graph",
-           "detint_set_option", "detint_argmax_noalloc", "detint_sample", "detint_fork_seq", "detint_gemm_w16", "detint_split_w16",
+           "detint_set_option", "detint_argmax_noalloc", "detint_sample", "detint_fork_seq", "detint_reorder_seqs", "detint_gemm_w16", "detint_split_w16",
            "detint_int8_peak_loop", "detint_kv4_append", "detint_kv4_workspace", "detint_kv4_decode",
            "detint_kv4_prefill", "detint_kv4_append_axes", "detint_kv4_weigh", "detint_kv4_weigh_block",
            "detint_kv4_evict", "detint_kv4_copy", "detint_beam_select", "detint_beam_workspace",
@@ -60,6 +60,7 @@ def lib():
         L.detint_set_option.argtypes = [vp, C.c_int, C.c_int]
         L.detint_argmax_noalloc.argtypes = [vp, C.c_int, C.c_int, vp, vp]
         L.detint_fork_seq.argtypes = [vp, C.c_int, C.c_int, C.c_int, vp]
+        L.detint_reorder_seqs.argtypes = [vp, C.c_int, i32p, i32p, vp]
         L.detint_gemm_w16.argtypes = [vp, vp, vp, vp, C.c_int, C.c_int, C.c_int, vp]
         L.detint_split_w16.argtypes = [vp, vp, vp, C.c_longlong, vp]
         L.detint_sample.argtypes = [vp, C.c_int, C.c_int, C.POINTER(SamplingParams), vp, vp]
@@ -565,12 +566,17 @@ def detint_beam_select(logits, scores, n_out: int, done=None, end_id: int = -1, 
     groups, beams = scores.shape
     rows, n = logits.shape
     stride = _row_stride(w, "logits", logits, i32, rows, n, index)
-    if n_out >> 31 or not -(1 << 31) <= end_id < 1 << 31:
+    if n_out < 1 or n_out >> 31 or not -(1 << 31) <= end_id < 1 << 31:
         raise DetintError(1, w, f"n_out {n_out} or end_id {end_id} out of range")
     m = groups * n_out
     if out is None:
-        parent, token, end = _new(stream, (3, groups, n_out), i32, logits.device).unbind(0)
-        score = _new(stream, (groups, n_out), i64, logits.device)
+        shape, dev = (groups, n_out), logits.device
+        if stream is None:
+            parent, token, score, end = (torch.empty(shape, dtype=i32, device=dev), torch.empty(shape, dtype=i32, device=dev),
+                                         torch.empty(shape, dtype=i64, device=dev), torch.empty(shape, dtype=i32, device=dev))
+        else:
+            parent, token, end = (_new(stream, shape, i32, dev) for _ in range(3))
+            score = _new(stream, shape, i64, dev)
     else:
         parent, token, score, end = out
     if workspace is None:
@@ -685,6 +691,15 @@ class Model:
         _check(lib().detint_fork_seq(self._h, int(src), int(dst), int(n_tokens), self.stream.cuda_stream),
                "detint_fork_seq")
 
+    def reorder_seqs(self, seq_ids, parents):
+        """seq_ids[i] becomes what seq_ids[parents[i]] was (shared KV blocks)."""
+        seq, par = _i32(seq_ids), _i32(parents)
+        if seq.size != par.size:
+            raise ValueError("reorder_seqs: one parent for each sequence expected")
+        _check(lib().detint_reorder_seqs(self._h, seq.size, seq.ctypes.data_as(C.POINTER(C.c_int32)),
+                                         par.ctypes.data_as(C.POINTER(C.c_int32)), self.stream.cuda_stream),
+               "detint_reorder_seqs")
+
     def seq_len(self, seq_id: int) -> int:
         v = C.c_int32()
         _check(lib().detint_seq_len(self._h, int(seq_id), C.byref(v)), "detint_seq_len")
@@ -762,3 +777,51 @@ class Model:
                     rows.append(lg)
         self.stream.synchronize()
         return toks, (hashes if keep_logits == "hash" else rows)
+
+    def beam_search(self, prompts, beams: int, max_new: int, end_id: int = -1, seq_ids=None):
+        """The `beams` best continuations of each prompt by integer beam search.
+
+        Returns (tokens [len(prompts)][beams][max_new] int32 numpy, scores
+        [len(prompts)][beams] int64 numpy: log-probabilities in Q16), best first.
+        A beam that chose end_id keeps its score and continues with end_id; the
+        search stops early once every beam has. The beams of prompt g run on the
+        empty sequences seq_ids[g * beams : (g + 1) * beams] (0, 1, ... by default) and
+        share their common pages. Scores and tokens do not depend on the other
+        prompts of the batch.
+        """
+        torch = self.torch
+        G, dev = len(prompts), torch.device("cuda")
+        if G < 1 or not 1 <= beams <= 64 or max_new < 1 or beams > self.vocab:
+            raise ValueError("beam_search: at least one prompt and token, 1 to 64 beams expected")
+        seq_ids = list(range(G * beams)) if seq_ids is None else list(seq_ids)
+        if len(seq_ids) != G * beams:
+            raise ValueError(f"beam_search: {G * beams} sequences expected, got {len(seq_ids)}")
+        cu = np.zeros(G + 1, np.int64)
+        cu[1:] = np.cumsum([len(p) for p in prompts])
+        flat = torch.tensor(np.concatenate([np.asarray(p, np.int32) for p in prompts]), dtype=torch.int32, device=dev)
+        toks = np.zeros((G, beams, max_new), np.int32)
+        with torch.cuda.stream(self.stream):
+            logits = torch.empty((G * beams, self.vocab), dtype=torch.int32, device=dev)
+            ws = torch.empty(detint_beam_workspace(G * beams, self.vocab, beams), dtype=torch.uint8, device=dev)
+            tok = torch.empty(G * beams, dtype=torch.int32, device=dev)
+            self.prefill(seq_ids[::beams], flat, cu, logits, tok)
+            # the prompts' rows: one beam of each group so far
+            parent, token, scores, done = detint_beam_select(logits[:G], torch.zeros((G, 1), dtype=torch.int64, device=dev),
+                                                             beams, None, end_id, workspace=ws)
+            base = np.arange(G)[:, None] * beams
+            for step in range(max_new):
+                if step:
+                    self.decode_step(seq_ids, tok, logits, tok)
+                    parent, token, scores, done = detint_beam_select(logits, scores, beams, done if end_id >= 0 else None,
+                                                                     end_id, workspace=ws)
+                tok.copy_(token.view(-1))
+                par, new = parent.cpu().numpy(), token.cpu().numpy()
+                toks = np.take_along_axis(toks, par[:, :, None], 1)
+                toks[:, :, step] = new
+                if step + 1 == max_new or end_id >= 0 and bool(done.all()):
+                    toks[:, :, step + 1:] = end_id if end_id >= 0 else 0
+                    break
+                self.reorder_seqs(seq_ids, (par + base).reshape(-1))
+            out = scores.cpu().numpy()
+        self.stream.synchronize()
+        return toks, out

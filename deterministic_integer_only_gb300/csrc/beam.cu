@@ -90,6 +90,20 @@ constexpr int MAX_VOCAB = 1 << 24;           // the sum of a row's exponentials 
 constexpr int MAX_ROWS = 65535;
 
 }  // namespace
+
+cudaError_t launch_copy_blocks(const BlockParts& b, const int* src, const int* dst, int n, cudaStream_t s) {
+    for (int i = 0; i < n; i += CB_PAIRS) {
+        BlockPairs p{};
+        const int m = std::min(n - i, CB_PAIRS);
+        std::copy(src + i, src + i + m, p.src);
+        std::copy(dst + i, dst + i + m, p.dst);
+        k_copy_blocks<<<dim3(m, b.parts * b.layers), 256, 0, s>>>(b, p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
 }  // namespace detint
 
 using namespace detint;

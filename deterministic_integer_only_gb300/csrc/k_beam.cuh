@@ -380,6 +380,22 @@ __global__ void __launch_bounds__(BM_MERGE) k_beam_merge(BeamArgs a) {
         }
 }
 
+// cache blocks of a model: pair blockIdx.x, part and layer blockIdx.y
+constexpr int CB_PAIRS = 64;
+struct BlockPairs {
+    int src[CB_PAIRS], dst[CB_PAIRS];
+};
+__global__ void __launch_bounds__(256) k_copy_blocks(BlockParts b, BlockPairs p) {
+    int part = 0, layer = blockIdx.y;
+    while (layer >= b.layers) { layer -= b.layers; ++part; }
+    const size_t bytes = b.bytes[part];
+    uint8_t* base = b.base[part] + (size_t)layer * b.nblocks * bytes;
+    const int4* s = (const int4*)(base + (size_t)p.src[blockIdx.x] * bytes);
+    int4* d = (int4*)(base + (size_t)p.dst[blockIdx.x] * bytes);
+#pragma unroll 4
+    for (int i = threadIdx.x; i < (int)(bytes >> 4); i += 256) d[i] = s[i];
+}
+
 // ---- the chosen beams' block tables. Whole pages are shared. Of the page that
 // is still being filled (column len / 64) a beam's first child becomes the
 // owner; every other child takes the page of a beam without children, into

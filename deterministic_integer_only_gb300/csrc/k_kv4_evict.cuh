@@ -329,11 +329,11 @@ __global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv
             const int4 cv = __ldg((const int4*)(a.ks + u * KV_BLK) + tig);
             const int cw[4] = {cv.x, cv.y, cv.z, cv.w};
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int hf = 0; hf < 2; ++hf) {
                 int w[4][KS];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const unsigned char* at = kr + 2 * (4 * half + j) * (D / 2);
+                    const unsigned char* at = kr + 2 * (4 * hf + j) * (D / 2);
                     if (D == 128) {
                         const int4 v = __ldg((const int4*)at);
                         w[j][0] = v.x; w[j][1] = v.y; w[j][KS - 2] = v.z; w[j][KS - 1] = v.w;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    int (&c)[4] = t[4 * half + j];
+                    int (&c)[4] = t[4 * hf + j];
                     c[0] = c[1] = qo[0];
                     c[2] = c[3] = qo[1];
 #pragma unroll
@@ -711,8 +711,8 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
     unsigned take = 0, ties = 0;
     for (int b = w0; b < w1; ++b)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int x = 32 * half + lane, j = j0 + (b << 6) + x;
+        for (int hf = 0; hf < 2; ++hf) {
+            const int x = 32 * hf + lane, j = j0 + (b << 6) + x;
             u64 k = ev_key(0);
             if (p.held) k = keys[(b << 6) + x];
             else if (page[b] >= 0) k = ev_key(p.weight[((size_t)page[b] * a.n_kv + g) * KV_BLK + x]);
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
             const bool in = j >= lo && j < hi;
             const unsigned mk = __ballot_sync(0xffffffffu, j < len && (!in || (any && (d > edge || (whole && d == edge)))));
             const unsigned mt = __ballot_sync(0xffffffffu, in && !whole && d == edge);
-            if (lane < 2) mask[4 * b + 2 * half + lane] = lane ? mt : mk;
+            if (lane < 2) mask[4 * b + 2 * hf + lane] = lane ? mt : mk;
             take += __popc(mk);
             ties += __popc(mt);
         }
@@ -740,10 +740,10 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
     }
     for (int b = w0; b < w1; ++b)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const unsigned mk = mask[4 * b + 2 * half], mt = mask[4 * b + 2 * half + 1], lt = (1u << lane) - 1;
+        for (int hf = 0; hf < 2; ++hf) {
+            const unsigned mk = mask[4 * b + 2 * hf], mt = mask[4 * b + 2 * hf + 1], lt = (1u << lane) - 1;
             const unsigned e = be + __popc(mt & lt);
-            if ((mk >> lane & 1) || ((mt >> lane & 1) && e < want)) out[bt + __popc(mk & lt) + min(e, want)] = j0 + (b << 6) + 32 * half + lane;
+            if ((mk >> lane & 1) || ((mt >> lane & 1) && e < want)) out[bt + __popc(mk & lt) + min(e, want)] = j0 + (b << 6) + 32 * hf + lane;
             bt += __popc(mk);
             be += __popc(mt);
         }

@@ -285,6 +285,14 @@ cudaError_t launch_kv4_prefill(const Kv4Args& a, const Kv4Attn& p, int d, cudaSt
 size_t kv4_decode_ws(const Kv4Args& a, int d, int T, int max_len);
 size_t kv4_decode_need(const Kv4Args& a, int d, int T, int max_len, int window);
 cudaError_t launch_kv4_decode(const Kv4Args& a, const Kv4Attn& p, int d, void* ws, cudaStream_t s);
+// cache blocks copied in every layer: part i of a layer is nblocks blocks of bytes[i] (a
+// multiple of 16) from base[i] on, the layers one after another
+struct BlockParts {
+    uint8_t* base[4];
+    size_t bytes[4];
+    int parts, layers, nblocks;
+};
+cudaError_t launch_copy_blocks(const BlockParts& b, const int* src, const int* dst, int n, cudaStream_t s);
 // called by every entry point: sets the kernels' attributes once per device, and
 // makes no call that a stream capture forbids
 cudaError_t kv4_init();

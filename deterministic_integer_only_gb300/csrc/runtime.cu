@@ -1318,6 +1318,77 @@ int detint_fork_seq(detint_model* m, int src, int dst, int n_tokens, detint_stre
     return DETINT_OK;
 }
 
+int detint_reorder_seqs(detint_model* m, int n, const int32_t* seq_ids, const int32_t* parents, detint_stream_t sp) {
+    if (!m || !seq_ids || !parents) return fail(DETINT_E_ARG, "detint_reorder_seqs: null pointer");
+    if (n < 1 || n > m->max_batch) return fail(DETINT_E_ARG, "detint_reorder_seqs: n must be in 1..max_batch");
+    std::vector<char> seen(m->max_batch, 0);
+    for (int i = 0; i < n; ++i) {
+        if (seq_ids[i] < 0 || seq_ids[i] >= m->max_batch || seen[seq_ids[i]]) return fail(DETINT_E_SEQ, "detint_reorder_seqs: sequence id out of range or repeated");
+        seen[seq_ids[i]] = 1;
+        if (parents[i] < 0 || parents[i] >= n) return fail(DETINT_E_ARG, "detint_reorder_seqs: a parent outside 0..n - 1");
+    }
+    cudaStream_t s = (cudaStream_t)sp;
+    // The new lists on copies of the bookkeeping, which replace it once they are
+    // complete: whole blocks shared; the block that is still being filled goes to
+    // its owner's first child, the others copy it into blocks that are free by then
+    // (those of sequences without children among them, which nothing reads).
+    std::vector<int> refs = m->refcnt, free_blocks = m->free_blocks, src, dst;
+    std::vector<std::vector<int>> lists(n);
+    std::vector<int32_t> lens(n);
+    std::vector<char> taken(n, 0);
+    for (int i = 0; i < n; ++i) {
+        const int p = seq_ids[parents[i]], len = m->seq_len[p], full = len / KV_BLK;
+        lens[i] = len;
+        lists[i].assign(m->seq_blocks[p].begin(), m->seq_blocks[p].begin() + full);
+        if (len % KV_BLK) {
+            lists[i].push_back(taken[parents[i]] ? -1 : m->seq_blocks[p][full]);
+            taken[parents[i]] = 1;
+        }
+        for (int b : lists[i])
+            if (b >= 0) ++refs[b];
+    }
+    for (int i = 0; i < n; ++i)
+        for (int b : m->seq_blocks[seq_ids[i]])
+            if (--refs[b] == 0) free_blocks.push_back(b);
+    for (int i = 0; i < n; ++i) {
+        if (lists[i].empty() || lists[i].back() >= 0) continue;
+        if (free_blocks.empty()) return fail(DETINT_E_CTX, "KV block pool exhausted");
+        const int b = free_blocks.back();
+        free_blocks.pop_back();
+        refs[b] = 1;
+        src.push_back(m->seq_blocks[seq_ids[parents[i]]][lens[i] / KV_BLK]);
+        dst.push_back(b);
+        lists[i].back() = b;
+    }
+    const size_t slots = (size_t)m->nkv * KV_BLK;                  // token slots of one block of one layer
+    BlockParts parts{};
+    parts.layers = m->L;
+    parts.nblocks = m->nblocks;
+    parts.parts = m->kv4 ? 4 : 2;
+    parts.base[0] = m->kv4 ? m->k4 : (uint8_t*)m->kcache;
+    parts.base[1] = m->kv4 ? m->v4 : (uint8_t*)m->vcache;
+    parts.base[2] = m->ks4;
+    parts.base[3] = m->vs4;
+    parts.bytes[0] = parts.bytes[1] = m->kv4 ? slots * m->d / 2 : slots * m->d;
+    parts.bytes[2] = parts.bytes[3] = slots;
+    CK(launch_copy_blocks(parts, src.data(), dst.data(), (int)src.size(), s));
+    m->refcnt = std::move(refs);
+    m->free_blocks = std::move(free_blocks);
+    for (int i = 0; i < n; ++i) {
+        int32_t* row = m->bt_host.data() + (size_t)seq_ids[i] * m->mbs;
+        std::fill(row, row + m->mbs, 0);
+        std::copy(lists[i].begin(), lists[i].end(), row);
+        m->seq_blocks[seq_ids[i]] = std::move(lists[i]);
+        m->seq_len[seq_ids[i]] = lens[i];
+    }
+    m->bt_dirty = true;
+    std::vector<int32_t> all(m->max_batch);
+    for (int i = 0; i < m->max_batch; ++i) all[i] = m->seq_len[i];
+    const int rc = stage_copies(m, s, {{m->block_table, &m->bt_host}, {m->seq_len_dev, &all}});
+    if (rc == DETINT_OK) m->bt_dirty = false;
+    return rc;
+}
+
 int detint_seq_len(detint_model* m, int seq_id, int32_t* len) {
     if (!m || !len) return fail(DETINT_E_ARG, "null pointer");
     if (seq_id < 0 || seq_id >= m->max_batch) return fail(DETINT_E_SEQ, "sequence id out of range");

@@ -183,6 +183,18 @@ int detint_split_w16(const int16_t* W, int8_t* w_hi, uint8_t* w_lo, long long co
  * empty), CTX (block pool exhausted), CUDA. */
 int detint_fork_seq(detint_model* m, int src, int dst, int n_tokens, detint_stream_t s);
 
+/* Reorder sequences, as beam search does between steps: sequence seq_ids[i]
+ * (host int32[n], distinct) becomes what sequence seq_ids[parents[i]] was (host
+ * int32[n], values 0..n - 1), several of them the same one where parents
+ * repeat. Whole blocks are shared by reference count, as detint_fork_seq shares
+ * them; a block that is still being filled goes to the first of its sequence's
+ * children and is copied for the others, in every layer, into blocks that
+ * sequences without children give back: a beam search needs no more of them.
+ * Continuing a sequence gives the same logits, bit for bit, as prefilling its
+ * tokens afresh. ARG, SEQ and CTX change nothing. Stream-ordered on s. Errors: ARG,
+ * SEQ, CTX (block pool exhausted), CUDA. */
+int detint_reorder_seqs(detint_model* m, int n, const int32_t* seq_ids, const int32_t* parents, detint_stream_t s);
+
 /* Integer sampling parameters of one row (see detint_sample). */
 typedef struct {
     uint64_t seed;      /* SplitMix64 seed */
