@@ -17,6 +17,12 @@ __device__ __forceinline__ unsigned kv4_p24(int E, unsigned RS, int bl) {
     return (unsigned)(((u64)(unsigned)E * RS + (1ull << (bl - 2))) >> (bl - 1));
 }
 
+// the same for sums below 2^32, whose shift one funnel shift does
+__device__ __forceinline__ unsigned kv4_p24s(int E, unsigned RS, int bl) {
+    const u64 x = (u64)(unsigned)E * RS + (1u << (bl - 2));
+    return __funnelshift_r((unsigned)x, (unsigned)(x >> 32), bl - 1);
+}
+
 // ------------------------------------------------- weights, single tokens
 // A unit is a token, a kv head and up to GT of its q heads; its pages are
 // split over a cluster of CTAs that keep their scores in shared memory, as in
@@ -215,19 +221,19 @@ __global__ void __launch_bounds__(KV4_DT, 3) k_kv4_weigh(Kv4Args a, Kv4Attn p, K
 // come straight from the pages: a warp's load is eight whole rows. A block's
 // tokens may belong to several sequences: each run of one sequence whose pages
 // fit the cluster is a round of its own with the other rows masked.
-constexpr int WB_NW = 8;                 // warps of a CTA
 constexpr int WB_ROWS = 16;
 constexpr int WB_PG = 4;                 // pages of a warp
-constexpr int WB_SMEM = WB_NW * (WB_PG - 1) * 4096;
+constexpr int WB_SMEM = (WB_PG - 1) * 4096;      // shared memory of a warp
 
-template <int D>
-__global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv4Attn p, Kv4Weigh wg) {
-    constexpr int KS = D / 32, PG = KV_BLK * D / 2;
+template <int D, int LGW>
+__global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Args a, Kv4Attn p, Kv4Weigh wg) {
+    constexpr int KS = D / 32, PG = KV_BLK * D / 2, NW = 1 << LGW;
     extern __shared__ __align__(16) unsigned char kv4_raw[];
-    __shared__ int r_pos[WB_ROWS], w_top[WB_NW][WB_ROWS];
-    __shared__ unsigned w_sum[WB_NW][WB_ROWS];
+    __shared__ int r_pos[WB_ROWS], w_top[NW][WB_ROWS];
+    __shared__ unsigned w_sum[NW][WB_ROWS];
     __shared__ int c_top[2][16][WB_ROWS];                // by rounds in turn: [CTA][row]
     __shared__ unsigned c_sum[2][16][WB_ROWS];
+    __shared__ Kv4Row r_row[WB_ROWS];
     __shared__ unsigned r_RS[WB_ROWS];
     __shared__ int r_bl[WB_ROWS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
@@ -251,9 +257,11 @@ __global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv
             }
         }
         r_pos[tid] = pos;
+        const bool in = i < nt && hh < nh;
+        const size_t qi = (size_t)(t0 + i) * a.nq + h0 + hh;
+        r_row[tid] = kv4_row(in ? p.mq[qi] : 0, in ? p.kq[qi] : 0, kvp[6], kvp[7]);
     }
     const int rA = gid, rB = gid + 8;
-    Kv4Row rw[2];
     int qf[KS][4], qo[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -261,16 +269,11 @@ __global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv
         int w[2 * KS];
 #pragma unroll
         for (int j = 0; j < 2 * KS; ++j) w[j] = 0;
-        int mq = 0, kq = 0;
         if (i < nt && hh < nh) {
-            const size_t qi = (size_t)(t0 + i) * a.nq + h0 + hh;
-            const int* qp = (const int*)(p.q8 + qi * D + tig * (D / 4));
+            const int* qp = (const int*)(p.q8 + ((size_t)(t0 + i) * a.nq + h0 + hh) * D + tig * (D / 4));
 #pragma unroll
             for (int j = 0; j < 2 * KS; ++j) w[j] = __ldg(qp + j);
-            mq = p.mq[qi];
-            kq = p.kq[qi];
         }
-        rw[x] = kv4_row(mq, kq, kvp[6], kvp[7]);
         int sq = 0;
 #pragma unroll
         for (int j = 0; j < 2 * KS; ++j) sq = __dp4a(w[j], 0x01010101, sq);
@@ -284,6 +287,7 @@ __global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv
         }
     }
     __syncthreads();
+    const Kv4Row rw[2] = {r_row[rA], r_row[rB]};
     if (S > 1) cl_wait();                                // every CTA runs: its shared memory may be written
     int round = 0;
     for (int s0 = 0; s0 < nt;) {
@@ -294,7 +298,7 @@ __global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv
             const int pos = r_pos[s1 << p.lgGp];
             if (pos < 0) continue;
             const int hi = max(kmax, pos), lo = min(kmin, p.window > 0 ? max(0, pos + 1 - p.window) : 0);
-            if (kmax >= 0 && (hi >> 6) - (lo >> 6) >= S * WB_NW * WB_PG) break;
+            if (kmax >= 0 && (hi >> 6) - (lo >> 6) >= S * NW * WB_PG) break;
             kmax = hi;
             kmin = lo;
         }
@@ -307,19 +311,19 @@ __global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv
         if (kmax < 0) continue;
         const int p0 = kmin >> 6, np = (kmax >> 6) - p0 + 1, buf = round & 1;
         ++round;
-        // ---- scores of this warp's pages rank WB_NW + warp, + S WB_NW, ...; the first one's stay in registers
-        const int first = rank * WB_NW + warp, mine = np > first ? ((np - first - 1) >> (p.lgC + 3)) + 1 : 0;
+        // ---- scores of this warp's pages rank NW + warp, + S NW, ...; the first one's stay in registers
+        const int first = rank * NW + warp, mine = np > first ? ((np - first - 1) >> (p.lgC + LGW)) + 1 : 0;
         int4* const store = (int4*)kv4_raw + warp * ((WB_PG - 1) * 256) + lane - 256;      // page q from [256 q]
         int t[8][4], T[2] = {p.none, p.none}, blk_l = -1;
         if (lane < mine) {
-            blk_l = a.block_table[(size_t)seq * a.max_blocks + p0 + first + (lane << (p.lgC + 3))];
+            blk_l = a.block_table[(size_t)seq * a.max_blocks + p0 + first + (lane << (p.lgC + LGW))];
             if (blk_l < 0 || blk_l >= a.n_blocks) {
                 blk_l = -1;
                 if (a.status) a.status[ST_CTX] = 1;
             }
         }
         auto page_of = [&](int q) { return __shfl_sync(0xffffffffu, blk_l, q); };          // -1: its scores are not looked at
-        auto key_of = [&](int q) { return (p0 + first + (q << (p.lgC + 3))) << 6; };
+        auto key_of = [&](int q) { return (p0 + first + (q << (p.lgC + LGW))) << 6; };
 #pragma unroll 1
         for (int q = mine - 1; q >= 0; --q) {
             const int blk = page_of(q);
@@ -389,12 +393,12 @@ __global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv
             if (tig == 0) w_top[warp][x ? rB : rA] = T[x];
         }
         __syncthreads();
-        if (tid < 16 * S) {                              // every CTA of the cluster gets this one's
-            const int r = tid & 15;
+        for (int x = tid; x < 16 * S; x += 32 * NW) { // every CTA of the cluster gets this one's
+            const int r = x & 15;
             int m = w_top[0][r];
 #pragma unroll
-            for (int w = 1; w < WB_NW; ++w) m = max(m, w_top[w][r]);
-            cl_st32(&c_top[buf][rank][r], tid >> 4, m);
+            for (int w = 1; w < NW; ++w) m = max(m, w_top[w][r]);
+            cl_st32(&c_top[buf][rank][r], x >> 4, m);
         }
         if (S > 1) cl_sync();
         else __syncthreads();
@@ -450,12 +454,12 @@ __global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv
             if (tig == 0) w_sum[warp][x ? rB : rA] = sum[x];
         }
         __syncthreads();
-        if (tid < 16 * S) {
-            const int r = tid & 15;
+        for (int x = tid; x < 16 * S; x += 32 * NW) {
+            const int r = x & 15;
             unsigned m = 0;
 #pragma unroll
-            for (int w = 0; w < WB_NW; ++w) m += w_sum[w][r];        // 2^11 keys: below 2^26
-            cl_st32((int*)&c_sum[buf][rank][r], tid >> 4, (int)m);
+            for (int w = 0; w < NW; ++w) m += w_sum[w][r];        // at most 2^11 keys: below 2^26
+            cl_st32((int*)&c_sum[buf][rank][r], x >> 4, (int)m);
         }
         if (S > 1) cl_sync();
         else __syncthreads();
@@ -479,8 +483,8 @@ __global__ void __launch_bounds__(32 * WB_NW, 2) k_kv4_weigh_block(Kv4Args a, Kv
             for (int j = 0; j < 8; ++j) {
                 int4 s = make_int4(t[j][0], t[j][1], t[j][2], t[j][3]);
                 if (q) s = store[256 * q + 32 * j];
-                v[2 * j] = kv4_p24(s.x, RSa, bla) + kv4_p24(s.z, RSb, blb);
-                v[2 * j + 1] = kv4_p24(s.y, RSa, bla) + kv4_p24(s.w, RSb, blb);
+                v[2 * j] = kv4_p24s(s.x, RSa, bla) + kv4_p24s(s.z, RSb, blb);
+                v[2 * j + 1] = kv4_p24s(s.y, RSa, bla) + kv4_p24s(s.w, RSb, blb);
             }
 #pragma unroll
             for (int n = 8, o = 16; o >= 4; n >>= 1, o >>= 1) {

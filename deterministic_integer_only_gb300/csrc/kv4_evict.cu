@@ -29,7 +29,7 @@ using WeighFn = void (*)(Kv4Args, Kv4Attn, Kv4Weigh);
 constexpr int NGT = 3;                       // 1, 2 or 4 heads of a CTA
 const WeighFn WEIGH[2][NGT] = {{k_kv4_weigh<64, 1>, k_kv4_weigh<64, 2>, k_kv4_weigh<64, 4>},
                                {k_kv4_weigh<128, 1>, k_kv4_weigh<128, 2>, k_kv4_weigh<128, 4>}};
-const WeighFn WEIGH_BLOCK[2] = {k_kv4_weigh_block<64>, k_kv4_weigh_block<128>};
+const WeighFn WEIGH_BLOCK[2][2] = {{k_kv4_weigh_block<64, 2>, k_kv4_weigh_block<64, 3>}, {k_kv4_weigh_block<128, 2>, k_kv4_weigh_block<128, 3>}};   // 4 or 8 warps
 int lg2(int n) { return n >= 4 ? 2 : n >= 2 ? 1 : 0; }
 size_t weigh_fixed(int gt) { return gt == 4 ? sizeof(Kv4WeighSm<4>) : gt == 2 ? sizeof(Kv4WeighSm<2>) : sizeof(Kv4WeighSm<1>); }
 size_t weigh_smem(int gt, int cap) {
@@ -74,11 +74,13 @@ cudaError_t init(DevInfo** out) {
             if (e == cudaSuccess) e = cudaFuncSetAttribute(WEIGH[d][l], cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e == cudaSuccess) mc = std::min(mc, cluster_of((const void*)WEIGH[d][l], KV4_DT, room));
         }
-    for (int d : {0, 1}) {
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(WEIGH_BLOCK[d], cudaFuncAttributeMaxDynamicSharedMemorySize, WB_SMEM);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(WEIGH_BLOCK[d], cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e == cudaSuccess) mc = std::min(mc, cluster_of((const void*)WEIGH_BLOCK[d], 32 * WB_NW, WB_SMEM));
-    }
+    for (int d : {0, 1})
+        for (int l = 0; l < 2 && e == cudaSuccess; ++l) {
+            const WeighFn f = WEIGH_BLOCK[d][l];
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, WB_SMEM * (4 << l));
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e == cudaSuccess) mc = std::min(mc, cluster_of((const void*)f, 128 << l, WB_SMEM * (4 << l)));
+        }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv4_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_HELD);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv4_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e == cudaSuccess) {
@@ -123,11 +125,20 @@ cudaError_t launch_weigh(const DevInfo& di, const Kv4Args& a, Kv4Attn p, const K
 
 cudaError_t launch_weigh_block(const DevInfo& di, const Kv4Args& a, Kv4Attn p, const Kv4Weigh& w, int d, cudaStream_t s) {
     p.none = KV4_NEG;
+    // few tokens: one wave of the single-token form, whose keys are spread over more
+    // CTAs (4 sequences of 16 tokens after 1000, 16 + 8 heads of 128: 13.4 us, 18.7 in
+    // blocks; 32 after 4000 17.1 and 20; 183 after 8000, 32 + 8 of 64: 241 and 118)
+    if ((long long)p.T * a.n_kv * ((p.G + 3) / 4) <= 4LL * di.sms) return launch_weigh(di, a, p, w, d, s);
     int mp = (p.max_len + 63) >> 6;                                 // pages a token can have, and one for its neighbours
     if (p.window > 0) mp = std::min(mp, ((p.window + 62) >> 6) + 2);
+    // CTAs of 4 warps while 16 of them hold the pages (1 x 4096 tokens, 16 + 8 heads
+    // of 128: 482 us, with 8 warps 495), then of 8; past 32768 keys the scores are
+    // not kept at once, and each token goes by itself
     p.lgC = 0;
-    while (mp > (WB_NW * WB_PG) << p.lgC && (2 << p.lgC) <= di.max_cluster) ++p.lgC;
-    if (mp > (WB_NW * WB_PG) << p.lgC) return launch_weigh(di, a, p, w, d, s);   // too long to be kept at once
+    int nw = 4;
+    while (mp > (nw * WB_PG) << p.lgC && (2 << p.lgC) <= di.max_cluster) ++p.lgC;
+    if (mp > (nw * WB_PG) << p.lgC) nw = 8;
+    if (mp > (nw * WB_PG) << p.lgC) return launch_weigh(di, a, p, w, d, s);
     p.lgGp = 0;
     while (p.lgGp < 4 && (1 << p.lgGp) < p.G) ++p.lgGp;
     const int bq = WB_ROWS >> p.lgGp, hg = (p.G + (1 << p.lgGp) - 1) >> p.lgGp, tiles = (p.T + bq - 1) / bq;
@@ -139,12 +150,12 @@ cudaError_t launch_weigh_block(const DevInfo& di, const Kv4Args& a, Kv4Attn p, c
     cfg.attrs = at;
     cfg.numAttrs = p.lgC ? 1 : 0;
     cfg.stream = s;
-    cfg.blockDim = dim3(32 * WB_NW);
-    cfg.dynamicSmemBytes = mp > WB_NW ? WB_SMEM : 0;
+    cfg.blockDim = dim3(32 * nw);
+    cfg.dynamicSmemBytes = WB_SMEM * nw;          // (a round may have more pages than a token)
     for (int b0 = 0; b0 < tiles; b0 += 65535) {
         p.t0 = b0 * bq;
         cfg.gridDim = dim3(1 << p.lgC, a.n_kv * hg, std::min(65535, tiles - b0));
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, WEIGH_BLOCK[d == 128], a, p, w);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, WEIGH_BLOCK[d == 128][nw == 8], a, p, w);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -149,6 +149,15 @@ WEIGHS = [
 ]
 
 
+def crowd(block, seq, pos, q8, mq, kq):
+    """For the form of blocks: padding behind the tokens, so that there are too
+    many for one wave of single tokens, which it would hand them to."""
+    if not block:
+        return seq, pos, q8, mq, kq
+    more = lambda x, v: np.concatenate([x, np.full((1000,) + x.shape[1:], v, x.dtype)])  # noqa: E731
+    return more(seq, 0), more(pos, -1), more(q8, 3), more(mq, 20000), more(kq, 20)
+
+
 @pytest.mark.parametrize("block", [False, True])
 @pytest.mark.parametrize("n_q,n_kv,d,window,runs", WEIGHS)
 def test_weigh(torch, n_q, n_kv, d, window, runs, block):
@@ -166,6 +175,7 @@ def test_weigh(torch, n_q, n_kv, d, window, runs, block):
     w = rng.integers(0, 1 << 40, (pool, n_kv, 64))       # added to, not set
     wt = cuda(torch, w)
     bp.weigh(pages, w, tab, prm, n_q, q8, mq, kq, seq, pos, window)
+    seq, pos, q8, mq, kq = crowd(block, seq, pos, q8, mq, kq)
     f = pkg.detint_kv4_weigh_block if block else pkg.detint_kv4_weigh
     got = f(dev.cache, *(cuda(torch, x) for x in (q8, mq, kq, seq, pos)), max(lens), wt, window=window)
     assert got is wt and np.array_equal(wt.cpu().numpy(), w)
@@ -192,9 +202,33 @@ def test_weigh_shared_pages_padding_and_bad_pages(torch, block):
         wt = cuda(torch, w)
         bp.weigh(pages, w, tab, prm, n_q, q8, mq, kq, seq, pos, window, max_len)
         f = pkg.detint_kv4_weigh_block if block else pkg.detint_kv4_weigh
-        f(dev.cache, *(cuda(torch, x) for x in (q8, mq, kq, seq, pos)), max_len, wt, window=window)
+        s_, p_, *q_ = crowd(block, seq, pos, q8, mq, kq)
+        f(dev.cache, *(cuda(torch, x) for x in (*q_, s_, p_)), max_len, wt, window=window)
         assert np.array_equal(wt.cpu().numpy(), w)
     assert dev.status[1] == 1 and not dev.status[6]
+
+
+@pytest.mark.parametrize("block", [False, True])
+@pytest.mark.parametrize("window", [0, 1, 10, 64, 200])
+def test_weigh_tokens_in_any_order(torch, window, block):
+    """Neighbouring tokens of a sequence far apart from each other, forwards and
+    back, the same one twice: a block's pages are not next to each other."""
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(window)
+    n_q, n_kv, d, n = 4, 2, 64, 4000
+    pages = kp.Pages(64, n_kv, d, rng)
+    tab, prm = rng.permutation(63).astype(np.int32)[None], kp.params(n_kv, d, rng, units=90.0)
+    dev = Dev(torch, pages, tab, prm, n_q)
+    pos = np.array([0, 3999, 1, 2000, 2000, 63, 64, -1, 3000, 10, 3998, 700, 701, 702, 5, 1500, 1400, 1300, 3999], np.int32)
+    seq = np.zeros(len(pos), np.int32)
+    q8, mq, kq = kp.queries(len(pos), n_q, d, rng)
+    w = np.zeros((64, n_kv, 64), np.int64)
+    wt = cuda(torch, w)
+    bp.weigh(pages, w, tab, prm, n_q, q8, mq, kq, seq, pos, window)
+    seq, pos, q8, mq, kq = crowd(block, seq, pos, q8, mq, kq)
+    f = pkg.detint_kv4_weigh_block if block else pkg.detint_kv4_weigh
+    f(dev.cache, *(cuda(torch, x) for x in (q8, mq, kq, seq, pos)), n, wt, window=window)
+    assert np.array_equal(wt.cpu().numpy(), w) and not dev.status.any()
 
 
 @pytest.mark.parametrize("block", [False, True])
@@ -217,6 +251,7 @@ def test_weigh_extreme_queries(torch, block):
     wt, dev = cuda(torch, w), Dev(torch, pages, tab, prm, n_q)
     seq = np.zeros(33, np.int32)
     bp.weigh(pages, w, tab, prm, n_q, q8, mq, kq, seq, pos)
+    seq, pos, q8, mq, kq = crowd(block, seq, pos, q8, mq, kq)
     f = pkg.detint_kv4_weigh_block if block else pkg.detint_kv4_weigh
     f(dev.cache, *(cuda(torch, x) for x in (q8, mq, kq, seq, pos)), 384, wt)
     assert np.array_equal(wt.cpu().numpy(), w)
@@ -238,6 +273,7 @@ def test_weigh_long_contexts(torch, n_q, n_kv, d, n, new, window, block):
     w = np.zeros((blocks, n_kv, 64), np.int64)
     wt, seq = cuda(torch, w), np.zeros(new, np.int32)
     bp.weigh(pages, w, tab, prm, n_q, q8, mq, kq, seq, pos, window)
+    seq, pos, q8, mq, kq = crowd(block, seq, pos, q8, mq, kq)
     f = pkg.detint_kv4_weigh_block if block else pkg.detint_kv4_weigh
     f(dev.cache, *(cuda(torch, x) for x in (q8, mq, kq, seq, pos)), n, wt, window=window)
     assert np.array_equal(wt.cpu().numpy(), w) and not dev.status.any()
