@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(BR_THREADS) k_beam_reorder(const int32_t* tabl
     __shared__ int32_t old[BM_MAX_OUT][BR_COLS];
     __shared__ int par[BM_MAX_OUT], first[BM_MAX_OUT], used[BM_MAX_OUT], spare[BM_MAX_OUT];
     const int tid = threadIdx.x, c0 = (int)blockIdx.x * BR_COLS, r0 = (int)blockIdx.y * W;
+    pdl_launch();                                        // (k_kv4_copy waits for the lists)
     const int len = max(lens[blockIdx.y], 0), full = len >> 6;
     const bool grows = (len & 63) && full < max_blocks, here = grows && full >= c0 && full < c0 + BR_COLS;
     if (blockIdx.x == 0 && !grows)

@@ -874,6 +874,7 @@ __global__ void __launch_bounds__(128) k_kv4_evict_move(Kv4Args a, Kv4Evict p) {
 
 // whole pages of every kv head, src[i] to dst[i]; -1 on either side: none
 __global__ void __launch_bounds__(256) k_kv4_copy(Kv4Args a, const int32_t* src, const int32_t* dst, int page_bytes, long long* weight) {
+    pdl_wait();
     const int s = src[blockIdx.x], d = dst[blockIdx.x], g = blockIdx.y;
     if (s < 0 || d < 0) return;
     if (s >= a.n_blocks || d >= a.n_blocks) {

@@ -270,8 +270,16 @@ int detint_kv4_copy(const detint_kv4_t* c, const int32_t* src, const int32_t* ds
     if (!src || !dst) return err(DETINT_E_ARG, "null pointer");
     if (n < 1) return err(DETINT_E_ARG, "n must be positive");
     if (mis(src, 4) || mis(dst, 4) || mis(weight, 16)) return err(DETINT_E_ARG, "lists must be 4-byte, weights 16-byte aligned");
-    k_kv4_copy<<<dim3(n, a.n_kv), 256, 0, (cudaStream_t)sp>>>(a, src, dst, KV_BLK * c->head_dim / 2, (long long*)weight);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;       // starts while detint_beam_reorder drains
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cfg.stream = (cudaStream_t)sp;
+    cfg.gridDim = dim3(n, a.n_kv);
+    cfg.blockDim = dim3(256);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_copy, a, src, dst, KV_BLK * c->head_dim / 2, (long long*)weight);
     return e == cudaSuccess ? DETINT_OK : cuda_fail(where, e);
 }
 
