@@ -509,11 +509,11 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
 // and last `recent` ones and, between them, those of the largest weights, the
 // lower place first among equal ones. A cluster per sequence and kv head, a run
 // of whole pages per CTA, the weights in shared memory as order-preserving
-// keys. The least kept key is found in a histogram of the distances from the
-// least key, 32 bins to an octave (attention weights are heavy-tailed: in even
-// bins most would share one), whose few keys in the bin in question are then
-// ranked by counting; where that bin is too full, its keys are split by 11 bits
-// at a time first. Then every warp deals the kept places of its run out.
+// keys. The least kept key is found in a histogram with 16 bins to an octave on
+// either side of zero (attention weights are heavy-tailed: in even bins most
+// would share one), whose few keys in the bin in question are then ranked by
+// counting; where that bin is too full, its keys are split by 11 bits at a time
+// first. Then every warp deals the kept places of its run out.
 constexpr int EV_THREADS = 512, EV_WARPS = EV_THREADS / 32;
 constexpr int EV_BITS = 11, EV_BINS = 1 << EV_BITS;
 constexpr int EV_LIST = 512;             // keys that are ranked by counting
@@ -531,19 +531,29 @@ struct Kv4Evict {
 };
 
 __device__ __forceinline__ u64 ev_key(long long w) { return (u64)w ^ (1ull << 63); }
-// bin of a distance, and the open bits of the distances in it
-__device__ __forceinline__ int ev_bin(u64 d) {
-    const int e = bitlen_u64(d);
-    return e <= 5 ? (int)d : ((e - 5) << 5) + (int)(d >> (e - 6) & 31);
+// octave bin of a key, the bits of a key that its bin leaves open, and the least key in it
+__device__ __forceinline__ int ev_bin(u64 key) {
+    const bool neg = !(key >> 63);
+    const u64 v = neg ? ~key & ~(1ull << 63) : key & ~(1ull << 63);     // w, or -1 - w below zero
+    const int e = bitlen_u64(v), b = e <= 4 ? (int)v : ((e - 4) << 4) + (int)(v >> (e - 5) & 15);
+    return neg ? EV_BINS / 2 - 1 - b : EV_BINS / 2 + b;
 }
-__device__ __forceinline__ int ev_open(int bin) { return bin < 32 ? 0 : (bin >> 5) - 1; }
-__device__ __forceinline__ u64 ev_least(int bin) { return bin < 32 ? (u64)bin : (u64)(32 + (bin & 31)) << ev_open(bin); }
+__device__ __forceinline__ int ev_open(int bin) {
+    const int b = bin < EV_BINS / 2 ? EV_BINS / 2 - 1 - bin : bin - EV_BINS / 2;
+    return b < 16 ? 0 : (b >> 4) - 1;
+}
+__device__ __forceinline__ u64 ev_least(int bin) {
+    const bool neg = bin < EV_BINS / 2;
+    const int b = neg ? EV_BINS / 2 - 1 - bin : bin - EV_BINS / 2, open = ev_open(bin);
+    const u64 v = b < 16 ? (u64)b : (u64)(16 + (b & 15)) << open;
+    return neg ? (~v & ~(1ull << 63)) >> open << open : v | 1ull << 63;
+}
 
 __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4Evict p) {
     extern __shared__ __align__(16) unsigned char ev_raw[];
     u64* keys = (u64*)ev_raw;                            // the CTA's, where they are held
     __shared__ unsigned hist[EV_BINS];
-    __shared__ u64 list[EV_LIST], red[EV_WARPS], least_s, found;
+    __shared__ u64 list[EV_LIST], found;
     __shared__ unsigned scan[2][EV_WARPS], mine[2], pick[3], count;
     __shared__ int page[EV_PAGES];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -591,29 +601,13 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
             if (j + 1 >= lo && j + 1 < hi) f(k.y);
         }
     };
-    u64 least = ~0ull;
+    if (p.held) {
 #pragma unroll 4
-    for (int b = warp; b < nb; b += EV_WARPS) {
-        const ulonglong2 k = fetch(b);
-        if (p.held) *((ulonglong2*)(keys + (b << 6)) + lane) = k;
-        const int j = j0 + (b << 6) + 2 * lane;
-        if (j >= lo && j < hi) least = k.x < least ? k.x : least;
-        if (j + 1 >= lo && j + 1 < hi) least = k.y < least ? k.y : least;
+        for (int b = warp; b < nb; b += EV_WARPS) *((ulonglong2*)(keys + (b << 6)) + lane) = fetch(b);
+        __syncwarp();                                    // (`each` gives a lane its own keys back)
     }
-    least = ~redux_max_u64(~least);
-    if (lane == 0) red[warp] = least;
-    __syncthreads();
-    if (warp == 0) {
-        least = ~redux_max_u64(~red[lane & (EV_WARPS - 1)]);
-        if (lane == 0) least_s = least;
-    }
-    cl_sync();
-    least = ~0ull;
-    for (int r = 0; r < S; ++r) {
-        const u64 x = (u64)cl_ld64((const i64*)&least_s, r);
-        least = x < least ? x : least;
-    }
-    // ---- the want-th largest distance: cut, whose `open` low bits are yet to be found
+    cl_sync();                                           // the first CTA's bins are clear and may be added to
+    // the want-th largest key: cut, whose `open` low bits are yet to be found
     int open = 64;
     u64 cut = 0;
     const bool any = want > 0;
@@ -623,9 +617,8 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
         const int sh = max(open - EV_BITS, 0);
         const u64 agree = open >= 64 ? 0 : cut >> open, bins = (1ull << (open - sh)) - 1;
         each([&](u64 k) {
-            const u64 d = k - least;
-            if (open >= 64) atomicAdd(&hist[ev_bin(d)], 1u);
-            else if (d >> open == agree) atomicAdd(&hist[(d >> sh) & bins], 1u);
+            if (open >= 64) atomicAdd(&hist[ev_bin(k)], 1u);
+            else if (k >> open == agree) atomicAdd(&hist[(k >> sh) & bins], 1u);
         });
         __syncthreads();
         if (rank)                                        // the first CTA's bins become the cluster's
@@ -681,8 +674,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
         if (!whole && open > 0 && n <= EV_LIST) {        // few: ranked by the first CTA
             const u64 near = cut >> open;
             each([&](u64 k) {
-                const u64 d = k - least;
-                if (d >> open == near) cl_st64(&list[cl_add32(&count, 0, 1)], 0, d);
+                if (k >> open == near) cl_st64(&list[cl_add32(&count, 0, 1)], 0, k);
             });
             cl_sync();
             if (rank == 0) {
@@ -705,10 +697,10 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
             want = cl_ld32u(&pick[1], 0);
             open = 0;
         }
-        cl_sync();                                       // what was read is not written again before all have read it
+        if (open > 0 && !whole) cl_sync();               // what was read is not written again before all have read it
     }
-    // ---- kept: places outside [lo, hi), distances past the closed bits of cut (all
-    // that agree with them too when whole), and the first `want` of those equal to it
+    // ---- kept: places outside [lo, hi), keys past the closed bits of cut (all that
+    // agree with them too when whole), and the first `want` of those equal to it
     const u64 edge = cut >> open;
     const int bpw = (nb + EV_WARPS - 1) / EV_WARPS, w0 = min(nb, warp * bpw), w1 = min(nb, w0 + bpw);   // this warp's pages
     unsigned* mask = hist;                               // [page][half][kept, equal to the cut] of 32 places (the bins are done)
@@ -720,7 +712,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
             u64 k = ev_key(0);
             if (p.held) k = keys[(b << 6) + x];
             else if (page[b] >= 0) k = ev_key(p.weight[((size_t)page[b] * a.n_kv + g) * KV_BLK + x]);
-            const u64 d = (k - least) >> open;
+            const u64 d = k >> open;
             const bool in = j >= lo && j < hi;
             const unsigned mk = __ballot_sync(0xffffffffu, j < len && (!in || (any && (d > edge || (whole && d == edge)))));
             const unsigned mt = __ballot_sync(0xffffffffu, in && !whole && d == edge);
@@ -808,7 +800,7 @@ __global__ void __launch_bounds__(128) k_kv4_evict_move(Kv4Args a, Kv4Evict p) {
             const int s = run[r], blk = page[s];
             return blk >= 0 ? vin[(size_t)blk * a.n_kv * (PW / 4) + (from[s] >> 4)] : make_int4(KV4_ZEROS, KV4_ZEROS, KV4_ZEROS, KV4_ZEROS);
         };
-        constexpr int AHEAD = 4;
+        constexpr int AHEAD = 2;                         // (4 and 6 leave room for fewer CTAs: 105 and 114 us in place of 101)
         int4 next[AHEAD];
 #pragma unroll
         for (int r = 0; r < AHEAD; ++r)

@@ -132,8 +132,8 @@ cudaError_t launch_weigh_block(const DevInfo& di, const Kv4Args& a, Kv4Attn p, c
     int mp = (p.max_len + 63) >> 6;                                 // pages a token can have, and one for its neighbours
     if (p.window > 0) mp = std::min(mp, ((p.window + 62) >> 6) + 2);
     // CTAs of 4 warps while 16 of them hold the pages (1 x 4096 tokens, 16 + 8 heads
-    // of 128: 482 us, with 8 warps 495), then of 8; past 32768 keys the scores are
-    // not kept at once, and each token goes by itself
+    // of 128: 482 us, with 8 warps 495, with 16 536), then of 8; past 32768 keys the
+    // scores are not kept at once, and each token goes by itself
     p.lgC = 0;
     int nw = 4;
     while (mp > (nw * WB_PG) << p.lgC && (2 << p.lgC) <= di.max_cluster) ++p.lgC;
@@ -167,7 +167,7 @@ cudaError_t launch_evict(const DevInfo& di, const Kv4Args& a, Kv4Evict p, int n,
     auto pages = [&]() { return (mp + (1 << lg) - 1) >> lg; };
     // CTAs of 32 pages or less while there are few of them (4 sequences of 8192
     // keys, 8 kv heads: 23.6 us, with one CTA 26.3, with 8 27.1; 16 of up to 32768
-    // 105.7 with 4, with 2 117.6, with 8 124; 64 of 2048 50 with one, with two 67),
+    // 106 with 4, with 2 118, with 8 124; 64 of 2048 50 with one, with two 67),
     // 16 of them only for long contexts (1 of 32768: 27.8 with 8, with 16 32)
     while ((2 << lg) <= di.max_cluster &&
            (pages() > EV_PAGES || (pages() > (lg < 3 ? 32 : 128) && ((long long)n * a.n_kv << (lg + 1)) * 2 <= 7LL * di.sms)))
