@@ -223,21 +223,21 @@ __global__ void __launch_bounds__(KV4_DT, 3) k_kv4_weigh(Kv4Args a, Kv4Attn p, K
 // fit the cluster is a round of its own with the other rows masked.
 constexpr int WB_ROWS = 16;
 constexpr int WB_PG = 4;                 // pages of a warp
-constexpr int WB_SMEM = (WB_PG - 1) * 4096;      // shared memory of a warp
+constexpr int WB_SMEM = (WB_PG - 1) * 4096;      // shared memory of a warp, and per warp of the cluster
+constexpr int WB_EXCH = 2 * WB_ROWS * 4;
 
 template <int D, int LGW>
 __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Args a, Kv4Attn p, Kv4Weigh wg) {
     constexpr int KS = D / 32, PG = KV_BLK * D / 2, NW = 1 << LGW;
     extern __shared__ __align__(16) unsigned char kv4_raw[];
-    __shared__ int r_pos[WB_ROWS], w_top[NW][WB_ROWS];
-    __shared__ unsigned w_sum[NW][WB_ROWS];
-    __shared__ int c_top[2][16][WB_ROWS];                // by rounds in turn: [CTA][row]
-    __shared__ unsigned c_sum[2][16][WB_ROWS];
+    __shared__ int r_pos[WB_ROWS];
     __shared__ Kv4Row r_row[WB_ROWS];
-    __shared__ unsigned r_RS[WB_ROWS];
-    __shared__ int r_bl[WB_ROWS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, tig = lane & 3;
     const int S = 1 << p.lgC, rank = (int)blockIdx.x;
+    // the warps' maxima and sums, [warp of the cluster][row]: every warp writes its
+    // own to every CTA, so that one cluster barrier is an exchange
+    int* const x_top = (int*)(kv4_raw + NW * WB_SMEM);
+    int* const x_sum = x_top + S * NW * WB_ROWS;
     int g = blockIdx.y, hg = 0;
     while (g >= a.n_kv) { g -= a.n_kv; ++hg; }
     const int BQ = WB_ROWS >> p.lgGp, Gp = 1 << p.lgGp, h0 = g * p.G + hg * Gp, nh = min(Gp, p.G - hg * Gp);
@@ -289,7 +289,14 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
     __syncthreads();
     const Kv4Row rw[2] = {r_row[rA], r_row[rB]};
     if (S > 1) cl_wait();                                // every CTA runs: its shared memory may be written
-    int round = 0;
+    // gives row lane mod 16's value of this warp to every CTA / waits for all of them
+    auto give = [&](int* x, int va, int vb) {
+        const int u = __shfl_sync(0xffffffffu, va, 4 * (lane & 7)), v = __shfl_sync(0xffffffffu, vb, 4 * (lane & 7));
+        int* at = x + (rank * NW + warp) * WB_ROWS + (lane & 15);
+        for (int c = lane >> 4; c < S; c += 2) cl_st32(at, c, lane & 8 ? v : u);
+        if (S > 1) cl_sync();
+        else __syncthreads();
+    };
     for (int s0 = 0; s0 < nt;) {
         // tokens [s0, s1) of one sequence whose pages fit the cluster (one token's always do)
         const int seq = p.tok_seq[t0 + s0];
@@ -309,8 +316,7 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
         const int cmax = __reduce_min_sync(0xffffffffu, min(hiA, hiB)), cmin = __reduce_max_sync(0xffffffffu, max(loA, loB));
         s0 = s1;
         if (kmax < 0) continue;
-        const int p0 = kmin >> 6, np = (kmax >> 6) - p0 + 1, buf = round & 1;
-        ++round;
+        const int p0 = kmin >> 6, np = (kmax >> 6) - p0 + 1;
         // ---- scores of this warp's pages rank NW + warp, + S NW, ...; the first one's stay in registers
         const int first = rank * NW + warp, mine = np > first ? ((np - first - 1) >> (p.lgC + LGW)) + 1 : 0;
         int4* const store = (int4*)kv4_raw + warp * ((WB_PG - 1) * 256) + lane - 256;      // page q from [256 q]
@@ -390,22 +396,14 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
         for (int x = 0; x < 2; ++x) {
             T[x] = max(T[x], __shfl_xor_sync(0xffffffffu, T[x], 1));
             T[x] = max(T[x], __shfl_xor_sync(0xffffffffu, T[x], 2));
-            if (tig == 0) w_top[warp][x ? rB : rA] = T[x];
         }
-        __syncthreads();
-        for (int x = tid; x < 16 * S; x += 32 * NW) { // every CTA of the cluster gets this one's
-            const int r = x & 15;
-            int m = w_top[0][r];
-#pragma unroll
-            for (int w = 1; w < NW; ++w) m = max(m, w_top[w][r]);
-            cl_st32(&c_top[buf][rank][r], x >> 4, m);
-        }
-        if (S > 1) cl_sync();
-        else __syncthreads();
-#pragma unroll 4
-        for (int c = 0; c < S; ++c) {
-            T[0] = max(T[0], c_top[buf][c][rA]);
-            T[1] = max(T[1], c_top[buf][c][rB]);
+        give(x_top, T[0], T[1]);
+        {
+            int m = p.none;
+            for (int e = lane >> 4; e < S * NW; e += 2) m = max(m, x_top[e * WB_ROWS + (lane & 15)]);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            T[0] = __shfl_sync(0xffffffffu, m, rA);
+            T[1] = __shfl_sync(0xffffffffu, m, rB);
         }
         // ---- exponentials in the scores' places, and their sums
         unsigned sum[2] = {0, 0};
@@ -451,29 +449,22 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
         for (int x = 0; x < 2; ++x) {
             sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 1);
             sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], 2);
-            if (tig == 0) w_sum[warp][x ? rB : rA] = sum[x];
         }
-        __syncthreads();
-        for (int x = tid; x < 16 * S; x += 32 * NW) {
-            const int r = x & 15;
-            unsigned m = 0;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) m += w_sum[w][r];        // at most 2^11 keys: below 2^26
-            cl_st32((int*)&c_sum[buf][rank][r], x >> 4, (int)m);
-        }
-        if (S > 1) cl_sync();
-        else __syncthreads();
-        if (tid < WB_ROWS) {
-            unsigned m = 0;                              // at most 2^15 keys: below 2^30
-            for (int c = 0; c < S; ++c) m += c_sum[buf][c][tid];
-            const int bl = 32 - __clz(m);
-            r_RS[tid] = m ? (unsigned)pow2_recip(m, bl, 1, 23) : 0;
-            r_bl[tid] = max(bl, 2);
-        }
-        __syncthreads();
+        give(x_sum, (int)sum[0], (int)sum[1]);           // (the maxima are read before any warp gets past this)
         // ---- the rows' probabilities of each key, added over the lanes: lane gid ends with keys 2 gid, 2 gid + 1 of its 16
-        const unsigned RSa = r_RS[rA], RSb = r_RS[rB];
-        const int bla = r_bl[rA], blb = r_bl[rB];
+        unsigned RSa, RSb;
+        int bla, blb;
+        {
+            unsigned m = 0;                              // at most 2^15 keys: below 2^30
+            for (int e = lane >> 4; e < S * NW; e += 2) m += (unsigned)x_sum[e * WB_ROWS + (lane & 15)];
+            m += __shfl_xor_sync(0xffffffffu, m, 16);
+            const int bl = 32 - __clz(m);
+            const unsigned RS = m ? (unsigned)pow2_recip(m, bl, 1, 23) : 0;
+            RSa = __shfl_sync(0xffffffffu, RS, rA);
+            RSb = __shfl_sync(0xffffffffu, RS, rB);
+            bla = max(__shfl_sync(0xffffffffu, bl, rA), 2);
+            blb = max(__shfl_sync(0xffffffffu, bl, rB), 2);
+        }
 #pragma unroll 1
         for (int q = 0; q < mine; ++q) {
             const int blk = page_of(q);
@@ -501,7 +492,6 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
             if (v[1]) atomicAdd(w + 1, (unsigned long long)v[1]);
         }
     }
-    if (S > 1) cl_sync();                                // no CTA leaves while another writes to it
 }
 
 // ------------------------------------------------------------------ eviction
@@ -558,7 +548,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
     __shared__ int page[EV_PAGES];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = 1 << p.lg_s, rank = (int)blockIdx.x & (S - 1), i = (int)blockIdx.x >> p.lg_s, g = blockIdx.y;
-    const int seq = p.seq[i], max_len = min(p.max_len, a.max_blocks * KV_BLK);
+    const int seq = p.seq[i], max_len = min(p.max_len, min(a.max_blocks, 1 << 13) * KV_BLK);
     int len = p.lens[i];
     pdl_launch();
     int32_t* out = p.kept + ((size_t)i * a.n_kv + g) * p.keep;

@@ -77,9 +77,10 @@ cudaError_t init(DevInfo** out) {
     for (int d : {0, 1})
         for (int l = 0; l < 2 && e == cudaSuccess; ++l) {
             const WeighFn f = WEIGH_BLOCK[d][l];
-            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, WB_SMEM * (4 << l));
+            const int bytes = (WB_SMEM + 16 * WB_EXCH) * (4 << l);
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
             if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e == cudaSuccess) mc = std::min(mc, cluster_of((const void*)f, 128 << l, WB_SMEM * (4 << l)));
+            if (e == cudaSuccess) mc = std::min(mc, cluster_of((const void*)f, 128 << l, bytes));
         }
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv4_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_HELD);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv4_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -132,7 +133,7 @@ cudaError_t launch_weigh_block(const DevInfo& di, const Kv4Args& a, Kv4Attn p, c
     int mp = (p.max_len + 63) >> 6;                                 // pages a token can have, and one for its neighbours
     if (p.window > 0) mp = std::min(mp, ((p.window + 62) >> 6) + 2);
     // CTAs of 4 warps while 16 of them hold the pages (1 x 4096 tokens, 16 + 8 heads
-    // of 128: 482 us, with 8 warps 495, with 16 536), then of 8; past 32768 keys the
+    // of 128: 482 us, with 8 warps 497, with 16 536), then of 8; past 32768 keys the
     // scores are not kept at once, and each token goes by itself
     p.lgC = 0;
     int nw = 4;
@@ -151,7 +152,7 @@ cudaError_t launch_weigh_block(const DevInfo& di, const Kv4Args& a, Kv4Attn p, c
     cfg.numAttrs = p.lgC ? 1 : 0;
     cfg.stream = s;
     cfg.blockDim = dim3(32 * nw);
-    cfg.dynamicSmemBytes = WB_SMEM * nw;          // (a round may have more pages than a token)
+    cfg.dynamicSmemBytes = (WB_SMEM + (WB_EXCH << p.lgC)) * nw;      // (a round may have more pages than a token)
     for (int b0 = 0; b0 < tiles; b0 += 65535) {
         p.t0 = b0 * bq;
         cfg.gridDim = dim3(1 << p.lgC, a.n_kv * hg, std::min(65535, tiles - b0));

@@ -1318,7 +1318,7 @@ int detint_fork_seq(detint_model* m, int src, int dst, int n_tokens, detint_stre
     return DETINT_OK;
 }
 
-int detint_reorder_seqs(detint_model* m, int n, const int32_t* seq_ids, const int32_t* parents, detint_stream_t sp) {
+static int reorder_seqs(detint_model* m, int n, const int32_t* seq_ids, const int32_t* parents, cudaStream_t s) {
     if (!m || !seq_ids || !parents) return fail(DETINT_E_ARG, "detint_reorder_seqs: null pointer");
     if (n < 1 || n > m->max_batch) return fail(DETINT_E_ARG, "detint_reorder_seqs: n must be in 1..max_batch");
     std::vector<char> seen(m->max_batch, 0);
@@ -1327,14 +1327,13 @@ int detint_reorder_seqs(detint_model* m, int n, const int32_t* seq_ids, const in
         seen[seq_ids[i]] = 1;
         if (parents[i] < 0 || parents[i] >= n) return fail(DETINT_E_ARG, "detint_reorder_seqs: a parent outside 0..n - 1");
     }
-    cudaStream_t s = (cudaStream_t)sp;
     // The new lists on copies of the bookkeeping, which replace it once they are
     // complete: whole blocks shared; the block that is still being filled goes to
     // its owner's first child, the others copy it into blocks that are free by then
     // (those of sequences without children among them, which nothing reads).
     std::vector<int> refs = m->refcnt, free_blocks = m->free_blocks, src, dst;
     std::vector<std::vector<int>> lists(n);
-    std::vector<int32_t> lens(n);
+    std::vector<int32_t> lens(n), all(m->max_batch);
     std::vector<char> taken(n, 0);
     for (int i = 0; i < n; ++i) {
         const int p = seq_ids[parents[i]], len = m->seq_len[p], full = len / KV_BLK;
@@ -1382,11 +1381,18 @@ int detint_reorder_seqs(detint_model* m, int n, const int32_t* seq_ids, const in
         m->seq_len[seq_ids[i]] = lens[i];
     }
     m->bt_dirty = true;
-    std::vector<int32_t> all(m->max_batch);
     for (int i = 0; i < m->max_batch; ++i) all[i] = m->seq_len[i];
     const int rc = stage_copies(m, s, {{m->block_table, &m->bt_host}, {m->seq_len_dev, &all}});
     if (rc == DETINT_OK) m->bt_dirty = false;
     return rc;
+}
+
+int detint_reorder_seqs(detint_model* m, int n, const int32_t* seq_ids, const int32_t* parents, detint_stream_t sp) {
+    try {
+        return reorder_seqs(m, n, seq_ids, parents, (cudaStream_t)sp);
+    } catch (const std::bad_alloc&) {                              // (of the copies, before anything changes)
+        return fail(DETINT_E_OOM, "detint_reorder_seqs: out of host memory");
+    }
 }
 
 int detint_seq_len(detint_model* m, int seq_id, int32_t* len) {

@@ -191,8 +191,8 @@ int detint_fork_seq(detint_model* m, int src, int dst, int n_tokens, detint_stre
  * children and is copied for the others, in every layer, into blocks that
  * sequences without children give back: a beam search needs no more of them.
  * Continuing a sequence gives the same logits, bit for bit, as prefilling its
- * tokens afresh. ARG, SEQ and CTX change nothing. Stream-ordered on s. Errors: ARG,
- * SEQ, CTX (block pool exhausted), CUDA. */
+ * tokens afresh. ARG, SEQ, CTX and OOM change nothing. Stream-ordered on s. Errors:
+ * ARG, SEQ, CTX (block pool exhausted), OOM (host memory), CUDA. */
 int detint_reorder_seqs(detint_model* m, int n, const int32_t* seq_ids, const int32_t* parents, detint_stream_t s);
 
 /* Integer sampling parameters of one row (see detint_sample). */
