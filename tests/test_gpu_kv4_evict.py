@@ -317,6 +317,15 @@ def test_evict(torch, n_kv, d, lens, keep, sinks, recent):
     check_evict(torch, pages, w, tab, np.arange(len(lens), dtype=np.int32), np.array(lens, np.int32), keep, sinks, recent, new, max(lens))
 
 
+@pytest.mark.parametrize("lens,keep", [([3000, 17, 900], 200), ([400001], 700)])
+def test_evict_under_the_largest_bound(torch, lens, keep):
+    """max_len 524288, where the keys of a CTA's share do not fit its shared memory."""
+    rng = np.random.default_rng(keep)
+    pages, tab, new = setup(rng, lens, keep, 1, 64)
+    w = np.rint(np.exp(rng.normal(8, 4, (pages.n_blocks, 1, 64)))).astype(np.int64)
+    check_evict(torch, pages, w, tab, np.arange(len(lens), dtype=np.int32), np.array(lens, np.int32), keep, 4, 9, new, 524288)
+
+
 WEIGHTS = {
     "zeros": lambda rng, s: np.zeros(s, np.int64),
     "few values": lambda rng, s: rng.integers(0, 3, s),
