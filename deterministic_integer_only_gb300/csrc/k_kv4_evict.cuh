@@ -33,6 +33,10 @@ __device__ __forceinline__ unsigned kv4_p24s(int E, unsigned RS, int bl) {
 // heads' probabilities of a key are added and sent to the key's weight by one
 // 64-bit integer atomic (exact, so the order does not matter; tokens of
 // sequences that share pages meet there).
+// Bound: integer instructions, 117 per 32 scores (32 of them dp4a, the rest
+// unpacking, exponentials and probabilities), issued at half of the rate with 24
+// warps on an SM: 64 tokens of 4001..16384 keys, 32 + 8 heads of 128, 135 us, 2.9
+// TB/s; 1 token of 4000 by latency, 5 us.
 template <int GT>
 struct Kv4WeighSm {
     int red[8][GT];
@@ -216,7 +220,10 @@ __global__ void __launch_bounds__(KV4_DT, 3) k_kv4_weigh(Kv4Args a, Kv4Attn p, K
 // would take the tensor pipe three times).
 // Two exchanges settle the rows' maxima and sums over the warps and CTAs; then
 // the 16 rows' probabilities of a key are added over the lanes and go to the
-// key's weight by one 64-bit atomic. Column n of score tile j is key 16 (n / 2)
+// key's weight by one 64-bit atomic. Bound: the tensor pipe (47 % busy), the ALU
+// (35 %) and the exchanges take turns, as 16 warps fill an SM: 1 x 4096 tokens of 16
+// + 8 heads of 128 463 us (217 us would be the pipe's measured rate), 3 x 61 tokens
+// after 8000, 32 + 8 of 64, 118 us. Column n of score tile j is key 16 (n / 2)
 // + 2 j + (n & 1), so that a lane's scores are 16 neighbouring keys. K fragments
 // come straight from the pages: a warp's load is eight whole rows. A block's
 // tokens may belong to several sequences: each run of one sequence whose pages
@@ -504,6 +511,9 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
 // would share one), whose few keys in the bin in question are then ranked by
 // counting; where that bin is too full, its keys are split by 11 bits at a time
 // first. Then every warp deals the kept places of its run out.
+// Bound: latency of the phases, eight barriers of the cluster among them: 16
+// sequences of 9000..32768 keys, 8 kv heads, 36 us for 21 MB of weights in 1.7 waves
+// of CTAs; 1 of 4097 11 us.
 constexpr int EV_THREADS = 512, EV_WARPS = EV_THREADS / 32;
 constexpr int EV_BITS = 11, EV_BINS = 1 << EV_BITS;
 constexpr int EV_LIST = 512;             // keys that are ranked by counting
@@ -742,7 +752,8 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
 // kept places in order: one load for those that lie in the same 16, a nibble
 // out of it for each, one store for 16 new places. Places behind the last kept
 // token are left as they were. The new pages may not be among the sequences'
-// own.
+// own. Bound: memory, 62 us for those 16 sequences to 4099 keys each: 304 MB, most
+// of them values of which a sector holds 32 places, at 4.9 TB/s.
 constexpr int KV4_ZEROS = -0x77777778;   // eight codes of zero (8 each)
 template <int D>
 __global__ void __launch_bounds__(128) k_kv4_evict_move(Kv4Args a, Kv4Evict p) {
@@ -854,7 +865,9 @@ __global__ void __launch_bounds__(128) k_kv4_evict_move(Kv4Args a, Kv4Evict p) {
     }
 }
 
-// whole pages of every kv head, src[i] to dst[i]; -1 on either side: none
+// whole pages of every kv head, src[i] to dst[i]; -1 on either side: none. A CTA
+// per page and head, 16 bytes per thread and step; latency of one page (128 pages
+// of 8 heads of 128 with their weights 5 us).
 __global__ void __launch_bounds__(256) k_kv4_copy(Kv4Args a, const int32_t* src, const int32_t* dst, int page_bytes, long long* weight) {
     pdl_wait();
     const int s = src[blockIdx.x], d = dst[blockIdx.x], g = blockIdx.y;
