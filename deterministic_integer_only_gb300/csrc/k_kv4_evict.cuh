@@ -511,10 +511,9 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
 // would share one), whose few keys in the bin in question are then ranked by
 // counting; where that bin is too full, its keys are split by 11 bits at a time
 // first. Then every warp deals the kept places of its run out.
-// Bound: latency of the phases, eight barriers of the cluster among them: 16
-// sequences of 9000..32768 keys, 8 kv heads, 36 us for 21 MB of weights in 1.7 waves
-// of CTAs; 1 of 4097 11 us.
-constexpr int EV_THREADS = 512, EV_WARPS = EV_THREADS / 32;
+// Bound: latency of the phases, eight barriers of the cluster among them, so that
+// three CTAs per SM (five of 256 threads) take turns: 16 sequences of 9000..32768
+// keys, 8 kv heads, 34 us for 21 MB of weights (two CTAs per SM 37); 1 of 4097 11 us.
 constexpr int EV_BITS = 11, EV_BINS = 1 << EV_BITS;
 constexpr int EV_LIST = 512;             // keys that are ranked by counting
 constexpr int EV_PAGES = EV_BINS / 4;    // pages of a CTA
@@ -549,11 +548,14 @@ __device__ __forceinline__ u64 ev_least(int bin) {
     return neg ? (~v & ~(1ull << 63)) >> open << open : v | 1ull << 63;
 }
 
-__global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4Evict p) {
+template <int EV_THREADS>
+__global__ void __launch_bounds__(EV_THREADS, EV_THREADS == 512 ? 3 : 5) k_kv4_evict_select(Kv4Args a, Kv4Evict p) {
+    constexpr int EV_WARPS = EV_THREADS / 32;
     extern __shared__ __align__(16) unsigned char ev_raw[];
     u64* keys = (u64*)ev_raw;                            // the CTA's, where they are held
-    __shared__ unsigned hist[EV_BINS];
-    __shared__ u64 list[EV_LIST], found;
+    __shared__ __align__(16) unsigned hist[EV_BINS];
+    __shared__ u64 found;
+    u64* const list = (u64*)hist;                        // (the bins are clear and done with when it is filled)
     __shared__ unsigned scan[2][EV_WARPS], mine[2], pick[3], count;
     __shared__ int page[EV_PAGES];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(EV_THREADS) k_kv4_evict_select(Kv4Args a, Kv4E
 // out of it for each, one store for 16 new places. Places behind the last kept
 // token are left as they were. The new pages may not be among the sequences'
 // own. Bound: memory, 62 us for those 16 sequences to 4099 keys each: 304 MB, most
-// of them values of which a sector holds 32 places, at 4.9 TB/s.
+// of them values of which a sector holds 32 places, at 5.1 TB/s.
 constexpr int KV4_ZEROS = -0x77777778;   // eight codes of zero (8 each)
 template <int D>
 __global__ void __launch_bounds__(128) k_kv4_evict_move(Kv4Args a, Kv4Evict p) {

@@ -30,6 +30,7 @@ constexpr int NGT = 3;                       // 1, 2 or 4 heads of a CTA
 const WeighFn WEIGH[2][NGT] = {{k_kv4_weigh<64, 1>, k_kv4_weigh<64, 2>, k_kv4_weigh<64, 4>},
                                {k_kv4_weigh<128, 1>, k_kv4_weigh<128, 2>, k_kv4_weigh<128, 4>}};
 const WeighFn WEIGH_BLOCK[2][2] = {{k_kv4_weigh_block<64, 2>, k_kv4_weigh_block<64, 3>}, {k_kv4_weigh_block<128, 2>, k_kv4_weigh_block<128, 3>}};   // 4 or 8 warps
+void (*const EV_SELECT[2])(Kv4Args, Kv4Evict) = {k_kv4_evict_select<256>, k_kv4_evict_select<512>};
 int lg2(int n) { return n >= 4 ? 2 : n >= 2 ? 1 : 0; }
 size_t weigh_fixed(int gt) { return gt == 4 ? sizeof(Kv4WeighSm<4>) : gt == 2 ? sizeof(Kv4WeighSm<2>) : sizeof(Kv4WeighSm<1>); }
 size_t weigh_smem(int gt, int cap) {
@@ -82,10 +83,13 @@ cudaError_t init(DevInfo** out) {
             if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e == cudaSuccess) mc = std::min(mc, cluster_of((const void*)f, 128 << l, bytes));
         }
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv4_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_HELD);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv4_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int w : {0, 1}) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(EV_SELECT[w], cudaFuncAttributeMaxDynamicSharedMemorySize, EV_HELD);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(EV_SELECT[w], cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) mc = std::min(mc, cluster_of((const void*)EV_SELECT[w], 256 << w, EV_HELD));
+    }
     if (e == cudaSuccess) {
-        di->max_cluster = std::min(mc, cluster_of((const void*)k_kv4_evict_select, EV_THREADS, EV_HELD));
+        di->max_cluster = mc;
         di->ready = true;
     }
     return e;
@@ -167,9 +171,9 @@ cudaError_t launch_evict(const DevInfo& di, const Kv4Args& a, Kv4Evict p, int n,
     int lg = 0;
     auto pages = [&]() { return (mp + (1 << lg) - 1) >> lg; };
     // CTAs of 32 pages or less while there are few of them (4 sequences of 8192
-    // keys, 8 kv heads: 23.6 us, with one CTA 26.3, with 8 27.1; 16 of up to 32768
-    // 106 with 4, with 2 118, with 8 124; 64 of 2048 50 with one, with two 67),
-    // 16 of them only for long contexts (1 of 32768: 27.8 with 8, with 16 32)
+    // keys, 8 kv heads: 22.4 us, with 8 CTAs 23.4; 16 of up to 32768 96 with 4, with
+    // 2 112, with 8 107; 32 of 4096 47 with 2, with one 45), 16 of them only for long
+    // contexts (1 of 32768: 27.8 with 8, with 16 32)
     while ((2 << lg) <= di.max_cluster &&
            (pages() > EV_PAGES || (pages() > (lg < 3 ? 32 : 128) && ((long long)n * a.n_kv << (lg + 1)) * 2 <= 7LL * di.sms)))
         ++lg;
@@ -186,13 +190,22 @@ cudaError_t launch_evict(const DevInfo& di, const Kv4Args& a, Kv4Evict p, int n,
     cfg.numAttrs = lg ? 1 : 0;
     cfg.stream = s;
     cfg.gridDim = dim3(n << lg, a.n_kv);
-    cfg.blockDim = dim3(EV_THREADS);
+    // 256 threads where two CTAs of 512 per SM would not hold all and a CTA has few
+    // pages, as the phases' latencies then overlap (8 sequences of 16384 keys, 8 kv
+    // heads: 41 us, with 512 48; 256 of 700 77 and 87; 16 of up to 32768, 128 pages
+    // a CTA: 104, with 512 96). The move starts while the selection drains only where
+    // an SM has one CTA of it: past that its CTAs would find the SMs set to much
+    // shared memory and little L1 (16 of up to 32768: 96 us, then 123; 1 of 4097:
+    // 16.1, after it 16.7)
+    const long long ctas = (long long)n * a.n_kv << lg;
+    const bool small = pages() <= 32 && ctas > 2LL * di.sms;
+    cfg.blockDim = dim3(small ? 256 : 512);
     cfg.dynamicSmemBytes = p.held ? bytes : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_evict_select, a, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, EV_SELECT[!small], a, p);
     if (e != cudaSuccess) return e;
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ctas <= di.sms;
     cfg.gridDim = dim3(p.new_blocks, a.n_kv, n);
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;

@@ -347,6 +347,18 @@ def test_evict_values(torch, kind, lens, keep, sinks, recent):
     check_evict(torch, pages, w, tab, np.arange(len(lens), dtype=np.int32), np.array(lens, np.int32), keep, sinks, recent, new, max(lens))
 
 
+@pytest.mark.parametrize("kind", WEIGHTS)
+@pytest.mark.parametrize("n,n_kv,most,keep", [(50, 8, 700, 190), (20, 4, 8192, 300)])
+def test_evict_many_sequences(torch, kind, n, n_kv, most, keep):
+    """More CTAs than the GPU holds at two per SM, by themselves and in clusters."""
+    rng = np.random.default_rng(n + len(kind))
+    lens = rng.integers(0, 500, n)
+    lens[[3, n - 2]] = most, most - 1
+    pages, tab, new = setup(rng, list(lens), keep, n_kv, 64)
+    w = np.asarray(WEIGHTS[kind](rng, (pages.n_blocks, n_kv, 64)), np.int64)
+    check_evict(torch, pages, w, tab, np.arange(n, dtype=np.int32), lens.astype(np.int32), keep, 2, 7, new, most)
+
+
 def test_evict_rows_of_the_table_and_bad_entries(torch):
     """Any rows in any order, the same one twice; lengths and sequences out of
     range move nothing; a page outside the pool moves as zeros of weight 0."""
