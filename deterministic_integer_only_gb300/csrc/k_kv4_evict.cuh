@@ -510,7 +510,9 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
 // either side of zero (attention weights are heavy-tailed: in even bins most
 // would share one), whose few keys in the bin in question are then ranked by
 // counting; where that bin is too full, its keys are split by 11 bits at a time
-// first. Then every warp deals the kept places of its run out.
+// first. Then every warp deals the kept places of its run out. Keys that are not
+// held are read again in each pass: weights that another stream changes meanwhile
+// give some choice, but nothing is written past the lists.
 // Bound: latency of the phases, eight barriers of the cluster among them, so that
 // three CTAs per SM (five of 256 threads) take turns: 16 sequences of 9000..32768
 // keys, 8 kv heads, 34 us for 21 MB of weights (two CTAs per SM 37); 1 of 4097 11 us.
@@ -676,7 +678,10 @@ __global__ void __launch_bounds__(EV_THREADS, EV_THREADS == 512 ? 3 : 5) k_kv4_e
         if (!whole && open > 0 && n <= EV_LIST) {        // few: ranked by the first CTA
             const u64 near = cut >> open;
             each([&](u64 k) {
-                if (k >> open == near) cl_st64(&list[cl_add32(&count, 0, 1)], 0, k);
+                if (k >> open == near) {
+                    const unsigned to = cl_add32(&count, 0, 1);
+                    if (to < EV_LIST) cl_st64(&list[to], 0, k);
+                }
             });
             cl_sync();
             if (rank == 0) {
@@ -741,7 +746,8 @@ __global__ void __launch_bounds__(EV_THREADS, EV_THREADS == 512 ? 3 : 5) k_kv4_e
         for (int hf = 0; hf < 2; ++hf) {
             const unsigned mk = mask[4 * b + 2 * hf], mt = mask[4 * b + 2 * hf + 1], lt = (1u << lane) - 1;
             const unsigned e = be + __popc(mt & lt);
-            if ((mk >> lane & 1) || ((mt >> lane & 1) && e < want)) out[bt + __popc(mk & lt) + min(e, want)] = j0 + (b << 6) + 32 * hf + lane;
+            const unsigned to = bt + __popc(mk & lt) + min(e, want);
+            if (((mk >> lane & 1) || ((mt >> lane & 1) && e < want)) && to < (unsigned)p.keep) out[to] = j0 + (b << 6) + 32 * hf + lane;
             bt += __popc(mk);
             be += __popc(mt);
         }
@@ -770,8 +776,9 @@ __global__ void __launch_bounds__(128) k_kv4_evict_move(Kv4Args a, Kv4Evict p) {
     if (tid < KV_BLK) {
         const int s = b * KV_BLK + tid, j = s < p.keep ? __ldcg(kept + s) : -1;
         int blk = -1;
-        if (j >= 0) blk = a.block_table[(size_t)seq * a.max_blocks + (j >> 6)];
-        from[tid] = j < 0 ? -1 : j & 63;
+        const bool in = j >= 0 && (j >> 6) < a.max_blocks && seq >= 0 && seq < a.n_seq;
+        if (in) blk = a.block_table[(size_t)seq * a.max_blocks + (j >> 6)];
+        from[tid] = in ? j & 63 : -1;
         page[tid] = blk >= 0 && blk < a.n_blocks ? blk : -1;
         move[tid] = make_int2((8 * (j & 3) + (j & 4)) | (j & 8 ? (int)0x80000000 : 0), 1 << (8 * (tid & 3) + (tid & 4)));
     }
