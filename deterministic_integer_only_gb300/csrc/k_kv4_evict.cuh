@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
 // give some choice, but nothing is written past the lists.
 // Bound: latency of the phases, eight barriers of the cluster among them, so that
 // three CTAs per SM (five of 256 threads) take turns: 16 sequences of 9000..32768
-// keys, 8 kv heads, 34 us for 21 MB of weights (two CTAs per SM 37); 1 of 4097 11 us.
+// keys, 8 kv heads, 36 us for 21 MB of weights (two CTAs per SM 38); 1 of 4097 11 us.
 constexpr int EV_BITS = 11, EV_BINS = 1 << EV_BITS;
 constexpr int EV_LIST = 512;             // keys that are ranked by counting
 constexpr int EV_PAGES = EV_BINS / 4;    // pages of a CTA
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(128) k_kv4_evict_move(Kv4Args a, Kv4Evict p) {
     if (tid < KV_BLK) {
         const int s = b * KV_BLK + tid, j = s < p.keep ? __ldcg(kept + s) : -1;
         int blk = -1;
-        const bool in = j >= 0 && (j >> 6) < a.max_blocks && seq >= 0 && seq < a.n_seq;
+        const bool in = (unsigned)(j >> 6) < (unsigned)a.max_blocks;      // (none of a sequence out of range is kept)
         if (in) blk = a.block_table[(size_t)seq * a.max_blocks + (j >> 6)];
         from[tid] = in ? j & 63 : -1;
         page[tid] = blk >= 0 && blk < a.n_blocks ? blk : -1;

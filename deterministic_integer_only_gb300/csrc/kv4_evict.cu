@@ -171,8 +171,8 @@ cudaError_t launch_evict(const DevInfo& di, const Kv4Args& a, Kv4Evict p, int n,
     int lg = 0;
     auto pages = [&]() { return (mp + (1 << lg) - 1) >> lg; };
     // CTAs of 32 pages or less while there are few of them (4 sequences of 8192
-    // keys, 8 kv heads: 22.4 us, with 8 CTAs 23.4; 16 of up to 32768 96 with 4, with
-    // 2 112, with 8 107; 32 of 4096 47 with 2, with one 45), 16 of them only for long
+    // keys, 8 kv heads: 22.4 us, with 8 CTAs 23.4; 16 of up to 32768 98 with 4, with
+    // 2 112, with 8 107; 32 of 4096 48 with 2, with one 45), 16 of them only for long
     // contexts (1 of 32768: 27.8 with 8, with 16 32)
     while ((2 << lg) <= di.max_cluster &&
            (pages() > EV_PAGES || (pages() > (lg < 3 ? 32 : 128) && ((long long)n * a.n_kv << (lg + 1)) * 2 <= 7LL * di.sms)))
@@ -192,11 +192,11 @@ cudaError_t launch_evict(const DevInfo& di, const Kv4Args& a, Kv4Evict p, int n,
     cfg.gridDim = dim3(n << lg, a.n_kv);
     // 256 threads where two CTAs of 512 per SM would not hold all and a CTA has few
     // pages, as the phases' latencies then overlap (8 sequences of 16384 keys, 8 kv
-    // heads: 41 us, with 512 48; 256 of 700 77 and 87; 16 of up to 32768, 128 pages
-    // a CTA: 104, with 512 96). The move starts while the selection drains only where
+    // heads: 42 us, with 512 48; 256 of 700 78 and 87; 16 of up to 32768, 128 pages
+    // a CTA: 104, with 512 98). The move starts while the selection drains only where
     // an SM has one CTA of it: past that its CTAs would find the SMs set to much
-    // shared memory and little L1 (16 of up to 32768: 96 us, then 123; 1 of 4097:
-    // 16.1, after it 16.7)
+    // shared memory and little L1 (16 of up to 32768: 98 us, then 123; 1 of 4097:
+    // 16.3, after it 16.7)
     const long long ctas = (long long)n * a.n_kv << lg;
     const bool small = pages() <= 32 && ctas > 2LL * di.sms;
     cfg.blockDim = dim3(small ? 256 : 512);
