@@ -512,7 +512,8 @@ __global__ void __launch_bounds__(32 << LGW, 16 >> LGW) k_kv4_weigh_block(Kv4Arg
 // counting; where that bin is too full, its keys are split by 11 bits at a time
 // first. Then every warp deals the kept places of its run out. Keys that are not
 // held are read again in each pass: weights that another stream changes meanwhile
-// give some choice, but nothing is written past the lists.
+// give some choice, of fewer places perhaps, but every entry of the lists is written
+// (-1 behind the last place) and nothing past them.
 // Bound: latency of the phases, eight barriers of the cluster among them, so that
 // three CTAs per SM (five of 256 threads) take turns: 16 sequences of 9000..32768
 // keys, 8 kv heads, 36 us for 21 MB of weights (two CTAs per SM 38); 1 of 4097 11 us.
@@ -751,6 +752,8 @@ __global__ void __launch_bounds__(EV_THREADS, EV_THREADS == 512 ? 3 : 5) k_kv4_e
             bt += __popc(mk);
             be += __popc(mt);
         }
+    if (rank == S - 1 && warp == EV_WARPS - 1)           // behind the last place (nothing is left over unless weights changed meanwhile)
+        for (unsigned j = bt + min(be, want) + lane; j < (unsigned)p.keep; j += 32) out[j] = -1;
     cl_sync();                                           // no CTA leaves while another reads its shared memory
 }
 
@@ -865,7 +868,7 @@ __global__ void __launch_bounds__(128) k_kv4_evict_move(Kv4Args a, Kv4Evict p) {
     }
     if (kt < n) {
         const int blk = page[kt];
-        const size_t o = ((size_t)max(blk, 0) * a.n_kv + g) * KV_BLK + from[kt];
+        const size_t o = ((size_t)max(blk, 0) * a.n_kv + g) * KV_BLK + max(from[kt], 0);
         const uint8_t ck = a.ks[o], cv = a.vs[o];
         const long long w = p.weight[o];
         a.ks[u * KV_BLK + kt] = blk >= 0 ? ck : 1;
