@@ -599,9 +599,11 @@ def detint_beam_select(logits, scores, n_out: int, done=None, end_id: int = -1, 
 
 def detint_beam_reorder(block_table, parent, lens, out=None, src=None, dst=None, stream=None):
     """Give every beam its parent's pages: block_table int32 [groups * beams,
-    max_blocks], parent int32 [groups, beams], lens int32 [groups]; out: another
-    table, or None for block_table itself. Returns (src, dst), int32 [groups,
-    beams]: the pages that detint_kv4_copy has to copy in every layer."""
+    max_blocks], parent int32 [groups, beams] (a beam that goes on as it is names
+    itself; outside 0..beams - 1 the row holds no beam any more, and the tokens of
+    its last page are lost), lens int32 [groups]; out: another table, or None for
+    block_table itself. Returns (src, dst), int32 [groups, beams]: the pages that
+    detint_kv4_copy has to copy in every layer."""
     import torch
     w, i32 = "detint_beam_reorder", torch.int32
     index = _beam_device(w, torch, block_table)

@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(256) k_copy_blocks(BlockParts b, BlockPairs p)
 // ---- the chosen beams' block tables. Whole pages are shared. Of the page that
 // is still being filled (column len / 64) a beam's first child becomes the
 // owner; every other child takes the page of a beam without children, into
-// which its parent's is to be copied (src, dst: -1 where nothing is). So a
+// which its parent's is to be copied (src, dst: -1 where nothing is), and so does a
+// row without a parent, which holds no beam any more and gets no copy. So a
 // group's beams keep as many growing pages as they had, nothing is allocated,
 // and no page that is copied to is copied from. A column's entries are read by
 // one CTA before it writes them: out may be the table itself.

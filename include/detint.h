@@ -444,15 +444,19 @@ int detint_beam_workspace(int rows, int n, int n_out, long long* bytes);
 
 /* The block tables of the chosen beams. block_table: device int32 [groups *
  * beams][max_blocks]; parent: device int32 [groups][beams], as detint_beam_select
- * gives it (outside 0..beams - 1: the beam keeps its own pages); lens: device
- * int32 [groups], the tokens that every beam of the group holds. Row b of out
+ * gives it; lens: device int32 [groups], the tokens that every beam of the group
+ * holds. A beam that goes on as it is names itself. Row b of out
  * (which may be block_table itself) gets its parent's whole pages, shared. Of
  * the page that is still being filled, a beam's first child becomes the owner;
  * each other child gets the page of a beam that has no child, and an entry of
  * src and dst (device int32 [groups][beams], -1: none) that detint_kv4_copy
  * takes, once per layer, before the next append. So a group needs no page that it
  * does not have; its beams' growing pages and the entries behind them must be
- * distinct from the start. Later columns stay. Errors: ARG, CUDA. */
+ * distinct from the start. Later columns stay. A parent outside 0..beams - 1 (-1
+ * where continuations ran out) means that the row holds no beam from now on: its
+ * whole pages stay, but the page that is still being filled is dealt out with
+ * those of the beams that have no child, so the row may end with the last tokens
+ * of another beam, and nothing is copied for it. Errors: ARG, CUDA. */
 int detint_beam_reorder(const int32_t* block_table, int32_t* out, int max_blocks, const int32_t* parent, const int32_t* lens,
                         int groups, int beams, int32_t* src, int32_t* dst, detint_stream_t s);
 

@@ -54,3 +54,50 @@ def test_evict_while_another_stream_changes_the_weights(torch, max_len):
             assert m >= sinks and (row[m:] == -1).all()
             assert (np.diff(row[:m]) > 0).all() and row[m - 1] < n and row[:sinks].tolist() == list(range(sinks))
     assert not dev.status.any()
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("parents,n", [
+    ([[2, 1, 2]], 70), ([[0, 1, 2]], 70), ([[1, 1, 2]], 129), ([[2, -1, 2]], 70), ([[1, -1, 1]], 63), ([[-1, -1, -1]], 1),
+    ([[3, 3, 3, 3], [0, 0, 2, 3]], 200), ([[1, 0, -1, 7], [3, 1, 1, -1]], 100), ([[0, 0]], 128), ([[0]], 5), (None, 191)])
+def test_reorder_moves_what_the_beams_hold(torch, parents, n, inplace):
+    """Every token's slot is marked with its beam and place; after tables and
+    copies a row reads its parent's marks. A beam that names itself reads its own.
+    A row without a parent reads its own whole pages and a growing page that is
+    no other row's."""
+    import deterministic_integer_only_gb300 as pkg
+    if parents is None:
+        parents = np.random.default_rng(n).integers(-1, 16, (5, 16)).tolist()
+    G, W = len(parents), len(parents[0])
+    n_kv, d, blocks = 2, 64, n // 64 + 2
+    pool = G * W * blocks
+    rng = np.random.default_rng(n + W)
+    tab = rng.permutation(pool).astype(np.int32).reshape(G * W, blocks)
+    pages = kp.Pages(pool, n_kv, d, rng)
+    mark = np.zeros((pool, n_kv, 64), np.int64)
+    for r in range(G * W):
+        for h in range(n_kv):
+            mark[tab[r], h] = (r * 1000 + h) * 1000 + np.arange(blocks * 64).reshape(blocks, 64)
+    pages.ck[:] = mark % 251 + 1
+    dev, w = Dev(torch, pages, tab, kp.params(n_kv, d, rng), n_kv), cuda(torch, mark)
+    lens = torch.full((G,), n, dtype=torch.int32, device="cuda")
+    out = None if inplace else torch.empty_like(dev.table)
+    src, dst = pkg.detint_beam_reorder(dev.table, cuda(torch, np.array(parents, np.int32)), lens, out=out)
+    pkg.detint_kv4_copy(dev.cache, src, dst, weight=w)
+    new, w, ck = (dev.table if inplace else out).cpu().numpy(), w.cpu().numpy(), dev.ck.cpu().numpy()
+    for g in range(G):
+        for b in range(W):
+            p = parents[g][b]
+            if 0 <= p < W:
+                size, of = n, g * W + p
+            else:
+                size, of = n // 64 * 64, g * W + b
+            at = np.arange(size)
+            for h in range(n_kv):
+                want = (of * 1000 + h) * 1000 + at
+                got = new[g * W + b, at // 64]
+                assert np.array_equal(w[got, h, at % 64], want)
+                assert np.array_equal(ck.reshape(w.shape)[got, h, at % 64], want % 251 + 1)
+        if n % 64:
+            assert len(set(new[g * W:(g + 1) * W, n // 64])) == W
+    assert not dev.status.any()
