@@ -136,6 +136,11 @@ int detint_beam_select(const int32_t* logits, long long stride, int n, const int
     if (rc) return rc;
     if (!workspace || workspace_bytes < need || mis(workspace, 16))
         return err(DETINT_E_ARG, "a 16-byte aligned workspace of detint_beam_workspace bytes is needed");
+    // (a group's outputs are written while others' inputs are still read)
+    const size_t rows = (size_t)groups * beams, outs = (size_t)groups * n_out;
+    const Span written[] = {{parent, outs * 4}, {token, outs * 4}, {score, outs * 8}, {done_out, outs * 4}, {workspace, (size_t)need}};
+    const Span read[] = {{logits, ((rows - 1) * (size_t)stride + n) * 4}, {scores, rows * 8}, {done, rows * 4}};
+    if (clash(written, read)) return err(DETINT_E_ARG, "an output or the workspace overlaps another array of the call");
     BeamArgs a{};
     a.logits = logits; a.stride = (size_t)stride; a.scores = (const long long*)scores; a.done = done;
     a.n = n; a.n_out = n_out; a.end_id = end_id; a.beams = beams;
@@ -164,6 +169,10 @@ int detint_beam_reorder(const int32_t* block_table, int32_t* out, int max_blocks
     if (max_blocks < 1) return err(DETINT_E_ARG, "max_blocks must be positive");
     if (mis(block_table, 4) || mis(out, 4) || mis(parent, 4) || mis(lens, 4) || mis(src, 4) || mis(dst, 4))
         return err(DETINT_E_ARG, "arrays must be 4-byte aligned");
+    const size_t rows = (size_t)groups * beams, cells = rows * (size_t)max_blocks;
+    const Span written[] = {{out, cells * 4}, {src, rows * 4}, {dst, rows * 4}};
+    const Span read[] = {{out == block_table ? nullptr : block_table, cells * 4}, {parent, rows * 4}, {lens, (size_t)groups * 4}};
+    if (clash(written, read)) return err(DETINT_E_ARG, "out (unless it is block_table itself), src or dst overlaps another array of the call");
     k_beam_reorder<<<dim3((max_blocks + BR_COLS - 1) / BR_COLS, groups), BR_THREADS, 0, (cudaStream_t)sp>>>(
         block_table, out, parent, lens, beams, max_blocks, src, dst);
     const cudaError_t e = cudaGetLastError();

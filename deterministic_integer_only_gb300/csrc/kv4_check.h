@@ -23,6 +23,26 @@ inline int cuda_fail(const char* where, cudaError_t e) {
     return failed(DETINT_E_CUDA, where, cudaGetErrorString(e));
 }
 inline bool mis(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) != 0; }
+// an array of a call; null ones overlap nothing
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+inline bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+// whether an array that is written overlaps another one, written or read
+template <int NO, int NI>
+inline bool clash(const Span (&out)[NO], const Span (&in)[NI]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return true;
+        for (int j = 0; j < NI; ++j)
+            if (overlap(out[i], in[j])) return true;
+    }
+    return false;
+}
 
 // the checks every entry point shares; fills the kernels' view of the cache
 inline int check_cache(const char* where, const detint_kv4_t* c, Kv4Args* a) {

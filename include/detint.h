@@ -430,9 +430,10 @@ int detint_kv4_copy(const detint_kv4_t* c, const int32_t* src, const int32_t* ds
  * score, and done_out (1 where the parent was finished or the token is end_id);
  * where there are fewer continuations, parent and token -1, score -2^63 and
  * done 0. scores and done may be the outputs of the call before but not of this
- * one. end_id -1: no token ends a beam. workspace: detint_beam_workspace bytes,
- * 16-byte aligned; calls that may overlap on the GPU, captured ones included,
- * need one each. Up to 65535 rows of up to 2^24 logits.
+ * one: outputs or a workspace that overlap another array are refused. end_id -1:
+ * no token ends a beam. workspace: detint_beam_workspace bytes, 16-byte aligned;
+ * calls that may overlap on the GPU, captured ones included, need one each. Up to
+ * 65535 rows of up to 2^24 logits.
  * Errors: ARG, SHAPE, CUDA. */
 int detint_beam_select(const int32_t* logits, long long stride, int n, const int64_t* scores, const int32_t* done,
                        int groups, int beams, int end_id, int n_out, int32_t* parent, int32_t* token, int64_t* score,
@@ -445,9 +446,9 @@ int detint_beam_workspace(int rows, int n, int n_out, long long* bytes);
 /* The block tables of the chosen beams. block_table: device int32 [groups *
  * beams][max_blocks]; parent: device int32 [groups][beams], as detint_beam_select
  * gives it; lens: device int32 [groups], the tokens that every beam of the group
- * holds. A beam that goes on as it is names itself. Row b of out
- * (which may be block_table itself) gets its parent's whole pages, shared. Of
- * the page that is still being filled, a beam's first child becomes the owner;
+ * holds. A beam that goes on as it is names itself. Row b of out (which may be
+ * block_table itself) gets its parent's whole pages, shared. Of the page that is
+ * still being filled, a beam's first child becomes the owner;
  * each other child gets the page of a beam that has no child, and an entry of
  * src and dst (device int32 [groups][beams], -1: none) that detint_kv4_copy
  * takes, once per layer, before the next append. So a group needs no page that it
@@ -456,7 +457,8 @@ int detint_beam_workspace(int rows, int n, int n_out, long long* bytes);
  * where continuations ran out) means that the row holds no beam from now on: its
  * whole pages stay, but the page that is still being filled is dealt out with
  * those of the beams that have no child, so the row may end with the last tokens
- * of another beam, and nothing is copied for it. Errors: ARG, CUDA. */
+ * of another beam, and nothing is copied for it. src, dst and an out that is not
+ * block_table may overlap no other array. Errors: ARG, CUDA. */
 int detint_beam_reorder(const int32_t* block_table, int32_t* out, int max_blocks, const int32_t* parent, const int32_t* lens,
                         int groups, int beams, int32_t* src, int32_t* dst, detint_stream_t s);
 

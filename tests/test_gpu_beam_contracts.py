@@ -101,3 +101,32 @@ def test_reorder_moves_what_the_beams_hold(torch, parents, n, inplace):
         if n % 64:
             assert len(set(new[g * W:(g + 1) * W, n // 64])) == W
     assert not dev.status.any()
+
+
+def test_beam_search_arrays_may_touch_but_not_overlap(torch):
+    """Neighbouring slices of one buffer are fine; in place is refused."""
+    import beam_plain as bp
+    import deterministic_integer_only_gb300 as pkg
+    rng = np.random.default_rng(4)
+    G, W, V = 3, 4, 500
+    logits, scores = np.rint(rng.normal(0, 99999, (G * W, V))).astype(np.int32), -rng.integers(0, 1 << 20, (G, W))
+    want = bp.select(logits, scores, W, None, -1)
+    buf = torch.zeros(8 * G * W, dtype=torch.int32, device="cuda")
+    part = [buf[i * G * W:(i + 1) * G * W] for i in range(8)]
+    sc = buf[4 * G * W:6 * G * W].view(torch.int64).view(G, W)
+    sc.copy_(cuda(torch, scores))
+    lg, s2 = cuda(torch, logits), buf[2 * G * W:4 * G * W].view(torch.int64)
+    got = pkg.detint_beam_select(lg, sc, W, out=(part[0], part[1], s2, part[6]))
+    assert all(np.array_equal(a.cpu().numpy().reshape(b.shape), b) for a, b in zip(got, want))
+    assert np.array_equal(sc.cpu().numpy(), scores)
+    done = torch.zeros(G, W, dtype=torch.int32, device="cuda")
+    tab, lens = torch.arange(G * W * 3, dtype=torch.int32, device="cuda").view(G * W, 3), torch.full((G,), 70, dtype=torch.int32, device="cuda")
+    par = cuda(torch, want[0])
+    for f in (lambda: pkg.detint_beam_select(lg, sc, W, out=(part[0], part[1], sc, part[6])),
+              lambda: pkg.detint_beam_select(lg, sc, W, done, 3, out=(part[0], part[1], s2, done)),
+              lambda: pkg.detint_beam_select(lg, sc, W, out=(part[0], part[0], s2, part[6])),
+              lambda: pkg.detint_beam_reorder(tab, par, lens, src=par),
+              lambda: pkg.detint_beam_reorder(tab, par, lens, src=done, dst=done)):
+        with pytest.raises(pkg.DetintError):
+            f()
+    assert np.array_equal(sc.cpu().numpy(), scores) and np.array_equal(par.cpu().numpy(), want[0]) and not done.any()
