@@ -785,11 +785,11 @@ class Model:
 
         Returns (tokens [len(prompts)][beams][max_new] int32 numpy, scores
         [len(prompts)][beams] int64 numpy: log-probabilities in Q16), best first.
-        A beam that chose end_id keeps its score and continues with end_id; the
-        search stops early once every beam has. The beams of prompt g run on the
-        empty sequences seq_ids[g * beams : (g + 1) * beams] (0, 1, ... by default) and
-        share their common pages. Scores and tokens do not depend on the other
-        prompts of the batch.
+        A beam that chose end_id keeps its score and continues with end_id; a
+        prompt's search stops early once all of its beams have. The beams of prompt g
+        run on the empty sequences seq_ids[g * beams : (g + 1) * beams] (0, 1, ... by
+        default) and share their common pages. Scores and tokens, and whether the
+        contexts hold them, do not depend on the other prompts of the batch.
         """
         torch = self.torch
         G, dev = len(prompts), torch.device("cuda")
@@ -810,20 +810,29 @@ class Model:
             # the prompts' rows: one beam of each group so far
             parent, token, scores, done = detint_beam_select(logits[:G], torch.zeros((G, 1), dtype=torch.int64, device=dev),
                                                              beams, None, end_id, workspace=ws)
-            base = np.arange(G)[:, None] * beams
+            live, ids, out = np.arange(G), seq_ids, np.zeros((G, beams), np.int64)    # prompts that go on, their sequences
             for step in range(max_new):
                 if step:
-                    self.decode_step(seq_ids, tok, logits, tok)
-                    parent, token, scores, done = detint_beam_select(logits, scores, beams, done if end_id >= 0 else None,
+                    self.decode_step(ids, tok, logits, tok)
+                    parent, token, scores, done = detint_beam_select(logits[:len(ids)], scores, beams, done if end_id >= 0 else None,
                                                                      end_id, workspace=ws)
-                tok.copy_(token.view(-1))
+                tok[:len(ids)].copy_(token.view(-1))
                 par, new = parent.cpu().numpy(), token.cpu().numpy()
-                toks = np.take_along_axis(toks, par[:, :, None], 1)
-                toks[:, :, step] = new
-                if step + 1 == max_new or end_id >= 0 and bool(done.all()):
-                    toks[:, :, step + 1:] = end_id if end_id >= 0 else 0
-                    break
-                self.reorder_seqs(seq_ids, (par + base).reshape(-1))
-            out = scores.cpu().numpy()
+                toks[live] = np.take_along_axis(toks[live], par[:, :, None], 1)
+                toks[live, :, step] = new
+                over = done.cpu().numpy().all(1) if end_id >= 0 else np.zeros(len(live), bool)
+                if step + 1 == max_new:
+                    over[:] = True
+                if over.any():
+                    out[live[over]] = scores.cpu().numpy()[over]
+                    toks[live[over], :, step + 1:] = max(end_id, 0)
+                    if over.all():
+                        break
+                    # a finished prompt's beams take no more places of their contexts
+                    at = torch.from_numpy(np.flatnonzero(~over)).to(dev)
+                    scores, done, live, par = scores[at], done[at], live[~over], par[~over]
+                    ids = [seq_ids[g * beams + b] for g in live for b in range(beams)]
+                    tok[:len(ids)].copy_(token[at].view(-1))
+                self.reorder_seqs(ids, (par + np.arange(len(live))[:, None] * beams).reshape(-1))
         self.stream.synchronize()
         return toks, out
