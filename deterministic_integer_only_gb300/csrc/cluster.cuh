@@ -1,4 +1,4 @@
-// Thread-block clusters: rank, barrier and accesses to another CTA's shared
+// Thread-block clusters: barrier and accesses to another CTA's shared
 // memory. A launch without a cluster is one of a single CTA.
 #pragma once
 #include <stdint.h>
@@ -8,11 +8,6 @@
 
 namespace detint {
 
-__device__ __forceinline__ unsigned cl_rank() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cl_sync() {
     asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -32,11 +27,6 @@ __device__ __forceinline__ i64 cl_ld64(const i64* p, unsigned rank) {
     i64 v;
     asm volatile("ld.shared::cluster.s64 %0, [%1];" : "=l"(v) : "r"(cl_addr(p, rank)) : "memory");
     return v;
-}
-__device__ __forceinline__ unsigned cl_size() {
-    unsigned r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
 }
 __device__ __forceinline__ unsigned cl_ld32u(const unsigned* p, unsigned rank) { return (unsigned)cl_ld32((const int*)p, rank); }
 __device__ __forceinline__ void cl_st64(u64* p, unsigned rank, u64 v) {

@@ -65,7 +65,6 @@ __device__ __forceinline__ u64 bm_key(int v, int idx) { return ((u64)((unsigned)
 __device__ __forceinline__ int bm_value(u64 key) { return (int)((unsigned)(key >> 32) ^ 0x80000000u); }
 __device__ __forceinline__ int bm_index(u64 key) { return 0x7fffffff - (int)(unsigned)key; }
 __device__ __forceinline__ u64 umax64(u64 a, u64 b) { return a > b ? a : b; }
-__device__ __forceinline__ u64 umin64(u64 a, u64 b) { return a < b ? a : b; }
 
 // exp(l - M) in Q30 of Q16 logits l <= M: with d = M - l, -delta = (d L2E + 2^20 -
 // 1) >> 21 octaves in Q10, which is the high word of d (L2E 2^11) + (2^20 - 1)

@@ -96,7 +96,6 @@ cudaError_t init(DevInfo** out) {
 }
 
 cudaError_t launch_weigh(const DevInfo& di, const Kv4Args& a, Kv4Attn p, const Kv4Weigh& w, int d, cudaStream_t s) {
-    p.polls = SG_SPIN;
     p.none = KV4_NEG;
     int mp = (p.max_len + 63) >> 6;                                 // pages a token can have
     if (p.window > 0) mp = std::min(mp, ((p.window + 62) >> 6) + 1);
