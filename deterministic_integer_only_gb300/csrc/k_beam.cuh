@@ -70,7 +70,7 @@ __device__ __forceinline__ u64 umax64(u64 a, u64 b) { return a > b ? a : b; }
 // 1) >> 21 octaves in Q10, which is the high word of d (L2E 2^11) + (2^20 - 1)
 // 2^11; here m = -delta - 1, so that the fraction is ~m and the octaves down
 // are (m >> 10) + 1. exp2q's cubic p of the fraction comes from a table of the
-// CTA's (2^16 p; computing it took 25 instructions a value in place of 17); then
+// CTA's (2^16 p; computing it took 25 instructions a logit in place of 21); then
 // rshr(2^15 p, sh) = (((2^16 p) >> sh) + 1) >> 1. Zero from 31 octaves down:
 // below `least` (what it is there is not used, but computed: a branch for each
 // value cost more).

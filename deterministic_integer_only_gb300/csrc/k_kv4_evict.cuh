@@ -33,10 +33,11 @@ __device__ __forceinline__ unsigned kv4_p24s(int E, unsigned RS, int bl) {
 // heads' probabilities of a key are added and sent to the key's weight by one
 // 64-bit integer atomic (exact, so the order does not matter; tokens of
 // sequences that share pages meet there).
-// Bound: integer instructions, 117 per 32 scores (32 of them dp4a, the rest
-// unpacking, exponentials and probabilities), issued at half of the rate with 24
-// warps on an SM: 64 tokens of 4001..16384 keys, 32 + 8 heads of 128, 135 us, 2.9
-// TB/s; 1 token of 4000 by latency, 5 us.
+// Bound: phases that wait for memory and for each other: 64 tokens of 4001..16384
+// keys, 32 + 8 heads of 128, take 135 us, 2.9 TB/s, for 117 instructions per 32
+// scores (32 of them dp4a, the rest unpacking, exponentials and probabilities) that
+// would issue in about 65; the ALU is 33 % busy with 24 warps on an SM. 1 token of
+// 4000 by latency, 5 us.
 template <int GT>
 struct Kv4WeighSm {
     int red[8][GT];
@@ -220,8 +221,8 @@ __global__ void __launch_bounds__(KV4_DT, 3) k_kv4_weigh(Kv4Args a, Kv4Attn p, K
 // would take the tensor pipe three times).
 // Two exchanges settle the rows' maxima and sums over the warps and CTAs; then
 // the 16 rows' probabilities of a key are added over the lanes and go to the
-// key's weight by one 64-bit atomic. Bound: the tensor pipe (47 % busy), the ALU
-// (35 %) and the exchanges take turns, as 16 warps fill an SM: 1 x 4096 tokens of 16
+// key's weight by one 64-bit atomic. Bound: the tensor pipe (45 % busy), the ALU
+// (32 %) and the exchanges take turns, as 16 warps fill an SM: 1 x 4096 tokens of 16
 // + 8 heads of 128 463 us (217 us would be the pipe's measured rate), 3 x 61 tokens
 // after 8000, 32 + 8 of 64, 118 us. Column n of score tile j is key 16 (n / 2)
 // + 2 j + (n & 1), so that a lane's scores are 16 neighbouring keys. K fragments
@@ -813,7 +814,7 @@ __global__ void __launch_bounds__(128) k_kv4_evict_move(Kv4Args a, Kv4Evict p) {
             const int s = run[r], blk = page[s];
             return blk >= 0 ? vin[(size_t)blk * a.n_kv * (PW / 4) + (from[s] >> 4)] : make_int4(KV4_ZEROS, KV4_ZEROS, KV4_ZEROS, KV4_ZEROS);
         };
-        constexpr int AHEAD = 2;                         // (4 and 6 leave room for fewer CTAs: 105 and 114 us in place of 101)
+        constexpr int AHEAD = 2;                         // (4 and 6 leave room for fewer CTAs: those 16 sequences 103 and 111 us in place of 98; 8 of 16384 40 and 39 in place of 42)
         int4 next[AHEAD];
 #pragma unroll
         for (int r = 0; r < AHEAD; ++r)

@@ -130,14 +130,16 @@ cudaError_t launch_weigh(const DevInfo& di, const Kv4Args& a, Kv4Attn p, const K
 cudaError_t launch_weigh_block(const DevInfo& di, const Kv4Args& a, Kv4Attn p, const Kv4Weigh& w, int d, cudaStream_t s) {
     p.none = KV4_NEG;
     // few tokens: one wave of the single-token form, whose keys are spread over more
-    // CTAs (4 sequences of 16 tokens after 1000, 16 + 8 heads of 128: 13.4 us, 18.7 in
-    // blocks; 32 after 4000 17.1 and 20; 183 after 8000, 32 + 8 of 64: 241 and 118)
+    // CTAs (4 sequences of 16 tokens after 1000, 16 + 8 heads of 128: 13.3 us, 18.7 in
+    // blocks; 32 after 4000 17.0 and 19.7; 183 after 8000, 32 + 8 of 64: 143 and 118)
     if ((long long)p.T * a.n_kv * ((p.G + 3) / 4) <= 4LL * di.sms) return launch_weigh(di, a, p, w, d, s);
     int mp = (p.max_len + 63) >> 6;                                 // pages a token can have, and one for its neighbours
     if (p.window > 0) mp = std::min(mp, ((p.window + 62) >> 6) + 2);
     // CTAs of 4 warps while 16 of them hold the pages (1 x 4096 tokens, 16 + 8 heads
-    // of 128: 482 us, with 8 warps 497, with 16 536), then of 8; past 32768 keys the
-    // scores are not kept at once, and each token goes by itself
+    // of 128: 463 us, with 8 warps 477, with 16 524; 1 x 1000 34, 44 and 66), then of
+    // 8 (512 after 16000 631, with 16 737); past a bound of 32768 keys the scores are
+    // not kept at once, and each token goes by itself (512 after 30000 972 us, after
+    // 40000 1780)
     p.lgC = 0;
     int nw = 4;
     while (mp > (nw * WB_PG) << p.lgC && (2 << p.lgC) <= di.max_cluster) ++p.lgC;

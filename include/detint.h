@@ -385,7 +385,10 @@ int detint_kv4_weigh(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq,
 
 /* The same weights, bit for bit, for many tokens of a sequence, which should
  * stand together: blocks of consecutive tokens of the call share a sweep over
- * their keys on the int8 tensor pipe. Errors: ARG, SHAPE, CUDA. */
+ * their keys on the int8 tensor pipe. Few tokens, and all of a call that allows a
+ * token more than 32768 keys (by max_len, or by window where there is one), are
+ * weighed one by one as by detint_kv4_weigh, so a max_len far above the tokens'
+ * contexts costs time. Errors: ARG, SHAPE, CUDA. */
 int detint_kv4_weigh_block(const detint_kv4_t* c, const int8_t* q8, const int32_t* mq, const int32_t* kq,
                            const int32_t* tok_seq, const int32_t* tok_pos, int n_tok, int max_len, int window,
                            int64_t* weight, detint_stream_t s);
