@@ -407,7 +407,9 @@ int detint_kv4_weigh_block(const detint_kv4_t* c, const int8_t* q8, const int32_
  * detint_kv4_append_axes, and may free the old pages. A token on a page outside
  * the pool weighs 0 and moves as a zero key and value; it, a sequence outside
  * the table, a length outside 0..max_len and a new page outside the pool (which
- * is skipped) set slot 1 of `status`. Errors: ARG, SHAPE, CUDA. */
+ * is skipped) set slot 1 of `status`. Weights that another stream changes during
+ * the call may give any choice, even of fewer than keep tokens, and nothing
+ * worse; the other inputs must not change. Errors: ARG, SHAPE, CUDA. */
 int detint_kv4_evict(const detint_kv4_t* c, int64_t* weight, const int32_t* seq, const int32_t* lens, int n, int max_len,
                      int keep, int sinks, int recent, const int32_t* new_table, int32_t* kept, detint_stream_t s);
 
